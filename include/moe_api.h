@@ -58,8 +58,10 @@ typedef struct CUevent_st* moe_event_t;   /* same type as cudaEvent_t */
  * INT4 (expert weights only): 4-bit two's complement codes q in [-8, 7], eight
  * consecutive K elements per little-endian 32-bit word, element e of the word in
  * nibble (e even ? e/2 : 4 + e/2); one bf16 scale s per (weight row, 128 K
- * elements); the weight is q * s rounded once to bf16 (nearest even). */
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_INT4 = 3 } moe_dtype;
+ * elements); the weight is q * s rounded once to bf16 (nearest even).
+ * E4M3_B128 (expert weights only): E4M3 codes with one fp32 scale per block of 128 weight
+ * rows x 128 K elements. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_INT4 = 3, MOE_E4M3_B128 = 4 } moe_dtype;
 
 /* Return codes (0 or negative). */
 enum {
@@ -203,6 +205,36 @@ MOE_API int moe_route(const void* hidden, const void* router_w, int T, int H, in
 MOE_API int moe_topk_from_logits(const float* logits, int T, int E, int topk, int renorm, float* topk_w,
                          int32_t* topk_ids, moe_stream_t stream);
 
+/* Routing by expert groups, as fine-grained expert layers use it.  For one token with logits l:
+ *   s = sigmoid(l) (MOE_SCORE_SIGMOID) or softmax(l) over all E (MOE_SCORE_SOFTMAX);
+ *   r = s + bias (bias [E] fp32, nullable: it steers the choice, never the weights);
+ *   the experts form n_group groups of E / n_group consecutive ones; a group's score is its
+ *   largest r (group_sum == 1) or the sum of its two largest (group_sum == 2);
+ *   ids = the topk largest r among the topk_group best groups, in descending order;
+ *   w = s[ids], divided by their sum when renorm != 0 (0 where that sum is 0), times scale.
+ * Equal values rank the lower group and the lower expert first; a NaN ranks like -inf.  Softmax
+ * scores without a bias rank by their logits (the same order; group_sum == 2 adds scores and so
+ * ranks by them), which makes n_group == 1 the ranking of moe_topk_from_logits.  fp32 throughout. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct {
+  int score;      /* MOE_SCORE_* */
+  int n_group;    /* 1 <= n_group <= 32, E % n_group == 0 */
+  int topk_group; /* 1 <= topk_group <= n_group, topk <= topk_group * (E / n_group) */
+  int group_sum;  /* 1 or 2 */
+  int renorm;
+  float scale;
+} moe_route_rule;
+/* From given fp32 logits [T][E]: topk_w [T][topk] fp32, topk_ids [T][topk] int32.  rule is
+ * required.  Limits as moe_route (topk <= 32, E <= 1024); MOE_ERR_ARG for a rule outside the
+ * ranges above.  bias 4-byte aligned, the other pointers 16. */
+MOE_API int moe_topk_grouped(const float* logits, const float* bias, int T, int E, int topk,
+                             const moe_route_rule* rule, float* topk_w, int32_t* topk_ids, moe_stream_t stream);
+/* moe_route with the rule above: logits_out [T][E] = hidden . router_w^T as there, then
+ * moe_topk_grouped on them. */
+MOE_API int moe_route_grouped(const void* hidden, const void* router_w, const float* bias, int T, int H, int E,
+                              int topk, const moe_route_rule* rule, moe_dtype act_dtype, float* logits_out,
+                              float* topk_w, int32_t* topk_ids, moe_stream_t stream);
+
 /* Step 3: token-to-expert permutation
  *   ("FusedMoE vs MegaMoE", section 3.1: sort routed tokens by expert and
  *    build the index of which rows belong to which expert; page 1, section
@@ -231,7 +263,9 @@ MOE_API int moe_align(const int32_t* topk_ids, int T, int topk, int E, int block
  *   w2       [E][H][I]   w_dtype
  *   w13_scale, w2_scale  MOE_E4M3 weights: [E] fp32 per-expert dequantisation scales;
  *                        MOE_INT4 weights: bf16 group scales, group-major per expert,
- *                        [E][H/128][2I] and [E][I/128][H]; ignored otherwise
+ *                        [E][H/128][2I] and [E][I/128][H];
+ *                        MOE_E4M3_B128 weights: fp32 block scales [E][2I/128][H/128] and
+ *                        [E][H/128][I/128]; ignored otherwise
  *   (MOE_INT4: w13 [E][2I][H/2] and w2 [E][H][I/2] bytes of packed codes)
  *   out      [T][H]      act_dtype
  *   workspace            >= moe_workspace_size(...) bytes, 256-byte aligned, contents ignored
@@ -247,6 +281,9 @@ MOE_API int moe_align(const int32_t* topk_ids, int T, int topk, int E, int block
  *                from there; "FusedMoE vs MegaMoE", section 6.3: quantised expert
  *                weights); SWAP_AB orientation only,
  *                T <= 128, H % 256 == 0 and I % 256 == 0 (else MOE_ERR_UNSUPPORTED)
+ *   (BF16, E4M3_B128) tcgen05 kind::f8f6f4 path: input and intermediate are quantised by
+ *                blocks of 128 columns per token (moe_quant_block), every K block's products
+ *                are scaled and summed in fp32; options split_k and act_split are ignored
  *   tensor-core paths need H % 128 == 0 and I % 128 == 0.
  * The intermediate SiLU(gate)*up is stored in bf16 (as a bf16 hi + lo pair in SWAP_AB
  * mode, see moe_options.act_split; fp32 on the fp32 path; e4m3 on the FP8 path);
@@ -306,6 +343,32 @@ MOE_API int moe_forward_host(const void* hidden_host, void* hidden_dev, const vo
 MOE_API int moe_inv_rope_fp8_quant(const void* x, int T, int heads, int head_dim, int rot_dim,
                                    const int32_t* positions, const float* cos_sin, int max_pos, uint8_t* q_out,
                                    float* scale_out, moe_stream_t stream);
+
+/* Quantisation to e4m3 by blocks: for each row t and block b of 128 consecutive columns (the last
+ * block of a row may be shorter),
+ *   a = max |x| of the block;  scale[t][b] = max(a * c, 2^-126) with c = 1/448 in fp32, 1 where a = 0;
+ *   q[t][i] = e4m3(x[t][i] * r), r = 1 / scale[t][b] once per block (nearest even, saturating);
+ * both products and the reciprocal are one fp32 rounding each.  A block holding a NaN
+ * or an infinity gets that as its scale, and its codes stand for no finite value.
+ *   x [T][K] MOE_F32 or MOE_BF16;  q [T][K] e4m3 codes;  scale [T][ceil(K/128)] fp32
+ * K % 16 == 0 (MOE_ERR_UNSUPPORTED otherwise); scale 4-byte aligned, x and q 16. */
+MOE_API int moe_quant_block(const void* x, int T, int K, moe_dtype x_dtype, uint8_t* q, float* scale,
+                            moe_stream_t stream);
+/* The same of h = SiLU(g) * u (fp32, not rounded in between), with gate_up [T][2I] holding the row
+ * [g | u]: q [T][I], scale [T][ceil(I/128)].  I % 16 == 0. */
+MOE_API int moe_silu_quant_block(const void* gate_up, int T, int I, moe_dtype x_dtype, uint8_t* q, float* scale,
+                                 moe_stream_t stream);
+
+/* Matrix product of block-scaled e4m3 operands:
+ *   out[t][n] = sum_b a_scale[t][b] * w_scale[n/128][b] * sum_{k in block b} a[t][k] * w[n][k]
+ * over the blocks b of 128 k (the last may be shorter); products exact, sums fp32, one rounding to
+ * out_dtype.
+ *   a [T][K] e4m3, a_scale [T][ceil(K/128)] (moe_quant_block's outputs)
+ *   w [N][K] e4m3, w_scale [ceil(N/128)][ceil(K/128)];  out [T][N] MOE_BF16 or MOE_F32
+ * Any T >= 0 and N >= 1, K % 16 == 0 (MOE_ERR_UNSUPPORTED otherwise).  No workspace.  Scales 4-byte
+ * aligned, the other pointers 16. */
+MOE_API int moe_gemm_block(const void* a, const float* a_scale, const void* w, const float* w_scale, int T, int N,
+                           int K, moe_dtype out_dtype, void* out, moe_stream_t stream);
 
 /* Steps 3-7 of the layer on a routing the caller provides (its own router, or
  * expert ids remapped to the slots of an expert cache): the same permutation,

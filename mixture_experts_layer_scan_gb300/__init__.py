@@ -17,7 +17,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_gb300.so")
 
-MOE_F32, MOE_BF16, MOE_E4M3, MOE_INT4 = 0, 1, 2, 3
+MOE_F32, MOE_BF16, MOE_E4M3, MOE_INT4, MOE_E4M3_B128 = 0, 1, 2, 3, 4
 MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, -1, -2, -3
 MOE_ERR_CUDA, MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_DEVICE_INDEX, MOE_ERR_ALIGNMENT = -4, -5, -6, -7
 ORIENT_AUTO, ORIENT_SWAP_AB, ORIENT_TOKEN_MAJOR = 0, 1, 2
@@ -33,7 +33,8 @@ EXPORTS = ("moe_strerror", "moe_workspace_size", "moe_plan_info", "moe_align_cap
            "moe_topk_from_logits", "moe_align", "moe_forward", "moe_forward_noalloc", "moe_get_status",
            "moe_version", "moe_inv_rope_fp8_quant", "moe_forward_routed", "moe_cache_create", "moe_cache_destroy",
            "moe_cache_workspace_size", "moe_forward_cached", "moe_cache_stats", "moe_cache_lru_plan",
-           "moe_cache_set_copy_mode", "moe_copy_from_host", "moe_forward_host")
+           "moe_cache_set_copy_mode", "moe_copy_from_host", "moe_forward_host", "moe_topk_grouped",
+           "moe_route_grouped", "moe_quant_block", "moe_silu_quant_block", "moe_gemm_block")
 NOALLOC_MAX_WORKSPACE = 32 << 20
 
 
@@ -54,6 +55,14 @@ class moe_plan(ctypes.Structure):
     _fields_ = [("orientation", ctypes.c_int), ("block", ctypes.c_int), ("splits_gemm1", ctypes.c_int),
                 ("splits_gemm2", ctypes.c_int), ("act_split", ctypes.c_int), ("kernel_launches", ctypes.c_int),
                 ("single_launch", ctypes.c_int), ("workspace_bytes", ctypes.c_size_t), ("cta_pair", ctypes.c_int)]
+
+
+class moe_route_rule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("n_group", ctypes.c_int), ("topk_group", ctypes.c_int),
+                ("group_sum", ctypes.c_int), ("renorm", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 class moe_cache_stats_t(ctypes.Structure):
@@ -113,6 +122,16 @@ def _load():
                                        ctypes.POINTER(ctypes.c_ulonglong)]
     lib.moe_inv_rope_fp8_quant.restype = i
     lib.moe_inv_rope_fp8_quant.argtypes = [P, i, i, i, i, P, P, i, P, P, P]
+    lib.moe_topk_grouped.restype = i
+    lib.moe_topk_grouped.argtypes = [P, P, i, i, i, ctypes.POINTER(moe_route_rule), P, P, P]
+    lib.moe_route_grouped.restype = i
+    lib.moe_route_grouped.argtypes = [P, P, P, i, i, i, i, ctypes.POINTER(moe_route_rule), i, P, P, P, P]
+    lib.moe_quant_block.restype = i
+    lib.moe_quant_block.argtypes = [P, i, i, i, P, P, P]
+    lib.moe_silu_quant_block.restype = i
+    lib.moe_silu_quant_block.argtypes = [P, i, i, i, P, P, P]
+    lib.moe_gemm_block.restype = i
+    lib.moe_gemm_block.argtypes = [P, P, P, P, i, i, i, i, P, P]
     return lib
 
 
@@ -220,6 +239,91 @@ def moe_topk_from_logits(logits: torch.Tensor, topk: int, renorm: bool, topk_w=N
     return topk_w, topk_ids
 
 
+def _route_rule(E: int, score: str, n_group: int, topk_group: Optional[int], group_sum: int, renorm: bool,
+                scale: float) -> moe_route_rule:
+    return moe_route_rule(SCORES[score], n_group, n_group if topk_group is None else topk_group, group_sum,
+                          int(bool(renorm)), float(scale))
+
+
+def moe_topk_grouped(logits: torch.Tensor, topk: int, bias=None, score: str = "sigmoid", n_group: int = 1,
+                     topk_group: Optional[int] = None, group_sum: int = 2, renorm: bool = True, scale: float = 1.0,
+                     topk_w=None, topk_ids=None, stream=None):
+    """Routing by expert groups from fp32 logits [T,E]: (weights fp32 [T,topk], ids int32 [T,topk]).
+
+    score: "sigmoid" or "softmax"; bias: fp32 [E] added for the choice only; the topk_group best of
+    n_group groups are kept (topk_group None: all), a group scored by the sum of its group_sum largest."""
+    T, E = logits.shape
+    if logits.dtype != torch.float32 or (bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,))):
+        raise ValueError("logits must be float32 [T, E] and bias float32 [E]")
+    dev = logits.device
+    topk_w = torch.empty(T, topk, dtype=torch.float32, device=dev) if topk_w is None else topk_w
+    topk_ids = torch.empty(T, topk, dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
+    rule = _route_rule(E, score, n_group, topk_group, group_sum, renorm, scale)
+    _check(_lib.moe_topk_grouped(_p(logits), _p(bias), T, E, topk, ctypes.byref(rule), _p(topk_w), _p(topk_ids),
+                                 _stream(stream)), "moe_topk_grouped")
+    return topk_w, topk_ids
+
+
+def moe_route_grouped(hidden: torch.Tensor, router_w: torch.Tensor, topk: int, bias=None, score: str = "sigmoid",
+                      n_group: int = 1, topk_group: Optional[int] = None, group_sum: int = 2, renorm: bool = True,
+                      scale: float = 1.0, logits=None, topk_w=None, topk_ids=None, stream=None):
+    """moe_topk_grouped on the router logits hidden . router_w^T: (logits [T,E], weights, ids)."""
+    T, H = hidden.shape
+    E = router_w.shape[0]
+    if router_w.shape != (E, H) or router_w.dtype != hidden.dtype or (
+            bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,))):
+        raise ValueError("router_w must be [E, H] of hidden's type and bias float32 [E]")
+    dev = hidden.device
+    logits = torch.empty(T, E, dtype=torch.float32, device=dev) if logits is None else logits
+    topk_w = torch.empty(T, topk, dtype=torch.float32, device=dev) if topk_w is None else topk_w
+    topk_ids = torch.empty(T, topk, dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
+    rule = _route_rule(E, score, n_group, topk_group, group_sum, renorm, scale)
+    _check(_lib.moe_route_grouped(_p(hidden), _p(router_w), _p(bias), T, H, E, topk, ctypes.byref(rule), _dt(hidden),
+                                  _p(logits), _p(topk_w), _p(topk_ids), _stream(stream)), "moe_route_grouped")
+    return logits, topk_w, topk_ids
+
+
+def moe_quant_block(x: torch.Tensor, q=None, scale=None, stream=None):
+    """e4m3 codes [T,K] (float8_e4m3fn) and float32 scales [T,ceil(K/128)] of x [T,K] by blocks of 128 columns."""
+    T, K = x.shape
+    q = torch.empty(T, K, dtype=torch.float8_e4m3fn, device=x.device) if q is None else q
+    scale = torch.empty(T, (K + 127) // 128, dtype=torch.float32, device=x.device) if scale is None else scale
+    _check(_lib.moe_quant_block(_p(x), T, K, _dt(x), _p(q), _p(scale), _stream(stream)), "moe_quant_block")
+    return q, scale
+
+
+def moe_silu_quant_block(gate_up: torch.Tensor, q=None, scale=None, stream=None):
+    """moe_quant_block of SiLU(g) * u for rows [g | u] of gate_up [T, 2I]: codes [T,I], scales [T,ceil(I/128)]."""
+    T, two_i = gate_up.shape
+    if two_i % 2:
+        raise ValueError("gate_up must be [T, 2 I]")
+    I = two_i // 2
+    dev = gate_up.device
+    q = torch.empty(T, I, dtype=torch.float8_e4m3fn, device=dev) if q is None else q
+    scale = torch.empty(T, (I + 127) // 128, dtype=torch.float32, device=dev) if scale is None else scale
+    _check(_lib.moe_silu_quant_block(_p(gate_up), T, I, _dt(gate_up), _p(q), _p(scale), _stream(stream)),
+           "moe_silu_quant_block")
+    return q, scale
+
+
+def moe_gemm_block(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                   out_dtype: torch.dtype = torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """a [T,K] . w [N,K]^T of block-scaled e4m3 operands -> out [T,N] (bfloat16 or float32).
+
+    a_scale float32 [T,ceil(K/128)] (moe_quant_block), w_scale float32 [ceil(N/128),ceil(K/128)]."""
+    T, K = a.shape
+    N = w.shape[0]
+    kb = (K + 127) // 128
+    if w.shape != (N, K) or a_scale.shape != (T, kb) or w_scale.shape != ((N + 127) // 128, kb):
+        raise ValueError("inconsistent shapes")
+    if _dt(a) != MOE_E4M3 or _dt(w) != MOE_E4M3 or a_scale.dtype != torch.float32 or w_scale.dtype != torch.float32:
+        raise ValueError("a and w must be e4m3 codes with float32 scales")
+    out = torch.empty(T, N, dtype=out_dtype, device=a.device) if out is None else out
+    _check(_lib.moe_gemm_block(_p(a), _p(a_scale), _p(w), _p(w_scale), T, N, K, _dt(out), _p(out), _stream(stream)),
+           "moe_gemm_block")
+    return out
+
+
 def moe_align(topk_ids: torch.Tensor, E: int, block: int, stream=None, with_counts: bool = True):
     """(sorted_ids, expert_ids, num_post_pad[1], expert_counts) as full-capacity int32 device tensors."""
     T, k = topk_ids.shape
@@ -234,20 +338,37 @@ def moe_align(topk_ids: torch.Tensor, E: int, block: int, stream=None, with_coun
     return sorted_ids, expert_ids, npp[:1], counts
 
 
+def _w_dtype(w13: torch.Tensor, w_format: Optional[str]) -> int:
+    if w_format is None:
+        return _dt(w13)
+    return {"int4": MOE_INT4, "e4m3_block": MOE_E4M3_B128}[w_format]
+
+
+def _check_block_scales(w_format, E, H, I, w13_scale, w2_scale) -> None:
+    if w_format != "e4m3_block":
+        return
+    for s, shape in ((w13_scale, (E, 2 * I // 128, H // 128)), (w2_scale, (E, H // 128, I // 128))):
+        if s is None or s.dtype != torch.float32 or tuple(s.shape) != shape:
+            raise ValueError(f"block scales must be float32 {shape}")
+
+
 def moe_forward(hidden: torch.Tensor, router_w: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, topk: int,
                 renorm: bool, w13_scale=None, w2_scale=None, out=None, workspace=None, options=None, stream=None,
                 w_format=None):
     """One fused MoE layer forward; returns out [T,H] in the activation dtype.
 
     w_format="int4": w13 [E,2I,H/2] and w2 [E,H,I/2] are packed INT4 codes (uint8) with bf16 group
-    scales, group-major per expert: w13_scale [E,H/128,2I] and w2_scale [E,I/128,H]."""
+    scales, group-major per expert: w13_scale [E,H/128,2I] and w2_scale [E,I/128,H].
+    w_format="e4m3_block": w13 and w2 are e4m3 codes with one float32 scale per 128 x 128 block:
+    w13_scale [E,2I/128,H/128] and w2_scale [E,H/128,I/128]."""
     T, H = hidden.shape
     E, twoI, H2 = w13.shape
     I = twoI // 2
     div = 2 if w_format == "int4" else 1
     if H2 * div != H or w2.shape != (E, H, I // div) or router_w.shape != (E, H):
         raise ValueError("inconsistent shapes")
-    act, wdt = _dt(hidden), (MOE_INT4 if w_format == "int4" else _dt(w13))
+    _check_block_scales(w_format, E, H, I, w13_scale, w2_scale)
+    act, wdt = _dt(hidden), _w_dtype(w13, w_format)
     opts = _opts(options)
     need = moe_workspace_size(T, H, I, E, topk, act, wdt, options)
     if workspace is None:
@@ -272,8 +393,9 @@ def moe_forward_host(hidden_host: torch.Tensor, router_w: torch.Tensor, w13: tor
     div = 2 if w_format == "int4" else 1
     if H2 * div != H or w2.shape != (E, H, I // div) or router_w.shape != (E, H):
         raise ValueError("inconsistent shapes")
+    _check_block_scales(w_format, E, H, I, w13_scale, w2_scale)
     dev = router_w.device
-    act, wdt = _dt(hidden_host), (MOE_INT4 if w_format == "int4" else _dt(w13))
+    act, wdt = _dt(hidden_host), _w_dtype(w13, w_format)
     need = moe_workspace_size(T, H, I, E, topk, act, wdt, options)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -301,7 +423,8 @@ def moe_forward_noalloc(hidden: torch.Tensor, router_w: torch.Tensor, w13: torch
     div = 2 if w_format == "int4" else 1
     if H2 * div != H or w2.shape != (E, H, I // div) or router_w.shape != (E, H):
         raise ValueError("inconsistent shapes")
-    wdt = MOE_INT4 if w_format == "int4" else _dt(w13)
+    _check_block_scales(w_format, E, H, I, w13_scale, w2_scale)
+    wdt = _w_dtype(w13, w_format)
     out = torch.empty_like(hidden) if out is None else out
     _check(_lib.moe_forward_noalloc(_p(hidden), _p(router_w), _p(w13), _p(w2), T, H, I, E, topk, int(bool(renorm)),
                                     _dt(hidden), wdt, _p(w13_scale), _p(w2_scale), _p(out), _opts(options),
@@ -330,13 +453,16 @@ def moe_inv_rope_fp8_quant(x: torch.Tensor, positions: torch.Tensor, cos_sin: to
 
 def moe_forward_routed(hidden: torch.Tensor, topk_w: torch.Tensor, topk_ids: torch.Tensor, w13: torch.Tensor,
                        w2: torch.Tensor, w13_scale=None, w2_scale=None, out=None, workspace=None, options=None,
-                       stream=None):
-    """Steps 3-7 of the layer on a given routing (topk_w fp32 [T,k], topk_ids int32 [T,k])."""
+                       stream=None, w_format=None):
+    """Steps 3-7 of the layer on a given routing (topk_w fp32 [T,k], topk_ids int32 [T,k]).
+
+    w_format="e4m3_block": e4m3 weights with a scale per 128 x 128 block, as in moe_forward."""
     T, H = hidden.shape
     E, twoI, _ = w13.shape
     I = twoI // 2
     k = topk_ids.shape[1]
-    act, wdt = _dt(hidden), _dt(w13)
+    _check_block_scales(w_format, E, H, I, w13_scale, w2_scale)
+    act, wdt = _dt(hidden), _w_dtype(w13, w_format)
     o = dict(options or {})
     o["single_launch"] = 2
     need = moe_workspace_size(T, H, I, E, k, act, wdt, o)

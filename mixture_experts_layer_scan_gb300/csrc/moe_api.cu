@@ -50,6 +50,8 @@ constexpr int kRouterTcMinTokens = 256;
 constexpr int kGatherTokenOrderMinTokens = 4096;
 // Largest swap-AB activation tile whose rows GEMM1 gathers itself.
 constexpr int kGatherInGemmMaxRows = 32;
+// Largest batch of the block-scaled swap-AB products (tokens of one tile).
+constexpr int kBlockSwapMaxTokens = 64;
 // Single-launch decode kernel limits (shared-memory tables, one token column per epilogue thread).
 constexpr int kFusedMaxTokens = 64;
 constexpr int kFusedMaxPairs = 512;
@@ -61,7 +63,7 @@ constexpr int kFinMaxTokens = 8;
 // moe_options.single_launch == 0 picks the single-launch kernel for eligible shapes.
 constexpr bool kFusedAuto = false;
 
-enum Path { PATH_F32 = 0, PATH_BF16 = 1, PATH_FP8 = 2, PATH_W4 = 3 };
+enum Path { PATH_F32 = 0, PATH_BF16 = 1, PATH_FP8 = 2, PATH_W4 = 3, PATH_BLK = 4 };
 
 struct Plan {
   int path = 0;
@@ -78,6 +80,7 @@ struct Plan {
   bool pair = false;            // token-major GEMMs on CTA pairs (256-row permutation blocks)
   bool fin = false;             // bf16 swap-AB GEMM1 splits summed by the last-arriving CTA (no reduction kernel)
   size_t o_sync = 0;
+  size_t o_xscale = 0, o_ascale = 0;  // block scales of the gathered input and of the intermediate
   size_t o_logits = 0, o_tw = 0, o_tid = 0, o_meta = 0, o_sorted = 0, o_eids = 0, o_xs = 0, o_aint = 0, o_af32 = 0,
          o_p1 = 0, o_y = 0, o_misc = 0, o_pblk = 0, o_fin = 0, o_inv = 0, total = 0;
   size_t p1_stride = 0, y_stride = 0;
@@ -165,8 +168,10 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
     p.path = PATH_FP8;
   } else if (act == MOE_BF16 && w == MOE_INT4) {
     p.path = PATH_W4;
+  } else if (act == MOE_BF16 && w == MOE_E4M3_B128) {
+    p.path = PATH_BLK;
   } else {
-    return (act > MOE_INT4 || w > MOE_INT4 || act < 0 || w < 0) ? MOE_ERR_ARG : MOE_ERR_UNSUPPORTED;
+    return (act > MOE_E4M3_B128 || w > MOE_E4M3_B128 || act < 0 || w < 0) ? MOE_ERR_ARG : MOE_ERR_UNSUPPORTED;
   }
   const int orient = opts ? opts->orientation : MOE_ORIENT_AUTO;
   if (orient < 0 || orient > 2) return MOE_ERR_ARG;
@@ -178,10 +183,19 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
     p.swap = orient == MOE_ORIENT_SWAP_AB ||
              (orient == MOE_ORIENT_AUTO && (T <= 64 || (p.path == PATH_W4 && T <= 128)));
     if (p.swap && T > 256) return MOE_ERR_UNSUPPORTED;
+    // block-scaled weights: a swap-AB tile holds all of an expert's tokens
+    if (p.path == PATH_BLK && p.swap && T > kBlockSwapMaxTokens) return MOE_ERR_UNSUPPORTED;
     // INT4 weights: swap-AB batches of up to 128 tokens, whole 256-row weight tiles
     if (p.path == PATH_W4 && (!p.swap || T > 128 || H % 256 || I % 256)) return MOE_ERR_UNSUPPORTED;
-    const int eb = p.path == PATH_FP8 ? 1 : 2;
-    if (p.swap) {
+    const int eb = (p.path == PATH_FP8 || p.path == PATH_BLK) ? 1 : 2;
+    if (p.path == PATH_BLK) {
+      if (opts && (opts->cta_pair < 0 || opts->cta_pair > 2 || opts->split_k < 0)) return MOE_ERR_ARG;
+      if (opts && opts->cta_pair == 1) return MOE_ERR_UNSUPPORTED;
+      p.B = p.swap ? 16 : kBlockSwapMaxTokens;
+      p.xbox = p.swap ? (T <= 16 ? 16 : T <= 32 ? 32 : 64) : kBlockSwapMaxTokens;
+      p.kb1 = H / 128;
+      p.kb2 = I / 128;
+    } else if (p.swap) {
       p.B = 16;
       p.xbox = std::max(16, (T + 15) / 16 * 16);
       const long act_upper = std::min<long>(E, n);
@@ -223,7 +237,7 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
     // GEMM1 gathers token rows itself (one tile::gather4 per 4 rows) when the
     // activation tile is short; for wider tiles the per-stage TMA instruction
     // count outweighs the saved kernel, so rows are gathered beforehand.
-    p.gather_in_gemm = p.swap && p.xbox <= kGatherInGemmMaxRows;
+    p.gather_in_gemm = p.swap && p.xbox <= kGatherInGemmMaxRows && p.path != PATH_BLK;
   } else {
     p.B = 16;
     p.swap = false;
@@ -251,7 +265,7 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
     o = align_up(o + std::max<size_t>(bytes, 1), A);
     return at;
   };
-  const size_t xb = p.path == PATH_F32 ? 4 : (p.path == PATH_FP8 ? 1 : 2);  // activation element bytes
+  const size_t xb = p.path == PATH_F32 ? 4 : (p.path == PATH_FP8 || p.path == PATH_BLK) ? 1 : 2;  // activation element bytes
   p.o_logits = take((size_t)T * E * 4);
   p.o_tw = take((size_t)n * 4);
   p.o_tid = take((size_t)n * 4);
@@ -264,6 +278,10 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
   if (p.gather_in_gemm) xs_bytes = p.path == PATH_FP8 ? (size_t)T * H : 0;  // token order (FP8: e4m3 copy)
   p.o_xs = take(xs_bytes);
   p.o_aint = take((size_t)p.cap * I * xb * (p.act_split ? 2 : 1));
+  if (p.path == PATH_BLK) {
+    p.o_xscale = take((size_t)p.cap * (H / 128) * 4);
+    p.o_ascale = take((size_t)p.cap * (I / 128) * 4);
+  }
   if (p.path == PATH_FP8) p.o_af32 = take((size_t)p.cap * I * 4);
   if (p.s1 > 1) {
     p.p1_stride = (size_t)n * 2 * I;
@@ -273,8 +291,9 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
   p.o_y = take(p.y_stride * p.s2 * (p.y_bf16 ? 2 : 4));
   p.o_misc = take(256);
   if (p.pair) p.o_pblk = take((size_t)std::max<long>(p.nblk_cap, 1) * 4);
-  // pair -> sorted row, for the token-order gather of long batches
-  if (p.gather_in_gemm || p.path == PATH_FP8 || T < kGatherTokenOrderMinTokens) p.o_inv = 0;
+  // pair -> sorted row, for the token-order gather of long batches and the block quantisation
+  if (p.path == PATH_BLK) p.o_inv = take((size_t)n * 4);
+  else if (p.gather_in_gemm || p.path == PATH_FP8 || T < kGatherTokenOrderMinTokens) p.o_inv = 0;
   else p.o_inv = take((size_t)n * 4);
   // (the last arriver sums the splits token by token: a chain of L2 round trips that
   // outgrows the separate reduction kernel past a few tokens)
@@ -366,6 +385,8 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
   void* aint = ws + pl.o_aint;
   float* af32 = reinterpret_cast<float*>(ws + pl.o_af32);
   float* p1 = reinterpret_cast<float*>(ws + pl.o_p1);
+  float* xscale = reinterpret_cast<float*>(ws + pl.o_xscale);
+  float* ascale = reinterpret_cast<float*>(ws + pl.o_ascale);
   void* y = ws + pl.o_y;
   unsigned* amax = reinterpret_cast<unsigned*>(ws + pl.o_misc);  // [0] input amax, [1] intermediate amax
   int* flag = reinterpret_cast<int*>(ws + pl.o_misc + 64);
@@ -476,7 +497,9 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
   // 4. activations: the fp32 path gathers rows into expert order here; the
   // tensor-core paths gather inside GEMM1 (FP8: quantise the input to e4m3 first)
   if (o) record(o->stage_begin[MOE_STAGE_GATHER], s);
-  if (pl.path == PATH_FP8) {
+  if (pl.path == PATH_BLK) {
+    MOE_TRY(launch_quant_block_scatter(hidden, T, H, topk, inv, (uint8_t*)xs, xscale, s));
+  } else if (pl.path == PATH_FP8) {
     MOE_TRY(launch_amax_bf16(hidden, (size_t)T * H, amax, s));
     if (pl.gather_in_gemm)
       MOE_TRY(launch_quant_x(hidden, (size_t)T * H, amax, (uint8_t*)xs, s));
@@ -497,6 +520,50 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
     if (o) record(o->stage_begin[MOE_STAGE_GEMM2], s);
     MOE_TRY(launch_gemm2_simt((const float*)aint, (const float*)w2, H, I, pl.B, T, topk, sorted, eids, meta, cap,
                               (float*)y, s));
+    if (o) record(o->stage_end[MOE_STAGE_GEMM2], s);
+  } else if (pl.path == PATH_BLK) {
+    BlockGemmArgs g = {};
+    g.T = T;
+    g.k = topk;
+    g.E = E;
+    g.cap = cap;
+    g.nt = pl.xbox;
+    g.by_block = !pl.swap;
+    g.sorted = sorted;
+    g.eids = eids;
+    g.meta = meta;
+    g.status = st;
+    g.num_sms = sms;
+    // 5. GEMM1 on w13, its epilogue forming the e4m3 blocks of SiLU(gate)*up
+    BlockGemmArgs g1 = g;
+    g1.epi = BG_EPI_G1;
+    g1.K = H;
+    g1.n_out = I;
+    g1.w_rows = 2 * I;
+    g1.x = xs;
+    g1.a_scale = xscale;
+    g1.w = w13;
+    g1.w_scale = static_cast<const float*>(w13_scale);
+    g1.out = aint;
+    g1.out_scale = ascale;
+    if (o) record(o->stage_begin[MOE_STAGE_GEMM1], s);
+    MOE_TRY(launch_gemm_block(g1, s));
+    if (o) record(o->stage_end[MOE_STAGE_GEMM1], s);
+    if (o) record(o->stage_begin[MOE_STAGE_ACT], s);
+    if (o) record(o->stage_end[MOE_STAGE_ACT], s);
+    // 6. GEMM2 on w2
+    BlockGemmArgs g2 = g;
+    g2.epi = BG_EPI_G2;
+    g2.K = I;
+    g2.n_out = H;
+    g2.w_rows = H;
+    g2.x = aint;
+    g2.a_scale = ascale;
+    g2.w = w2;
+    g2.w_scale = static_cast<const float*>(w2_scale);
+    g2.out = y;
+    if (o) record(o->stage_begin[MOE_STAGE_GEMM2], s);
+    MOE_TRY(launch_gemm_block(g2, s));
     if (o) record(o->stage_end[MOE_STAGE_GEMM2], s);
   } else {
     const bool fp8 = pl.path == PATH_FP8;
@@ -715,6 +782,48 @@ int moe_topk_from_logits(const float* logits, int T, int E, int topk, int renorm
   return cuda_rc(launch_topk(logits, T, E, topk, renorm != 0, topk_w, topk_ids, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+static int check_route_rule(const moe_route_rule* r, int E, int topk) {
+  if (!r || (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID)) return MOE_ERR_ARG;
+  if (r->n_group < 1 || r->n_group > 32 || E % r->n_group) return MOE_ERR_ARG;
+  if (r->topk_group < 1 || r->topk_group > r->n_group || topk > r->topk_group * (E / r->n_group)) return MOE_ERR_ARG;
+  if (r->group_sum != 1 && r->group_sum != 2) return MOE_ERR_ARG;
+  return MOE_OK;
+}
+
+int moe_topk_grouped(const float* logits, const float* bias, int T, int E, int topk, const moe_route_rule* rule,
+                     float* topk_w, int32_t* topk_ids, moe_stream_t stream) {
+  if (T < 0 || E < 1 || E > 1024 || topk < 1 || topk > E || topk > 32) return MOE_ERR_ARG;
+  const int rc = check_route_rule(rule, E, topk);
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_w || !topk_ids) return MOE_ERR_ARG;
+  if (misaligned(logits) || misaligned(topk_w) || misaligned(topk_ids) || (bias && misaligned(bias, 4)))
+    return MOE_ERR_ALIGNMENT;
+  return cuda_rc(launch_topk_grouped(logits, bias, T, E, topk, *rule, topk_w, topk_ids,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_route_grouped(const void* hidden, const void* router_w, const float* bias, int T, int H, int E, int topk,
+                      const moe_route_rule* rule, moe_dtype act_dtype, float* logits_out, float* topk_w,
+                      int32_t* topk_ids, moe_stream_t stream) {
+  if (T < 0 || H < 1 || E < 1 || E > 1024 || topk < 1 || topk > E || topk > 32) return MOE_ERR_ARG;
+  const int rc = check_route_rule(rule, E, topk);
+  if (rc) return rc;
+  if (act_dtype != MOE_F32 && act_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (H % (act_dtype == MOE_BF16 ? 8 : 4)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!hidden || !router_w || !logits_out || !topk_w || !topk_ids) return MOE_ERR_ARG;
+  if (misaligned(hidden) || misaligned(router_w) || misaligned(logits_out) || misaligned(topk_w) ||
+      misaligned(topk_ids) || (bias && misaligned(bias, 4)))
+    return MOE_ERR_ALIGNMENT;
+  int* st = status_word();
+  if (!st) return MOE_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_router(hidden, router_w, T, H, E, act_dtype, logits_out, st, s);
+  if (e == cudaSuccess) e = launch_topk_grouped(logits_out, bias, T, E, topk, *rule, topk_w, topk_ids, s);
+  return cuda_rc(e);
+}
+
 int moe_align(const int32_t* topk_ids, int T, int topk, int E, int block, int32_t* sorted_ids, int32_t* expert_ids,
               int32_t* num_post_pad, int32_t* expert_counts, moe_stream_t stream) {
   if (T < 0 || topk < 1 || E < 1 || E > 1024 || block < 1 || block > 1024) return MOE_ERR_ARG;
@@ -740,7 +849,7 @@ int moe_forward(const void* hidden, const void* router_w, const void* w13, const
   if (rc) return rc;
   if (T == 0) return MOE_OK;
   if (!hidden || !router_w || !w13 || !w2 || !out || !workspace) return MOE_ERR_ARG;
-  if ((pl.path == PATH_FP8 || pl.path == PATH_W4) && (!w13_scale || !w2_scale)) return MOE_ERR_ARG;
+  if ((pl.path == PATH_FP8 || pl.path == PATH_W4 || pl.path == PATH_BLK) && (!w13_scale || !w2_scale)) return MOE_ERR_ARG;
   if (misaligned(hidden) || misaligned(router_w) || misaligned(w13) || misaligned(w2) || misaligned(out) ||
       misaligned(workspace, 256) || (w13_scale && misaligned(w13_scale, 4)) || (w2_scale && misaligned(w2_scale, 4)))
     return MOE_ERR_ALIGNMENT;
@@ -806,7 +915,7 @@ int moe_forward_routed(const void* hidden, const float* topk_w, const int32_t* t
   if (rc) return rc;
   if (T == 0) return MOE_OK;
   if (!hidden || !topk_w || !topk_ids || !w13 || !w2 || !out || !workspace) return MOE_ERR_ARG;
-  if ((pl.path == PATH_FP8 || pl.path == PATH_W4) && (!w13_scale || !w2_scale)) return MOE_ERR_ARG;
+  if ((pl.path == PATH_FP8 || pl.path == PATH_W4 || pl.path == PATH_BLK) && (!w13_scale || !w2_scale)) return MOE_ERR_ARG;
   if (misaligned(hidden) || misaligned(topk_w, 4) || misaligned(topk_ids, 4) || misaligned(w13) || misaligned(w2) ||
       misaligned(out) || misaligned(workspace, 256) || (w13_scale && misaligned(w13_scale, 4)) ||
       (w2_scale && misaligned(w2_scale, 4)))
@@ -836,6 +945,59 @@ int moe_inv_rope_fp8_quant(const void* x, int T, int heads, int head_dim, int ro
   if (!st) return MOE_ERR_CUDA;
   return cuda_rc(launch_inv_rope_fp8(x, T, heads, head_dim, rot_dim, positions, cos_sin, max_pos, q_out, scale_out,
                                      st, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static int quant_block(const void* x, int T, int K, moe_dtype x_dtype, bool silu_form, uint8_t* q, float* scale,
+                       moe_stream_t stream) {
+  if (T < 0 || K < 1) return MOE_ERR_ARG;
+  if (x_dtype != MOE_F32 && x_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (K % 16) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !q || !scale) return MOE_ERR_ARG;
+  if (misaligned(x) || misaligned(q) || misaligned(scale, 4)) return MOE_ERR_ALIGNMENT;
+  return cuda_rc(launch_quant_block(x, x_dtype == MOE_BF16, silu_form, T, K, q, scale,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_quant_block(const void* x, int T, int K, moe_dtype x_dtype, uint8_t* q, float* scale, moe_stream_t stream) {
+  return quant_block(x, T, K, x_dtype, false, q, scale, stream);
+}
+
+int moe_silu_quant_block(const void* gate_up, int T, int I, moe_dtype x_dtype, uint8_t* q, float* scale,
+                         moe_stream_t stream) {
+  return quant_block(gate_up, T, I, x_dtype, true, q, scale, stream);
+}
+
+int moe_gemm_block(const void* a, const float* a_scale, const void* w, const float* w_scale, int T, int N, int K,
+                   moe_dtype out_dtype, void* out, moe_stream_t stream) {
+  if (T < 0 || N < 1 || K < 1) return MOE_ERR_ARG;
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (K % 16) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!a || !a_scale || !w || !w_scale || !out) return MOE_ERR_ARG;
+  if (misaligned(a) || misaligned(w) || misaligned(out) || misaligned(a_scale, 4) || misaligned(w_scale, 4))
+    return MOE_ERR_ALIGNMENT;
+  int* st = status_word();
+  const int sms = num_sms();
+  if (!st || sms <= 0) return MOE_ERR_CUDA;
+  BlockGemmArgs g = {};
+  g.epi = BG_EPI_DENSE;
+  g.T = T;
+  g.k = 1;
+  g.E = 1;
+  g.K = K;
+  g.n_out = N;
+  g.w_rows = N;
+  g.nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  g.out_bf16 = out_dtype == MOE_BF16;
+  g.x = a;
+  g.a_scale = a_scale;
+  g.w = w;
+  g.w_scale = w_scale;
+  g.out = out;
+  g.status = st;
+  g.num_sms = sms;
+  return cuda_rc(launch_gemm_block(g, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int moe_get_status(moe_stream_t stream) {

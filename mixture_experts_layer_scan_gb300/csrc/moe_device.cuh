@@ -40,6 +40,28 @@ __device__ __forceinline__ uint8_t f32_to_e4m3(float v) {
 // dynamic per-tensor e4m3 scale from an amax (same formula the oracle states)
 __device__ __forceinline__ float e4m3_scale_from_amax(float amax) { return amax > 0.0f ? amax / 448.0f : 1.0f; }
 
+// maximum that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// scale of a 128-element e4m3 block from its amax: amax times 1/448, the reciprocal a 32-bit
+// constant (a product where a division by 448 would cost ten instructions; a largest code past 448
+// by the two roundings saturates).  NaN and infinity pass through; 2^-126 keeps 1 / s finite.
+__device__ __forceinline__ float block_scale_from_amax(float amax) {
+  const float s = amax * (1.0f / 448.0f);
+  return amax == 0.0f ? 1.0f : (s < 0x1p-126f ? 0x1p-126f : s);
+}
+
+// four floats -> packed e4m3 codes (a in the low byte), round to nearest even, saturating
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
 __device__ __forceinline__ float silu(float z) { return z / (1.0f + expf(-z)); }
 
 // ---------------------------------------------------------------------------

@@ -76,6 +76,43 @@ cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_s
 // lanes G that share one output vector in the combine (H % 8 == 0); fixes its addition order
 int combine_lanes(int T, int H, int k);
 
+// ---- routing by groups, block-scaled FP8 ----------------------------------------
+cudaError_t launch_topk_grouped(const float* logits, const float* bias, int T, int E, int k,
+                                const moe_route_rule& rule, float* w, int32_t* ids, cudaStream_t s);
+// e4m3 codes [T][K] and scales [T][ceil(K/128)] of x [T][K] (silu_form: of SiLU(g)*u, x [T][2K])
+cudaError_t launch_quant_block(const void* x, bool bf16, bool silu_form, int T, int K, uint8_t* q, float* scale,
+                               cudaStream_t s);
+// the same for bf16 x [T][K], each row written at the sorted rows of its k pairs (launch_align's inv)
+cudaError_t launch_quant_block_scatter(const void* x, int T, int K, int k, const int32_t* inv, uint8_t* q,
+                                       float* scale, cudaStream_t s);
+enum BlockGemmEpilogue {
+  BG_EPI_DENSE = 0,  // out [T][n_out] bf16 or fp32
+  BG_EPI_G1 = 1,     // expert GEMM1: SiLU(gate)*up -> e4m3 out [cap][I] + out_scale [cap][I/128]
+  BG_EPI_G2 = 2      // expert GEMM2: fp32 Y[pair][H]
+};
+struct BlockGemmArgs {
+  int epi;
+  int T, k, E, K;
+  int n_out;              // N, I (GEMM1) or H (GEMM2)
+  int w_rows;             // weight rows per expert (N, 2I, H)
+  int cap;                // rows of the sorted activations (grouped)
+  int nt;                 // tokens per tile: 16, 32 or 64
+  bool by_block;          // grouped: tiles are the permutation's blocks of nt rows, else whole experts (<= nt tokens)
+  bool out_bf16;          // dense
+  const void* x;          // e4m3 [rows][K]
+  const float* a_scale;   // [rows][ceil(K/128)]
+  const void* w;          // e4m3 [E * w_rows][K]
+  const float* w_scale;   // [E][ceil(w_rows/128)][ceil(K/128)]
+  const int32_t* sorted;
+  const int32_t* eids;
+  const int32_t* meta;
+  void* out;
+  float* out_scale;
+  int* status;
+  int num_sms;
+};
+cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s);
+
 // ---- fp32 CUDA-core grouped GEMMs ---------------------------------------------
 cudaError_t launch_gemm1_simt(const float* Xs, const float* W13, int H, int I, int B, const int32_t* eids,
                               const int32_t* meta, int cap, float* A, cudaStream_t s);
