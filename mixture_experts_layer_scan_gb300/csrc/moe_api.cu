@@ -154,6 +154,9 @@ static int check_shape(int T, int H, int I, int E, int topk) {
   return MOE_OK;
 }
 
+// tokens of a block-scaled swap-AB tile
+static int block_swap_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : kBlockSwapMaxTokens; }
+
 static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dtype w, const moe_options* opts,
                      Plan* pl) {
   int rc = check_shape(T, H, I, E, topk);
@@ -190,9 +193,10 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
     const int eb = (p.path == PATH_FP8 || p.path == PATH_BLK) ? 1 : 2;
     if (p.path == PATH_BLK) {
       if (opts && (opts->cta_pair < 0 || opts->cta_pair > 2 || opts->split_k < 0)) return MOE_ERR_ARG;
-      if (opts && opts->cta_pair == 1) return MOE_ERR_UNSUPPORTED;
-      p.B = p.swap ? 16 : kBlockSwapMaxTokens;
-      p.xbox = p.swap ? (T <= 16 ? 16 : T <= 32 ? 32 : 64) : kBlockSwapMaxTokens;
+      if (opts && opts->cta_pair == 2 && !p.swap) return MOE_ERR_UNSUPPORTED;
+      p.pair = !p.swap;
+      p.B = p.swap ? 16 : 128;
+      p.xbox = p.swap ? block_swap_tokens(T) : 128;
       p.kb1 = H / 128;
       p.kb2 = I / 128;
     } else if (p.swap) {
@@ -528,7 +532,8 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
     g.E = E;
     g.cap = cap;
     g.nt = pl.xbox;
-    g.by_block = !pl.swap;
+    g.pair = pl.pair;
+    g.pblk = pblk;
     g.sorted = sorted;
     g.eids = eids;
     g.meta = meta;
@@ -988,7 +993,8 @@ int moe_gemm_block(const void* a, const float* a_scale, const void* w, const flo
   g.K = K;
   g.n_out = N;
   g.w_rows = N;
-  g.nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  g.pair = T > kBlockSwapMaxTokens;
+  g.nt = block_swap_tokens(T);
   g.out_bf16 = out_dtype == MOE_BF16;
   g.x = a;
   g.a_scale = a_scale;

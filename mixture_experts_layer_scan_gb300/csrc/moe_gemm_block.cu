@@ -39,14 +39,15 @@ struct BgDev {
   int w_rows, w_pair_off, w_tile_rows;  // weight rows per expert, offset of D1's rows, rows per tile
   int w_scale_rows;     // scale rows per expert
   int s_pair_off;       // offset of D1's scale row from D0's
-  int by_block;         // grouped: 1: tiles are the permutation's token blocks, 0: whole experts
   int stages, out_bf16;
+  int out_v8;           // fp32 rows of out are 32-byte aligned
   uint32_t stage_bytes, bar_off, scale_off, out_off;
   const float* a_scale;  // [rows][kb_total]
   const float* w_scale;  // [E][w_scale_rows][kb_total]
   const int32_t* sorted;
   const int32_t* eids;
   const int32_t* meta;
+  const int32_t* pblk;   // CTA pairs: the permutation's 256- and 128-row chunks
   void* out;
   float* out_scale;
   int* status;
@@ -59,7 +60,7 @@ struct BgTile {
 template <int EPI, int NT>
 __device__ __forceinline__ int bg_tile_count(const BgDev& p) {
   if constexpr (EPI == BG_EPI_DENSE) return (p.T + NT - 1) / NT * p.n_tiles;
-  return (p.by_block ? p.meta[META_NPP] / NT : p.meta[META_NACT]) * p.n_tiles;
+  return p.meta[META_NACT] * p.n_tiles;
 }
 
 template <int EPI, int NT>
@@ -71,10 +72,6 @@ __device__ __forceinline__ BgTile bg_tile_at(const BgDev& p, int t) {
     d.e = 0;
     d.xrow = m * NT;
     d.ntok = min(NT, p.T - d.xrow);
-  } else if (p.by_block) {
-    d.e = p.eids[m];
-    d.xrow = m * NT;
-    d.ntok = NT;
   } else {
     d.e = p.meta[meta_active(p.E) + m];
     d.xrow = p.meta[meta_offsets(p.E) + d.e];
@@ -417,13 +414,431 @@ cudaError_t launch_bg_nt(const CUtensorMap& mw, const CUtensorMap& mx, const BgD
   return cudaErrorInvalidValue;
 }
 
+// ---------------------------------------------------------------------------
+// Token-major products on CTA pairs (tcgen05 cta_group::2)
+// ---------------------------------------------------------------------------
+// A cluster of two CTAs computes 256 token rows x 256 weight rows; CTA r stages token rows
+// [128r, 128r + 128) and weight box r, CTA 0 issues M = 256, N = 256 MMAs for both, and each CTA's
+// tensor memory receives its 128 rows x 256 columns of every K block.  The last tile of an expert
+// (or of the batch) runs as M = 128 when it has at most 128 rows: CTA r then stages 64 of them, and
+// tensor-memory lane i of CTA r holds row 64r + (i mod 64), columns 128 (i / 64) + c of the tile.
+//
+// The fold is the work beside the MMAs: a K block of the tile is 128 x 256 sums per SM, one packed
+// fma per two of them.  Eight warps (two per tensor-memory quadrant) hold the 128 x 256 fp32
+// accumulators, 128 to a thread, each thread one row, so a block's scale is one product per thread
+// and 128 columns.  Two blocks of 256 tensor-memory columns alternate: while the tensor core sums
+// block b + 1, the warps fold block b.
+constexpr int kBpThreads = 320;
+constexpr int kBpStages = 6;
+constexpr uint32_t kBpHalf = 128u * 128u;       // bytes of a 128-row box of one K block
+constexpr uint32_t kBpStage = 2u * kBpHalf;     // this CTA's weight box and token rows
+constexpr uint32_t kBpRed = kBpStages * kBpStage;  // [2][256] block maxima of the epilogue halves
+constexpr uint32_t kBpBar = kBpRed + 2 * 256 * 4;
+constexpr uint32_t kBpSmem = 1024 + kBpBar + 8 * (2 * kBpStages + 2 * 2 + 1) + 16;
+
+struct BpTile {
+  int e, n, xrow, wr0;
+  bool tail;
+};
+
+template <int EPI>
+__device__ __forceinline__ BpTile bp_tile_at(const BgDev& p, int t) {
+  BpTile d;
+  const int c = t / p.n_tiles;
+  d.n = t - c * p.n_tiles;
+  if constexpr (EPI == BG_EPI_DENSE) {
+    d.e = 0;
+    d.xrow = 256 * c;
+    d.tail = p.T - d.xrow <= 128;
+  } else {
+    const int v = p.pblk[c];
+    d.xrow = v >> 1;
+    d.tail = (v & 1) != 0;
+    d.e = p.eids[d.xrow / 128];
+  }
+  d.wr0 = d.e * p.w_rows + d.n * p.w_tile_rows;
+  return d;
+}
+
+// acc[0..15] += s * (16 loaded sums)
+__device__ __forceinline__ void bp_fold16(float2* acc, const uint32_t (&r)[16], float s) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) fma2(acc[j], s, s, __uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+}
+
+// 8 floats to 32-byte aligned global memory in one store
+__device__ __forceinline__ void st_global_v8(float* p, const float2* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0].x), "f"(v[0].y),
+               "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
+               : "memory");
+}
+
+// A thread's 2 * PAIRS consecutive output columns from column n of one row.
+template <int EPI, int PAIRS>
+__device__ __forceinline__ void bp_store(const BgDev& p, size_t row, int n, const float2* acc) {
+  const size_t o = row * (size_t)p.n_out + n;
+  if (EPI == BG_EPI_G2 || (!p.out_bf16 && p.out_v8)) {
+    float* y = static_cast<float*>(p.out) + o;
+#pragma unroll
+    for (int i = 0; i < PAIRS; i += 4)
+      if (n + 2 * i < p.n_out) st_global_v8(y + 2 * i, acc + i);
+  } else if (!p.out_bf16 && p.n_out % 4 == 0) {
+    float* y = static_cast<float*>(p.out) + o;
+#pragma unroll
+    for (int i = 0; i < PAIRS; i += 2)
+      if (n + 2 * i < p.n_out)
+        *reinterpret_cast<float4*>(y + 2 * i) = make_float4(acc[i].x, acc[i].y, acc[i + 1].x, acc[i + 1].y);
+  } else if (p.out_bf16 && p.n_out % 8 == 0) {
+    uint16_t* y = static_cast<uint16_t*>(p.out) + o;
+#pragma unroll
+    for (int i = 0; i < PAIRS; i += 4)
+      if (n + 2 * i < p.n_out)
+        *reinterpret_cast<uint4*>(y + 2 * i) =
+            make_uint4(pack_bf16x2(acc[i].x, acc[i].y), pack_bf16x2(acc[i + 1].x, acc[i + 1].y),
+                       pack_bf16x2(acc[i + 2].x, acc[i + 2].y), pack_bf16x2(acc[i + 3].x, acc[i + 3].y));
+  } else {
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      const float v[2] = {acc[i].x, acc[i].y};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (n + 2 * i + h >= p.n_out) continue;
+        if (p.out_bf16)
+          static_cast<__nv_bfloat16*>(p.out)[o + 2 * i + h] = __float2bfloat16_rn(v[h]);
+        else
+          static_cast<float*>(p.out)[o + 2 * i + h] = v[h];
+      }
+    }
+  }
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(kBpThreads, 1)
+    k_gemm_block_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                      const __grid_constant__ CUtensorMap tmW64, const __grid_constant__ CUtensorMap tmX64,
+                      const BgDev p) {
+  constexpr bool G1 = EPI == BG_EPI_G1;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar_full = sbase + kBpBar;
+  const uint32_t bar_empty = bar_full + 8 * kBpStages;
+  const uint32_t bar_tfull = bar_empty + 8 * kBpStages;
+  const uint32_t bar_tempty = bar_tfull + 16;
+  const uint32_t bar_drain = bar_tempty + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBpBar + 8 * (2 * kBpStages + 5));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kBpStages; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_tfull + 8 * b, 1);
+      mbar_init(bar_tempty + 8 * b, 16);  // epilogue warps of both CTAs
+    }
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW64);
+    tma_prefetch_desc(&tmX64);
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  cta_sync();
+  cluster_sync_all();  // both CTAs' barriers are initialised before any remote signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  pdl_wait();
+  const int chunks = EPI == BG_EPI_DENSE ? (p.T + 255) / 256 : p.meta[META_NPB];
+  const int ntiles = chunks * p.n_tiles;
+
+  if (warp == 0) {
+    // ---------------- TMA producer (both CTAs) ----------------
+    // completion is counted on CTA 0's full barrier, which CTA 0 arms for both CTAs' bytes
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int t = pair; t < ntiles && ok; t += npairs) {
+      const BpTile d = bp_tile_at<EPI>(p, t);
+      for (int kb = 0; kb < p.kb_total; ++kb) {
+        if (!mbar_wait_all(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t sw = sbase + stage * kBpStage, fb = bar_full + 8 * stage, fb0 = mapa_shared(fb, 0);
+          if (leader) mbar_arrive_expect_tx(fb, (d.tail ? 3u : 4u) * kBpHalf);
+          if (G1 && d.tail) {  // 64 gate rows and the matching 64 up rows
+            tma_load_2d_pair(sw, &tmW64, kb * 128, d.wr0 + 64 * (int)rank, fb0);
+            tma_load_2d_pair(sw + kBpHalf / 2, &tmW64, kb * 128, d.wr0 + p.w_pair_off + 64 * (int)rank, fb0);
+          } else {
+            tma_load_2d_pair(sw, &tmW, kb * 128, d.wr0 + (rank ? p.w_pair_off : 0), fb0);
+          }
+          if (d.tail)
+            tma_load_2d_pair(sw + kBpHalf, &tmX64, kb * 128, d.xrow + 64 * (int)rank, fb0);
+          else
+            tma_load_2d_pair(sw + kBpHalf, &tmX, kb * 128, d.xrow + 128 * (int)rank, fb0);
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == kBpStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (lane == 0) {
+      pdl_launch_dependents();
+      if (!ok && leader) {  // let the copies already in flight land before the CTA exits
+        const uint32_t first = issued > (uint32_t)kBpStages ? issued - kBpStages : 0u;
+        for (uint32_t i = first; i < issued; ++i)
+          mbar_wait_drain(bar_full + 8 * (i % kBpStages), (i / kBpStages) & 1u, 100000000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (CTA 0) ----------------
+    if (leader) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool ok = true, any = false;
+      for (int t = pair; t < ntiles && ok; t += npairs) {
+        const BpTile d = bp_tile_at<EPI>(p, t);
+        const uint32_t idesc = idesc_make(d.tail ? 128 : 256, 256, true);
+        for (int kb = 0; kb < p.kb_total; ++kb) {
+          if (!mbar_wait_all(bar_tempty + 8 * buf, buf_phase ^ 1u, abort_flag, p.status) ||
+              !mbar_wait_all(bar_full + 8 * stage, phase, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t sw = sbase + stage * kBpStage, sx = sw + kBpHalf;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_pair<true>(tmem_base + 256u * buf, sdesc_k_sw128(sx + kk * 32), sdesc_k_sw128(sw + kk * 32),
+                                idesc, kk > 0);
+            tc_commit_pair(bar_empty + 8 * stage);
+            tc_commit_pair(mapa_shared(bar_empty + 8 * stage, 1));
+            tc_commit_pair(bar_tfull + 8 * buf);
+            tc_commit_pair(mapa_shared(bar_tfull + 8 * buf, 1));
+          }
+          __syncwarp();
+          any = true;
+          if (++stage == kBpStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          buf ^= 1;
+          if (buf == 0) buf_phase ^= 1u;
+        }
+      }
+      if (!ok && any) {  // the tensor cores must be idle before tensor memory is freed
+        if (lane == 0) tc_commit_pair(bar_drain);
+        __syncwarp();
+        mbar_wait_drain(bar_drain, 0, 100000000ull);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- epilogue (warps 2..9 of both CTAs) ----------------
+    const int q = warp & 3, h = (warp - 2) >> 2;  // tensor-memory quadrant; which half of a row's columns
+    const int lrow = q * 32 + lane;
+    float* red = reinterpret_cast<float*>(smem + kBpRed);
+    const uint32_t tempty0 = mapa_shared(bar_tempty, 0);
+    int buf = 0, par = 0;
+    uint32_t buf_phase = 0;
+    bool ok = true;
+    for (int t = pair; t < ntiles; t += npairs) {
+      const BpTile d = bp_tile_at<EPI>(p, t);
+      // This thread's row and its two runs of `wide` tensor-memory columns (from ca and cb): the
+      // gate and up sums of the same intermediate columns (GEMM1), or one run of 2 * wide columns.
+      const int hf = d.tail ? lrow >> 6 : 0;  // half of N held by this lane
+      const int row = d.xrow + (d.tail ? 64 * (int)rank + (lrow & 63) : 128 * (int)rank + lrow);
+      const int wide = d.tail ? 32 : 64;
+      const int ca = (G1 ? wide : 2 * wide) * h;
+      const int cb = G1 ? 2 * wide + ca : ca + wide;
+      const int sr = G1 ? d.n : min(2 * d.n + (d.tail ? hf : h), p.w_scale_rows - 1);
+      const float* wsa = p.w_scale + ((size_t)d.e * p.w_scale_rows + sr) * p.kb_total;
+      const float* wsb = G1 ? wsa + (size_t)p.s_pair_off * p.kb_total : wsa;
+      const bool row_ok = EPI != BG_EPI_DENSE || row < p.T;
+      const float* xs = p.a_scale + (size_t)(row_ok ? row : 0) * p.kb_total;
+      float2 acca[32], accb[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) acca[i] = accb[i] = make_float2(0.0f, 0.0f);
+      float sa = xs[0] * wsa[0], sb = G1 ? xs[0] * wsb[0] : 0.0f;
+      for (int kb = 0; kb < p.kb_total; ++kb) {
+        // the next block's scales are on their way while this block is folded
+        const int nk = min(kb + 1, p.kb_total - 1);
+        const float nx = xs[nk], na = wsa[nk], nb = G1 ? wsb[nk] : 0.0f;
+        ok = ok && mbar_wait_all(bar_tfull + 8 * buf, buf_phase, abort_flag, p.status);
+        if (ok) {
+          tc_fence_after();
+          const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + 256u * buf;
+          const float s2 = G1 ? sb : sa;
+          uint32_t r0[16], r1[16];
+          if (!d.tail) {
+            tmem_ld16_issue(tb + ca, r0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              tmem_ld16_wait(r0);
+              tmem_ld16_issue(tb + cb + 16 * i, r1);
+              bp_fold16(acca + 8 * i, r0, sa);
+              tmem_ld16_wait(r1);
+              if (i < 3) tmem_ld16_issue(tb + ca + 16 * (i + 1), r0);
+              bp_fold16(accb + 8 * i, r1, s2);
+            }
+          } else {
+            tmem_ld16_issue(tb + ca, r0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              tmem_ld16_wait(r0);
+              tmem_ld16_issue(tb + cb + 16 * i, r1);
+              bp_fold16(acca + 8 * i, r0, sa);
+              tmem_ld16_wait(r1);
+              if (i < 1) tmem_ld16_issue(tb + ca + 16, r0);
+              bp_fold16(accb + 8 * i, r1, s2);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader)
+              mbar_arrive(bar_tempty + 8 * buf);
+            else
+              mbar_arrive_cluster(tempty0 + 8 * buf);
+          }
+        }
+        buf ^= 1;
+        if (buf == 0) buf_phase ^= 1u;
+        sa = nx * na;
+        if (G1) sb = nx * nb;
+      }
+      if constexpr (G1) {
+        // SiLU(gate) * up of `wide` columns, the block's maximum over the two (tail: four) threads
+        // of the row, then this thread's codes
+        float a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (i < wide / 2) {
+            acca[i].x = silu(acca[i].x) * accb[i].x;
+            acca[i].y = silu(acca[i].y) * accb[i].y;
+            a = max_nan(a, max_nan(fabsf(acca[i].x), fabsf(acca[i].y)));
+          }
+        }
+        float* rd = red + 256 * par;
+        rd[128 * h + lrow] = a;
+        named_bar_sync(1, 256);
+        a = max_nan(rd[lrow], rd[128 + lrow]);
+        if (d.tail) a = max_nan(a, max_nan(rd[lrow ^ 64], rd[128 + (lrow ^ 64)]));
+        par ^= 1;  // (the other half of red: a slower warp may still read this one)
+        const float s = block_scale_from_amax(a);
+        const float r = 1.0f / s;
+        if (ok) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (size_t)row * p.n_out +
+                                                (size_t)d.n * 128 + 64 * hf + wide * h);
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            if (i < wide / 2) {
+              uint32_t c[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                c[j] = pack_e4m3x4(acca[i + 2 * j].x * r, acca[i + 2 * j].y * r, acca[i + 2 * j + 1].x * r,
+                                   acca[i + 2 * j + 1].y * r);
+              dst[i / 8] = make_uint4(c[0], c[1], c[2], c[3]);
+            }
+          }
+          if (h == 0 && hf == 0) p.out_scale[(size_t)row * (p.n_out / 128) + d.n] = s;
+        }
+      } else if (ok && row_ok) {
+        const int n = d.n * 256 + 128 * hf + ca;
+        size_t orow = (size_t)row;
+        bool store = true;
+        if constexpr (EPI == BG_EPI_G2) {
+          const int f = p.sorted[row];
+          store = f < p.T * p.k;
+          orow = (size_t)f;
+        }
+        if (store) {
+          if (!d.tail) {
+            bp_store<EPI, 32>(p, orow, n, acca);
+            bp_store<EPI, 32>(p, orow, n + 64, accb);
+          } else {
+            bp_store<EPI, 16>(p, orow, n, acca);
+            bp_store<EPI, 16>(p, orow, n + 32, accb);
+          }
+        }
+      }
+    }
+  }
+
+  // Both CTAs finish every role (and with it every read of the other CTA's shared memory or tensor
+  // memory) before either frees tensor memory or exits.
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+// Clusters of 2 on a persistent grid of as many pairs as are resident at once.
+template <int EPI>
+cudaError_t launch_bp(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& mw64, const CUtensorMap& mx64,
+                      const BgDev& p, long tiles, cudaStream_t s) {
+  static bool attr_set[64] = {};
+  static int max_clusters[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  auto kern = k_gemm_block_pair<EPI>;
+  if (!attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kBpThreads);
+  cfg.dynamicSmemBytes = kBpSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3(2);
+  if (max_clusters[dev] == 0) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = -1;
+    }
+    max_clusters[dev] = n;
+  }
+  if (max_clusters[dev] < 1) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3(2 * (unsigned)std::max<long>(1, std::min<long>(tiles, max_clusters[dev])));
+  return cudaLaunchKernelEx(&cfg, kern, mw, mx, mw64, mx64, p);
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
   CUtensorMap mw, mx;
   const uint64_t x_rows = a.epi == BG_EPI_DENSE ? (uint64_t)a.T : (uint64_t)a.cap;
   if (!make_tensor_map_2d(&mw, a.w, 1, (uint64_t)a.K, (uint64_t)a.E * a.w_rows, 128u) ||
-      !make_tensor_map_2d(&mx, a.x, 1, (uint64_t)a.K, x_rows, 16u))
+      !make_tensor_map_2d(&mx, a.x, 1, (uint64_t)a.K, x_rows, a.pair ? 128u : 16u))
     return cudaErrorInvalidValue;
   BgDev p = {};
   p.T = a.T;
@@ -444,8 +859,8 @@ cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
     p.w_tile_rows = 256;
     p.s_pair_off = 1;
   }
-  p.by_block = a.by_block ? 1 : 0;
   p.out_bf16 = a.out_bf16 ? 1 : 0;
+  p.out_v8 = a.n_out % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   p.a_scale = a.a_scale;
   p.w_scale = a.w_scale;
   p.sorted = a.sorted;
@@ -454,11 +869,23 @@ cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
   p.out = a.out;
   p.out_scale = a.out_scale;
   p.status = a.status;
+  if (a.pair) {
+    CUtensorMap mw64, mx64;
+    if (!make_tensor_map_2d(&mw64, a.w, 1, (uint64_t)a.K, (uint64_t)a.E * a.w_rows, 64u) ||
+        !make_tensor_map_2d(&mx64, a.x, 1, (uint64_t)a.K, x_rows, 64u))
+      return cudaErrorInvalidValue;
+    p.pblk = a.pblk;
+    if (a.epi == BG_EPI_DENSE)
+      return launch_bp<BG_EPI_DENSE>(mw, mx, mw64, mx64, p, ((long)a.T + 255) / 256 * p.n_tiles, s);
+    const long tiles = (long)(a.cap / 128) * p.n_tiles;
+    if (a.epi == BG_EPI_G1) return launch_bp<BG_EPI_G1>(mw, mx, mw64, mx64, p, tiles, s);
+    return launch_bp<BG_EPI_G2>(mw, mx, mw64, mx64, p, tiles, s);
+  }
   if (a.epi == BG_EPI_DENSE) {
     const long tiles = ((long)a.T + a.nt - 1) / a.nt * p.n_tiles;
     return launch_bg_nt<BG_EPI_DENSE>(mw, mx, p, a.nt, tiles, a.num_sms, s);
   }
-  const long groups = a.by_block ? (long)a.cap / a.nt : std::min<long>(a.E, (long)a.T * a.k);
+  const long groups = std::min<long>(a.E, (long)a.T * a.k);  // active experts at most
   if (a.epi == BG_EPI_G1) return launch_bg_nt<BG_EPI_G1>(mw, mx, p, a.nt, groups * p.n_tiles, a.num_sms, s);
   return launch_bg_nt<BG_EPI_G2>(mw, mx, p, a.nt, groups * p.n_tiles, a.num_sms, s);
 }

@@ -96,8 +96,8 @@ struct BlockGemmArgs {
   int n_out;              // N, I (GEMM1) or H (GEMM2)
   int w_rows;             // weight rows per expert (N, 2I, H)
   int cap;                // rows of the sorted activations (grouped)
-  int nt;                 // tokens per tile: 16, 32 or 64
-  bool by_block;          // grouped: tiles are the permutation's blocks of nt rows, else whole experts (<= nt tokens)
+  bool pair;              // token-major on CTA pairs (grouped: permutation blocks of 128, tiles from pblk)
+  int nt;                 // swap-AB: tokens per tile, 16, 32 or 64 (grouped: at least an expert's tokens)
   bool out_bf16;          // dense
   const void* x;          // e4m3 [rows][K]
   const float* a_scale;   // [rows][ceil(K/128)]
@@ -106,6 +106,7 @@ struct BlockGemmArgs {
   const int32_t* sorted;
   const int32_t* eids;
   const int32_t* meta;
+  const int32_t* pblk;
   void* out;
   float* out_scale;
   int* status;

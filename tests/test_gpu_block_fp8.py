@@ -174,6 +174,21 @@ def test_gemm_against_64_bits(moe, T, N, K, out_dtype):
     assert (np.abs(got - ref) <= tol).all(), np.max((np.abs(got - ref)) / S)
 
 
+@pytest.mark.parametrize("T", [40, 200])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_gemm_output_on_a_16_byte_boundary(moe, T, out_dtype):
+    """An output that starts 16 bytes into a 256-byte boundary (the contract asks for no more)."""
+    gen = torch.Generator().manual_seed(T)
+    q, s = moe.moe_quant_block(torch.randn(T, 256, generator=gen).cuda())
+    w, sw = (v.cuda() for v in block_weights(320, 256, gen))
+    off = 16 // torch.empty(0, dtype=out_dtype).element_size()
+    buf = torch.full((T * 320 + 2 * off,), 7.0, dtype=out_dtype, device="cuda")
+    out = buf[off : off + T * 320].view(T, 320)
+    moe.moe_gemm_block(q, s, w, sw, out=out)
+    assert torch.equal(out, moe.moe_gemm_block(q, s, w, sw, out_dtype=out_dtype))
+    assert (buf[:off] == 7.0).all() and (buf[-off:] == 7.0).all()
+
+
 def test_gemm_sums_in_32_bits(moe):
     """A long sum with one large block: the small blocks' share survives (it would not in 16 bits)."""
     K = 8192
