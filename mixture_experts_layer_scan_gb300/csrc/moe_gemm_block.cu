@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
       const BgTile d = bg_tile_at<EPI, NT>(p, t);
       for (int kb = 0; kb < p.kb_total; ++kb) {
-        if (!mbar_wait_all(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
+        if (!mbar_wait_hot(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
           ok = false;
           break;
         }
@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(kBgThreads, 1)
       const BgTile d = bg_tile_at<EPI, NT>(p, t);
       const uint32_t idesc = idesc_make(128, d.npad, true);
       for (int kb = 0; kb < p.kb_total; ++kb) {
-        if (!mbar_wait_all(bar_tempty + 8 * buf, buf_phase ^ 1u, abort_flag, p.status) ||
-            !mbar_wait_all(bar_full + 8 * stage, phase, abort_flag, p.status)) {
+        if (!mbar_wait_hot(bar_tempty + 8 * buf, buf_phase ^ 1u, abort_flag, p.status) ||
+            !mbar_wait_hot(bar_full + 8 * stage, phase, abort_flag, p.status)) {
           ok = false;
           break;
         }
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
         if (kc + kScaleChunk < p.kb_total) fetch(kc + kScaleChunk);
         const int kn = min(kScaleChunk, p.kb_total - kc);
         for (int kb = 0; kb < kn; ++kb) {
-          ok = ok && mbar_wait_all(bar_tfull + 8 * buf, buf_phase, abort_flag, p.status);
+          ok = ok && mbar_wait_hot(bar_tfull + 8 * buf, buf_phase, abort_flag, p.status);
           if (ok) {
             tc_fence_after();
             const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * 2 * NT);
@@ -418,23 +418,27 @@ cudaError_t launch_bg_nt(const CUtensorMap& mw, const CUtensorMap& mx, const BgD
 // Token-major products on CTA pairs (tcgen05 cta_group::2)
 // ---------------------------------------------------------------------------
 // A cluster of two CTAs computes 256 token rows x 256 weight rows; CTA r stages token rows
-// [128r, 128r + 128) and weight box r, CTA 0 issues M = 256, N = 256 MMAs for both, and each CTA's
-// tensor memory receives its 128 rows x 256 columns of every K block.  The last tile of an expert
-// (or of the batch) runs as M = 128 when it has at most 128 rows: CTA r then stages 64 of them, and
-// tensor-memory lane i of CTA r holds row 64r + (i mod 64), columns 128 (i / 64) + c of the tile.
+// [128r, 128r + 128) and weight box r (GEMM1: 128 gate rows, the matching 128 up rows).  Half j of a
+// K block is one set of M = 256, N = 128 MMAs over rows [64j, 64j + 64) of both weight boxes, issued
+// by CTA 0, and leaves each CTA 128 rows x (64 sums of box 0, 64 of box 1) in its tensor memory.
+// The last tile of an expert (or of the batch) runs as M = 128 when it has at most 128 rows: CTA r
+// then stages 64 of them, and lane i of its tensor memory holds row 64r + (i mod 64) and the 64 sums
+// of box i / 64; for GEMM1 the boxes of such a tile interleave 32 gate and 32 up rows, so that gate
+// and up of a column still meet in one thread.
 //
-// The fold is the work beside the MMAs: a K block of the tile is 128 x 256 sums per SM, one packed
-// fma per two of them.  Eight warps (two per tensor-memory quadrant) hold the 128 x 256 fp32
-// accumulators, 128 to a thread, each thread one row, so a block's scale is one product per thread
-// and 128 columns.  Two blocks of 256 tensor-memory columns alternate: while the tensor core sums
-// block b + 1, the warps fold block b.
+// The fold is the work beside the MMAs: 128 x 256 sums per SM and K block, one packed fma for two of
+// them.  Eight warps hold the 128 x 256 fp32 accumulators, 128 to a thread; four of them fold half 0,
+// four half 1.  A sum can be overwritten only after its fold, and tensor memory holds two K blocks of
+// the tile, so what limits the rate is the round trip MMA -> commit -> fold -> release -> MMA.  Halves
+// cut it into four buffers instead of two: one is filled while three travel (N = 128 reads the token
+// rows from shared memory twice, which costs less than waiting).
 constexpr int kBpThreads = 320;
 constexpr int kBpStages = 6;
 constexpr uint32_t kBpHalf = 128u * 128u;       // bytes of a 128-row box of one K block
 constexpr uint32_t kBpStage = 2u * kBpHalf;     // this CTA's weight box and token rows
 constexpr uint32_t kBpRed = kBpStages * kBpStage;  // [2][256] block maxima of the epilogue halves
 constexpr uint32_t kBpBar = kBpRed + 2 * 256 * 4;
-constexpr uint32_t kBpSmem = 1024 + kBpBar + 8 * (2 * kBpStages + 2 * 2 + 1) + 16;
+constexpr uint32_t kBpSmem = 1024 + kBpBar + 8 * (2 * kBpStages + 2 * 4 + 1) + 16;
 
 struct BpTile {
   int e, n, xrow, wr0;
@@ -515,7 +519,7 @@ __device__ __forceinline__ void bp_store(const BgDev& p, size_t row, int n, cons
 template <int EPI>
 __global__ void __launch_bounds__(kBpThreads, 1)
     k_gemm_block_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                      const __grid_constant__ CUtensorMap tmW64, const __grid_constant__ CUtensorMap tmX64,
+                      const __grid_constant__ CUtensorMap tmW32, const __grid_constant__ CUtensorMap tmX64,
                       const BgDev p) {
   constexpr bool G1 = EPI == BG_EPI_G1;
   extern __shared__ uint8_t smem_raw[];
@@ -524,9 +528,9 @@ __global__ void __launch_bounds__(kBpThreads, 1)
   const uint32_t bar_full = sbase + kBpBar;
   const uint32_t bar_empty = bar_full + 8 * kBpStages;
   const uint32_t bar_tfull = bar_empty + 8 * kBpStages;
-  const uint32_t bar_tempty = bar_tfull + 16;
-  const uint32_t bar_drain = bar_tempty + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBpBar + 8 * (2 * kBpStages + 5));
+  const uint32_t bar_tempty = bar_tfull + 32;  // [buffer][half]
+  const uint32_t bar_drain = bar_tempty + 32;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBpBar + 8 * (2 * kBpStages + 9));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -538,16 +542,16 @@ __global__ void __launch_bounds__(kBpThreads, 1)
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 4; ++b) {
       mbar_init(bar_tfull + 8 * b, 1);
-      mbar_init(bar_tempty + 8 * b, 16);  // epilogue warps of both CTAs
+      mbar_init(bar_tempty + 8 * b, 8);  // this half's epilogue warps of both CTAs
     }
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
-    tma_prefetch_desc(&tmW64);
+    tma_prefetch_desc(&tmW32);
     tma_prefetch_desc(&tmX64);
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
@@ -570,16 +574,20 @@ __global__ void __launch_bounds__(kBpThreads, 1)
     for (int t = pair; t < ntiles && ok; t += npairs) {
       const BpTile d = bp_tile_at<EPI>(p, t);
       for (int kb = 0; kb < p.kb_total; ++kb) {
-        if (!mbar_wait_all(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
+        if (!mbar_wait_hot(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
           ok = false;
           break;
         }
         if (lane == 0) {
           const uint32_t sw = sbase + stage * kBpStage, fb = bar_full + 8 * stage, fb0 = mapa_shared(fb, 0);
           if (leader) mbar_arrive_expect_tx(fb, (d.tail ? 3u : 4u) * kBpHalf);
-          if (G1 && d.tail) {  // 64 gate rows and the matching 64 up rows
-            tma_load_2d_pair(sw, &tmW64, kb * 128, d.wr0 + 64 * (int)rank, fb0);
-            tma_load_2d_pair(sw + kBpHalf / 2, &tmW64, kb * 128, d.wr0 + p.w_pair_off + 64 * (int)rank, fb0);
+          if (G1 && d.tail) {  // 32 gate rows, the matching 32 up rows, the next 32 of each
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int wr = d.wr0 + 64 * (int)rank + 32 * j;
+              tma_load_2d_pair(sw + j * (kBpHalf / 2), &tmW32, kb * 128, wr, fb0);
+              tma_load_2d_pair(sw + j * (kBpHalf / 2) + kBpHalf / 4, &tmW32, kb * 128, wr + p.w_pair_off, fb0);
+            }
           } else {
             tma_load_2d_pair(sw, &tmW, kb * 128, d.wr0 + (rank ? p.w_pair_off : 0), fb0);
           }
@@ -613,27 +621,31 @@ __global__ void __launch_bounds__(kBpThreads, 1)
       bool ok = true, any = false;
       for (int t = pair; t < ntiles && ok; t += npairs) {
         const BpTile d = bp_tile_at<EPI>(p, t);
-        const uint32_t idesc = idesc_make(d.tail ? 128 : 256, 256, true);
-        for (int kb = 0; kb < p.kb_total; ++kb) {
-          if (!mbar_wait_all(bar_tempty + 8 * buf, buf_phase ^ 1u, abort_flag, p.status) ||
-              !mbar_wait_all(bar_full + 8 * stage, phase, abort_flag, p.status)) {
+        const uint32_t idesc = idesc_make(d.tail ? 128 : 256, 128, true);
+        for (int kb = 0; kb < p.kb_total && ok; ++kb) {
+          if (!mbar_wait_hot(bar_full + 8 * stage, phase, abort_flag, p.status)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t sw = sbase + stage * kBpStage, sx = sw + kBpHalf;
+          const uint32_t sw = sbase + stage * kBpStage, sx = sw + kBpHalf;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_pair<true>(tmem_base + 256u * buf, sdesc_k_sw128(sx + kk * 32), sdesc_k_sw128(sw + kk * 32),
-                                idesc, kk > 0);
-            tc_commit_pair(bar_empty + 8 * stage);
-            tc_commit_pair(mapa_shared(bar_empty + 8 * stage, 1));
-            tc_commit_pair(bar_tfull + 8 * buf);
-            tc_commit_pair(mapa_shared(bar_tfull + 8 * buf, 1));
+          for (int j = 0; j < 2; ++j) {
+            if (!mbar_wait_hot(bar_tempty + 8 * (2 * buf + j), buf_phase ^ 1u, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_pair<true>(tmem_base + 256u * buf + 128u * j, sdesc_k_sw128(sx + kk * 32),
+                                  sdesc_k_sw128(sw + j * (kBpHalf / 2) + kk * 32), idesc, kk > 0);
+              tc_commit_both(bar_tfull + 8 * (2 * buf + j));
+              if (j == 1) tc_commit_both(bar_empty + 8 * stage);
+            }
+            __syncwarp();
+            any = true;
           }
-          __syncwarp();
-          any = true;
           if (++stage == kBpStages) {
             stage = 0;
             phase ^= 1u;
@@ -651,7 +663,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
     __syncwarp();
   } else {
     // ---------------- epilogue (warps 2..9 of both CTAs) ----------------
-    const int q = warp & 3, h = (warp - 2) >> 2;  // tensor-memory quadrant; which half of a row's columns
+    const int q = warp & 3, h = (warp - 2) >> 2;  // tensor-memory quadrant; half of the K block
     const int lrow = q * 32 + lane;
     float* red = reinterpret_cast<float*>(smem + kBpRed);
     const uint32_t tempty0 = mapa_shared(bar_tempty, 0);
@@ -660,68 +672,67 @@ __global__ void __launch_bounds__(kBpThreads, 1)
     bool ok = true;
     for (int t = pair; t < ntiles; t += npairs) {
       const BpTile d = bp_tile_at<EPI>(p, t);
-      // This thread's row and its two runs of `wide` tensor-memory columns (from ca and cb): the
-      // gate and up sums of the same intermediate columns (GEMM1), or one run of 2 * wide columns.
-      const int hf = d.tail ? lrow >> 6 : 0;  // half of N held by this lane
+      // This thread's row and its two runs of `wide` sums, tensor-memory columns [0, wide) and
+      // [wide, 2 wide) of its half: of box 0 and box 1, or (tail) of box hf alone.
+      const int hf = d.tail ? lrow >> 6 : 0;
       const int row = d.xrow + (d.tail ? 64 * (int)rank + (lrow & 63) : 128 * (int)rank + lrow);
       const int wide = d.tail ? 32 : 64;
-      const int ca = (G1 ? wide : 2 * wide) * h;
-      const int cb = G1 ? 2 * wide + ca : ca + wide;
-      const int sr = G1 ? d.n : min(2 * d.n + (d.tail ? hf : h), p.w_scale_rows - 1);
-      const float* wsa = p.w_scale + ((size_t)d.e * p.w_scale_rows + sr) * p.kb_total;
-      const float* wsb = G1 ? wsa + (size_t)p.s_pair_off * p.kb_total : wsa;
+      const int last = p.w_scale_rows - 1;
+      const int sra = G1 ? d.n : min(2 * d.n + hf, last);
+      const int srb = G1 ? d.n + p.s_pair_off : d.tail ? sra : min(2 * d.n + 1, last);
+      const float* wsa = p.w_scale + ((size_t)d.e * p.w_scale_rows + sra) * p.kb_total;
+      const float* wsb = p.w_scale + ((size_t)d.e * p.w_scale_rows + srb) * p.kb_total;
       const bool row_ok = EPI != BG_EPI_DENSE || row < p.T;
       const float* xs = p.a_scale + (size_t)(row_ok ? row : 0) * p.kb_total;
       float2 acca[32], accb[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acca[i] = accb[i] = make_float2(0.0f, 0.0f);
-      float sa = xs[0] * wsa[0], sb = G1 ? xs[0] * wsb[0] : 0.0f;
+      float sa = xs[0] * wsa[0], sb = xs[0] * wsb[0];
       for (int kb = 0; kb < p.kb_total; ++kb) {
         // the next block's scales are on their way while this block is folded
         const int nk = min(kb + 1, p.kb_total - 1);
-        const float nx = xs[nk], na = wsa[nk], nb = G1 ? wsb[nk] : 0.0f;
-        ok = ok && mbar_wait_all(bar_tfull + 8 * buf, buf_phase, abort_flag, p.status);
+        const float nx = xs[nk], na = wsa[nk], nb = wsb[nk];
+        ok = ok && mbar_wait_hot(bar_tfull + 8 * (2 * buf + h), buf_phase, abort_flag, p.status);
         if (ok) {
           tc_fence_after();
-          const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + 256u * buf;
-          const float s2 = G1 ? sb : sa;
+          const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + 256u * buf + 128u * h;
           uint32_t r0[16], r1[16];
           if (!d.tail) {
-            tmem_ld16_issue(tb + ca, r0);
+            tmem_ld16_issue(tb, r0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               tmem_ld16_wait(r0);
-              tmem_ld16_issue(tb + cb + 16 * i, r1);
+              tmem_ld16_issue(tb + 64 + 16 * i, r1);
               bp_fold16(acca + 8 * i, r0, sa);
               tmem_ld16_wait(r1);
-              if (i < 3) tmem_ld16_issue(tb + ca + 16 * (i + 1), r0);
-              bp_fold16(accb + 8 * i, r1, s2);
+              if (i < 3) tmem_ld16_issue(tb + 16 * (i + 1), r0);
+              bp_fold16(accb + 8 * i, r1, sb);
             }
           } else {
-            tmem_ld16_issue(tb + ca, r0);
+            tmem_ld16_issue(tb, r0);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               tmem_ld16_wait(r0);
-              tmem_ld16_issue(tb + cb + 16 * i, r1);
+              tmem_ld16_issue(tb + 32 + 16 * i, r1);
               bp_fold16(acca + 8 * i, r0, sa);
               tmem_ld16_wait(r1);
-              if (i < 1) tmem_ld16_issue(tb + ca + 16, r0);
-              bp_fold16(accb + 8 * i, r1, s2);
+              if (i < 1) tmem_ld16_issue(tb + 16, r0);
+              bp_fold16(accb + 8 * i, r1, sb);
             }
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
             if (leader)
-              mbar_arrive(bar_tempty + 8 * buf);
+              mbar_arrive(bar_tempty + 8 * (2 * buf + h));
             else
-              mbar_arrive_cluster(tempty0 + 8 * buf);
+              mbar_arrive_remote(tempty0 + 8 * (2 * buf + h));
           }
         }
         buf ^= 1;
         if (buf == 0) buf_phase ^= 1u;
         sa = nx * na;
-        if (G1) sb = nx * nb;
+        sb = nx * nb;
       }
       if constexpr (G1) {
         // SiLU(gate) * up of `wide` columns, the block's maximum over the two (tail: four) threads
@@ -760,7 +771,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
           if (h == 0 && hf == 0) p.out_scale[(size_t)row * (p.n_out / 128) + d.n] = s;
         }
       } else if (ok && row_ok) {
-        const int n = d.n * 256 + 128 * hf + ca;
+        const int n = d.n * 256 + 128 * hf + 64 * h;  // columns of box 0 (tail: of box hf)
         size_t orow = (size_t)row;
         bool store = true;
         if constexpr (EPI == BG_EPI_G2) {
@@ -771,7 +782,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
         if (store) {
           if (!d.tail) {
             bp_store<EPI, 32>(p, orow, n, acca);
-            bp_store<EPI, 32>(p, orow, n + 64, accb);
+            bp_store<EPI, 32>(p, orow, n + 128, accb);
           } else {
             bp_store<EPI, 16>(p, orow, n, acca);
             bp_store<EPI, 16>(p, orow, n + 32, accb);
@@ -792,7 +803,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
 
 // Clusters of 2 on a persistent grid of as many pairs as are resident at once.
 template <int EPI>
-cudaError_t launch_bp(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& mw64, const CUtensorMap& mx64,
+cudaError_t launch_bp(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& mw32, const CUtensorMap& mx64,
                       const BgDev& p, long tiles, cudaStream_t s) {
   static bool attr_set[64] = {};
   static int max_clusters[64] = {};
@@ -829,7 +840,7 @@ cudaError_t launch_bp(const CUtensorMap& mw, const CUtensorMap& mx, const CUtens
   }
   if (max_clusters[dev] < 1) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3(2 * (unsigned)std::max<long>(1, std::min<long>(tiles, max_clusters[dev])));
-  return cudaLaunchKernelEx(&cfg, kern, mw, mx, mw64, mx64, p);
+  return cudaLaunchKernelEx(&cfg, kern, mw, mx, mw32, mx64, p);
 }
 
 }  // namespace
@@ -870,16 +881,16 @@ cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
   p.out_scale = a.out_scale;
   p.status = a.status;
   if (a.pair) {
-    CUtensorMap mw64, mx64;
-    if (!make_tensor_map_2d(&mw64, a.w, 1, (uint64_t)a.K, (uint64_t)a.E * a.w_rows, 64u) ||
+    CUtensorMap mw32, mx64;
+    if (!make_tensor_map_2d(&mw32, a.w, 1, (uint64_t)a.K, (uint64_t)a.E * a.w_rows, 32u) ||
         !make_tensor_map_2d(&mx64, a.x, 1, (uint64_t)a.K, x_rows, 64u))
       return cudaErrorInvalidValue;
     p.pblk = a.pblk;
     if (a.epi == BG_EPI_DENSE)
-      return launch_bp<BG_EPI_DENSE>(mw, mx, mw64, mx64, p, ((long)a.T + 255) / 256 * p.n_tiles, s);
+      return launch_bp<BG_EPI_DENSE>(mw, mx, mw32, mx64, p, ((long)a.T + 255) / 256 * p.n_tiles, s);
     const long tiles = (long)(a.cap / 128) * p.n_tiles;
-    if (a.epi == BG_EPI_G1) return launch_bp<BG_EPI_G1>(mw, mx, mw64, mx64, p, tiles, s);
-    return launch_bp<BG_EPI_G2>(mw, mx, mw64, mx64, p, tiles, s);
+    if (a.epi == BG_EPI_G1) return launch_bp<BG_EPI_G1>(mw, mx, mw32, mx64, p, tiles, s);
+    return launch_bp<BG_EPI_G2>(mw, mx, mw32, mx64, p, tiles, s);
   }
   if (a.epi == BG_EPI_DENSE) {
     const long tiles = ((long)a.T + a.nt - 1) / a.nt * p.n_tiles;
