@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
       const BgTile d = bg_tile_at<EPI, NT>(p, t);
       for (int kb = 0; kb < p.kb_total; ++kb) {
-        if (!mbar_wait_hot(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
+        if (!mbar_wait_all(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
           ok = false;
           break;
         }
@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(kBgThreads, 1)
       const BgTile d = bg_tile_at<EPI, NT>(p, t);
       const uint32_t idesc = idesc_make(128, d.npad, true);
       for (int kb = 0; kb < p.kb_total; ++kb) {
-        if (!mbar_wait_hot(bar_tempty + 8 * buf, buf_phase ^ 1u, abort_flag, p.status) ||
-            !mbar_wait_hot(bar_full + 8 * stage, phase, abort_flag, p.status)) {
+        if (!mbar_wait_all(bar_tempty + 8 * buf, buf_phase ^ 1u, abort_flag, p.status) ||
+            !mbar_wait_all(bar_full + 8 * stage, phase, abort_flag, p.status)) {
           ok = false;
           break;
         }
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
         if (kc + kScaleChunk < p.kb_total) fetch(kc + kScaleChunk);
         const int kn = min(kScaleChunk, p.kb_total - kc);
         for (int kb = 0; kb < kn; ++kb) {
-          ok = ok && mbar_wait_hot(bar_tfull + 8 * buf, buf_phase, abort_flag, p.status);
+          ok = ok && mbar_wait_all(bar_tfull + 8 * buf, buf_phase, abort_flag, p.status);
           if (ok) {
             tc_fence_after();
             const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * 2 * NT);
@@ -432,13 +432,14 @@ cudaError_t launch_bg_nt(const CUtensorMap& mw, const CUtensorMap& mx, const BgD
 // the tile, so what limits the rate is the round trip MMA -> commit -> fold -> release -> MMA.  Halves
 // cut it into four buffers instead of two: one is filled while three travel (N = 128 reads the token
 // rows from shared memory twice, which costs less than waiting).
-constexpr int kBpThreads = 320;
+constexpr int kBpThreads = 384;                 // 4 warps of roles, 8 epilogue warps
+constexpr int kBpRoleRegs = 72, kBpEpiRegs = 216;  // 72 + 2 * 216 = 3 * 168, the launch's registers
 constexpr int kBpStages = 6;
 constexpr uint32_t kBpHalf = 128u * 128u;       // bytes of a 128-row box of one K block
 constexpr uint32_t kBpStage = 2u * kBpHalf;     // this CTA's weight box and token rows
 constexpr uint32_t kBpRed = kBpStages * kBpStage;  // [2][256] block maxima of the epilogue halves
 constexpr uint32_t kBpBar = kBpRed + 2 * 256 * 4;
-constexpr uint32_t kBpSmem = 1024 + kBpBar + 8 * (2 * kBpStages + 2 * 4 + 1) + 16;
+constexpr uint32_t kBpSmem = 1024 + kBpBar + 8 * (2 * kBpStages + 2 * 4 + 2) + 16;
 
 struct BpTile {
   int e, n, xrow, wr0;
@@ -464,11 +465,15 @@ __device__ __forceinline__ BpTile bp_tile_at(const BgDev& p, int t) {
   return d;
 }
 
-// acc[0..15] += s * (16 loaded sums)
-__device__ __forceinline__ void bp_fold16(float2* acc, const uint32_t (&r)[16], float s) {
+// acc[0..31] += s * (32 loaded sums)
+__device__ __forceinline__ void bp_fold32(float2* acc, const uint32_t (&r)[32], float s) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) fma2(acc[j], s, s, __uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+  for (int j = 0; j < 16; ++j) fma2(acc[j], s, s, __uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
 }
+
+// SiLU(g) * u for an intermediate that becomes e4m3 (4 significant bits) right away: the approximate
+// exponential and quotient are within a few 2^-22, and 64 of them per thread stand between two tiles.
+__device__ __forceinline__ float silu_mul_fast(float g, float u) { return __fdividef(g * u, 1.0f + __expf(-g)); }
 
 // 8 floats to 32-byte aligned global memory in one store
 __device__ __forceinline__ void st_global_v8(float* p, const float2* v) {
@@ -516,6 +521,86 @@ __device__ __forceinline__ void bp_store(const BgDev& p, size_t row, int n, cons
   }
 }
 
+// What a thread needs to fold the blocks of a tile.
+struct BpFold {
+  uint32_t tmem;            // tensor-memory address of its half in buffer 0 (buffer 1: + 256 columns)
+  uint32_t tfull, tempty;   // barriers of its half in buffer 0 (buffer 1: + 16)
+  bool remote;              // tempty lies in the other CTA
+  volatile int* abort_flag;
+  int* status;
+  int buf;
+  uint32_t phase;
+  bool ok;                  // (per lane: a lane whose wait gave up goes on without waiting, and stores nothing)
+};
+
+__device__ __forceinline__ void bp_arrived(BpFold& f) {
+  if (f.ok) f.ok = mbar_wait_one(f.tfull + 16 * f.buf, f.phase, f.abort_flag, f.status);
+  __syncwarp();
+  tc_fence_after();
+}
+
+__device__ __forceinline__ void bp_release(BpFold& f, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) {
+    if (f.remote)
+      mbar_arrive_remote(f.tempty + 16 * f.buf);
+    else
+      mbar_arrive(f.tempty + 16 * f.buf);
+  }
+  f.buf ^= 1;
+  if (f.buf == 0) f.phase ^= 1u;
+}
+
+// All K blocks of a tile into acca / accb.  One chain of loads of 32 columns runs through the whole
+// tile, also across blocks: while a chunk is folded the next one is on its way, and a block is
+// released, and the next one's arrival awaited, before its last chunk is folded.  (Waiting, fences and
+// loads one after another took about 1100 cycles a block; the MMAs of a block take about 600.)
+template <bool TAIL>
+__device__ __forceinline__ void bp_fold_tile(BpFold& f, int nkb, const float* __restrict__ xs,
+                                             const float* __restrict__ wsa, const float* __restrict__ wsb, int lane,
+                                             float2 (&acca)[32], float2 (&accb)[32]) {
+  uint32_t r0[32], r1[32];
+  // scales: this block's, the next one's (in flight for a block), the one after
+  float sa = xs[0] * wsa[0], sb = xs[0] * wsb[0];
+  const int k1 = min(1, nkb - 1);
+  float x1 = xs[k1], a1 = wsa[k1], b1 = wsb[k1];
+  bp_arrived(f);
+  tmem_ld32_issue(f.tmem + 256 * f.buf, r0);
+  for (int kb = 0; kb < nkb; ++kb) {
+    const int k2 = min(kb + 2, nkb - 1);
+    const float x2 = xs[k2], a2 = wsa[k2], b2 = wsb[k2];
+    const uint32_t tb = f.tmem + 256 * f.buf;
+    tmem_wait_ld();
+    tmem_landed(r0);
+    tmem_ld32_issue(tb + 32, r1);
+    bp_fold32(acca, r0, sa);
+    if constexpr (!TAIL) {
+      tmem_wait_ld();
+      tmem_landed(r1);
+      tmem_ld32_issue(tb + 64, r0);
+      bp_fold32(acca + 16, r1, sa);
+      tmem_wait_ld();
+      tmem_landed(r0);
+      tmem_ld32_issue(tb + 96, r1);
+      bp_fold32(accb, r0, sb);
+    }
+    tmem_wait_ld();
+    tmem_landed(r1);
+    bp_release(f, lane);
+    if (kb + 1 < nkb) {
+      bp_arrived(f);
+      tmem_ld32_issue(f.tmem + 256 * f.buf, r0);
+    }
+    bp_fold32(TAIL ? accb : accb + 16, r1, sb);
+    sa = x1 * a1;
+    sb = x1 * b1;
+    x1 = x2;
+    a1 = a2;
+    b1 = b2;
+  }
+}
+
 template <int EPI>
 __global__ void __launch_bounds__(kBpThreads, 1)
     k_gemm_block_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -530,7 +615,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
   const uint32_t bar_tfull = bar_empty + 8 * kBpStages;
   const uint32_t bar_tempty = bar_tfull + 32;  // [buffer][half]
   const uint32_t bar_drain = bar_tempty + 32;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBpBar + 8 * (2 * kBpStages + 9));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBpBar + 8 * (2 * kBpStages + 10));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -540,13 +625,14 @@ __global__ void __launch_bounds__(kBpThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kBpStages; ++s) {
       mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_empty + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 2);  // the MMAs of both halves
     }
     for (int b = 0; b < 4; ++b) {
       mbar_init(bar_tfull + 8 * b, 1);
       mbar_init(bar_tempty + 8 * b, 8);  // this half's epilogue warps of both CTAs
     }
     mbar_init(bar_drain, 1);
+    mbar_init(bar_drain + 8, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmW);
@@ -565,6 +651,8 @@ __global__ void __launch_bounds__(kBpThreads, 1)
   const int chunks = EPI == BG_EPI_DENSE ? (p.T + 255) / 256 : p.meta[META_NPB];
   const int ntiles = chunks * p.n_tiles;
 
+  if (warp < 4) {
+  setmaxnreg_dec<kBpRoleRegs>();
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs) ----------------
     // completion is counted on CTA 0's full barrier, which CTA 0 arms for both CTAs' bytes
@@ -574,7 +662,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
     for (int t = pair; t < ntiles && ok; t += npairs) {
       const BpTile d = bp_tile_at<EPI>(p, t);
       for (int kb = 0; kb < p.kb_total; ++kb) {
-        if (!mbar_wait_hot(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
+        if (!mbar_wait_all(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
           ok = false;
           break;
         }
@@ -613,39 +701,34 @@ __global__ void __launch_bounds__(kBpThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ---------------- MMA issuer (CTA 0) ----------------
-    if (leader) {
+  } else if (warp < 3) {
+    // ---------------- MMA issuers (CTA 0): one thread for each half of a K block ----------------
+    // The thread's own instructions are the limit here: a satisfied wait takes about 70 cycles, the
+    // issue 90, and one thread doing both halves with its waits in turn took longer than the MMAs
+    // (600 to 1100 cycles a block for 545).  So each half has its thread, on different SM quarters,
+    // and both waits of a block are polled together.
+    if (leader && elect_one()) {
+      const uint32_t h = warp - 1;
+      const uint64_t a0 = sdesc_k_sw128(sbase + kBpHalf), b0 = sdesc_k_sw128(sbase + h * (kBpHalf / 2));
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true, any = false;
       for (int t = pair; t < ntiles && ok; t += npairs) {
-        const BpTile d = bp_tile_at<EPI>(p, t);
-        const uint32_t idesc = idesc_make(d.tail ? 128 : 256, 128, true);
-        for (int kb = 0; kb < p.kb_total && ok; ++kb) {
-          if (!mbar_wait_hot(bar_full + 8 * stage, phase, abort_flag, p.status)) {
-            ok = false;
-            break;
+        const uint32_t idesc = idesc_make(bp_tile_at<EPI>(p, t).tail ? 128 : 256, 128, true);
+        for (int kb = 0; kb < p.kb_total; ++kb) {
+          const uint32_t fb = bar_full + 8 * stage, eb = bar_tempty + 8 * (2 * buf + h);
+          const bool full = mbar_try_wait(fb, phase), free_buf = mbar_try_wait(eb, buf_phase ^ 1u);
+          if (!(full && free_buf)) {
+            ok = mbar_wait_one(fb, phase, abort_flag, p.status) &&
+                 mbar_wait_one(eb, buf_phase ^ 1u, abort_flag, p.status);
+            if (!ok) break;
           }
-          const uint32_t sw = sbase + stage * kBpStage, sx = sw + kBpHalf;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (!mbar_wait_hot(bar_tempty + 8 * (2 * buf + j), buf_phase ^ 1u, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_pair<true>(tmem_base + 256u * buf + 128u * j, sdesc_k_sw128(sx + kk * 32),
-                                  sdesc_k_sw128(sw + j * (kBpHalf / 2) + kk * 32), idesc, kk > 0);
-              tc_commit_both(bar_tfull + 8 * (2 * buf + j));
-              if (j == 1) tc_commit_both(bar_empty + 8 * stage);
-            }
-            __syncwarp();
-            any = true;
-          }
+          tc_fence_after();
+          const uint64_t so = (uint64_t)(stage * (kBpStage >> 4));
+          tc_mma_pair_kblock(tmem_base + 256u * buf + 128u * h, a0 + so, b0 + so, idesc);
+          tc_commit_both(bar_tfull + 8 * (2 * buf + h));
+          tc_commit_both(bar_empty + 8 * stage);
+          any = true;
           if (++stage == kBpStages) {
             stage = 0;
             phase ^= 1u;
@@ -655,21 +738,29 @@ __global__ void __launch_bounds__(kBpThreads, 1)
         }
       }
       if (!ok && any) {  // the tensor cores must be idle before tensor memory is freed
-        if (lane == 0) tc_commit_pair(bar_drain);
-        __syncwarp();
-        mbar_wait_drain(bar_drain, 0, 100000000ull);
+        tc_commit_pair(bar_drain + 8 * h);
+        mbar_wait_drain(bar_drain + 8 * h, 0, 100000000ull);
       }
     }
     __syncwarp();
+  }
   } else {
-    // ---------------- epilogue (warps 2..9 of both CTAs) ----------------
-    const int q = warp & 3, h = (warp - 2) >> 2;  // tensor-memory quadrant; half of the K block
+    setmaxnreg_inc<kBpEpiRegs>();
+    // ---------------- epilogue (warps 4..11 of both CTAs) ----------------
+    const int q = warp & 3, h = (warp - 4) >> 2;  // tensor-memory quadrant; half of the K block
     const int lrow = q * 32 + lane;
     float* red = reinterpret_cast<float*>(smem + kBpRed);
-    const uint32_t tempty0 = mapa_shared(bar_tempty, 0);
-    int buf = 0, par = 0;
-    uint32_t buf_phase = 0;
-    bool ok = true;
+    BpFold f;
+    f.tmem = tmem_base + ((uint32_t)(q * 32) << 16) + 128u * h;
+    f.tfull = bar_tfull + 8 * h;
+    f.tempty = (leader ? bar_tempty : mapa_shared(bar_tempty, 0)) + 8 * h;
+    f.remote = !leader;
+    f.abort_flag = abort_flag;
+    f.status = p.status;
+    f.buf = 0;
+    f.phase = 0;
+    f.ok = true;
+    int par = 0;
     for (int t = pair; t < ntiles; t += npairs) {
       const BpTile d = bp_tile_at<EPI>(p, t);
       // This thread's row and its two runs of `wide` sums, tensor-memory columns [0, wide) and
@@ -687,53 +778,10 @@ __global__ void __launch_bounds__(kBpThreads, 1)
       float2 acca[32], accb[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acca[i] = accb[i] = make_float2(0.0f, 0.0f);
-      float sa = xs[0] * wsa[0], sb = xs[0] * wsb[0];
-      for (int kb = 0; kb < p.kb_total; ++kb) {
-        // the next block's scales are on their way while this block is folded
-        const int nk = min(kb + 1, p.kb_total - 1);
-        const float nx = xs[nk], na = wsa[nk], nb = wsb[nk];
-        ok = ok && mbar_wait_hot(bar_tfull + 8 * (2 * buf + h), buf_phase, abort_flag, p.status);
-        if (ok) {
-          tc_fence_after();
-          const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + 256u * buf + 128u * h;
-          uint32_t r0[16], r1[16];
-          if (!d.tail) {
-            tmem_ld16_issue(tb, r0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              tmem_ld16_wait(r0);
-              tmem_ld16_issue(tb + 64 + 16 * i, r1);
-              bp_fold16(acca + 8 * i, r0, sa);
-              tmem_ld16_wait(r1);
-              if (i < 3) tmem_ld16_issue(tb + 16 * (i + 1), r0);
-              bp_fold16(accb + 8 * i, r1, sb);
-            }
-          } else {
-            tmem_ld16_issue(tb, r0);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              tmem_ld16_wait(r0);
-              tmem_ld16_issue(tb + 32 + 16 * i, r1);
-              bp_fold16(acca + 8 * i, r0, sa);
-              tmem_ld16_wait(r1);
-              if (i < 1) tmem_ld16_issue(tb + 16, r0);
-              bp_fold16(accb + 8 * i, r1, sb);
-            }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (leader)
-              mbar_arrive(bar_tempty + 8 * (2 * buf + h));
-            else
-              mbar_arrive_remote(tempty0 + 8 * (2 * buf + h));
-          }
-        }
-        buf ^= 1;
-        if (buf == 0) buf_phase ^= 1u;
-        sa = nx * na;
-        sb = nx * nb;
-      }
+      if (!d.tail)
+        bp_fold_tile<false>(f, p.kb_total, xs, wsa, wsb, lane, acca, accb);
+      else
+        bp_fold_tile<true>(f, p.kb_total, xs, wsa, wsb, lane, acca, accb);
       if constexpr (G1) {
         // SiLU(gate) * up of `wide` columns, the block's maximum over the two (tail: four) threads
         // of the row, then this thread's codes
@@ -741,8 +789,8 @@ __global__ void __launch_bounds__(kBpThreads, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           if (i < wide / 2) {
-            acca[i].x = silu(acca[i].x) * accb[i].x;
-            acca[i].y = silu(acca[i].y) * accb[i].y;
+            acca[i].x = silu_mul_fast(acca[i].x, accb[i].x);
+            acca[i].y = silu_mul_fast(acca[i].y, accb[i].y);
             a = max_nan(a, max_nan(fabsf(acca[i].x), fabsf(acca[i].y)));
           }
         }
@@ -754,7 +802,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
         par ^= 1;  // (the other half of red: a slower warp may still read this one)
         const float s = block_scale_from_amax(a);
         const float r = 1.0f / s;
-        if (ok) {
+        if (f.ok) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (size_t)row * p.n_out +
                                                 (size_t)d.n * 128 + 64 * hf + wide * h);
 #pragma unroll
@@ -770,7 +818,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
           }
           if (h == 0 && hf == 0) p.out_scale[(size_t)row * (p.n_out / 128) + d.n] = s;
         }
-      } else if (ok && row_ok) {
+      } else if (f.ok && row_ok) {
         const int n = d.n * 256 + 128 * hf + 64 * h;  // columns of box 0 (tail: of box hf)
         size_t orow = (size_t)row;
         bool store = true;
