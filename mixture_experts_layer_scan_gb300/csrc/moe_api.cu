@@ -195,6 +195,7 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
       if (opts && (opts->cta_pair < 0 || opts->cta_pair > 2 || opts->split_k < 0)) return MOE_ERR_ARG;
       if (opts && opts->cta_pair == 2 && !p.swap) return MOE_ERR_UNSUPPORTED;
       p.pair = !p.swap;
+      p.y_bf16 = p.pair;  // (what k_gemm_block_pair stores)
       p.B = p.swap ? 16 : 128;
       p.xbox = p.swap ? block_swap_tokens(T) : 128;
       p.kb1 = H / 128;

@@ -40,7 +40,7 @@ struct BgDev {
   int w_scale_rows;     // scale rows per expert
   int s_pair_off;       // offset of D1's scale row from D0's
   int stages, out_bf16;
-  int out_v8;           // fp32 rows of out are 32-byte aligned
+  int out_v8;           // rows of out are 32-byte aligned
   uint32_t stage_bytes, bar_off, scale_off, out_off;
   const float* a_scale;  // [rows][kb_total]
   const float* w_scale;  // [E][w_scale_rows][kb_total]
@@ -438,8 +438,16 @@ constexpr int kBpStages = 6;
 constexpr uint32_t kBpHalf = 128u * 128u;       // bytes of a 128-row box of one K block
 constexpr uint32_t kBpStage = 2u * kBpHalf;     // this CTA's weight box and token rows
 constexpr uint32_t kBpRed = kBpStages * kBpStage;  // [2][256] block maxima of the epilogue halves
-constexpr uint32_t kBpBar = kBpRed + 2 * 256 * 4;
-constexpr uint32_t kBpSmem = 1024 + kBpBar + 8 * (2 * kBpStages + 2 * 4 + 2) + 16;
+constexpr int kBpChunk = 4;                     // K blocks of one scale chunk
+constexpr int kBpChunks = 4;                    // scale chunks in the ring (a power of two)
+constexpr uint32_t kBpScale = kBpRed + 2 * 256 * 4;  // [chunk][block][128 rows] (scale of run a, of run b)
+constexpr uint32_t kBpBar = kBpScale + kBpChunks * kBpChunk * 128 * 8;
+// barriers and words behind them, from kBpBar: full, empty [stage]; tfull, tempty [buffer][half];
+// drain [half]; sfull, sempty [chunk]; tensor-memory address, abort flag
+constexpr uint32_t kBpTfull = 8 * 2 * kBpStages, kBpTempty = kBpTfull + 32, kBpDrain = kBpTempty + 32,
+                   kBpSfull = kBpDrain + 16, kBpSempty = kBpSfull + 8 * kBpChunks,
+                   kBpWords = kBpSempty + 8 * kBpChunks;
+constexpr uint32_t kBpSmem = 1024 + kBpBar + kBpWords + 16;
 
 struct BpTile {
   int e, n, xrow, wr0;
@@ -482,11 +490,31 @@ __device__ __forceinline__ void st_global_v8(float* p, const float2* v) {
                : "memory");
 }
 
-// A thread's 2 * PAIRS consecutive output columns from column n of one row.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// A thread's 2 * PAIRS consecutive output columns from column n of one row.  A warp's lanes hold
+// different rows, so a store reaches 32 lines whatever its width: 32 bytes a lane, whole sectors.
+// GEMM2's rows leave as bf16: the outputs of a token's experts are rounded once more before their
+// fp32 sum, about 2^-9 of each, below the 2^-4 steps of the e4m3 intermediate they come from, and
+// their 2 bytes instead of 4 take 0.2 ms off a layer of 8192 tokens (stores, and the combine's reads).
 template <int EPI, int PAIRS>
 __device__ __forceinline__ void bp_store(const BgDev& p, size_t row, int n, const float2* acc) {
   const size_t o = row * (size_t)p.n_out + n;
-  if (EPI == BG_EPI_G2 || (!p.out_bf16 && p.out_v8)) {
+  if (EPI == BG_EPI_G2 || (p.out_bf16 && p.out_v8)) {
+    uint16_t* y = static_cast<uint16_t*>(p.out) + o;
+#pragma unroll
+    for (int i = 0; i < PAIRS; i += 8) {
+      if (n + 2 * i >= p.n_out) continue;
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = pack_bf16x2(acc[i + j].x, acc[i + j].y);
+      st_global_v8(y + 2 * i, v);
+    }
+  } else if (!p.out_bf16 && p.out_v8) {
     float* y = static_cast<float*>(p.out) + o;
 #pragma unroll
     for (int i = 0; i < PAIRS; i += 4)
@@ -521,35 +549,36 @@ __device__ __forceinline__ void bp_store(const BgDev& p, size_t row, int n, cons
   }
 }
 
-// What a thread needs to fold the blocks of a tile.
+// What a thread keeps for the folds beside its accumulators.  Registers are short (128 sums, 64 loaded
+// columns): a spilled word in the loop costs a tenth of the rate.
 struct BpFold {
-  uint32_t tmem;            // tensor-memory address of its half in buffer 0 (buffer 1: + 256 columns)
-  uint32_t tfull, tempty;   // barriers of its half in buffer 0 (buffer 1: + 16)
-  bool remote;              // tempty lies in the other CTA
-  volatile int* abort_flag;
-  int* status;
-  int buf;
-  uint32_t phase;
-  bool ok;                  // (per lane: a lane whose wait gave up goes on without waiting, and stores nothing)
+  uint32_t bars;    // barriers of this CTA (kBpBar)
+  uint32_t tmem;    // tensor-memory address of its half in buffer 0 (buffer 1: + 256 columns)
+  uint32_t tfull;   // arrival barrier of its half in buffer 0 (buffer 1: + 16)
+  uint32_t tempty;  // release barrier of its half in buffer 0 (buffer 1: + 16), in CTA 0
+  uint32_t scale;   // this row's scale pair of block 0 of chunk 0
+  uint32_t blocks;  // blocks folded so far: buffer and phase
+  uint32_t chunks;  // scale chunks used so far
+  bool ok;          // (per lane: a lane whose wait gave up goes on without waiting, and stores nothing)
 };
 
-__device__ __forceinline__ void bp_arrived(BpFold& f) {
-  if (f.ok) f.ok = mbar_wait_one(f.tfull + 16 * f.buf, f.phase, f.abort_flag, f.status);
+__device__ __forceinline__ bool bp_wait(const BpFold& f, uint32_t bar, uint32_t parity, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  volatile int* abort_flag = static_cast<volatile int*>(__cvta_shared_to_generic(f.bars + kBpWords + 4));
+  return mbar_wait_one(bar, parity, abort_flag, status);
+}
+
+__device__ __forceinline__ void bp_arrived(BpFold& f, int* status) {
+  if (f.ok) f.ok = bp_wait(f, f.tfull + 16 * (f.blocks & 1u), (f.blocks >> 1) & 1u, status);
   __syncwarp();
   tc_fence_after();
 }
 
-__device__ __forceinline__ void bp_release(BpFold& f, int lane) {
+__device__ __forceinline__ void bp_release(BpFold& f) {
   tc_fence_before();
   __syncwarp();
-  if (lane == 0) {
-    if (f.remote)
-      mbar_arrive_remote(f.tempty + 16 * f.buf);
-    else
-      mbar_arrive(f.tempty + 16 * f.buf);
-  }
-  f.buf ^= 1;
-  if (f.buf == 0) f.phase ^= 1u;
+  if (elect_one()) mbar_arrive_remote(f.tempty + 16 * (f.blocks & 1u));  // (CTA 0's own included)
+  ++f.blocks;
 }
 
 // All K blocks of a tile into acca / accb.  One chain of loads of 32 columns runs through the whole
@@ -557,48 +586,64 @@ __device__ __forceinline__ void bp_release(BpFold& f, int lane) {
 // released, and the next one's arrival awaited, before its last chunk is folded.  (Waiting, fences and
 // loads one after another took about 1100 cycles a block; the MMAs of a block take about 600.)
 template <bool TAIL>
-__device__ __forceinline__ void bp_fold_tile(BpFold& f, int nkb, const float* __restrict__ xs,
-                                             const float* __restrict__ wsa, const float* __restrict__ wsb, int lane,
-                                             float2 (&acca)[32], float2 (&accb)[32]) {
+__device__ __forceinline__ void bp_fold_tile(BpFold& f, int nkb, int* status, float2 (&acca)[32],
+                                             float2 (&accb)[32]) {
   uint32_t r0[32], r1[32];
-  // scales: this block's, the next one's (in flight for a block), the one after
-  float sa = xs[0] * wsa[0], sb = xs[0] * wsb[0];
-  const int k1 = min(1, nkb - 1);
-  float x1 = xs[k1], a1 = wsa[k1], b1 = wsb[k1];
-  bp_arrived(f);
-  tmem_ld32_issue(f.tmem + 256 * f.buf, r0);
+  bp_arrived(f, status);
+  tmem_ld32_issue(f.tmem + 256 * (f.blocks & 1u), r0);
+#pragma unroll 1
   for (int kb = 0; kb < nkb; ++kb) {
-    const int k2 = min(kb + 2, nkb - 1);
-    const float x2 = xs[k2], a2 = wsa[k2], b2 = wsb[k2];
-    const uint32_t tb = f.tmem + 256 * f.buf;
+    const uint32_t slot = f.chunks & (kBpChunks - 1), i = kb & (kBpChunk - 1);
+    if (i == 0) {
+      if (f.ok) f.ok = bp_wait(f, f.bars + kBpSfull + 8 * slot, (f.chunks / kBpChunks) & 1u, status);
+      __syncwarp();
+    }
+    const float2 s = lds_f32x2(f.scale + (slot * kBpChunk + i) * (128u * 8u));
+    if (i == kBpChunk - 1 || kb == nkb - 1) {  // the chunk's last block: its scales are in registers
+      __syncwarp();
+      if (elect_one()) mbar_arrive(f.bars + kBpSempty + 8 * slot);
+      ++f.chunks;
+    }
+    const uint32_t tb = f.tmem + 256 * (f.blocks & 1u);
     tmem_wait_ld();
     tmem_landed(r0);
     tmem_ld32_issue(tb + 32, r1);
-    bp_fold32(acca, r0, sa);
+    bp_fold32(acca, r0, s.x);
     if constexpr (!TAIL) {
       tmem_wait_ld();
       tmem_landed(r1);
       tmem_ld32_issue(tb + 64, r0);
-      bp_fold32(acca + 16, r1, sa);
+      bp_fold32(acca + 16, r1, s.x);
       tmem_wait_ld();
       tmem_landed(r0);
       tmem_ld32_issue(tb + 96, r1);
-      bp_fold32(accb, r0, sb);
+      bp_fold32(accb, r0, s.y);
     }
     tmem_wait_ld();
     tmem_landed(r1);
-    bp_release(f, lane);
+    bp_release(f);
     if (kb + 1 < nkb) {
-      bp_arrived(f);
-      tmem_ld32_issue(f.tmem + 256 * f.buf, r0);
+      bp_arrived(f, status);
+      tmem_ld32_issue(f.tmem + 256 * (f.blocks & 1u), r0);
     }
-    bp_fold32(TAIL ? accb : accb + 16, r1, sb);
-    sa = x1 * a1;
-    sb = x1 * b1;
-    x1 = x2;
-    a1 = a2;
-    b1 = b2;
+    bp_fold32(TAIL ? accb : accb + 16, r1, s.y);
   }
+}
+
+// The rows and scales of a tile as tensor-memory lane `lrow` sees them.
+template <int EPI>
+__device__ __forceinline__ int bp_row(const BpTile& d, uint32_t rank, int lrow) {
+  return d.xrow + (d.tail ? 64 * (int)rank + (lrow & 63) : 128 * (int)rank + lrow);
+}
+template <int EPI>
+__device__ __forceinline__ void bp_scale_rows(const BgDev& p, const BpTile& d, int lrow, const float*& wsa,
+                                              const float*& wsb) {
+  constexpr bool G1 = EPI == BG_EPI_G1;
+  const int hf = d.tail ? lrow >> 6 : 0, last = p.w_scale_rows - 1;
+  const int ra = G1 ? d.n : min(2 * d.n + hf, last);
+  const int rb = G1 ? d.n + p.s_pair_off : d.tail ? ra : min(2 * d.n + 1, last);
+  wsa = p.w_scale + ((size_t)d.e * p.w_scale_rows + ra) * p.kb_total;
+  wsb = p.w_scale + ((size_t)d.e * p.w_scale_rows + rb) * p.kb_total;
 }
 
 template <int EPI>
@@ -612,10 +657,12 @@ __global__ void __launch_bounds__(kBpThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar_full = sbase + kBpBar;
   const uint32_t bar_empty = bar_full + 8 * kBpStages;
-  const uint32_t bar_tfull = bar_empty + 8 * kBpStages;
-  const uint32_t bar_tempty = bar_tfull + 32;  // [buffer][half]
-  const uint32_t bar_drain = bar_tempty + 32;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBpBar + 8 * (2 * kBpStages + 10));
+  const uint32_t bar_tfull = bar_full + kBpTfull;
+  const uint32_t bar_tempty = bar_full + kBpTempty;
+  const uint32_t bar_drain = bar_full + kBpDrain;
+  const uint32_t bar_sfull = bar_full + kBpSfull;
+  const uint32_t bar_sempty = bar_full + kBpSempty;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBpBar + kBpWords);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -633,6 +680,10 @@ __global__ void __launch_bounds__(kBpThreads, 1)
     }
     mbar_init(bar_drain, 1);
     mbar_init(bar_drain + 8, 1);
+    for (int c = 0; c < kBpChunks; ++c) {
+      mbar_init(bar_sfull + 8 * c, 1);
+      mbar_init(bar_sempty + 8 * c, 8);
+    }
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmW);
@@ -743,45 +794,90 @@ __global__ void __launch_bounds__(kBpThreads, 1)
       }
     }
     __syncwarp();
+  } else {
+    // ---------------- scales (warp 3): products of row and weight scales, in chunks of K blocks ----------------
+    // (the fold's threads would wait for these loads: a row's scales lie kb_total floats from the
+    // next row's, so a warp's load touches 32 lines)
+    float2* ring = reinterpret_cast<float2*>(smem + kBpScale);
+    int chunk = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = pair; t < ntiles && ok; t += npairs) {
+      const BpTile d = bp_tile_at<EPI>(p, t);
+      for (int kc = 0; kc < p.kb_total; kc += kBpChunk) {
+        if (!mbar_wait_all(bar_sempty + 8 * chunk, phase ^ 1u, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        // 64 rows at a time: this warp shares its register budget with the other roles
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          const int r0 = bp_row<EPI>(d, rank, lane + 64 * hf), r1 = bp_row<EPI>(d, rank, lane + 64 * hf + 32);
+          const float* x0 = p.a_scale + (size_t)(EPI != BG_EPI_DENSE || r0 < p.T ? r0 : 0) * p.kb_total;
+          const float* x1 = p.a_scale + (size_t)(EPI != BG_EPI_DENSE || r1 < p.T ? r1 : 0) * p.kb_total;
+          const float *wa, *wb;
+          bp_scale_rows<EPI>(p, d, 64 * hf, wa, wb);
+          float v0[kBpChunk], v1[kBpChunk], a[kBpChunk], b[kBpChunk];
+#pragma unroll
+          for (int i = 0; i < kBpChunk; ++i) {
+            const int kb = min(kc + i, p.kb_total - 1);
+            v0[i] = x0[kb];
+            v1[i] = x1[kb];
+            a[i] = wa[kb];
+            b[i] = wb[kb];
+          }
+          float2* dst = ring + chunk * (kBpChunk * 128) + 64 * hf + lane;
+#pragma unroll
+          for (int i = 0; i < kBpChunk; ++i) {
+            dst[i * 128] = make_float2(v0[i] * a[i], v0[i] * b[i]);
+            dst[i * 128 + 32] = make_float2(v1[i] * a[i], v1[i] * b[i]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_sfull + 8 * chunk);
+        if (++chunk == kBpChunks) {
+          chunk = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
   }
   } else {
     setmaxnreg_inc<kBpEpiRegs>();
     // ---------------- epilogue (warps 4..11 of both CTAs) ----------------
-    const int q = warp & 3, h = (warp - 4) >> 2;  // tensor-memory quadrant; half of the K block
-    const int lrow = q * 32 + lane;
-    float* red = reinterpret_cast<float*>(smem + kBpRed);
     BpFold f;
-    f.tmem = tmem_base + ((uint32_t)(q * 32) << 16) + 128u * h;
-    f.tfull = bar_tfull + 8 * h;
-    f.tempty = (leader ? bar_tempty : mapa_shared(bar_tempty, 0)) + 8 * h;
-    f.remote = !leader;
-    f.abort_flag = abort_flag;
-    f.status = p.status;
-    f.buf = 0;
-    f.phase = 0;
-    f.ok = true;
+    {
+      const uint32_t q = warp & 3, h = (warp - 4) >> 2;  // tensor-memory quadrant; half of the K block
+      f.bars = bar_full;
+      f.tmem = tmem_base + ((q * 32) << 16) + 128u * h;
+      f.tfull = bar_tfull + 8 * h;
+      f.tempty = mapa_shared(bar_tempty, 0) + 8 * h;
+      f.scale = sbase + kBpScale + (q * 32 + lane) * 8u;
+      f.blocks = f.chunks = 0;
+      f.ok = true;
+    }
     int par = 0;
     for (int t = pair; t < ntiles; t += npairs) {
-      const BpTile d = bp_tile_at<EPI>(p, t);
       // This thread's row and its two runs of `wide` sums, tensor-memory columns [0, wide) and
       // [wide, 2 wide) of its half: of box 0 and box 1, or (tail) of box hf alone.
-      const int hf = d.tail ? lrow >> 6 : 0;
-      const int row = d.xrow + (d.tail ? 64 * (int)rank + (lrow & 63) : 128 * (int)rank + lrow);
-      const int wide = d.tail ? 32 : 64;
-      const int last = p.w_scale_rows - 1;
-      const int sra = G1 ? d.n : min(2 * d.n + hf, last);
-      const int srb = G1 ? d.n + p.s_pair_off : d.tail ? sra : min(2 * d.n + 1, last);
-      const float* wsa = p.w_scale + ((size_t)d.e * p.w_scale_rows + sra) * p.kb_total;
-      const float* wsb = p.w_scale + ((size_t)d.e * p.w_scale_rows + srb) * p.kb_total;
-      const bool row_ok = EPI != BG_EPI_DENSE || row < p.T;
-      const float* xs = p.a_scale + (size_t)(row_ok ? row : 0) * p.kb_total;
       float2 acca[32], accb[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acca[i] = accb[i] = make_float2(0.0f, 0.0f);
-      if (!d.tail)
-        bp_fold_tile<false>(f, p.kb_total, xs, wsa, wsb, lane, acca, accb);
+      if (!bp_tile_at<EPI>(p, t).tail)
+        bp_fold_tile<false>(f, p.kb_total, p.status, acca, accb);
       else
-        bp_fold_tile<true>(f, p.kb_total, xs, wsa, wsb, lane, acca, accb);
+        bp_fold_tile<true>(f, p.kb_total, p.status, acca, accb);
+      // the tile's place and the thread's, computed here again rather than kept through the fold
+      int t_again = t, tid = threadIdx.x - 128;
+      asm volatile("" : "+r"(t_again), "+r"(tid));
+      const BpTile d = bp_tile_at<EPI>(p, t_again);
+      const int lrow = tid & 127, h = tid >> 7;
+      const int hf = d.tail ? lrow >> 6 : 0;
+      const int row = bp_row<EPI>(d, rank, lrow);
+      const int wide = d.tail ? 32 : 64;
+      const bool row_ok = EPI != BG_EPI_DENSE || row < p.T;
+      float* red = reinterpret_cast<float*>(smem + kBpRed);
       if constexpr (G1) {
         // SiLU(gate) * up of `wide` columns, the block's maximum over the two (tail: four) threads
         // of the row, then this thread's codes
@@ -919,7 +1015,7 @@ cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
     p.s_pair_off = 1;
   }
   p.out_bf16 = a.out_bf16 ? 1 : 0;
-  p.out_v8 = a.n_out % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+  p.out_v8 = a.n_out % (a.out_bf16 ? 16 : 8) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   p.a_scale = a.a_scale;
   p.w_scale = a.w_scale;
   p.sorted = a.sorted;

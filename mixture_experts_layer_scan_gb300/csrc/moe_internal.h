@@ -88,7 +88,7 @@ cudaError_t launch_quant_block_scatter(const void* x, int T, int K, int k, const
 enum BlockGemmEpilogue {
   BG_EPI_DENSE = 0,  // out [T][n_out] bf16 or fp32
   BG_EPI_G1 = 1,     // expert GEMM1: SiLU(gate)*up -> e4m3 out [cap][I] + out_scale [cap][I/128]
-  BG_EPI_G2 = 2      // expert GEMM2: fp32 Y[pair][H]
+  BG_EPI_G2 = 2      // expert GEMM2: Y[pair][H], fp32 (swap-AB) or bf16 (CTA pairs)
 };
 struct BlockGemmArgs {
   int epi;

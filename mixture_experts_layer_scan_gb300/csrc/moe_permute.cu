@@ -725,6 +725,45 @@ __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, in
   }
 }
 
+// out[t] = sum_j w[t][j] * Y[t*k + j] for bf16 rows without K splits (the block-scaled expert layer):
+// j in order, fp32, one rounding at the end.  Bound by HBM (2 k + 2 bytes per output element): each
+// thread loads its 8 columns of up to 8 rows before their use, with no index arithmetic between them
+// (the general kernel's per-row divisions made it 209 us for 65536 x 4096 rows).
+constexpr int kCombineRows = 8;
+__global__ void __launch_bounds__(256) k_combine_bf16(const uint4* __restrict__ Y, const float* __restrict__ w, int T,
+                                                      int k, int vec_per_row, uint4* __restrict__ out) {
+  pdl_enter();
+  const int v = blockIdx.y * 256 + threadIdx.x;
+  if (v >= vec_per_row) return;
+  for (int t = blockIdx.x; t < T; t += gridDim.x) {
+    const uint4* y = Y + (size_t)t * k * vec_per_row + v;
+    const float* wt = w + (size_t)t * k;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < k; j0 += kCombineRows) {
+      uint4 u[kCombineRows];
+      float wj[kCombineRows];
+#pragma unroll
+      for (int j = 0; j < kCombineRows; ++j) {
+        const bool in = j0 + j < k;
+        u[j] = in ? __ldcs(y + (size_t)(j0 + j) * vec_per_row) : make_uint4(0, 0, 0, 0);
+        wj[j] = in ? wt[j0 + j] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kCombineRows; ++j) {
+        if (j0 + j >= k) break;
+        const uint32_t q[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc[2 * c] = fmaf(wj[j], bf16_bits_to_f32(q[c] & 0xffffu), acc[2 * c]);
+          acc[2 * c + 1] = fmaf(wj[j], bf16_bits_to_f32(q[c] >> 16), acc[2 * c + 1]);
+        }
+      }
+    }
+    out[(size_t)t * vec_per_row + v] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                                                  pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+  }
+}
+
 // Scalar fallback of the combine for H not divisible by 4 (fp32 path only).
 template <bool Y_BF16, bool OUT_BF16>
 __global__ void k_combine_scalar(const void* __restrict__ Yv, int splits, size_t split_stride,
@@ -891,6 +930,12 @@ static cudaError_t combine_vec(const void* Y, int splits, size_t split_stride, c
 
 cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_stride, const float* w, int T, int k,
                            int H, void* out, int out_bf16, cudaStream_t s) {
+  if (y_bf16 && out_bf16 && splits == 1 && H % 8 == 0) {
+    const int vpr = H / 8, cols = (vpr + 255) / 256;
+    MOE_LAUNCH(k_combine_bf16, dim3(std::min(T, std::max(1, 152 * 16 / cols)), cols), dim3(256), 0, s, (const uint4*)Y, w,
+               T, k, vpr, (uint4*)out);
+    return cudaGetLastError();
+  }
   if (H % 8 == 0) {
     if (y_bf16 && out_bf16) return combine_vec<true, true>(Y, splits, split_stride, w, T, k, H, out, s);
     if (y_bf16) return combine_vec<true, false>(Y, splits, split_stride, w, T, k, H, out, s);
