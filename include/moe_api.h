@@ -352,7 +352,8 @@ MOE_API int moe_inv_rope_fp8_quant(const void* x, int T, int heads, int head_dim
  * both products and the reciprocal are one fp32 rounding each.  A block holding a NaN
  * or an infinity gets that as its scale, and its codes stand for no finite value.
  *   x [T][K] MOE_F32 or MOE_BF16;  q [T][K] e4m3 codes;  scale [T][ceil(K/128)] fp32
- * K % 16 == 0 (MOE_ERR_UNSUPPORTED otherwise); scale 4-byte aligned, x and q 16. */
+ * K % 16 == 0 (MOE_ERR_UNSUPPORTED otherwise), T * ceil(K/128) < 2^31 - 2^24; scale 4-byte aligned,
+ * x and q 16. */
 MOE_API int moe_quant_block(const void* x, int T, int K, moe_dtype x_dtype, uint8_t* q, float* scale,
                             moe_stream_t stream);
 /* The same of h = SiLU(g) * u (fp32, not rounded in between), with gate_up [T][2I] holding the row

@@ -160,18 +160,21 @@ def _dt(t: torch.Tensor) -> int:
             torch.uint8: MOE_E4M3}[t.dtype]
 
 
-def _p(t: Optional[torch.Tensor]):
+def _p(t: Optional[torch.Tensor]) -> Optional[int]:
     if t is None:
         return None
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
+        # (the raw handle: building a Stream object costs 3 us of a call's 10 on the host)
+        if torch.cuda.is_initialized():
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _opts(options) -> Optional[ctypes.POINTER(moe_options)]:

@@ -958,6 +958,7 @@ static int quant_block(const void* x, int T, int K, moe_dtype x_dtype, bool silu
   if (T < 0 || K < 1) return MOE_ERR_ARG;
   if (x_dtype != MOE_F32 && x_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (K % 16) return MOE_ERR_UNSUPPORTED;
+  if ((long long)T * ((K + 127) / 128) >= (1ll << 31) - (1ll << 24)) return MOE_ERR_ARG;
   if (T == 0) return MOE_OK;
   if (!x || !q || !scale) return MOE_ERR_ARG;
   if (misaligned(x) || misaligned(q) || misaligned(scale, 4)) return MOE_ERR_ALIGNMENT;

@@ -10,8 +10,11 @@
 // The SiLU form quantises h = SiLU(g) * u of a row [g | u] without storing h.  The scatter form
 // serves the expert layer: row t's codes and scales go to the expert-sorted rows of its pairs.
 //
-// Bound by HBM: an element is read once and leaves as one byte.  16 lanes share a block (8
-// elements each: 16-byte loads of bf16, 8-byte stores), so its maximum is four shuffles.
+// Bound by HBM: an element is read once and leaves as one byte.  8 lanes share a block, 16 elements
+// each (two 16-byte loads of bf16, one 16-byte store, the block's maximum in three shuffles), and every
+// lane loads kUnroll blocks before it works on the first: with 8 elements a lane and one block at a time
+// too few bytes were in flight (8192 x 4096 bf16: 28.9 us, 3.5 TB/s).  The SiLU form is bound by its
+// exponential and quotient as much as by memory.
 #include <algorithm>
 
 #include "moe_device.cuh"
@@ -33,71 +36,93 @@ struct QuantDev {
   int k;
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// 16 elements, 16-byte loads; widened when they are used
+template <typename TIn>
+struct Raw16 {
+  uint4 v[sizeof(TIn)];
+  __device__ __forceinline__ void load(const TIn* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_bits_to_f32(w[i] & 0xffffu);
-    v[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
+    for (int i = 0; i < (int)sizeof(TIn); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(TIn); ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    constexpr int per = 16 / sizeof(TIn);  // elements of one vector
+    const uint4& q = v[i / per];
+    const int w = (i % per) * sizeof(TIn) / 4;
+    const uint32_t u = w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w;
+    if constexpr (sizeof(TIn) == 4) return __uint_as_float(u);
+    return bf16_bits_to_f32((i & 1) ? (u >> 16) : (u & 0xffffu));
+  }
+};
 
 template <typename TIn, bool SILU, bool SCATTER>
 __global__ void __launch_bounds__(kQuantThreads) k_quant_block(const QuantDev p) {
-  pdl_enter();
-  const int l16 = threadIdx.x & 15;
-  const long units = (long)p.T * p.nb;
-  const long step = (long)gridDim.x * (kQuantThreads / 16);
+  // (dependents launch once this kernel's own wait is over: what came before it is then complete)
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int kUnroll = SILU ? 1 : 2;
+  const uint32_t l8 = threadIdx.x & 7;
+  const uint32_t units = (uint32_t)p.T * (uint32_t)p.nb;
+  const uint32_t step = gridDim.x * (kQuantThreads / 8);
   const TIn* x = static_cast<const TIn*>(p.x);
-  // (both halves of a warp run the same number of rounds: the shuffles name all 32 lanes)
-  const long u0 = (long)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4);
-  for (long base = u0 & ~1l; base < units; base += step) {
-    const long u = base + (u0 & 1);
-    const bool live = u < units;
-    const int t = live ? (int)(u / p.nb) : 0;
-    const int b = live ? (int)(u - (long)t * p.nb) : 0;
-    const int c = b * 128 + l16 * 8;
-    const bool on = live && c < p.K;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (on) {
-      if constexpr (SILU) {
-        float g[8], w[8];
-        load8(x + (size_t)t * 2 * p.K + c, g);
-        load8(x + (size_t)t * 2 * p.K + p.K + c, w);
+  // (the four blocks of a warp run the same number of rounds: the shuffles name all 32 lanes)
+  const uint32_t u0 = blockIdx.x * (kQuantThreads / 8) + (threadIdx.x >> 3);
+  for (uint32_t base = u0 & ~3u; base < units; base += kUnroll * step) {
+    Raw16<TIn> ra[kUnroll], rb[SILU ? kUnroll : 1];
+    uint32_t t[kUnroll], b[kUnroll];
+    bool on[kUnroll];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = silu(g[i]) * w[i];
+    for (int i = 0; i < kUnroll; ++i) {
+      const uint32_t u = base + (u0 & 3u) + i * step;
+      t[i] = u / (uint32_t)p.nb;
+      b[i] = u - t[i] * (uint32_t)p.nb;
+      const uint32_t c = b[i] * 128u + l8 * 16u;
+      on[i] = u < units && c < (uint32_t)p.K;
+      if (on[i]) {
+        const TIn* row = x + (size_t)t[i] * p.K * (SILU ? 2 : 1) + c;
+        ra[i].load(row);
+        if constexpr (SILU) rb[i].load(row + p.K);
       } else {
-        load8(x + (size_t)t * p.K + c, v);
+        ra[i].zero();
+        if constexpr (SILU) rb[i].zero();
       }
     }
-    float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = max_nan(a, fabsf(v[i]));
+    for (int i = 0; i < kUnroll; ++i) {
+      const uint32_t u = base + (u0 & 3u) + i * step;
+      float v[16], a = 0.0f;
 #pragma unroll
-    for (int off = 8; off > 0; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
-    const float s = block_scale_from_amax(a);
-    const float r = 1.0f / s;
-    uint2 code;
-    code.x = pack_e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r);
-    code.y = pack_e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r);
-    if constexpr (SCATTER) {
-      if (live) {
-        for (int j = 0; j < p.k; ++j) {
-          const int row = p.inv[(size_t)t * p.k + j];
-          if (row < 0) continue;
-          if (on) *reinterpret_cast<uint2*>(p.q + (size_t)row * p.K + c) = code;
-          if (l16 == 0) p.scale[(size_t)row * p.nb + b] = s;
-        }
+      for (int j = 0; j < 16; ++j) {
+        v[j] = ra[i].get(j);
+        if constexpr (SILU) v[j] = silu(v[j]) * rb[i].get(j);
+        a = max_nan(a, fabsf(v[j]));
       }
-    } else {
-      if (on) *reinterpret_cast<uint2*>(p.q + (size_t)t * p.K + c) = code;
-      if (live && l16 == 0) p.scale[u] = s;
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
+      const float s = block_scale_from_amax(a);
+      const float r = 1.0f / s;
+      uint4 code;
+      code.x = pack_e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r);
+      code.y = pack_e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r);
+      code.z = pack_e4m3x4(v[8] * r, v[9] * r, v[10] * r, v[11] * r);
+      code.w = pack_e4m3x4(v[12] * r, v[13] * r, v[14] * r, v[15] * r);
+      const uint32_t c = b[i] * 128u + l8 * 16u;
+      if constexpr (SCATTER) {
+        if (u < units) {
+          for (int j = 0; j < p.k; ++j) {
+            const int row = p.inv[(size_t)t[i] * p.k + j];
+            if (row < 0) continue;
+            if (on[i]) *reinterpret_cast<uint4*>(p.q + (size_t)row * p.K + c) = code;
+            if (l8 == 0) p.scale[(size_t)row * p.nb + b[i]] = s;
+          }
+        }
+      } else {
+        if (on[i]) *reinterpret_cast<uint4*>(p.q + (size_t)t[i] * p.K + c) = code;
+        if (u < units && l8 == 0) p.scale[u] = s;
+      }
     }
   }
 }
@@ -105,7 +130,8 @@ __global__ void __launch_bounds__(kQuantThreads) k_quant_block(const QuantDev p)
 template <typename TIn, bool SILU, bool SCATTER>
 cudaError_t launch_inst(const QuantDev& p, cudaStream_t s) {
   const long units = (long)p.T * p.nb;
-  const long blocks = (units + kQuantThreads / 16 - 1) / (kQuantThreads / 16);
+  if (units >= (1l << 31) - (1l << 24)) return cudaErrorInvalidValue;  // (32-bit unit counts)
+  const long blocks = (units + kQuantThreads / 8 - 1) / (kQuantThreads / 8);
   const int grid = (int)std::min<long>(blocks, 152 * 8);
   MOE_LAUNCH((k_quant_block<TIn, SILU, SCATTER>), dim3(grid), dim3(kQuantThreads), 0, s, p);
   return cudaGetLastError();
