@@ -542,6 +542,8 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
     g.num_sms = sms;
     // 5. GEMM1 on w13, its epilogue forming the e4m3 blocks of SiLU(gate)*up
     BlockGemmArgs g1 = g;
+    // (the quantisation lets its dependents launch after its own wait, when the permutation is complete)
+    g1.early = true;
     g1.epi = BG_EPI_G1;
     g1.K = H;
     g1.n_out = I;
@@ -559,6 +561,7 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
     if (o) record(o->stage_end[MOE_STAGE_ACT], s);
     // 6. GEMM2 on w2
     BlockGemmArgs g2 = g;
+    g2.early = true;  // (as on the other paths: GEMM1's dependents launch after its wait)
     g2.epi = BG_EPI_G2;
     g2.K = I;
     g2.n_out = H;

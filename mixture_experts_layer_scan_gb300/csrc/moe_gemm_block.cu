@@ -17,6 +17,11 @@
 // issues the MMAs into a ring of tensor-memory blocks, warps 2-5 fold the blocks.  Every wait is
 // bounded; after one gives up, each role runs on without waiting or storing, so the barriers
 // between the epilogue warps stay matched and the kernel ends.
+//
+// Few tiles (small batches): a cluster of 2, 4 or 8 CTAs shares a tile, each taking a run of its K
+// blocks.  The sums meet in distributed shared memory -- every token's row is added up in rank order
+// by one warp of one of the CTAs -- so there is no workspace, no second kernel and no order that
+// changes between calls.
 #include <algorithm>
 
 #include "moe_device.cuh"
@@ -40,6 +45,9 @@ struct BgDev {
   int w_scale_rows;     // scale rows per expert
   int s_pair_off;       // offset of D1's scale row from D0's
   int stages, out_bf16;
+  int cl;               // CTAs of a cluster that share a tile's K blocks (1, 2, 4, 8)
+  int kb_per;           // K blocks of one of them
+  int early;            // the tile list and the weights may be read before the dependency wait
   int out_v8;           // rows of out are 32-byte aligned
   uint32_t stage_bytes, bar_off, scale_off, out_off;
   const float* a_scale;  // [rows][kb_total]
@@ -92,11 +100,11 @@ __device__ __forceinline__ void fma2(float2& a, float s0, float s1, float d0, fl
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(av));
 }
 
-// One token's 256 sums (shared memory, staged as [token][256]) by one warp.
+// One token's 256 sums by one warp: v0 columns 4 * lane.. of the tile's first 128 weight rows, v1 of
+// the second.
 template <int EPI>
-__device__ __forceinline__ void bg_store_row(const BgDev& p, const BgTile& d, const float* row, int c, int lane) {
-  const float4 v0 = *reinterpret_cast<const float4*>(row + 4 * lane);
-  const float4 v1 = *reinterpret_cast<const float4*>(row + 128 + 4 * lane);
+__device__ __forceinline__ void bg_store_row(const BgDev& p, const BgTile& d, const float4& v0, const float4& v1, int c,
+                                             int lane) {
   if constexpr (EPI == BG_EPI_G1) {
     const float h0 = silu(v0.x) * v1.x, h1 = silu(v0.y) * v1.y, h2 = silu(v0.z) * v1.z, h3 = silu(v0.w) * v1.w;
     float a = max_nan(max_nan(fabsf(h0), fabsf(h1)), max_nan(fabsf(h2), fabsf(h3)));
@@ -158,6 +166,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   constexpr uint32_t kCols = 2 * NT * kBgBufs;  // 128, 256 or 512: a power of two
   constexpr uint32_t kHalfBytes = 128 * 128;    // 128 weight rows of one K block
+  constexpr int kPass = NT < kStageTokens ? NT : kStageTokens;  // tokens transposed at a time
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -182,26 +191,47 @@ __global__ void __launch_bounds__(kBgThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  pdl_wait();
+  // this CTA's share of a tile's K blocks, and its first tile (clusters: its only one)
+  const int rank = p.cl > 1 ? (int)cluster_ctarank() : 0;
+  const int kb0 = rank * p.kb_per, kb1 = min(kb0 + p.kb_per, p.kb_total);
+  const int tile0 = blockIdx.x / p.cl, stride = gridDim.x / p.cl;
+  if (!p.early) pdl_wait();
   const int ntiles = bg_tile_count<EPI, NT>(p);
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
+    int pre = 0;  // stages whose weights are already on their way
+    if (p.early && tile0 < ntiles) {
+      const BgTile d = bg_tile_at<EPI, NT>(p, tile0);
+      pre = min(p.stages, kb1 - kb0);
+      if (elect_one())
+        for (int i = 0; i < pre; ++i) {
+          const uint32_t sw = sbase + i * p.stage_bytes, fb = bar_full + 8 * i;
+          mbar_arrive_expect_tx(fb, 2 * kHalfBytes + (uint32_t)d.npad * 128u);
+          tma_load_2d(sw, &tmW, (kb0 + i) * 128, d.wr0, fb);
+          tma_load_2d(sw + kHalfBytes, &tmW, (kb0 + i) * 128, d.wr0 + p.w_pair_off, fb);
+        }
+      __syncwarp();
+    }
+    if (p.early) pdl_wait();
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+    for (int t = tile0; t < ntiles && ok; t += stride) {
       const BgTile d = bg_tile_at<EPI, NT>(p, t);
-      for (int kb = 0; kb < p.kb_total; ++kb) {
-        if (!mbar_wait_all(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const bool weights = (int)issued >= pre;
+        if (weights && !mbar_wait_all(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
           ok = false;
           break;
         }
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t sw = sbase + stage * p.stage_bytes, fb = bar_full + 8 * stage;
-          mbar_arrive_expect_tx(fb, 2 * kHalfBytes + (uint32_t)d.npad * 128u);
-          tma_load_2d(sw, &tmW, kb * 128, d.wr0, fb);
-          tma_load_2d(sw + kHalfBytes, &tmW, kb * 128, d.wr0 + p.w_pair_off, fb);
+          if (weights) {
+            mbar_arrive_expect_tx(fb, 2 * kHalfBytes + (uint32_t)d.npad * 128u);
+            tma_load_2d(sw, &tmW, kb * 128, d.wr0, fb);
+            tma_load_2d(sw + kHalfBytes, &tmW, kb * 128, d.wr0 + p.w_pair_off, fb);
+          }
           for (int r = 0; r < d.npad; r += 16)
             tma_load_2d(sw + 2 * kHalfBytes + (uint32_t)r * 128u, &tmX, kb * 128, d.xrow + r, fb);
         }
@@ -223,21 +253,19 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
-    int stage = 0, buf = 0;
-    uint32_t phase = 0, buf_phase = 0;
-    bool ok = true, any = false;
-    for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-      const BgTile d = bg_tile_at<EPI, NT>(p, t);
-      const uint32_t idesc = idesc_make(128, d.npad, true);
-      for (int kb = 0; kb < p.kb_total; ++kb) {
-        if (!mbar_wait_all(bar_tempty + 8 * buf, buf_phase ^ 1u, abort_flag, p.status) ||
-            !mbar_wait_all(bar_full + 8 * stage, phase, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (lane == 0) {
+    // ---------------- MMA issuer: one thread ----------------
+    if (p.early) pdl_wait();
+    if (elect_one()) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool ok = true, any = false;
+      for (int t = tile0; t < ntiles && ok; t += stride) {
+        const uint32_t idesc = idesc_make(128, bg_tile_at<EPI, NT>(p, t).npad, true);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = mbar_wait_one(bar_tempty + 8 * buf, buf_phase ^ 1u, abort_flag, p.status) &&
+               mbar_wait_one(bar_full + 8 * stage, phase, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
           const uint32_t sw = sbase + stage * p.stage_bytes;
           const uint32_t dt = tmem_base + (uint32_t)(buf * 2 * NT);
 #pragma unroll
@@ -248,39 +276,43 @@ __global__ void __launch_bounds__(kBgThreads, 1)
           }
           tc_commit(bar_empty + 8 * stage);
           tc_commit(bar_tfull + 8 * buf);
-        }
-        __syncwarp();
-        any = true;
-        if (++stage == p.stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-        if (++buf == kBgBufs) {
-          buf = 0;
-          buf_phase ^= 1u;
+          any = true;
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == kBgBufs) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
         }
       }
-    }
-    if (!ok && any) {  // the tensor core must be idle before tensor memory is freed
-      if (lane == 0) tc_commit(bar_drain);
-      __syncwarp();
-      mbar_wait_drain(bar_drain, 0, 100000000ull);
+      if (!ok && any) {  // the tensor core must be idle before tensor memory is freed
+        tc_commit(bar_drain);
+        mbar_wait_drain(bar_drain, 0, 100000000ull);
+      }
     }
     __syncwarp();
+  }
+  if (warp < 2) {
+    if (p.cl > 1 && tile0 < ntiles) {  // the epilogue's cluster barriers take every thread
+      cluster_sync_all();
+      cluster_sync_all();
+    }
   } else {
     // ---------------- epilogue (warps 2..5): fold the blocks, then the outputs ----------------
+    if (p.early) pdl_wait();
     const int q = warp & 3;          // tensor-memory lane quadrant this warp may read
     const int lrow = q * 32 + lane;  // weight row of this thread in D0 and in D1
     const int tid = threadIdx.x - 64;
     float* sc = reinterpret_cast<float*>(smem + p.scale_off);  // [2][2][kScaleChunk][NT]
-    float* st = reinterpret_cast<float*>(smem + p.out_off);    // [kStageTokens][256]
     constexpr int kSet = kScaleChunk * NT;                     // scale products of one chunk and half
     constexpr int kPer = kSet / 128;
     const int lane_kb = tid % kScaleChunk, lane_c = tid / kScaleChunk;  // this thread's first scale of a chunk
     int buf = 0;
     uint32_t buf_phase = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
+    for (int t = tile0; t < ntiles; t += stride) {
       const BgTile d = bg_tile_at<EPI, NT>(p, t);
       const int srow = d.n * (p.w_tile_rows / 128);
       const float* ws0 = p.w_scale + ((size_t)d.e * p.w_scale_rows + srow) * p.kb_total;
@@ -289,7 +321,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
       // scales of the next chunk, one K block and every 16th token to a thread
       float ra[kPer], r0 = 0.0f, r1 = 0.0f;
       auto fetch = [&](int kb) {
-        const bool in = kb + lane_kb < p.kb_total;
+        const bool in = kb + lane_kb < kb1;
         r0 = in ? ws0[kb + lane_kb] : 0.0f;
         r1 = in ? ws1[kb + lane_kb] : 0.0f;
 #pragma unroll
@@ -301,8 +333,8 @@ __global__ void __launch_bounds__(kBgThreads, 1)
       float2 acc0[NT / 2], acc1[NT / 2];
 #pragma unroll
       for (int i = 0; i < NT / 2; ++i) acc0[i] = acc1[i] = make_float2(0.0f, 0.0f);
-      fetch(0);
-      for (int kc = 0, par = 0; kc < p.kb_total; kc += kScaleChunk, par ^= 1) {
+      fetch(kb0);
+      for (int kc = kb0, par = 0; kc < kb1; kc += kScaleChunk, par ^= 1) {
         float* s0 = sc + par * 2 * kSet;
         float* s1 = s0 + kSet;
 #pragma unroll
@@ -312,58 +344,90 @@ __global__ void __launch_bounds__(kBgThreads, 1)
           s1[lane_kb * NT + c] = ra[i] * r1;
         }
         named_bar_sync(1, 128);
-        if (kc + kScaleChunk < p.kb_total) fetch(kc + kScaleChunk);
-        const int kn = min(kScaleChunk, p.kb_total - kc);
+        if (kc + kScaleChunk < kb1) fetch(kc + kScaleChunk);
+        const int kn = min(kScaleChunk, kb1 - kc);
         for (int kb = 0; kb < kn; ++kb) {
-          ok = ok && mbar_wait_all(bar_tfull + 8 * buf, buf_phase, abort_flag, p.status);
-          if (ok) {
-            tc_fence_after();
-            const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * 2 * NT);
+          if (ok) ok = mbar_wait_one(bar_tfull + 8 * buf, buf_phase, abort_flag, p.status);
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * 2 * NT);
+          constexpr int W = NT < 32 ? 16 : 32;  // columns of one load
 #pragma unroll
-            for (int c0 = 0; c0 < NT; c0 += 16) {
-              if (c0 < d.npad) {
-                float v0[16], v1[16];
-                tmem_ld16(tb + c0, v0);
-                tmem_ld16(tb + NT + c0, v1);
+          for (int c0 = 0; c0 < NT; c0 += W) {
+            if (c0 < d.npad) {
+              uint32_t v0[W], v1[W];
+              tmem_ld_issue<W>(tb + c0, v0);
+              tmem_ld_issue<W>(tb + NT + c0, v1);
+              tmem_wait_ld();
+              tmem_landed(v0);
+              tmem_landed(v1);
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                  const float4 f0 = *reinterpret_cast<const float4*>(s0 + kb * NT + c0 + j);
-                  const float4 f1 = *reinterpret_cast<const float4*>(s1 + kb * NT + c0 + j);
-                  fma2(acc0[(c0 + j) / 2], f0.x, f0.y, v0[j], v0[j + 1]);
-                  fma2(acc0[(c0 + j) / 2 + 1], f0.z, f0.w, v0[j + 2], v0[j + 3]);
-                  fma2(acc1[(c0 + j) / 2], f1.x, f1.y, v1[j], v1[j + 1]);
-                  fma2(acc1[(c0 + j) / 2 + 1], f1.z, f1.w, v1[j + 2], v1[j + 3]);
-                }
+              for (int j = 0; j < W; j += 4) {
+                const float4 f0 = *reinterpret_cast<const float4*>(s0 + kb * NT + c0 + j);
+                const float4 f1 = *reinterpret_cast<const float4*>(s1 + kb * NT + c0 + j);
+                const int i = (c0 + j) / 2;
+                fma2(acc0[i], f0.x, f0.y, __uint_as_float(v0[j]), __uint_as_float(v0[j + 1]));
+                fma2(acc0[i + 1], f0.z, f0.w, __uint_as_float(v0[j + 2]), __uint_as_float(v0[j + 3]));
+                fma2(acc1[i], f1.x, f1.y, __uint_as_float(v1[j]), __uint_as_float(v1[j + 1]));
+                fma2(acc1[i + 1], f1.z, f1.w, __uint_as_float(v1[j + 2]), __uint_as_float(v1[j + 3]));
               }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_tempty + 8 * buf);
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_tempty + 8 * buf);
           if (++buf == kBgBufs) {
             buf = 0;
             buf_phase ^= 1u;
           }
         }
       }
-      // transpose kStageTokens tokens at a time: thread = weight row -> warp = token
+      // transpose through shared memory: thread = weight row -> warp = token
+      auto stage_tokens = [&](float* rows, int i0, int n) {  // (i0, n compile-time after unrolling)
 #pragma unroll
-      for (int c0 = 0; c0 < NT; c0 += kStageTokens) {
-        if (c0 < d.ntok) {
-#pragma unroll
-          for (int c = 0; c < (NT < kStageTokens ? NT : kStageTokens); c += 2) {
-            const int i = (c0 + c) / 2;
-            st[c * 256 + lrow] = acc0[i].x;
-            st[(c + 1) * 256 + lrow] = acc0[i].y;
-            st[c * 256 + 128 + lrow] = acc1[i].x;
-            st[(c + 1) * 256 + 128 + lrow] = acc1[i].y;
-          }
-          named_bar_sync(1, 128);
-          if (ok)
-            for (int c = c0 + q; c < min(d.ntok, c0 + kStageTokens); c += 4)
-              bg_store_row<EPI>(p, d, st + (c - c0) * 256, c, lane);
-          named_bar_sync(1, 128);
+        for (int c = 0; c < n; c += 2) {
+          rows[c * 256 + lrow] = acc0[i0 + c / 2].x;
+          rows[(c + 1) * 256 + lrow] = acc0[i0 + c / 2].y;
+          rows[c * 256 + 128 + lrow] = acc1[i0 + c / 2].x;
+          rows[(c + 1) * 256 + 128 + lrow] = acc1[i0 + c / 2].y;
         }
+      };
+      if (p.cl == 1) {
+        float* st = reinterpret_cast<float*>(smem + p.out_off);  // [kPass][256]
+#pragma unroll
+        for (int c0 = 0; c0 < NT; c0 += kPass) {
+          if (c0 < d.ntok) {
+            stage_tokens(st, c0 / 2, kPass);
+            named_bar_sync(1, 128);
+            if (ok)
+              for (int c = q; c < min(d.ntok - c0, kPass); c += 4) {
+                const float4* row = reinterpret_cast<const float4*>(st + c * 256) + lane;
+                bg_store_row<EPI>(p, d, row[0], row[32], c0 + c, lane);
+              }
+            named_bar_sync(1, 128);
+          }
+        }
+      } else {
+        // The ring is idle once the tile's last block has been folded (one tile to a CTA): it takes all
+        // tokens' sums at once.  Rank r of the cluster stores tokens r, r + cl, ..., each added up in rank
+        // order.
+        stage_tokens(reinterpret_cast<float*>(smem), 0, NT);
+        __syncwarp();
+        cluster_sync_all();
+        if (ok)
+          for (int c = rank + q * p.cl; c < d.ntok; c += 4 * p.cl) {
+            const uint32_t at = sbase + (uint32_t)(c * 256 + 4 * lane) * 4u;
+            float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
+            for (int r = 0; r < p.cl; ++r) {
+              const uint32_t from = mapa_shared(at, r);
+              const float4 a0 = ld_cluster_f32x4(from), a1 = ld_cluster_f32x4(from + 512u);
+              v0.x += a0.x; v0.y += a0.y; v0.z += a0.z; v0.w += a0.w;
+              v1.x += a1.x; v1.y += a1.y; v1.z += a1.z; v1.w += a1.w;
+            }
+            bg_store_row<EPI>(p, d, v0, v1, c, lane);
+          }
+        __syncwarp();
+        cluster_sync_all();  // (no CTA leaves while another reads its rows)
       }
     }
   }
@@ -380,6 +444,10 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     tmem_dealloc(tmem_base, kCols);
   }
 }
+
+// Smallest share of a tile's K blocks that a CTA of a cluster is given (below that its prologue and
+// the exchange cost more than its share).
+constexpr int kMinSplitBlocks = 3;
 
 template <int EPI, int NT>
 cudaError_t launch_bg(const CUtensorMap& mw, const CUtensorMap& mx, BgDev p, long tiles, int sms, cudaStream_t s) {
@@ -401,8 +469,46 @@ cudaError_t launch_bg(const CUtensorMap& mw, const CUtensorMap& mx, BgDev p, lon
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  const int grid = (int)std::max<long>(1, std::min<long>(tiles, sms));
-  return launch_pdl(kern, dim3(grid), dim3(kBgThreads), smem, s, mw, mx, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kBgThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  // CTAs that share one tile: as many as keep all tiles resident together (152 SMs hold 76 clusters
+  // of 2, 36 of 4, 15 of 8: a sixteenth cluster of 8 would double the time)
+  static int resident[4][64] = {};
+  p.cl = 1;
+  for (int i = 1; i < 4; ++i) {
+    const int cl = 1 << i;
+    if (p.kb_total / cl < kMinSplitBlocks || tiles * cl > sms) break;
+    if (dev < 0 || dev >= 64) break;
+    if (resident[i][dev] == 0) {
+      attr[0].val.clusterDim.x = cl;
+      cfg.gridDim = dim3(cl);
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = -1;
+      }
+      resident[i][dev] = n;
+    }
+    if (tiles > resident[i][dev]) break;
+    p.cl = cl;
+  }
+  p.kb_per = (p.kb_total + p.cl - 1) / p.cl;
+  // one tile to a CTA with clusters, a persistent grid without
+  cfg.gridDim = dim3((unsigned)(p.cl > 1 ? tiles * p.cl : std::max<long>(1, std::min<long>(tiles, sms))));
+  attr[0].val.clusterDim.x = p.cl;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
 }
 
 template <int EPI>
@@ -1015,6 +1121,7 @@ cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
     p.s_pair_off = 1;
   }
   p.out_bf16 = a.out_bf16 ? 1 : 0;
+  p.early = a.early ? 1 : 0;
   p.out_v8 = a.n_out % (a.out_bf16 ? 16 : 8) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   p.a_scale = a.a_scale;
   p.w_scale = a.w_scale;

@@ -99,6 +99,8 @@ struct BlockGemmArgs {
   bool pair;              // token-major on CTA pairs (grouped: permutation blocks of 128, tiles from pblk)
   int nt;                 // swap-AB: tokens per tile, 16, 32 or 64 (grouped: at least an expert's tokens)
   bool out_bf16;          // dense
+  bool early;             // swap-AB: the tile list and the weights may be read before the dependency wait (as
+                          // TcGemmArgs.early)
   const void* x;          // e4m3 [rows][K]
   const float* a_scale;   // [rows][ceil(K/128)]
   const void* w;          // e4m3 [E * w_rows][K]
