@@ -9,6 +9,7 @@ no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -155,9 +156,11 @@ def _check(rc: int, where: str) -> None:
         raise MoeError(rc, where)
 
 
+_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float8_e4m3fn: MOE_E4M3, torch.uint8: MOE_E4M3}
+
+
 def _dt(t: torch.Tensor) -> int:
-    return {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float8_e4m3fn: MOE_E4M3,
-            torch.uint8: MOE_E4M3}[t.dtype]
+    return _DTYPES[t.dtype]
 
 
 def _p(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -166,6 +169,15 @@ def _p(t: Optional[torch.Tensor]) -> Optional[int]:
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
+
+
+def _out(t: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != shape or (t.dtype != dtype and not (dtype == torch.float8_e4m3fn and t.dtype == torch.uint8)):
+        raise ValueError(f"an output must be {dtype} {tuple(shape)}")
+    return t
 
 
 def _stream(stream) -> int:
@@ -242,7 +254,8 @@ def moe_topk_from_logits(logits: torch.Tensor, topk: int, renorm: bool, topk_w=N
     return topk_w, topk_ids
 
 
-def _route_rule(E: int, score: str, n_group: int, topk_group: Optional[int], group_sum: int, renorm: bool,
+@functools.lru_cache(maxsize=256)
+def _route_rule(score: str, n_group: int, topk_group: Optional[int], group_sum: int, renorm: bool,
                 scale: float) -> moe_route_rule:
     return moe_route_rule(SCORES[score], n_group, n_group if topk_group is None else topk_group, group_sum,
                           int(bool(renorm)), float(scale))
@@ -259,9 +272,9 @@ def moe_topk_grouped(logits: torch.Tensor, topk: int, bias=None, score: str = "s
     if logits.dtype != torch.float32 or (bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,))):
         raise ValueError("logits must be float32 [T, E] and bias float32 [E]")
     dev = logits.device
-    topk_w = torch.empty(T, topk, dtype=torch.float32, device=dev) if topk_w is None else topk_w
-    topk_ids = torch.empty(T, topk, dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
-    rule = _route_rule(E, score, n_group, topk_group, group_sum, renorm, scale)
+    topk_w = _out(topk_w, (T, topk), torch.float32, dev)
+    topk_ids = _out(topk_ids, (T, topk), torch.int32, dev)
+    rule = _route_rule(score, n_group, topk_group, group_sum, renorm, scale)
     _check(_lib.moe_topk_grouped(_p(logits), _p(bias), T, E, topk, ctypes.byref(rule), _p(topk_w), _p(topk_ids),
                                  _stream(stream)), "moe_topk_grouped")
     return topk_w, topk_ids
@@ -277,10 +290,10 @@ def moe_route_grouped(hidden: torch.Tensor, router_w: torch.Tensor, topk: int, b
             bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,))):
         raise ValueError("router_w must be [E, H] of hidden's type and bias float32 [E]")
     dev = hidden.device
-    logits = torch.empty(T, E, dtype=torch.float32, device=dev) if logits is None else logits
-    topk_w = torch.empty(T, topk, dtype=torch.float32, device=dev) if topk_w is None else topk_w
-    topk_ids = torch.empty(T, topk, dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
-    rule = _route_rule(E, score, n_group, topk_group, group_sum, renorm, scale)
+    logits = _out(logits, (T, E), torch.float32, dev)
+    topk_w = _out(topk_w, (T, topk), torch.float32, dev)
+    topk_ids = _out(topk_ids, (T, topk), torch.int32, dev)
+    rule = _route_rule(score, n_group, topk_group, group_sum, renorm, scale)
     _check(_lib.moe_route_grouped(_p(hidden), _p(router_w), _p(bias), T, H, E, topk, ctypes.byref(rule), _dt(hidden),
                                   _p(logits), _p(topk_w), _p(topk_ids), _stream(stream)), "moe_route_grouped")
     return logits, topk_w, topk_ids
@@ -289,8 +302,8 @@ def moe_route_grouped(hidden: torch.Tensor, router_w: torch.Tensor, topk: int, b
 def moe_quant_block(x: torch.Tensor, q=None, scale=None, stream=None):
     """e4m3 codes [T,K] (float8_e4m3fn) and float32 scales [T,ceil(K/128)] of x [T,K] by blocks of 128 columns."""
     T, K = x.shape
-    q = torch.empty(T, K, dtype=torch.float8_e4m3fn, device=x.device) if q is None else q
-    scale = torch.empty(T, (K + 127) // 128, dtype=torch.float32, device=x.device) if scale is None else scale
+    q = _out(q, (T, K), torch.float8_e4m3fn, x.device)
+    scale = _out(scale, (T, (K + 127) // 128), torch.float32, x.device)
     _check(_lib.moe_quant_block(_p(x), T, K, _dt(x), _p(q), _p(scale), _stream(stream)), "moe_quant_block")
     return q, scale
 
@@ -302,8 +315,8 @@ def moe_silu_quant_block(gate_up: torch.Tensor, q=None, scale=None, stream=None)
         raise ValueError("gate_up must be [T, 2 I]")
     I = two_i // 2
     dev = gate_up.device
-    q = torch.empty(T, I, dtype=torch.float8_e4m3fn, device=dev) if q is None else q
-    scale = torch.empty(T, (I + 127) // 128, dtype=torch.float32, device=dev) if scale is None else scale
+    q = _out(q, (T, I), torch.float8_e4m3fn, dev)
+    scale = _out(scale, (T, (I + 127) // 128), torch.float32, dev)
     _check(_lib.moe_silu_quant_block(_p(gate_up), T, I, _dt(gate_up), _p(q), _p(scale), _stream(stream)),
            "moe_silu_quant_block")
     return q, scale
@@ -315,13 +328,16 @@ def moe_gemm_block(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_sc
 
     a_scale float32 [T,ceil(K/128)] (moe_quant_block), w_scale float32 [ceil(N/128),ceil(K/128)]."""
     T, K = a.shape
-    N = w.shape[0]
+    N, Kw = w.shape
     kb = (K + 127) // 128
-    if w.shape != (N, K) or a_scale.shape != (T, kb) or w_scale.shape != ((N + 127) // 128, kb):
+    if Kw != K or a_scale.shape != (T, kb) or w_scale.shape != ((N + 127) // 128, kb):
         raise ValueError("inconsistent shapes")
     if _dt(a) != MOE_E4M3 or _dt(w) != MOE_E4M3 or a_scale.dtype != torch.float32 or w_scale.dtype != torch.float32:
         raise ValueError("a and w must be e4m3 codes with float32 scales")
-    out = torch.empty(T, N, dtype=out_dtype, device=a.device) if out is None else out
+    if out is None:
+        out = torch.empty(T, N, dtype=out_dtype, device=a.device)
+    elif out.shape != (T, N):
+        raise ValueError("out must be [T, N]")
     _check(_lib.moe_gemm_block(_p(a), _p(a_scale), _p(w), _p(w_scale), T, N, K, _dt(out), _p(out), _stream(stream)),
            "moe_gemm_block")
     return out
@@ -454,6 +470,9 @@ def moe_inv_rope_fp8_quant(x: torch.Tensor, positions: torch.Tensor, cos_sin: to
     return q_out, scale_out
 
 
+_ROUTED_OPTIONS = moe_options(single_launch=2)  # (the library reads it only)
+
+
 def moe_forward_routed(hidden: torch.Tensor, topk_w: torch.Tensor, topk_ids: torch.Tensor, w13: torch.Tensor,
                        w2: torch.Tensor, w13_scale=None, w2_scale=None, out=None, workspace=None, options=None,
                        stream=None, w_format=None):
@@ -464,17 +483,23 @@ def moe_forward_routed(hidden: torch.Tensor, topk_w: torch.Tensor, topk_ids: tor
     E, twoI, _ = w13.shape
     I = twoI // 2
     k = topk_ids.shape[1]
+    if topk_ids.dtype != torch.int32 or topk_w.dtype != torch.float32 or topk_ids.shape[0] != T or (
+            topk_w.shape != topk_ids.shape):
+        raise ValueError("topk_w must be float32 and topk_ids int32, both [T, k]")
     _check_block_scales(w_format, E, H, I, w13_scale, w2_scale)
     act, wdt = _dt(hidden), _w_dtype(w13, w_format)
-    o = dict(options or {})
-    o["single_launch"] = 2
-    need = moe_workspace_size(T, H, I, E, k, act, wdt, o)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=hidden.device)
+    if options is None:
+        opts = _ROUTED_OPTIONS
+    else:
+        opts = moe_options.from_buffer_copy(options) if isinstance(options, moe_options) else _opts(options)._obj
+        opts.single_launch = 2
+    if workspace is None:  # (a caller's own is checked by the library)
+        workspace = torch.empty(moe_workspace_size(T, H, I, E, k, act, wdt, opts), dtype=torch.uint8,
+                                device=hidden.device)
     out = torch.empty_like(hidden) if out is None else out
     _check(_lib.moe_forward_routed(_p(hidden), _p(topk_w), _p(topk_ids), _p(w13), _p(w2), T, H, I, E, k, act, wdt,
-                                   _p(w13_scale), _p(w2_scale), _p(out), _p(workspace), workspace.numel(), _opts(o),
-                                   _stream(stream)), "moe_forward_routed")
+                                   _p(w13_scale), _p(w2_scale), _p(out), _p(workspace), workspace.numel(),
+                                   ctypes.byref(opts), _stream(stream)), "moe_forward_routed")
     return out
 
 

@@ -52,6 +52,8 @@ constexpr int kGatherTokenOrderMinTokens = 4096;
 constexpr int kGatherInGemmMaxRows = 32;
 // Largest batch of the block-scaled swap-AB products (tokens of one tile).
 constexpr int kBlockSwapMaxTokens = 64;
+// Shortest K (blocks of 128) whose swap-AB tiles of more than 32 tokens beat the CTA pairs' (moe_gemm_block).
+constexpr int kBlockSwapMinK = 12;
 // Single-launch decode kernel limits (shared-memory tables, one token column per epilogue thread).
 constexpr int kFusedMaxTokens = 64;
 constexpr int kFusedMaxPairs = 512;
@@ -998,7 +1000,16 @@ int moe_gemm_block(const void* a, const float* a_scale, const void* w, const flo
   g.K = K;
   g.n_out = N;
   g.w_rows = N;
-  g.pair = T > kBlockSwapMaxTokens;
+  // Orientation.  Swap-AB tiles take 64 tokens at most and may share their K blocks in clusters; CTA
+  // pairs take 256 tokens and the whole K.  Measured (us, swap-AB / pairs, K = 4096 unless said):
+  //   16 x 8192 8 / 15, 128 x 4096 9.4 / 14.4, 256 x 4096 12.8 / 18.7, 512 x 2048 12.7 / 18.6 (clusters);
+  //   256 x 8192 19.1 / 19.5, 512 x 4096 18.6 / 18.9, 1024 x 4096 37.7 / 19.9 (none);
+  //   K = 1024: 32 x 4096 5.4 / 6.1, 64 x 4096 7.1 / 6.3, 256 x 4096 7.5 / 8.1, 512 x 8192 13.5 / 9.1.
+  // So swap-AB where its tiles leave room for clusters and K is long enough to share, and for batches
+  // of one tile.
+  const long kb = (K + 127) / 128;
+  const long tiles64 = ((long)T + kBlockSwapMaxTokens - 1) / kBlockSwapMaxTokens * (((long)N + 255) / 256);
+  g.pair = !(T <= 32 || (kb >= kBlockSwapMinK && (T <= kBlockSwapMaxTokens || 2 * tiles64 <= sms)));
   g.nt = block_swap_tokens(T);
   g.out_bf16 = out_dtype == MOE_BF16;
   g.x = a;

@@ -13,8 +13,9 @@
 // tile ends with exactly one 128-column block of the intermediate for each of its tokens: SiLU,
 // the block's scale and its codes are formed in the epilogue and no wide intermediate is stored.
 //
-// Roles (192 threads): warp 0 streams operands by TMA into a ring of shared-memory stages, warp 1
-// issues the MMAs into a ring of tensor-memory blocks, warps 2-5 fold the blocks.  Every wait is
+// Roles (320 threads): warp 0 streams operands by TMA into a ring of shared-memory stages, warp 1
+// issues the MMAs into a ring of tensor-memory blocks, warps 2-9 fold the blocks (four
+// of them D0, four D1: with four for both, a block of 64 tokens took 0.6 us, longer than its load).  Every wait is
 // bounded; after one gives up, each role runs on without waiting or storing, so the barriers
 // between the epilogue warps stay matched and the kernel ends.
 //
@@ -31,7 +32,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kBgThreads = 192;
+constexpr int kBgThreads = 320;  // 2 warps of roles, 8 epilogue warps
 constexpr int kBgMaxStages = 8;
 constexpr int kBgBufs = 4;          // tensor-memory blocks in flight
 constexpr int kScaleChunk = 8;      // K blocks whose scale products are staged together
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     }
     for (int b = 0; b < kBgBufs; ++b) {
       mbar_init(bar_tfull + 8 * b, 1);
-      mbar_init(bar_tempty + 8 * b, 4);
+      mbar_init(bar_tempty + 8 * b, 8);
     }
     mbar_init(bar_drain, 1);
     mbar_init(bar_exit, kBgThreads / 32);
@@ -300,11 +301,12 @@ __global__ void __launch_bounds__(kBgThreads, 1)
       cluster_sync_all();
     }
   } else {
-    // ---------------- epilogue (warps 2..5): fold the blocks, then the outputs ----------------
+    // ---------------- epilogue (warps 2..9): fold the blocks, then the outputs ----------------
     if (p.early) pdl_wait();
     const int q = warp & 3;          // tensor-memory lane quadrant this warp may read
-    const int lrow = q * 32 + lane;  // weight row of this thread in D0 and in D1
-    const int tid = threadIdx.x - 64;
+    const int w8 = warp - 2, h = w8 >> 2;  // this warp's accumulator: D0 or D1
+    const int lrow = q * 32 + lane;        // weight row of this thread in it
+    const int tid = (threadIdx.x - 64) & 127;
     float* sc = reinterpret_cast<float*>(smem + p.scale_off);  // [2][2][kScaleChunk][NT]
     constexpr int kSet = kScaleChunk * NT;                     // scale products of one chunk and half
     constexpr int kPer = kSet / 128;
@@ -315,61 +317,52 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     for (int t = tile0; t < ntiles; t += stride) {
       const BgTile d = bg_tile_at<EPI, NT>(p, t);
       const int srow = d.n * (p.w_tile_rows / 128);
-      const float* ws0 = p.w_scale + ((size_t)d.e * p.w_scale_rows + srow) * p.kb_total;
-      const float* ws1 =
-          p.w_scale + ((size_t)d.e * p.w_scale_rows + min(srow + p.s_pair_off, p.w_scale_rows - 1)) * p.kb_total;
+      const float* ws = p.w_scale + ((size_t)d.e * p.w_scale_rows +
+                                     min(srow + h * p.s_pair_off, p.w_scale_rows - 1)) * p.kb_total;
       // scales of the next chunk, one K block and every 16th token to a thread
-      float ra[kPer], r0 = 0.0f, r1 = 0.0f;
+      float ra[kPer], rw = 0.0f;
       auto fetch = [&](int kb) {
         const bool in = kb + lane_kb < kb1;
-        r0 = in ? ws0[kb + lane_kb] : 0.0f;
-        r1 = in ? ws1[kb + lane_kb] : 0.0f;
+        rw = in ? ws[kb + lane_kb] : 0.0f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int c = lane_c + i * (128 / kScaleChunk);
           ra[i] = (in && c < d.ntok) ? p.a_scale[(size_t)(d.xrow + c) * p.kb_total + kb + lane_kb] : 0.0f;
         }
       };
-      float2 acc0[NT / 2], acc1[NT / 2];
+      float2 acc[NT / 2];
 #pragma unroll
-      for (int i = 0; i < NT / 2; ++i) acc0[i] = acc1[i] = make_float2(0.0f, 0.0f);
+      for (int i = 0; i < NT / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
       fetch(kb0);
       for (int kc = kb0, par = 0; kc < kb1; kc += kScaleChunk, par ^= 1) {
-        float* s0 = sc + par * 2 * kSet;
-        float* s1 = s0 + kSet;
+        float* sp = sc + (par * 2 + h) * kSet;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int c = lane_c + i * (128 / kScaleChunk);
-          s0[lane_kb * NT + c] = ra[i] * r0;
-          s1[lane_kb * NT + c] = ra[i] * r1;
+          sp[lane_kb * NT + c] = ra[i] * rw;
         }
-        named_bar_sync(1, 128);
+        named_bar_sync(1, 256);
         if (kc + kScaleChunk < kb1) fetch(kc + kScaleChunk);
         const int kn = min(kScaleChunk, kb1 - kc);
         for (int kb = 0; kb < kn; ++kb) {
           if (ok) ok = mbar_wait_one(bar_tfull + 8 * buf, buf_phase, abort_flag, p.status);
           __syncwarp();
           tc_fence_after();
-          const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * 2 * NT);
+          const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)((buf * 2 + h) * NT);
           constexpr int W = NT < 32 ? 16 : 32;  // columns of one load
 #pragma unroll
           for (int c0 = 0; c0 < NT; c0 += W) {
             if (c0 < d.npad) {
-              uint32_t v0[W], v1[W];
-              tmem_ld_issue<W>(tb + c0, v0);
-              tmem_ld_issue<W>(tb + NT + c0, v1);
+              uint32_t v[W];
+              tmem_ld_issue<W>(tb + c0, v);
               tmem_wait_ld();
-              tmem_landed(v0);
-              tmem_landed(v1);
+              tmem_landed(v);
 #pragma unroll
               for (int j = 0; j < W; j += 4) {
-                const float4 f0 = *reinterpret_cast<const float4*>(s0 + kb * NT + c0 + j);
-                const float4 f1 = *reinterpret_cast<const float4*>(s1 + kb * NT + c0 + j);
+                const float4 f = *reinterpret_cast<const float4*>(sp + kb * NT + c0 + j);
                 const int i = (c0 + j) / 2;
-                fma2(acc0[i], f0.x, f0.y, __uint_as_float(v0[j]), __uint_as_float(v0[j + 1]));
-                fma2(acc0[i + 1], f0.z, f0.w, __uint_as_float(v0[j + 2]), __uint_as_float(v0[j + 3]));
-                fma2(acc1[i], f1.x, f1.y, __uint_as_float(v1[j]), __uint_as_float(v1[j + 1]));
-                fma2(acc1[i + 1], f1.z, f1.w, __uint_as_float(v1[j + 2]), __uint_as_float(v1[j + 3]));
+                fma2(acc[i], f.x, f.y, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                fma2(acc[i + 1], f.z, f.w, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
               }
             }
           }
@@ -386,10 +379,8 @@ __global__ void __launch_bounds__(kBgThreads, 1)
       auto stage_tokens = [&](float* rows, int i0, int n) {  // (i0, n compile-time after unrolling)
 #pragma unroll
         for (int c = 0; c < n; c += 2) {
-          rows[c * 256 + lrow] = acc0[i0 + c / 2].x;
-          rows[(c + 1) * 256 + lrow] = acc0[i0 + c / 2].y;
-          rows[c * 256 + 128 + lrow] = acc1[i0 + c / 2].x;
-          rows[(c + 1) * 256 + 128 + lrow] = acc1[i0 + c / 2].y;
+          rows[c * 256 + 128 * h + lrow] = acc[i0 + c / 2].x;
+          rows[(c + 1) * 256 + 128 * h + lrow] = acc[i0 + c / 2].y;
         }
       };
       if (p.cl == 1) {
@@ -398,13 +389,13 @@ __global__ void __launch_bounds__(kBgThreads, 1)
         for (int c0 = 0; c0 < NT; c0 += kPass) {
           if (c0 < d.ntok) {
             stage_tokens(st, c0 / 2, kPass);
-            named_bar_sync(1, 128);
+            named_bar_sync(1, 256);
             if (ok)
-              for (int c = q; c < min(d.ntok - c0, kPass); c += 4) {
+              for (int c = w8; c < min(d.ntok - c0, kPass); c += 8) {
                 const float4* row = reinterpret_cast<const float4*>(st + c * 256) + lane;
                 bg_store_row<EPI>(p, d, row[0], row[32], c0 + c, lane);
               }
-            named_bar_sync(1, 128);
+            named_bar_sync(1, 256);
           }
         }
       } else {
@@ -415,7 +406,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
         __syncwarp();
         cluster_sync_all();
         if (ok)
-          for (int c = rank + q * p.cl; c < d.ntok; c += 4 * p.cl) {
+          for (int c = rank + w8 * p.cl; c < d.ntok; c += 8 * p.cl) {
             const uint32_t at = sbase + (uint32_t)(c * 256 + 4 * lane) * 4u;
             float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
             for (int r = 0; r < p.cl; ++r) {
