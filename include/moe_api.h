@@ -283,8 +283,10 @@ MOE_API int moe_align(const int32_t* topk_ids, int T, int topk, int E, int block
  *                T <= 128, H % 256 == 0 and I % 256 == 0 (else MOE_ERR_UNSUPPORTED)
  *   (BF16, E4M3_B128) tcgen05 kind::f8f6f4 path: input and intermediate are quantised by
  *                blocks of 128 columns per token (moe_quant_block), every K block's products
- *                are scaled and summed in fp32; SWAP_AB needs T <= 64, TOKEN_MAJOR always runs on
- *                CTA pairs; options split_k and act_split are ignored
+ *                are scaled and summed in fp32.  AUTO picks SWAP_AB up to 64 tokens or 32 pairs per
+ *                expert (T * topk <= 32 E), each orientation takes any T, and TOKEN_MAJOR always
+ *                runs on CTA pairs; split_k and act_split are ignored.  Above 64 tokens the
+ *                experts' outputs are rounded to bf16 before the combine
  *   tensor-core paths need H % 128 == 0 and I % 128 == 0.
  * The intermediate SiLU(gate)*up is stored in bf16 (as a bf16 hi + lo pair in SWAP_AB
  * mode, see moe_options.act_split; fp32 on the fp32 path; e4m3 on the FP8 path);

@@ -52,6 +52,12 @@ constexpr int kGatherTokenOrderMinTokens = 4096;
 constexpr int kGatherInGemmMaxRows = 32;
 // Largest batch of the block-scaled swap-AB products (tokens of one tile).
 constexpr int kBlockSwapMaxTokens = 64;
+// Block-scaled expert batches run swap-AB up to this many (token, expert) pairs per expert: their tiles
+// then mostly hold all of an expert's tokens and stream its weights once.  Measured (us, swap-AB / CTA
+// pairs): 64 experts of 4096 x 2048 at 8, 32, 48, 64 pairs 252 / 307, 290 / 319, 313 / 326, 374 / 333; 128
+// of 2048 x 768 at 32 pairs 155 / 170 (even routing), 152 / 139 (Zipf); 8 of 2048 x 1024 at 32, 64 pairs
+// 30.5 / 31.4, 33.8 / 31.9.
+constexpr int kBlockSwapPairsPerExpert = 32;
 // Shortest K (blocks of 128) whose swap-AB tiles of more than 32 tokens beat the CTA pairs' (moe_gemm_block).
 constexpr int kBlockSwapMinK = 12;
 // Single-launch decode kernel limits (shared-memory tables, one token column per epilogue thread).
@@ -80,6 +86,7 @@ struct Plan {
   bool gather_in_gemm = false;  // GEMM1 gathers its activation rows itself (TMA tile::gather4)
   bool fused = false;           // the whole layer as one cooperative kernel
   bool pair = false;            // token-major GEMMs on CTA pairs (256-row permutation blocks)
+  bool by_block = false;        // block-scaled swap-AB tiles over permutation blocks
   bool fin = false;             // bf16 swap-AB GEMM1 splits summed by the last-arriving CTA (no reduction kernel)
   size_t o_sync = 0;
   size_t o_xscale = 0, o_ascale = 0;  // block scales of the gathered input and of the intermediate
@@ -187,18 +194,19 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
     if (H % 128 || I % 128) return MOE_ERR_UNSUPPORTED;
     p.swap = orient == MOE_ORIENT_SWAP_AB ||
              (orient == MOE_ORIENT_AUTO && (T <= 64 || (p.path == PATH_W4 && T <= 128)));
-    if (p.swap && T > 256) return MOE_ERR_UNSUPPORTED;
-    // block-scaled weights: a swap-AB tile holds all of an expert's tokens
-    if (p.path == PATH_BLK && p.swap && T > kBlockSwapMaxTokens) return MOE_ERR_UNSUPPORTED;
+    if (p.swap && T > 256 && p.path != PATH_BLK) return MOE_ERR_UNSUPPORTED;
+    if (p.path == PATH_BLK && orient == MOE_ORIENT_AUTO && n <= (long)kBlockSwapPairsPerExpert * E) p.swap = true;
     // INT4 weights: swap-AB batches of up to 128 tokens, whole 256-row weight tiles
     if (p.path == PATH_W4 && (!p.swap || T > 128 || H % 256 || I % 256)) return MOE_ERR_UNSUPPORTED;
     const int eb = (p.path == PATH_FP8 || p.path == PATH_BLK) ? 1 : 2;
     if (p.path == PATH_BLK) {
       if (opts && (opts->cta_pair < 0 || opts->cta_pair > 2 || opts->split_k < 0)) return MOE_ERR_ARG;
       if (opts && opts->cta_pair == 2 && !p.swap) return MOE_ERR_UNSUPPORTED;
+      // swap-AB tiles hold all of an expert's tokens up to 64 tokens, one block of 64 of them above
       p.pair = !p.swap;
-      p.y_bf16 = p.pair;  // (what k_gemm_block_pair stores)
-      p.B = p.swap ? 16 : 128;
+      p.by_block = p.swap && T > kBlockSwapMaxTokens;
+      p.y_bf16 = p.pair || p.by_block;
+      p.B = p.pair ? 128 : p.by_block ? kBlockSwapMaxTokens : 16;
       p.xbox = p.swap ? block_swap_tokens(T) : 128;
       p.kb1 = H / 128;
       p.kb2 = I / 128;
@@ -537,6 +545,8 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
     g.nt = pl.xbox;
     g.pair = pl.pair;
     g.pblk = pblk;
+    g.by_block = pl.by_block;
+    g.out_bf16 = pl.y_bf16;
     g.sorted = sorted;
     g.eids = eids;
     g.meta = meta;

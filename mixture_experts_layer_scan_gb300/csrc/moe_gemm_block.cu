@@ -48,6 +48,7 @@ struct BgDev {
   int stages, out_bf16;
   int cl;               // CTAs of a cluster that share a tile's K blocks (1, 2, 4, 8)
   int kb_per;           // K blocks of one of them
+  int by_block;         // grouped: a tile's tokens are one block of the permutation (64 rows), not a whole expert
   int early;            // the tile list and the weights may be read before the dependency wait
   int out_v8;           // rows of out are 32-byte aligned
   uint32_t stage_bytes, bar_off, scale_off, out_off;
@@ -69,7 +70,7 @@ struct BgTile {
 template <int EPI, int NT>
 __device__ __forceinline__ int bg_tile_count(const BgDev& p) {
   if constexpr (EPI == BG_EPI_DENSE) return (p.T + NT - 1) / NT * p.n_tiles;
-  return p.meta[META_NACT] * p.n_tiles;
+  return (p.by_block ? p.meta[META_NBLK] : p.meta[META_NACT]) * p.n_tiles;
 }
 
 template <int EPI, int NT>
@@ -81,6 +82,10 @@ __device__ __forceinline__ BgTile bg_tile_at(const BgDev& p, int t) {
     d.e = 0;
     d.xrow = m * NT;
     d.ntok = min(NT, p.T - d.xrow);
+  } else if (p.by_block) {  // (an expert's blocks are neighbours: its weights come from L2 after the first)
+    d.e = p.eids[m];
+    d.xrow = m * NT;
+    d.ntok = min(NT, p.meta[meta_offsets(p.E) + d.e] + p.meta[meta_counts(p.E) + d.e] - d.xrow);
   } else {
     d.e = p.meta[meta_active(p.E) + m];
     d.xrow = p.meta[meta_offsets(p.E) + d.e];
@@ -120,9 +125,17 @@ __device__ __forceinline__ void bg_store_row(const BgDev& p, const BgTile& d, co
   } else if constexpr (EPI == BG_EPI_G2) {
     const int f = p.sorted[d.xrow + c];
     if (f >= p.T * p.k) return;
-    float* y = static_cast<float*>(p.out) + (size_t)f * p.n_out + (size_t)d.n * 256 + 4 * lane;
-    *reinterpret_cast<float4*>(y) = v0;
-    if (d.n * 256 + 128 < p.n_out) *reinterpret_cast<float4*>(y + 128) = v1;
+    const size_t o = (size_t)f * p.n_out + (size_t)d.n * 256 + 4 * lane;
+    const bool second = d.n * 256 + 128 < p.n_out;
+    if (p.out_bf16) {  // (as bp_store)
+      uint2* y = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o);
+      y[0] = make_uint2(pack_bf16x2(v0.x, v0.y), pack_bf16x2(v0.z, v0.w));
+      if (second) y[32] = make_uint2(pack_bf16x2(v1.x, v1.y), pack_bf16x2(v1.z, v1.w));
+    } else {
+      float* y = static_cast<float*>(p.out) + o;
+      *reinterpret_cast<float4*>(y) = v0;
+      if (second) *reinterpret_cast<float4*>(y + 128) = v1;
+    }
   } else {
     const size_t o = (size_t)(d.xrow + c) * p.n_out;
 #pragma unroll
@@ -1138,7 +1151,10 @@ cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
     const long tiles = ((long)a.T + a.nt - 1) / a.nt * p.n_tiles;
     return launch_bg_nt<BG_EPI_DENSE>(mw, mx, p, a.nt, tiles, a.num_sms, s);
   }
-  const long groups = std::min<long>(a.E, (long)a.T * a.k);  // active experts at most
+  p.by_block = a.by_block ? 1 : 0;
+  if (a.by_block && a.nt != 64) return cudaErrorInvalidValue;
+  // active experts, or blocks, at most
+  const long groups = a.by_block ? a.cap / 64 : std::min<long>(a.E, (long)a.T * a.k);
   if (a.epi == BG_EPI_G1) return launch_bg_nt<BG_EPI_G1>(mw, mx, p, a.nt, groups * p.n_tiles, a.num_sms, s);
   return launch_bg_nt<BG_EPI_G2>(mw, mx, p, a.nt, groups * p.n_tiles, a.num_sms, s);
 }

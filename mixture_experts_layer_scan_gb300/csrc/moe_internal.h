@@ -88,7 +88,7 @@ cudaError_t launch_quant_block_scatter(const void* x, int T, int K, int k, const
 enum BlockGemmEpilogue {
   BG_EPI_DENSE = 0,  // out [T][n_out] bf16 or fp32
   BG_EPI_G1 = 1,     // expert GEMM1: SiLU(gate)*up -> e4m3 out [cap][I] + out_scale [cap][I/128]
-  BG_EPI_G2 = 2      // expert GEMM2: Y[pair][H], fp32 (swap-AB) or bf16 (CTA pairs)
+  BG_EPI_G2 = 2      // expert GEMM2: Y[pair][H], fp32 or bf16 (out_bf16; always on CTA pairs)
 };
 struct BlockGemmArgs {
   int epi;
@@ -97,8 +97,10 @@ struct BlockGemmArgs {
   int w_rows;             // weight rows per expert (N, 2I, H)
   int cap;                // rows of the sorted activations (grouped)
   bool pair;              // token-major on CTA pairs (grouped: permutation blocks of 128, tiles from pblk)
-  int nt;                 // swap-AB: tokens per tile, 16, 32 or 64 (grouped: at least an expert's tokens)
-  bool out_bf16;          // dense
+  int nt;                 // swap-AB: tokens per tile, 16, 32 or 64 (grouped: at least an expert's tokens,
+                          // unless by_block)
+  bool by_block;          // grouped swap-AB: tiles are permutation blocks of nt = 64 rows
+  bool out_bf16;          // dense and GEMM2: bf16 rows, else fp32
   bool early;             // swap-AB: the tile list and the weights may be read before the dependency wait (as
                           // TcGemmArgs.early)
   const void* x;          // e4m3 [rows][K]

@@ -86,10 +86,14 @@ def test_block_weight_plans(moe):
     B = moe.MOE_E4M3_B128
     d = moe.moe_plan_info(64, 4096, 2048, 64, 8, moe.MOE_BF16, B)
     assert d["orientation"] == moe.ORIENT_SWAP_AB and d["block"] == 16
-    p = moe.moe_plan_info(65, 4096, 2048, 64, 8, moe.MOE_BF16, B)
-    assert p["orientation"] == moe.ORIENT_TOKEN_MAJOR
+    # above 64 tokens: blocks of 64 up to 32 pairs per expert, CTA pairs beyond
+    s = moe.moe_plan_info(256, 4096, 2048, 64, 8, moe.MOE_BF16, B)
+    assert s["orientation"] == moe.ORIENT_SWAP_AB and s["block"] == 64 and s["cta_pair"] == 0
+    p = moe.moe_plan_info(257, 4096, 2048, 64, 8, moe.MOE_BF16, B)
+    assert p["orientation"] == moe.ORIENT_TOKEN_MAJOR and p["block"] == 128 and p["cta_pair"] == 1
+    assert moe.moe_plan_info(48, 4096, 2048, 64, 8, moe.MOE_BF16, B, {"orientation": 2})["cta_pair"] == 1
     for args, opts in (((64, 4000, 2048, 64, 8), None), ((64, 4096, 2000, 64, 8), None),
-                       ((65, 4096, 2048, 64, 8), {"orientation": moe.ORIENT_SWAP_AB})):
+                       ((4096, 4096, 2048, 64, 8), {"cta_pair": 2})):
         with pytest.raises(moe.MoeError) as e:
             moe.moe_plan_info(*args, moe.MOE_BF16, B, opts)
         assert e.value.code == moe.MOE_ERR_UNSUPPORTED

@@ -305,8 +305,9 @@ def test_experts_against_64_bits(moe, T, H, I, E, k, hot):
     assert torch.equal(out, again)
 
 
-def test_both_orientations_agree(moe):
-    d = make_experts(48, 512, 256, 8, 3, torch.Generator().manual_seed(2))
+@pytest.mark.parametrize("T,hot", [(48, False), (90, True), (300, False), (400, True)])
+def test_both_orientations_agree(moe, T, hot):
+    d = make_experts(T, 512, 256, 8, 3, torch.Generator().manual_seed(2), hot)
     ref = experts_reference(d)
     c = {n: v.cuda() for n, v in d.items()}
     for o in (moe.ORIENT_SWAP_AB, moe.ORIENT_TOKEN_MAJOR):
