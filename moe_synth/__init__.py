@@ -269,3 +269,30 @@ def make_rope_inputs(rs: RopeSpec, device="cpu") -> dict:
     if device != "cpu":
         d = {k: (v.to(device) if isinstance(v, torch.Tensor) else v) for k, v in d.items()}
     return d
+
+
+def make_block_weights(rows: int, K: int, gen: torch.Generator, std: float = 0.02, device="cpu"):
+    """Block-scaled FP8 weights N(0, std): e4m3 codes [rows, K] and one float32 scale = amax / 448 per block
+    of 128 x 128, [ceil(rows/128), ceil(K/128)] (a stand-in for an offline quantiser)."""
+    n, k = -(-rows // 128), -(-K // 128)
+    w = torch.randn(rows, K, generator=gen, device=gen.device) * std
+    w = torch.nn.functional.pad(w, (0, k * 128 - K, 0, n * 128 - rows)).view(n, 128, k, 128)
+    s = (w.abs().amax(dim=(1, 3)) / 448.0).clamp_min(1e-30)
+    q = (w / s[:, None, :, None]).clamp_(-448.0, 448.0).to(torch.float8_e4m3fn)
+    return q.view(n * 128, k * 128)[:rows, :K].contiguous().to(device), s.to(device)
+
+
+def make_block_layer(H: int, I: int, E: int, I_shared: int, seed: int = 1240, device="cpu") -> dict:
+    """Weights of a fine-grained expert layer with block-scaled FP8 experts and one shared expert: router
+    (bf16 [E, H]) and its balance bias (float32 [E]), w13 / w2 per expert, shared w13 / w2, all with scales."""
+    g = _gen(seed, device)
+    d = {"router": (torch.randn(E, H, generator=g, device=device) / math.sqrt(H)).to(torch.bfloat16),
+         "bias": torch.randn(E, generator=g, device=device) * 0.05}
+    for name, lead, rows, K in (("w13", E, 2 * I, H), ("w2", E, H, I), ("shared13", 1, 2 * I_shared, H),
+                                ("shared2", 1, H, I_shared)):
+        w = [make_block_weights(rows, K, g, device=device) for _ in range(lead)]
+        d[name] = torch.stack([q for q, _ in w])
+        d[name + "_scale"] = torch.stack([s for _, s in w])
+    for name in ("shared13", "shared2"):
+        d[name], d[name + "_scale"] = d[name][0], d[name + "_scale"][0]
+    return d
