@@ -363,9 +363,11 @@ def _w_dtype(w13: torch.Tensor, w_format: Optional[str]) -> int:
     return {"int4": MOE_INT4, "e4m3_block": MOE_E4M3_B128}[w_format]
 
 
-def _check_block_scales(w_format, E, H, I, w13_scale, w2_scale) -> None:
+def _check_block_scales(w_format, E, H, I, w13, w2, w13_scale, w2_scale) -> None:
     if w_format != "e4m3_block":
         return
+    if _dt(w13) != MOE_E4M3 or _dt(w2) != MOE_E4M3 or w13.shape != (E, 2 * I, H) or w2.shape != (E, H, I):
+        raise ValueError("block-scaled weights must be e4m3 codes w13 [E, 2 I, H] and w2 [E, H, I]")
     for s, shape in ((w13_scale, (E, 2 * I // 128, H // 128)), (w2_scale, (E, H // 128, I // 128))):
         if s is None or s.dtype != torch.float32 or tuple(s.shape) != shape:
             raise ValueError(f"block scales must be float32 {shape}")
@@ -386,7 +388,7 @@ def moe_forward(hidden: torch.Tensor, router_w: torch.Tensor, w13: torch.Tensor,
     div = 2 if w_format == "int4" else 1
     if H2 * div != H or w2.shape != (E, H, I // div) or router_w.shape != (E, H):
         raise ValueError("inconsistent shapes")
-    _check_block_scales(w_format, E, H, I, w13_scale, w2_scale)
+    _check_block_scales(w_format, E, H, I, w13, w2, w13_scale, w2_scale)
     act, wdt = _dt(hidden), _w_dtype(w13, w_format)
     opts = _opts(options)
     need = moe_workspace_size(T, H, I, E, topk, act, wdt, options)
@@ -412,7 +414,7 @@ def moe_forward_host(hidden_host: torch.Tensor, router_w: torch.Tensor, w13: tor
     div = 2 if w_format == "int4" else 1
     if H2 * div != H or w2.shape != (E, H, I // div) or router_w.shape != (E, H):
         raise ValueError("inconsistent shapes")
-    _check_block_scales(w_format, E, H, I, w13_scale, w2_scale)
+    _check_block_scales(w_format, E, H, I, w13, w2, w13_scale, w2_scale)
     dev = router_w.device
     act, wdt = _dt(hidden_host), _w_dtype(w13, w_format)
     need = moe_workspace_size(T, H, I, E, topk, act, wdt, options)
@@ -442,7 +444,7 @@ def moe_forward_noalloc(hidden: torch.Tensor, router_w: torch.Tensor, w13: torch
     div = 2 if w_format == "int4" else 1
     if H2 * div != H or w2.shape != (E, H, I // div) or router_w.shape != (E, H):
         raise ValueError("inconsistent shapes")
-    _check_block_scales(w_format, E, H, I, w13_scale, w2_scale)
+    _check_block_scales(w_format, E, H, I, w13, w2, w13_scale, w2_scale)
     wdt = _w_dtype(w13, w_format)
     out = torch.empty_like(hidden) if out is None else out
     _check(_lib.moe_forward_noalloc(_p(hidden), _p(router_w), _p(w13), _p(w2), T, H, I, E, topk, int(bool(renorm)),
@@ -486,7 +488,7 @@ def moe_forward_routed(hidden: torch.Tensor, topk_w: torch.Tensor, topk_ids: tor
     if topk_ids.dtype != torch.int32 or topk_w.dtype != torch.float32 or topk_ids.shape[0] != T or (
             topk_w.shape != topk_ids.shape):
         raise ValueError("topk_w must be float32 and topk_ids int32, both [T, k]")
-    _check_block_scales(w_format, E, H, I, w13_scale, w2_scale)
+    _check_block_scales(w_format, E, H, I, w13, w2, w13_scale, w2_scale)
     act, wdt = _dt(hidden), _w_dtype(w13, w_format)
     if options is None:
         opts = _ROUTED_OPTIONS

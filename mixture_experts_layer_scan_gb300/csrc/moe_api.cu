@@ -86,7 +86,6 @@ struct Plan {
   bool gather_in_gemm = false;  // GEMM1 gathers its activation rows itself (TMA tile::gather4)
   bool fused = false;           // the whole layer as one cooperative kernel
   bool pair = false;            // token-major GEMMs on CTA pairs (256-row permutation blocks)
-  bool by_block = false;        // block-scaled swap-AB tiles over permutation blocks
   bool fin = false;             // bf16 swap-AB GEMM1 splits summed by the last-arriving CTA (no reduction kernel)
   size_t o_sync = 0;
   size_t o_xscale = 0, o_ascale = 0;  // block scales of the gathered input and of the intermediate
@@ -202,12 +201,11 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
     if (p.path == PATH_BLK) {
       if (opts && (opts->cta_pair < 0 || opts->cta_pair > 2 || opts->split_k < 0)) return MOE_ERR_ARG;
       if (opts && opts->cta_pair == 2 && !p.swap) return MOE_ERR_UNSUPPORTED;
-      // swap-AB tiles hold all of an expert's tokens up to 64 tokens, one block of 64 of them above
+      // a swap-AB tile's tokens are one block of the permutation, and a block holds all of an expert's
+      // tokens up to 64 tokens (unless the caller's routing names an expert twice for a token)
       p.pair = !p.swap;
-      p.by_block = p.swap && T > kBlockSwapMaxTokens;
-      p.y_bf16 = p.pair || p.by_block;
-      p.B = p.pair ? 128 : p.by_block ? kBlockSwapMaxTokens : 16;
-      p.xbox = p.swap ? block_swap_tokens(T) : 128;
+      p.y_bf16 = T > kBlockSwapMaxTokens || p.pair;
+      p.B = p.xbox = p.swap ? block_swap_tokens(T) : 128;
       p.kb1 = H / 128;
       p.kb2 = I / 128;
     } else if (p.swap) {
@@ -545,7 +543,6 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
     g.nt = pl.xbox;
     g.pair = pl.pair;
     g.pblk = pblk;
-    g.by_block = pl.by_block;
     g.out_bf16 = pl.y_bf16;
     g.sorted = sorted;
     g.eids = eids;

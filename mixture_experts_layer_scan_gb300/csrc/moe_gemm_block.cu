@@ -48,7 +48,6 @@ struct BgDev {
   int stages, out_bf16;
   int cl;               // CTAs of a cluster that share a tile's K blocks (1, 2, 4, 8)
   int kb_per;           // K blocks of one of them
-  int by_block;         // grouped: a tile's tokens are one block of the permutation (64 rows), not a whole expert
   int early;            // the tile list and the weights may be read before the dependency wait
   int out_v8;           // rows of out are 32-byte aligned
   uint32_t stage_bytes, bar_off, scale_off, out_off;
@@ -70,7 +69,7 @@ struct BgTile {
 template <int EPI, int NT>
 __device__ __forceinline__ int bg_tile_count(const BgDev& p) {
   if constexpr (EPI == BG_EPI_DENSE) return (p.T + NT - 1) / NT * p.n_tiles;
-  return (p.by_block ? p.meta[META_NBLK] : p.meta[META_NACT]) * p.n_tiles;
+  return p.meta[META_NBLK] * p.n_tiles;
 }
 
 template <int EPI, int NT>
@@ -82,14 +81,10 @@ __device__ __forceinline__ BgTile bg_tile_at(const BgDev& p, int t) {
     d.e = 0;
     d.xrow = m * NT;
     d.ntok = min(NT, p.T - d.xrow);
-  } else if (p.by_block) {  // (an expert's blocks are neighbours: its weights come from L2 after the first)
+  } else {  // one block of the permutation (an expert's are neighbours: its weights come from L2 after the first)
     d.e = p.eids[m];
     d.xrow = m * NT;
     d.ntok = min(NT, p.meta[meta_offsets(p.E) + d.e] + p.meta[meta_counts(p.E) + d.e] - d.xrow);
-  } else {
-    d.e = p.meta[meta_active(p.E) + m];
-    d.xrow = p.meta[meta_offsets(p.E) + d.e];
-    d.ntok = p.meta[meta_counts(p.E) + d.e];
   }
   d.npad = (d.ntok + 15) & ~15;
   d.wr0 = d.e * p.w_rows + d.n * p.w_tile_rows;
@@ -1151,10 +1146,7 @@ cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
     const long tiles = ((long)a.T + a.nt - 1) / a.nt * p.n_tiles;
     return launch_bg_nt<BG_EPI_DENSE>(mw, mx, p, a.nt, tiles, a.num_sms, s);
   }
-  p.by_block = a.by_block ? 1 : 0;
-  if (a.by_block && a.nt != 64) return cudaErrorInvalidValue;
-  // active experts, or blocks, at most
-  const long groups = a.by_block ? a.cap / 64 : std::min<long>(a.E, (long)a.T * a.k);
+  const long groups = a.cap / a.nt;  // blocks of the permutation at most
   if (a.epi == BG_EPI_G1) return launch_bg_nt<BG_EPI_G1>(mw, mx, p, a.nt, groups * p.n_tiles, a.num_sms, s);
   return launch_bg_nt<BG_EPI_G2>(mw, mx, p, a.nt, groups * p.n_tiles, a.num_sms, s);
 }

@@ -97,9 +97,7 @@ struct BlockGemmArgs {
   int w_rows;             // weight rows per expert (N, 2I, H)
   int cap;                // rows of the sorted activations (grouped)
   bool pair;              // token-major on CTA pairs (grouped: permutation blocks of 128, tiles from pblk)
-  int nt;                 // swap-AB: tokens per tile, 16, 32 or 64 (grouped: at least an expert's tokens,
-                          // unless by_block)
-  bool by_block;          // grouped swap-AB: tiles are permutation blocks of nt = 64 rows
+  int nt;                 // swap-AB: tokens per tile, 16, 32 or 64 (grouped: the permutation's block size)
   bool out_bf16;          // dense and GEMM2: bf16 rows, else fp32
   bool early;             // swap-AB: the tile list and the weights may be read before the dependency wait (as
                           // TcGemmArgs.early)

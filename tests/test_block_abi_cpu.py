@@ -82,10 +82,41 @@ def test_gemm_arguments(moe):
     assert f(None, None, None, None, 0, 8, 128, 1, None, None) == moe.MOE_OK
 
 
+def test_python_checks(moe):
+    """Shapes and types that the binding refuses before the library sees them (CPU tensors: nothing is launched)."""
+    import torch
+
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    a, sa, w, sw = torch.zeros(4, 256, dtype=f8), torch.zeros(4, 2), torch.zeros(300, 256, dtype=f8), torch.zeros(3, 2)
+    for bad in ((a, sa[:, :1], w, sw), (a, sa, w[:, :128], sw), (a, sa, w, sw[:2]), (a.float(), sa, w, sw),
+                (a, sa.double(), w, sw)):
+        with pytest.raises(ValueError):
+            moe.moe_gemm_block(*bad)
+    with pytest.raises(ValueError):
+        moe.moe_gemm_block(a, sa, w, sw, out=torch.zeros(4, 256, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        moe.moe_quant_block(torch.zeros(4, 256), q=torch.zeros(4, 128, dtype=f8))
+    with pytest.raises(ValueError):
+        moe.moe_silu_quant_block(torch.zeros(4, 255))
+    with pytest.raises(ValueError):
+        moe.moe_topk_grouped(torch.zeros(4, 64, dtype=torch.bfloat16), 8)
+    with pytest.raises(ValueError):
+        moe.moe_topk_grouped(torch.zeros(4, 64), 8, bias=torch.zeros(32))
+    x, tw, ids = torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(4, 2), torch.zeros(4, 2, dtype=torch.int32)
+    w13, w2 = torch.zeros(8, 256, 256, dtype=f8), torch.zeros(8, 256, 128, dtype=f8)
+    s13, s2 = torch.zeros(8, 2, 2), torch.zeros(8, 2, 1)
+    for bad in ((x, tw, ids.long(), w13, w2, s13, s2), (x, tw[:2], ids, w13, w2, s13, s2),
+                (x, tw, ids, w13, w2, s13[:, :1], s2), (x, tw, ids, w13, w2, s13, None),
+                (x, tw, ids, w13.to(f32), w2, s13, s2), (x, tw, ids, w13, w2[:, :128], s13, s2)):
+        with pytest.raises(ValueError):
+            moe.moe_forward_routed(*bad, w_format="e4m3_block")
+
+
 def test_block_weight_plans(moe):
     B = moe.MOE_E4M3_B128
     d = moe.moe_plan_info(64, 4096, 2048, 64, 8, moe.MOE_BF16, B)
-    assert d["orientation"] == moe.ORIENT_SWAP_AB and d["block"] == 16
+    assert d["orientation"] == moe.ORIENT_SWAP_AB and d["block"] == 64
+    assert moe.moe_plan_info(16, 4096, 2048, 64, 8, moe.MOE_BF16, B)["block"] == 16
     # above 64 tokens: blocks of 64 up to 32 pairs per expert, CTA pairs beyond
     s = moe.moe_plan_info(256, 4096, 2048, 64, 8, moe.MOE_BF16, B)
     assert s["orientation"] == moe.ORIENT_SWAP_AB and s["block"] == 64 and s["cta_pair"] == 0

@@ -345,6 +345,18 @@ def test_expert_id_out_of_range_is_dropped_and_flagged(moe):
         assert moe.moe_get_status() == 0
 
 
+@pytest.mark.parametrize("T", [1, 16, 20, 60, 100])
+def test_an_expert_named_twice_for_a_token(moe, T):
+    """A caller's routing may repeat an expert: its list is then longer than the batch."""
+    d = make_experts(T, 256, 128, 4, 3, torch.Generator().manual_seed(T))
+    d["ids"][:, 1] = d["ids"][:, 0]
+    d["ids"][: T // 2 + 1] = 2
+    c = {n: v.cuda() for n, v in d.items()}
+    out = moe.moe_forward_routed(c["x"], c["tw"], c["ids"], c["w13"], c["w2"], c["s13"], c["s2"], w_format="e4m3_block")
+    assert moe.moe_get_status() == 0
+    check(out, experts_reference(d), f"repeated experts T={T}")
+
+
 def test_empty_batch(moe):
     d = make_experts(1, 256, 128, 4, 2, torch.Generator().manual_seed(1))
     c = {n: v.cuda() for n, v in d.items()}
