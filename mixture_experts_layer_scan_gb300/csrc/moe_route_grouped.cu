@@ -15,8 +15,10 @@
 // round).  The scores of the chosen experts are computed again from their logits instead of being
 // carried next to the keys (half the registers; the same function of the same input, so the same
 // bits).  Bound by the instructions of the scores and the rounds, not by the 4 bytes a logit.
-#include "moe_internal.h"
+#include <type_traits>
+
 #include "moe_device.cuh"
+#include "moe_internal.h"
 
 namespace moe {
 
@@ -156,7 +158,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_topk_grouped(const Grouped
 #pragma unroll
   for (int j = 0; j < V; ++j) b.add(key[j], j);
   if (!keep) b.m1 = b.m2 = kTakenKey;
-  unsigned long long taken = 0;  // (V <= 64)
+  using Mask = std::conditional_t<V <= 32, uint32_t, unsigned long long>;
+  Mask taken = 0;  // this lane's experts chosen so far
   int my_id = 0;
   bool second = false;  // m1 is already the second of a look through the keys
   for (int r = 0; r < p.k; ++r) {
@@ -166,20 +169,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_topk_grouped(const Grouped
     if (lane == r) my_id = id;
     bool look = false;
     if (lane == winner) {
-      taken |= 1ull << b.j1;
+      taken |= Mask(1) << b.j1;
       b.m1 = b.m2;
       b.j1 = b.j2;
       look = second;
       second = true;
     }
-    if (__any_sync(kAll, look)) {
-      if (look) {
-        b = Best2();
+    if (look) {  // (one lane: the others wait for it)
+      b = Best2();
 #pragma unroll
-        for (int j = 0; j < V; ++j) b.add((taken >> j) & 1 ? kTakenKey : key[j], j);
-        second = false;
-      }
+      for (int j = 0; j < V; ++j) b.add((taken >> j) & 1 ? kTakenKey : key[j], j);
+      second = false;
     }
+    __syncwarp();
   }
 
   float s = 0.0f;
