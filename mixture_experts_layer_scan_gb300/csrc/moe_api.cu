@@ -490,6 +490,9 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
   // streams its first weight stages into shared memory while the gather runs.
   const bool g1_prefetch = pl.swap && !gate && (long)T * topk >= 8L * E;
   const bool g1_early = pl.swap && pl.path != PATH_W4 && !pl.gather_in_gemm && !inv && !gate && !g1_prefetch;
+  // a short batch of block-scaled experts is sorted by the launch that quantises it, and GEMM1's CTAs
+  // derive its tiles from the routing
+  const bool align_quant = pl.path == PATH_BLK && pl.swap && n <= kAlignSmallPairs;
 
   if (!(steps & (STEPS_EXPERTS | STEPS_COMBINE))) return MOE_OK;
   if (!(steps & STEPS_EXPERTS)) goto combine_step;
@@ -499,7 +502,7 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
   // the permutation kernel also zeroes the counters of this call's later kernels: the split
   // arrival counters (last-arriver sums) or the two FP8 amax words, so that no memset node
   // breaks the chain of programmatically dependent launches
-  {
+  if (!align_quant) {
     unsigned* zero_words = pl.fin ? fin : (pl.path == PATH_FP8 ? amax : nullptr);
     const int n_zero = pl.fin ? E * (I / 128) : (pl.path == PATH_FP8 ? 2 : 0);
     MOE_TRY(launch_align(tid, T, topk, E, pl.B, sorted, eids, meta + META_NPP, nullptr, meta, st, s, skip_minus_one,
@@ -510,7 +513,10 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
   // 4. activations: the fp32 path gathers rows into expert order here; the
   // tensor-core paths gather inside GEMM1 (FP8: quantise the input to e4m3 first)
   if (o) record(o->stage_begin[MOE_STAGE_GATHER], s);
-  if (pl.path == PATH_BLK) {
+  if (align_quant) {
+    MOE_TRY(launch_align_quant_small(hidden, T, H, topk, tid, E, pl.B, sorted, eids, meta, st, skip_minus_one,
+                                     (uint8_t*)xs, xscale, s));
+  } else if (pl.path == PATH_BLK) {
     MOE_TRY(launch_quant_block_scatter(hidden, T, H, topk, inv, (uint8_t*)xs, xscale, s));
   } else if (pl.path == PATH_FP8) {
     MOE_TRY(launch_amax_bf16(hidden, (size_t)T * H, amax, s));
@@ -551,8 +557,10 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
     g.num_sms = sms;
     // 5. GEMM1 on w13, its epilogue forming the e4m3 blocks of SiLU(gate)*up
     BlockGemmArgs g1 = g;
-    // (the quantisation lets its dependents launch after its own wait, when the permutation is complete)
+    // (the quantisation lets its dependents launch after its own wait, when the permutation -- for a short
+    // batch the routing -- is complete)
     g1.early = true;
+    g1.ids = align_quant ? tid : nullptr;
     g1.epi = BG_EPI_G1;
     g1.K = H;
     g1.n_out = I;

@@ -25,6 +25,7 @@
 // changes between calls.
 #include <algorithm>
 
+#include "moe_align.cuh"
 #include "moe_device.cuh"
 #include "moe_internal.h"
 
@@ -50,13 +51,14 @@ struct BgDev {
   int kb_per;           // K blocks of one of them
   int early;            // the tile list and the weights may be read before the dependency wait
   int out_v8;           // rows of out are 32-byte aligned
-  uint32_t stage_bytes, bar_off, scale_off, out_off;
+  uint32_t stage_bytes, bar_off, scale_off, out_off, list_off;
   const float* a_scale;  // [rows][kb_total]
   const float* w_scale;  // [E][w_scale_rows][kb_total]
   const int32_t* sorted;
   const int32_t* eids;
   const int32_t* meta;
   const int32_t* pblk;   // CTA pairs: the permutation's 256- and 128-row chunks
+  const int32_t* ids;    // nullable: the routing itself instead of eids and meta (BlockGemmArgs)
   void* out;
   float* out_scale;
   int* status;
@@ -66,24 +68,44 @@ struct BgTile {
   int e, n, xrow, ntok, npad, wr0;
 };
 
+// Tiles of a routing of at most 32 pairs, in shared memory: expert and tokens of each permutation block.
+struct BgList {
+  int2 blk[kAlignSmallPairs];
+  int n;
+};
+
+template <int NT>
+__device__ __forceinline__ void bg_make_list(const BgDev& p, BgList* list) {  // (one warp)
+  const SmallGroup g = align_small(p.ids, p.T * p.k, p.E, NT, nullptr, 1);
+  if (g.leader)
+    for (int b = 0; b < g.pad / NT; ++b) list->blk[g.off / NT + b] = make_int2(g.e, min(NT, g.count - b * NT));
+  const int blocks = __reduce_add_sync(0xffffffffu, g.leader ? g.pad / NT : 0);
+  if ((threadIdx.x & 31) == 0) list->n = blocks;
+}
+
 template <int EPI, int NT>
-__device__ __forceinline__ int bg_tile_count(const BgDev& p) {
+__device__ __forceinline__ int bg_tile_count(const BgDev& p, const BgList* list) {
   if constexpr (EPI == BG_EPI_DENSE) return (p.T + NT - 1) / NT * p.n_tiles;
+  if constexpr (EPI == BG_EPI_G1)
+    if (p.ids) return list->n * p.n_tiles;
   return p.meta[META_NBLK] * p.n_tiles;
 }
 
 template <int EPI, int NT>
-__device__ __forceinline__ BgTile bg_tile_at(const BgDev& p, int t) {
+__device__ __forceinline__ BgTile bg_tile_at(const BgDev& p, const BgList* list, int t) {
   BgTile d;
   const int m = t / p.n_tiles;
   d.n = t - m * p.n_tiles;
+  d.xrow = m * NT;
   if constexpr (EPI == BG_EPI_DENSE) {
     d.e = 0;
-    d.xrow = m * NT;
     d.ntok = min(NT, p.T - d.xrow);
+  } else if (EPI == BG_EPI_G1 && p.ids) {
+    const int2 b = list->blk[m];
+    d.e = b.x;
+    d.ntok = b.y;
   } else {  // one block of the permutation (an expert's are neighbours: its weights come from L2 after the first)
     d.e = p.eids[m];
-    d.xrow = m * NT;
     d.ntok = min(NT, p.meta[meta_offsets(p.E) + d.e] + p.meta[meta_counts(p.E) + d.e] - d.xrow);
   }
   d.npad = (d.ntok + 15) & ~15;
@@ -195,6 +217,9 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     tma_prefetch_desc(&tmX);
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), kCols);
+  BgList* list = reinterpret_cast<BgList*>(smem + p.list_off);
+  if constexpr (EPI == BG_EPI_G1)
+    if (p.ids && warp == 2) bg_make_list<NT>(p, list);
   tc_fence_before();
   cta_sync();
   tc_fence_after();
@@ -205,13 +230,13 @@ __global__ void __launch_bounds__(kBgThreads, 1)
   const int kb0 = rank * p.kb_per, kb1 = min(kb0 + p.kb_per, p.kb_total);
   const int tile0 = blockIdx.x / p.cl, stride = gridDim.x / p.cl;
   if (!p.early) pdl_wait();
-  const int ntiles = bg_tile_count<EPI, NT>(p);
+  const int ntiles = bg_tile_count<EPI, NT>(p, list);
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     int pre = 0;  // stages whose weights are already on their way
     if (p.early && tile0 < ntiles) {
-      const BgTile d = bg_tile_at<EPI, NT>(p, tile0);
+      const BgTile d = bg_tile_at<EPI, NT>(p, list, tile0);
       pre = min(p.stages, kb1 - kb0);
       if (elect_one())
         for (int i = 0; i < pre; ++i) {
@@ -227,7 +252,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     uint32_t phase = 0, issued = 0;
     bool ok = true;
     for (int t = tile0; t < ntiles && ok; t += stride) {
-      const BgTile d = bg_tile_at<EPI, NT>(p, t);
+      const BgTile d = bg_tile_at<EPI, NT>(p, list, t);
       for (int kb = kb0; kb < kb1; ++kb) {
         const bool weights = (int)issued >= pre;
         if (weights && !mbar_wait_all(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
@@ -269,7 +294,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true, any = false;
       for (int t = tile0; t < ntiles && ok; t += stride) {
-        const uint32_t idesc = idesc_make(128, bg_tile_at<EPI, NT>(p, t).npad, true);
+        const uint32_t idesc = idesc_make(128, bg_tile_at<EPI, NT>(p, list, t).npad, true);
         for (int kb = kb0; kb < kb1; ++kb) {
           ok = mbar_wait_one(bar_tempty + 8 * buf, buf_phase ^ 1u, abort_flag, p.status) &&
                mbar_wait_one(bar_full + 8 * stage, phase, abort_flag, p.status);
@@ -323,7 +348,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     uint32_t buf_phase = 0;
     bool ok = true;
     for (int t = tile0; t < ntiles; t += stride) {
-      const BgTile d = bg_tile_at<EPI, NT>(p, t);
+      const BgTile d = bg_tile_at<EPI, NT>(p, list, t);
       const int srow = d.n * (p.w_tile_rows / 128);
       const float* ws = p.w_scale + ((size_t)d.e * p.w_scale_rows +
                                      min(srow + h * p.s_pair_off, p.w_scale_rows - 1)) * p.kb_total;
@@ -451,13 +476,15 @@ constexpr int kMinSplitBlocks = 3;
 template <int EPI, int NT>
 cudaError_t launch_bg(const CUtensorMap& mw, const CUtensorMap& mx, BgDev p, long tiles, int sms, cudaStream_t s) {
   p.stage_bytes = 2u * 128u * 128u + (uint32_t)NT * 128u;
-  const uint32_t bar_bytes = 8 * (2 * kBgMaxStages + 2 * kBgBufs + 2) + 16;
+  const uint32_t list_at = 8 * (2 * kBgMaxStages + 2 * kBgBufs + 2) + 16;  // behind the barriers and words
+  const uint32_t bar_bytes = list_at + (uint32_t)sizeof(BgList);
   const uint32_t scale_bytes = 2u * 2u * kScaleChunk * NT * 4u;
   const uint32_t out_bytes = (uint32_t)std::min(NT, kStageTokens) * 256u * 4u;
   p.stages = std::min<int>(kBgMaxStages, (227 * 1024 - 1024 - bar_bytes - scale_bytes - out_bytes) / p.stage_bytes);
   p.out_off = (uint32_t)p.stages * p.stage_bytes;
   p.scale_off = p.out_off + out_bytes;
   p.bar_off = p.scale_off + scale_bytes;
+  p.list_off = p.bar_off + list_at;
   const size_t smem = 1024 + (size_t)p.bar_off + bar_bytes;
   auto kern = k_gemm_block<EPI, NT>;
   static bool attr_set[64] = {};
@@ -808,146 +835,146 @@ __global__ void __launch_bounds__(kBpThreads, 1)
   const int ntiles = chunks * p.n_tiles;
 
   if (warp < 4) {
-  setmaxnreg_dec<kBpRoleRegs>();
-  if (warp == 0) {
-    // ---------------- TMA producer (both CTAs) ----------------
-    // completion is counted on CTA 0's full barrier, which CTA 0 arms for both CTAs' bytes
-    int stage = 0;
-    uint32_t phase = 0, issued = 0;
-    bool ok = true;
-    for (int t = pair; t < ntiles && ok; t += npairs) {
-      const BpTile d = bp_tile_at<EPI>(p, t);
-      for (int kb = 0; kb < p.kb_total; ++kb) {
-        if (!mbar_wait_all(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          const uint32_t sw = sbase + stage * kBpStage, fb = bar_full + 8 * stage, fb0 = mapa_shared(fb, 0);
-          if (leader) mbar_arrive_expect_tx(fb, (d.tail ? 3u : 4u) * kBpHalf);
-          if (G1 && d.tail) {  // 32 gate rows, the matching 32 up rows, the next 32 of each
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int wr = d.wr0 + 64 * (int)rank + 32 * j;
-              tma_load_2d_pair(sw + j * (kBpHalf / 2), &tmW32, kb * 128, wr, fb0);
-              tma_load_2d_pair(sw + j * (kBpHalf / 2) + kBpHalf / 4, &tmW32, kb * 128, wr + p.w_pair_off, fb0);
-            }
-          } else {
-            tma_load_2d_pair(sw, &tmW, kb * 128, d.wr0 + (rank ? p.w_pair_off : 0), fb0);
-          }
-          if (d.tail)
-            tma_load_2d_pair(sw + kBpHalf, &tmX64, kb * 128, d.xrow + 64 * (int)rank, fb0);
-          else
-            tma_load_2d_pair(sw + kBpHalf, &tmX, kb * 128, d.xrow + 128 * (int)rank, fb0);
-        }
-        __syncwarp();
-        ++issued;
-        if (++stage == kBpStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    if (lane == 0) {
-      pdl_launch_dependents();
-      if (!ok && leader) {  // let the copies already in flight land before the CTA exits
-        const uint32_t first = issued > (uint32_t)kBpStages ? issued - kBpStages : 0u;
-        for (uint32_t i = first; i < issued; ++i)
-          mbar_wait_drain(bar_full + 8 * (i % kBpStages), (i / kBpStages) & 1u, 100000000ull);
-      }
-    }
-    __syncwarp();
-  } else if (warp < 3) {
-    // ---------------- MMA issuers (CTA 0): one thread for each half of a K block ----------------
-    // The thread's own instructions are the limit here: a satisfied wait takes about 70 cycles, the
-    // issue 90, and one thread doing both halves with its waits in turn took longer than the MMAs
-    // (600 to 1100 cycles a block for 545).  So each half has its thread, on different SM quarters,
-    // and both waits of a block are polled together.
-    if (leader && elect_one()) {
-      const uint32_t h = warp - 1;
-      const uint64_t a0 = sdesc_k_sw128(sbase + kBpHalf), b0 = sdesc_k_sw128(sbase + h * (kBpHalf / 2));
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, buf_phase = 0;
-      bool ok = true, any = false;
+    setmaxnreg_dec<kBpRoleRegs>();
+    if (warp == 0) {
+      // ---------------- TMA producer (both CTAs) ----------------
+      // completion is counted on CTA 0's full barrier, which CTA 0 arms for both CTAs' bytes
+      int stage = 0;
+      uint32_t phase = 0, issued = 0;
+      bool ok = true;
       for (int t = pair; t < ntiles && ok; t += npairs) {
-        const uint32_t idesc = idesc_make(bp_tile_at<EPI>(p, t).tail ? 128 : 256, 128, true);
+        const BpTile d = bp_tile_at<EPI>(p, t);
         for (int kb = 0; kb < p.kb_total; ++kb) {
-          const uint32_t fb = bar_full + 8 * stage, eb = bar_tempty + 8 * (2 * buf + h);
-          const bool full = mbar_try_wait(fb, phase), free_buf = mbar_try_wait(eb, buf_phase ^ 1u);
-          if (!(full && free_buf)) {
-            ok = mbar_wait_one(fb, phase, abort_flag, p.status) &&
-                 mbar_wait_one(eb, buf_phase ^ 1u, abort_flag, p.status);
-            if (!ok) break;
+          if (!mbar_wait_all(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
           }
-          tc_fence_after();
-          const uint64_t so = (uint64_t)(stage * (kBpStage >> 4));
-          tc_mma_pair_kblock(tmem_base + 256u * buf + 128u * h, a0 + so, b0 + so, idesc);
-          tc_commit_both(bar_tfull + 8 * (2 * buf + h));
-          tc_commit_both(bar_empty + 8 * stage);
-          any = true;
+          if (lane == 0) {
+            const uint32_t sw = sbase + stage * kBpStage, fb = bar_full + 8 * stage, fb0 = mapa_shared(fb, 0);
+            if (leader) mbar_arrive_expect_tx(fb, (d.tail ? 3u : 4u) * kBpHalf);
+            if (G1 && d.tail) {  // 32 gate rows, the matching 32 up rows, the next 32 of each
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int wr = d.wr0 + 64 * (int)rank + 32 * j;
+                tma_load_2d_pair(sw + j * (kBpHalf / 2), &tmW32, kb * 128, wr, fb0);
+                tma_load_2d_pair(sw + j * (kBpHalf / 2) + kBpHalf / 4, &tmW32, kb * 128, wr + p.w_pair_off, fb0);
+              }
+            } else {
+              tma_load_2d_pair(sw, &tmW, kb * 128, d.wr0 + (rank ? p.w_pair_off : 0), fb0);
+            }
+            if (d.tail)
+              tma_load_2d_pair(sw + kBpHalf, &tmX64, kb * 128, d.xrow + 64 * (int)rank, fb0);
+            else
+              tma_load_2d_pair(sw + kBpHalf, &tmX, kb * 128, d.xrow + 128 * (int)rank, fb0);
+          }
+          __syncwarp();
+          ++issued;
           if (++stage == kBpStages) {
             stage = 0;
             phase ^= 1u;
           }
-          buf ^= 1;
-          if (buf == 0) buf_phase ^= 1u;
         }
       }
-      if (!ok && any) {  // the tensor cores must be idle before tensor memory is freed
-        tc_commit_pair(bar_drain + 8 * h);
-        mbar_wait_drain(bar_drain + 8 * h, 0, 100000000ull);
-      }
-    }
-    __syncwarp();
-  } else {
-    // ---------------- scales (warp 3): products of row and weight scales, in chunks of K blocks ----------------
-    // (the fold's threads would wait for these loads: a row's scales lie kb_total floats from the
-    // next row's, so a warp's load touches 32 lines)
-    float2* ring = reinterpret_cast<float2*>(smem + kBpScale);
-    int chunk = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int t = pair; t < ntiles && ok; t += npairs) {
-      const BpTile d = bp_tile_at<EPI>(p, t);
-      for (int kc = 0; kc < p.kb_total; kc += kBpChunk) {
-        if (!mbar_wait_all(bar_sempty + 8 * chunk, phase ^ 1u, abort_flag, p.status)) {
-          ok = false;
-          break;
+      if (lane == 0) {
+        pdl_launch_dependents();
+        if (!ok && leader) {  // let the copies already in flight land before the CTA exits
+          const uint32_t first = issued > (uint32_t)kBpStages ? issued - kBpStages : 0u;
+          for (uint32_t i = first; i < issued; ++i)
+            mbar_wait_drain(bar_full + 8 * (i % kBpStages), (i / kBpStages) & 1u, 100000000ull);
         }
-        // 64 rows at a time: this warp shares its register budget with the other roles
+      }
+      __syncwarp();
+    } else if (warp < 3) {
+      // ---------------- MMA issuers (CTA 0): one thread for each half of a K block ----------------
+      // The thread's own instructions are the limit here: a satisfied wait takes about 70 cycles, the
+      // issue 90, and one thread doing both halves with its waits in turn took longer than the MMAs
+      // (600 to 1100 cycles a block for 545).  So each half has its thread, on different SM quarters,
+      // and both waits of a block are polled together.
+      if (leader && elect_one()) {
+        const uint32_t h = warp - 1;
+        const uint64_t a0 = sdesc_k_sw128(sbase + kBpHalf), b0 = sdesc_k_sw128(sbase + h * (kBpHalf / 2));
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, buf_phase = 0;
+        bool ok = true, any = false;
+        for (int t = pair; t < ntiles && ok; t += npairs) {
+          const uint32_t idesc = idesc_make(bp_tile_at<EPI>(p, t).tail ? 128 : 256, 128, true);
+          for (int kb = 0; kb < p.kb_total; ++kb) {
+            const uint32_t fb = bar_full + 8 * stage, eb = bar_tempty + 8 * (2 * buf + h);
+            const bool full = mbar_try_wait(fb, phase), free_buf = mbar_try_wait(eb, buf_phase ^ 1u);
+            if (!(full && free_buf)) {
+              ok = mbar_wait_one(fb, phase, abort_flag, p.status) &&
+                   mbar_wait_one(eb, buf_phase ^ 1u, abort_flag, p.status);
+              if (!ok) break;
+            }
+            tc_fence_after();
+            const uint64_t so = (uint64_t)(stage * (kBpStage >> 4));
+            tc_mma_pair_kblock(tmem_base + 256u * buf + 128u * h, a0 + so, b0 + so, idesc);
+            tc_commit_both(bar_tfull + 8 * (2 * buf + h));
+            tc_commit_both(bar_empty + 8 * stage);
+            any = true;
+            if (++stage == kBpStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            buf ^= 1;
+            if (buf == 0) buf_phase ^= 1u;
+          }
+        }
+        if (!ok && any) {  // the tensor cores must be idle before tensor memory is freed
+          tc_commit_pair(bar_drain + 8 * h);
+          mbar_wait_drain(bar_drain + 8 * h, 0, 100000000ull);
+        }
+      }
+      __syncwarp();
+    } else {
+      // ---------------- scales (warp 3): products of row and weight scales, in chunks of K blocks ----------------
+      // (the fold's threads would wait for these loads: a row's scales lie kb_total floats from the
+      // next row's, so a warp's load touches 32 lines)
+      float2* ring = reinterpret_cast<float2*>(smem + kBpScale);
+      int chunk = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = pair; t < ntiles && ok; t += npairs) {
+        const BpTile d = bp_tile_at<EPI>(p, t);
+        for (int kc = 0; kc < p.kb_total; kc += kBpChunk) {
+          if (!mbar_wait_all(bar_sempty + 8 * chunk, phase ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          // 64 rows at a time: this warp shares its register budget with the other roles
 #pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          const int r0 = bp_row<EPI>(d, rank, lane + 64 * hf), r1 = bp_row<EPI>(d, rank, lane + 64 * hf + 32);
-          const float* x0 = p.a_scale + (size_t)(EPI != BG_EPI_DENSE || r0 < p.T ? r0 : 0) * p.kb_total;
-          const float* x1 = p.a_scale + (size_t)(EPI != BG_EPI_DENSE || r1 < p.T ? r1 : 0) * p.kb_total;
-          const float *wa, *wb;
-          bp_scale_rows<EPI>(p, d, 64 * hf, wa, wb);
-          float v0[kBpChunk], v1[kBpChunk], a[kBpChunk], b[kBpChunk];
+          for (int hf = 0; hf < 2; ++hf) {
+            const int r0 = bp_row<EPI>(d, rank, lane + 64 * hf), r1 = bp_row<EPI>(d, rank, lane + 64 * hf + 32);
+            const float* x0 = p.a_scale + (size_t)(EPI != BG_EPI_DENSE || r0 < p.T ? r0 : 0) * p.kb_total;
+            const float* x1 = p.a_scale + (size_t)(EPI != BG_EPI_DENSE || r1 < p.T ? r1 : 0) * p.kb_total;
+            const float *wa, *wb;
+            bp_scale_rows<EPI>(p, d, 64 * hf, wa, wb);
+            float v0[kBpChunk], v1[kBpChunk], a[kBpChunk], b[kBpChunk];
 #pragma unroll
-          for (int i = 0; i < kBpChunk; ++i) {
-            const int kb = min(kc + i, p.kb_total - 1);
-            v0[i] = x0[kb];
-            v1[i] = x1[kb];
-            a[i] = wa[kb];
-            b[i] = wb[kb];
-          }
-          float2* dst = ring + chunk * (kBpChunk * 128) + 64 * hf + lane;
+            for (int i = 0; i < kBpChunk; ++i) {
+              const int kb = min(kc + i, p.kb_total - 1);
+              v0[i] = x0[kb];
+              v1[i] = x1[kb];
+              a[i] = wa[kb];
+              b[i] = wb[kb];
+            }
+            float2* dst = ring + chunk * (kBpChunk * 128) + 64 * hf + lane;
 #pragma unroll
-          for (int i = 0; i < kBpChunk; ++i) {
-            dst[i * 128] = make_float2(v0[i] * a[i], v0[i] * b[i]);
-            dst[i * 128 + 32] = make_float2(v1[i] * a[i], v1[i] * b[i]);
+            for (int i = 0; i < kBpChunk; ++i) {
+              dst[i * 128] = make_float2(v0[i] * a[i], v0[i] * b[i]);
+              dst[i * 128 + 32] = make_float2(v1[i] * a[i], v1[i] * b[i]);
+            }
           }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_sfull + 8 * chunk);
-        if (++chunk == kBpChunks) {
-          chunk = 0;
-          phase ^= 1u;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_sfull + 8 * chunk);
+          if (++chunk == kBpChunks) {
+            chunk = 0;
+            phase ^= 1u;
+          }
         }
       }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     setmaxnreg_inc<kBpEpiRegs>();
     // ---------------- epilogue (warps 4..11 of both CTAs) ----------------
@@ -1127,6 +1154,7 @@ cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
   p.sorted = a.sorted;
   p.eids = a.eids;
   p.meta = a.meta;
+  p.ids = a.ids;
   p.out = a.out;
   p.out_scale = a.out_scale;
   p.status = a.status;

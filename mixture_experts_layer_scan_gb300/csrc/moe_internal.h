@@ -85,6 +85,11 @@ cudaError_t launch_quant_block(const void* x, bool bf16, bool silu_form, int T, 
 // the same for bf16 x [T][K], each row written at the sorted rows of its k pairs (launch_align's inv)
 cudaError_t launch_quant_block_scatter(const void* x, int T, int K, int k, const int32_t* inv, uint8_t* q,
                                        float* scale, cudaStream_t s);
+constexpr int kAlignSmallPairs = 32;  // pairs that one warp sorts (moe_align.cuh)
+// launch_align (at most 32 pairs, block size B, no CTA-pair list) and launch_quant_block_scatter in one launch
+cudaError_t launch_align_quant_small(const void* x, int T, int K, int k, const int32_t* ids, int E, int B,
+                                     int32_t* sorted, int32_t* eids, int32_t* meta, int* status, bool skip_minus_one,
+                                     uint8_t* q, float* scale, cudaStream_t s);
 enum BlockGemmEpilogue {
   BG_EPI_DENSE = 0,  // out [T][n_out] bf16 or fp32
   BG_EPI_G1 = 1,     // expert GEMM1: SiLU(gate)*up -> e4m3 out [cap][I] + out_scale [cap][I/128]
@@ -109,6 +114,8 @@ struct BlockGemmArgs {
   const int32_t* eids;
   const int32_t* meta;
   const int32_t* pblk;
+  const int32_t* ids;     // swap-AB GEMM1, early: the routing of at most 32 pairs, from which each CTA derives the
+                          // tile list (eids and meta are not complete before the dependency wait); else null
   void* out;
   float* out_scale;
   int* status;

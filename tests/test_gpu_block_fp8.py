@@ -333,6 +333,17 @@ def test_forward_and_noalloc_route_themselves(moe):
     assert torch.equal(out, ref.cpu())
 
 
+def test_short_batch_routes_itself(moe):
+    d = make_experts(3, 512, 256, 8, 2, torch.Generator().manual_seed(6))
+    c = {n: v.cuda() for n, v in d.items()}
+    wr = (torch.randn(8, 512, generator=torch.Generator().manual_seed(7)) / 16).to(torch.bfloat16).cuda()
+    _, tw, ids = moe.moe_route(c["x"], wr, 2, True)
+    ref = moe.moe_forward_routed(c["x"], tw, ids, c["w13"], c["w2"], c["s13"], c["s2"], w_format="e4m3_block")
+    for _ in range(5):
+        out = moe.moe_forward(c["x"], wr, c["w13"], c["w2"], 2, True, c["s13"], c["s2"], w_format="e4m3_block")
+        assert torch.equal(out, ref)
+
+
 def test_expert_id_out_of_range_is_dropped_and_flagged(moe):
     for T in (9, 90):
         d = make_experts(T, 256, 128, 4, 2, torch.Generator().manual_seed(T))
@@ -355,6 +366,33 @@ def test_an_expert_named_twice_for_a_token(moe, T):
     out = moe.moe_forward_routed(c["x"], c["tw"], c["ids"], c["w13"], c["w2"], c["s13"], c["s2"], w_format="e4m3_block")
     assert moe.moe_get_status() == 0
     check(out, experts_reference(d), f"repeated experts T={T}")
+
+
+@pytest.mark.parametrize("T,k", [(32, 1), (16, 2), (17, 2), (10, 3), (11, 3), (4, 8), (5, 8), (1, 16)])
+@pytest.mark.parametrize("one", [False, True])
+def test_short_batches_around_32_pairs(moe, T, k, one):
+    """Up to 32 pairs are sorted by the launch that quantises them; one: all pairs at a single expert."""
+    d = make_experts(T, 384, 256, 19, k, torch.Generator().manual_seed(T * k))
+    if one:
+        d["ids"][:] = 7
+    c = {n: v.cuda() for n, v in d.items()}
+    out = moe.moe_forward_routed(c["x"], c["tw"], c["ids"], c["w13"], c["w2"], c["s13"], c["s2"], w_format="e4m3_block")
+    assert moe.moe_get_status() == 0
+    check(out, experts_reference(d), f"{T} x {k}")
+
+
+def test_a_short_batch_depends_on_no_other_call(moe):
+    """Calls of different batches back to back in one workspace: each reads its own routing."""
+    ds = [make_experts(T, 256, 128, 12, 4, torch.Generator().manual_seed(T)) for T in (2, 8, 1, 5)]
+    n = moe.moe_workspace_size(8, 256, 128, 12, 4, moe.MOE_BF16, moe.MOE_E4M3_B128)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    cs = [{n: v.cuda() for n, v in d.items()} for d in ds]
+    outs = [[moe.moe_forward_routed(c["x"], c["tw"], c["ids"], c["w13"], c["w2"], c["s13"], c["s2"], workspace=ws,
+                                    w_format="e4m3_block") for c in cs] for _ in range(20)]
+    assert moe.moe_get_status() == 0
+    for i, d in enumerate(ds):
+        check(outs[0][i], experts_reference(d), f"batch {i}")
+        assert all(torch.equal(o[i], outs[0][i]) for o in outs)
 
 
 def test_empty_batch(moe):
