@@ -369,7 +369,7 @@ def _check_block_scales(w_format, E, H, I, w13, w2, w13_scale, w2_scale) -> None
     if _dt(w13) != MOE_E4M3 or _dt(w2) != MOE_E4M3 or w13.shape != (E, 2 * I, H) or w2.shape != (E, H, I):
         raise ValueError("block-scaled weights must be e4m3 codes w13 [E, 2 I, H] and w2 [E, H, I]")
     for s, shape in ((w13_scale, (E, 2 * I // 128, H // 128)), (w2_scale, (E, H // 128, I // 128))):
-        if s is None or s.dtype != torch.float32 or tuple(s.shape) != shape:
+        if s is None or s.dtype != torch.float32 or s.shape != shape:
             raise ValueError(f"block scales must be float32 {shape}")
 
 

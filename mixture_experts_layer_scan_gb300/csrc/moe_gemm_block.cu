@@ -613,7 +613,7 @@ __device__ __forceinline__ void bp_fold32(float2* acc, const uint32_t (&r)[32], 
 
 // SiLU(g) * u for an intermediate that becomes e4m3 (4 significant bits) right away: the approximate
 // exponential and quotient are within a few 2^-22, and 64 of them per thread stand between two tiles.
-__device__ __forceinline__ float silu_mul_fast(float g, float u) { return __fdividef(g * u, 1.0f + __expf(-g)); }
+__device__ __forceinline__ float silu_mul_fast(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // 8 floats to 32-byte aligned global memory in one store
 __device__ __forceinline__ void st_global_v8(float* p, const float2* v) {

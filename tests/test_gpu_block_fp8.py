@@ -130,6 +130,21 @@ def test_silu_quant(moe, T, I, dtype):
     assert (np.abs(q - v) <= step / 2 + 2e-6 * np.abs(v)).all()
 
 
+def test_silu_quant_of_large_values(moe):
+    """The product is finite wherever its value is, gate and up of any size."""
+    x = torch.zeros(4, 256)
+    x[0, :128], x[0, 128:] = -20.0, 1e38  # g * u alone would overflow
+    x[1, :128], x[1, 128:] = 1e30, 1e-30
+    x[2, :128], x[2, 128:] = -200.0, 1e30  # SiLU is 0 in 32 bits
+    x[3, :128], x[3, 128:] = 90.0, -3.0
+    q, s = moe.moe_silu_quant_block(x.cuda())
+    got = q.float().cpu().double() * s.cpu().double()
+    g, u = x.double().split(128, 1)
+    ref = g / (1 + torch.exp(-g)) * u
+    ref[2] = 0
+    assert torch.allclose(got, ref, rtol=2 ** -4, atol=0)
+
+
 def test_quant_empty_and_far_offsets(moe):
     q, s = moe.moe_quant_block(torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"))
     assert q.shape == (0, 256) and s.shape == (0, 2)
