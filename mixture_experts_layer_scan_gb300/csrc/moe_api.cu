@@ -300,7 +300,8 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
     p.p1_stride = (size_t)n * 2 * I;
     p.o_p1 = take(p.p1_stride * p.s1 * 4);
   }
-  p.y_stride = (size_t)n * H;
+  // (block-scaled experts on CTA pairs leave their rows in expert order)
+  p.y_stride = (size_t)(p.path == PATH_BLK && p.pair ? p.cap : n) * H;
   p.o_y = take(p.y_stride * p.s2 * (p.y_bf16 ? 2 : 4));
   p.o_misc = take(256);
   if (p.pair) p.o_pblk = take((size_t)std::max<long>(p.nblk_cap, 1) * 4);
@@ -707,7 +708,7 @@ combine_step:
   // 7. combine
   if (o) record(o->stage_begin[MOE_STAGE_COMBINE], s);
   MOE_TRY(launch_combine(y, pl.y_bf16 ? 1 : 0, pl.s2, pl.y_stride, tw, T, topk, H, out, act_dtype == MOE_BF16 ? 1 : 0,
-                         s));
+                         s, pl.path == PATH_BLK && pl.pair ? inv : nullptr));
   if (o) record(o->stage_end[MOE_STAGE_COMBINE], s);
 #undef MOE_TRY
   return MOE_OK;

@@ -50,7 +50,8 @@ struct BgDev {
   int cl;               // CTAs of a cluster that share a tile's K blocks (1, 2, 4, 8)
   int kb_per;           // K blocks of one of them
   int early;            // the tile list and the weights may be read before the dependency wait
-  int out_v8;           // rows of out are 32-byte aligned
+  int out_tma;          // CTA pairs: rows of out are whole 16-byte units
+  int out_rows;         // rows of out
   uint32_t stage_bytes, bar_off, scale_off, out_off, list_off;
   const float* a_scale;  // [rows][kb_total]
   const float* w_scale;  // [E][w_scale_rows][kb_total]
@@ -144,7 +145,7 @@ __device__ __forceinline__ void bg_store_row(const BgDev& p, const BgTile& d, co
     if (f >= p.T * p.k) return;
     const size_t o = (size_t)f * p.n_out + (size_t)d.n * 256 + 4 * lane;
     const bool second = d.n * 256 + 128 < p.n_out;
-    if (p.out_bf16) {  // (as bp_store)
+    if (p.out_bf16) {  // (as k_gemm_block_pair)
       uint2* y = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o);
       y[0] = make_uint2(pack_bf16x2(v0.x, v0.y), pack_bf16x2(v0.z, v0.w));
       if (second) y[32] = make_uint2(pack_bf16x2(v1.x, v1.y), pack_bf16x2(v1.z, v1.w));
@@ -566,10 +567,12 @@ cudaError_t launch_bg_nt(const CUtensorMap& mw, const CUtensorMap& mx, const BgD
 // rows from shared memory twice, which costs less than waiting).
 constexpr int kBpThreads = 384;                 // 4 warps of roles, 8 epilogue warps
 constexpr int kBpRoleRegs = 72, kBpEpiRegs = 216;  // 72 + 2 * 216 = 3 * 168, the launch's registers
-constexpr int kBpStages = 6;
+constexpr int kBpStages = 5;                    // (as fast as 6; the rows on their way out take the room)
 constexpr uint32_t kBpHalf = 128u * 128u;       // bytes of a 128-row box of one K block
 constexpr uint32_t kBpStage = 2u * kBpHalf;     // this CTA's weight box and token rows
-constexpr uint32_t kBpRed = kBpStages * kBpStage;  // [2][256] block maxima of the epilogue halves
+constexpr uint32_t kBpOut = kBpStages * kBpStage;   // [8 warps][32 rows][128 bytes] output rows on their way
+constexpr uint32_t kBpOutWarp = 32 * 128;
+constexpr uint32_t kBpRed = kBpOut + 8 * kBpOutWarp;  // [2][256] block maxima of the epilogue halves
 constexpr int kBpChunk = 4;                     // K blocks of one scale chunk
 constexpr int kBpChunks = 4;                    // scale chunks in the ring (a power of two)
 constexpr uint32_t kBpScale = kBpRed + 2 * 256 * 4;  // [chunk][block][128 rows] (scale of run a, of run b)
@@ -615,68 +618,51 @@ __device__ __forceinline__ void bp_fold32(float2* acc, const uint32_t (&r)[32], 
 // exponential and quotient are within a few 2^-22, and 64 of them per thread stand between two tiles.
 __device__ __forceinline__ float silu_mul_fast(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-// 8 floats to 32-byte aligned global memory in one store
-__device__ __forceinline__ void st_global_v8(float* p, const float2* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0].x), "f"(v[0].y),
-               "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
-               : "memory");
+// A warp's 32 rows (one to a lane) x 128 bytes from column col on, through shared memory by one TMA store:
+// get(i) is columns 2i and 2i + 1 of the lane's row from there.  A lane's own stores, a row each, reach 32
+// lines whatever their width, and until they were out the next tile's folds waited (32-byte stores took 15 us
+// of 119 for 8192 x 4096 x 4096, 105 of 577 for 65536 expert rows of the same width; TMA_NOW).  Rows and
+// columns past the end of out are clipped by the tensor map.
+template <bool BF16, class Get>
+__device__ __forceinline__ void bp_store_box(const BgDev& p, const CUtensorMap* tm, uint32_t buf, int lane, int row0,
+                                             int col, Get get) {
+  if (row0 >= p.out_rows || col >= p.n_out) return;  // (the same for the whole warp)
+  if (lane == 0) bulk_wait_read();  // the rows stored before have left the buffer
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint4 v;
+    if constexpr (BF16) {
+      v = make_uint4(pack_bf16x2(get(4 * c).x, get(4 * c).y), pack_bf16x2(get(4 * c + 1).x, get(4 * c + 1).y),
+                     pack_bf16x2(get(4 * c + 2).x, get(4 * c + 2).y), pack_bf16x2(get(4 * c + 3).x, get(4 * c + 3).y));
+    } else {
+      v = make_uint4(__float_as_uint(get(2 * c).x), __float_as_uint(get(2 * c).y), __float_as_uint(get(2 * c + 1).x),
+                     __float_as_uint(get(2 * c + 1).y));
+    }
+    sts_v4(buf + lane * 128u + (uint32_t)((c ^ (lane & 7)) << 4), v);  // (the map's 128-byte swizzle)
+  }
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(tm, buf, BF16 ? col : 2 * col, row0);  // (fp32 rows as pairs of 16-bit elements)
+    bulk_commit();
+  }
 }
 
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
-// A thread's 2 * PAIRS consecutive output columns from column n of one row.  A warp's lanes hold
-// different rows, so a store reaches 32 lines whatever its width: 32 bytes a lane, whole sectors.
-// GEMM2's rows leave as bf16: the outputs of a token's experts are rounded once more before their
-// fp32 sum, about 2^-9 of each, below the 2^-4 steps of the e4m3 intermediate they come from, and
-// their 2 bytes instead of 4 take 0.2 ms off a layer of 8192 tokens (stores, and the combine's reads).
-template <int EPI, int PAIRS>
+// A thread's 2 * PAIRS consecutive output columns from column n of one row that is no whole 16-byte units.
+template <int PAIRS>
 __device__ __forceinline__ void bp_store(const BgDev& p, size_t row, int n, const float2* acc) {
   const size_t o = row * (size_t)p.n_out + n;
-  if (EPI == BG_EPI_G2 || (p.out_bf16 && p.out_v8)) {
-    uint16_t* y = static_cast<uint16_t*>(p.out) + o;
 #pragma unroll
-    for (int i = 0; i < PAIRS; i += 8) {
-      if (n + 2 * i >= p.n_out) continue;
-      uint32_t v[8];
+  for (int i = 0; i < PAIRS; ++i) {
+    const float v[2] = {acc[i].x, acc[i].y};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = pack_bf16x2(acc[i + j].x, acc[i + j].y);
-      st_global_v8(y + 2 * i, v);
-    }
-  } else if (!p.out_bf16 && p.out_v8) {
-    float* y = static_cast<float*>(p.out) + o;
-#pragma unroll
-    for (int i = 0; i < PAIRS; i += 4)
-      if (n + 2 * i < p.n_out) st_global_v8(y + 2 * i, acc + i);
-  } else if (!p.out_bf16 && p.n_out % 4 == 0) {
-    float* y = static_cast<float*>(p.out) + o;
-#pragma unroll
-    for (int i = 0; i < PAIRS; i += 2)
-      if (n + 2 * i < p.n_out)
-        *reinterpret_cast<float4*>(y + 2 * i) = make_float4(acc[i].x, acc[i].y, acc[i + 1].x, acc[i + 1].y);
-  } else if (p.out_bf16 && p.n_out % 8 == 0) {
-    uint16_t* y = static_cast<uint16_t*>(p.out) + o;
-#pragma unroll
-    for (int i = 0; i < PAIRS; i += 4)
-      if (n + 2 * i < p.n_out)
-        *reinterpret_cast<uint4*>(y + 2 * i) =
-            make_uint4(pack_bf16x2(acc[i].x, acc[i].y), pack_bf16x2(acc[i + 1].x, acc[i + 1].y),
-                       pack_bf16x2(acc[i + 2].x, acc[i + 2].y), pack_bf16x2(acc[i + 3].x, acc[i + 3].y));
-  } else {
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-      const float v[2] = {acc[i].x, acc[i].y};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (n + 2 * i + h >= p.n_out) continue;
-        if (p.out_bf16)
-          static_cast<__nv_bfloat16*>(p.out)[o + 2 * i + h] = __float2bfloat16_rn(v[h]);
-        else
-          static_cast<float*>(p.out)[o + 2 * i + h] = v[h];
-      }
+    for (int h = 0; h < 2; ++h) {
+      if (n + 2 * i + h >= p.n_out) continue;
+      if (p.out_bf16)
+        static_cast<__nv_bfloat16*>(p.out)[o + 2 * i + h] = __float2bfloat16_rn(v[h]);
+      else
+        static_cast<float*>(p.out)[o + 2 * i + h] = v[h];
     }
   }
 }
@@ -782,7 +768,7 @@ template <int EPI>
 __global__ void __launch_bounds__(kBpThreads, 1)
     k_gemm_block_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                       const __grid_constant__ CUtensorMap tmW32, const __grid_constant__ CUtensorMap tmX64,
-                      const BgDev p) {
+                      const __grid_constant__ CUtensorMap tmO, const BgDev p) {
   constexpr bool G1 = EPI == BG_EPI_G1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -822,6 +808,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW32);
     tma_prefetch_desc(&tmX64);
+    if (!G1) tma_prefetch_desc(&tmO);
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
   tc_fence_before();
@@ -1008,7 +995,6 @@ __global__ void __launch_bounds__(kBpThreads, 1)
       const int hf = d.tail ? lrow >> 6 : 0;
       const int row = bp_row<EPI>(d, rank, lrow);
       const int wide = d.tail ? 32 : 64;
-      const bool row_ok = EPI != BG_EPI_DENSE || row < p.T;
       float* red = reinterpret_cast<float*>(smem + kBpRed);
       if constexpr (G1) {
         // SiLU(gate) * up of `wide` columns, the block's maximum over the two (tail: four) threads
@@ -1046,26 +1032,46 @@ __global__ void __launch_bounds__(kBpThreads, 1)
           }
           if (h == 0 && hf == 0) p.out_scale[(size_t)row * (p.n_out / 128) + d.n] = s;
         }
-      } else if (f.ok && row_ok) {
-        const int n = d.n * 256 + 128 * hf + 64 * h;  // columns of box 0 (tail: of box hf)
-        size_t orow = (size_t)row;
-        bool store = true;
-        if constexpr (EPI == BG_EPI_G2) {
-          const int f = p.sorted[row];
-          store = f < p.T * p.k;
-          orow = (size_t)f;
-        }
-        if (store) {
-          if (!d.tail) {
-            bp_store<EPI, 32>(p, orow, n, acca);
-            bp_store<EPI, 32>(p, orow, n + 128, accb);
+      } else if (p.out_tma) {
+        // GEMM2's rows stay in expert order (the combine finds them through the inverse map) and leave as
+        // bf16: the outputs of a token's experts are rounded once more before their fp32 sum, about 2^-9 of
+        // each, below the 2^-4 steps of the e4m3 intermediate they come from, for half the bytes written
+        // here and read by the combine (0.2 ms of a layer of 8192 tokens).
+        if (__all_sync(0xffffffffu, f.ok)) {
+          const uint32_t buf = sbase + kBpOut + (uint32_t)(tid >> 5) * kBpOutWarp;
+          const int lane_ = tid & 31, row0 = row - lane_;
+          const int n = d.n * 256 + 128 * hf + 64 * h;  // columns of box 0 (tail: of box hf)
+          if (EPI == BG_EPI_G2 || p.out_bf16) {
+            if (!d.tail) {
+              bp_store_box<true>(p, &tmO, buf, lane_, row0, n, [&](int i) { return acca[i]; });
+              bp_store_box<true>(p, &tmO, buf, lane_, row0, n + 128, [&](int i) { return accb[i]; });
+            } else {
+              bp_store_box<true>(p, &tmO, buf, lane_, row0, n,
+                                 [&](int i) { return i < 16 ? acca[i & 15] : accb[i & 15]; });
+            }
           } else {
-            bp_store<EPI, 16>(p, orow, n, acca);
-            bp_store<EPI, 16>(p, orow, n + 32, accb);
+            bp_store_box<false>(p, &tmO, buf, lane_, row0, n, [&](int i) { return acca[i]; });
+            if (!d.tail) {
+              bp_store_box<false>(p, &tmO, buf, lane_, row0, n + 32, [&](int i) { return acca[16 + i]; });
+              bp_store_box<false>(p, &tmO, buf, lane_, row0, n + 128, [&](int i) { return accb[i]; });
+              bp_store_box<false>(p, &tmO, buf, lane_, row0, n + 160, [&](int i) { return accb[16 + i]; });
+            } else {
+              bp_store_box<false>(p, &tmO, buf, lane_, row0, n + 32, [&](int i) { return accb[i]; });
+            }
           }
+        }
+      } else if (EPI == BG_EPI_DENSE && f.ok && row < p.T) {
+        const int n = d.n * 256 + 128 * hf + 64 * h;
+        if (!d.tail) {
+          bp_store<32>(p, (size_t)row, n, acca);
+          bp_store<32>(p, (size_t)row, n + 128, accb);
+        } else {
+          bp_store<16>(p, (size_t)row, n, acca);
+          bp_store<16>(p, (size_t)row, n + 32, accb);
         }
       }
     }
+    if (!G1 && lane == 0) bulk_wait_all();  // no row is on its way when the CTA ends
   }
 
   // Both CTAs finish every role (and with it every read of the other CTA's shared memory or tensor
@@ -1080,7 +1086,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
 // Clusters of 2 on a persistent grid of as many pairs as are resident at once.
 template <int EPI>
 cudaError_t launch_bp(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& mw32, const CUtensorMap& mx64,
-                      const BgDev& p, long tiles, cudaStream_t s) {
+                      const CUtensorMap& mo, const BgDev& p, long tiles, cudaStream_t s) {
   static bool attr_set[64] = {};
   static int max_clusters[64] = {};
   int dev = 0;
@@ -1116,7 +1122,7 @@ cudaError_t launch_bp(const CUtensorMap& mw, const CUtensorMap& mx, const CUtens
   }
   if (max_clusters[dev] < 1) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3(2 * (unsigned)std::max<long>(1, std::min<long>(tiles, max_clusters[dev])));
-  return cudaLaunchKernelEx(&cfg, kern, mw, mx, mw32, mx64, p);
+  return cudaLaunchKernelEx(&cfg, kern, mw, mx, mw32, mx64, mo, p);
 }
 
 }  // namespace
@@ -1148,7 +1154,7 @@ cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
   }
   p.out_bf16 = a.out_bf16 ? 1 : 0;
   p.early = a.early ? 1 : 0;
-  p.out_v8 = a.n_out % (a.out_bf16 ? 16 : 8) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+  p.out_rows = (int)x_rows;
   p.a_scale = a.a_scale;
   p.w_scale = a.w_scale;
   p.sorted = a.sorted;
@@ -1159,16 +1165,22 @@ cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
   p.out_scale = a.out_scale;
   p.status = a.status;
   if (a.pair) {
-    CUtensorMap mw32, mx64;
+    CUtensorMap mw32, mx64, mo = {};
     if (!make_tensor_map_2d(&mw32, a.w, 1, (uint64_t)a.K, (uint64_t)a.E * a.w_rows, 32u) ||
         !make_tensor_map_2d(&mx64, a.x, 1, (uint64_t)a.K, x_rows, 64u))
       return cudaErrorInvalidValue;
     p.pblk = a.pblk;
+    if (a.epi != BG_EPI_G1) {
+      p.out_tma = (long)a.n_out * (a.out_bf16 ? 2 : 4) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+      if (!p.out_tma && a.epi == BG_EPI_G2) return cudaErrorInvalidValue;
+      if (p.out_tma && !make_tensor_map_2d(&mo, a.out, 2, (uint64_t)a.n_out * (a.out_bf16 ? 1 : 2), x_rows, 32u))
+        return cudaErrorInvalidValue;
+    }
     if (a.epi == BG_EPI_DENSE)
-      return launch_bp<BG_EPI_DENSE>(mw, mx, mw32, mx64, p, ((long)a.T + 255) / 256 * p.n_tiles, s);
+      return launch_bp<BG_EPI_DENSE>(mw, mx, mw32, mx64, mo, p, ((long)a.T + 255) / 256 * p.n_tiles, s);
     const long tiles = (long)(a.cap / 128) * p.n_tiles;
-    if (a.epi == BG_EPI_G1) return launch_bp<BG_EPI_G1>(mw, mx, mw32, mx64, p, tiles, s);
-    return launch_bp<BG_EPI_G2>(mw, mx, mw32, mx64, p, tiles, s);
+    if (a.epi == BG_EPI_G1) return launch_bp<BG_EPI_G1>(mw, mx, mw32, mx64, mo, p, tiles, s);
+    return launch_bp<BG_EPI_G2>(mw, mx, mw32, mx64, mo, p, tiles, s);
   }
   if (a.epi == BG_EPI_DENSE) {
     const long tiles = ((long)a.T + a.nt - 1) / a.nt * p.n_tiles;

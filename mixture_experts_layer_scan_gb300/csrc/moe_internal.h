@@ -72,7 +72,7 @@ cudaError_t launch_quant_act(const float* A, int I, const int32_t* meta, int cap
                              uint8_t* Aq, cudaStream_t s);
 // out[t] = sum_j w[t][j] * sum_s Y[s][t*k+j]   (Y fp32 or bf16, out fp32 or bf16)
 cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_stride, const float* w, int T, int k,
-                           int H, void* out, int out_bf16, cudaStream_t s);
+                           int H, void* out, int out_bf16, cudaStream_t s, const int32_t* inv = nullptr);
 // lanes G that share one output vector in the combine (H % 8 == 0); fixes its addition order
 int combine_lanes(int T, int H, int k);
 

@@ -678,17 +678,18 @@ __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, in
 }
 
 // out[t] = sum_j w[t][j] * Y[t*k + j] for bf16 rows without K splits (the block-scaled expert layer):
-// j in order, fp32, one rounding at the end.  Bound by HBM (2 k + 2 bytes per output element): each
+// j in order, fp32, one rounding at the end.  inv (nullable): Y is in expert order, inv[t*k + j] the row, -1
+// for a pair left out.  Bound by HBM (2 k + 2 bytes per output element): each
 // thread loads its 8 columns of up to 8 rows before their use, with no index arithmetic between them
 // (the general kernel's per-row divisions made it 209 us for 65536 x 4096 rows).
 constexpr int kCombineRows = 8;
-__global__ void __launch_bounds__(256) k_combine_bf16(const uint4* __restrict__ Y, const float* __restrict__ w, int T,
-                                                      int k, int vec_per_row, uint4* __restrict__ out) {
+__global__ void __launch_bounds__(256) k_combine_bf16(const uint4* __restrict__ Y, const float* __restrict__ w,
+                                                      const int32_t* __restrict__ inv, int T, int k, int vec_per_row,
+                                                      uint4* __restrict__ out) {
   pdl_enter();
   const int v = blockIdx.y * 256 + threadIdx.x;
   if (v >= vec_per_row) return;
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    const uint4* y = Y + (size_t)t * k * vec_per_row + v;
     const float* wt = w + (size_t)t * k;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int j0 = 0; j0 < k; j0 += kCombineRows) {
@@ -696,8 +697,10 @@ __global__ void __launch_bounds__(256) k_combine_bf16(const uint4* __restrict__ 
       float wj[kCombineRows];
 #pragma unroll
       for (int j = 0; j < kCombineRows; ++j) {
-        const bool in = j0 + j < k;
-        u[j] = in ? __ldcs(y + (size_t)(j0 + j) * vec_per_row) : make_uint4(0, 0, 0, 0);
+        const int f = t * k + j0 + j;
+        const int row = j0 + j < k ? (inv ? inv[f] : f) : -1;
+        const bool in = row >= 0;
+        u[j] = in ? __ldcs(Y + (size_t)row * vec_per_row + v) : make_uint4(0, 0, 0, 0);
         wj[j] = in ? wt[j0 + j] : 0.0f;
       }
 #pragma unroll
@@ -882,11 +885,12 @@ static cudaError_t combine_vec(const void* Y, int splits, size_t split_stride, c
 }
 
 cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_stride, const float* w, int T, int k,
-                           int H, void* out, int out_bf16, cudaStream_t s) {
+                           int H, void* out, int out_bf16, cudaStream_t s, const int32_t* inv) {
+  if (inv && !(y_bf16 && out_bf16 && splits == 1 && H % 8 == 0)) return cudaErrorInvalidValue;
   if (y_bf16 && out_bf16 && splits == 1 && H % 8 == 0) {
     const int vpr = H / 8, cols = (vpr + 255) / 256;
     MOE_LAUNCH(k_combine_bf16, dim3(std::min(T, std::max(1, 152 * 16 / cols)), cols), dim3(256), 0, s, (const uint4*)Y, w,
-               T, k, vpr, (uint4*)out);
+               inv, T, k, vpr, (uint4*)out);
     return cudaGetLastError();
   }
   if (H % 8 == 0) {
