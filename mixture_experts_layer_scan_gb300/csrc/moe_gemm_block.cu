@@ -618,11 +618,19 @@ __device__ __forceinline__ void bp_fold32(float2* acc, const uint32_t (&r)[32], 
 // exponential and quotient are within a few 2^-22, and 64 of them per thread stand between two tiles.
 __device__ __forceinline__ float silu_mul_fast(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
+// 32 bytes, 32-byte aligned, in one store
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // A warp's 32 rows (one to a lane) x 128 bytes from column col on, through shared memory by one TMA store:
 // get(i) is columns 2i and 2i + 1 of the lane's row from there.  A lane's own stores, a row each, reach 32
-// lines whatever their width, and until they were out the next tile's folds waited (32-byte stores took 15 us
-// of 119 for 8192 x 4096 x 4096, 105 of 577 for 65536 expert rows of the same width; TMA_NOW).  Rows and
-// columns past the end of out are clipped by the tensor map.
+// lines whatever their width, and until they were out the next tile's folds waited: with 32-byte stores
+// 8192 x 4096 x 4096 took 119.5 us (this way 111), an expert GEMM2 of 65536 rows 577 us (500); a second
+// buffer for a stage of the ring gains 1 % there and loses 4 % where weights are streamed.  Rows and columns
+// past the end of out are clipped by the tensor map.
 template <bool BF16, class Get>
 __device__ __forceinline__ void bp_store_box(const BgDev& p, const CUtensorMap* tm, uint32_t buf, int lane, int row0,
                                              int col, Get get) {
@@ -808,7 +816,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW32);
     tma_prefetch_desc(&tmX64);
-    if (!G1) tma_prefetch_desc(&tmO);
+    tma_prefetch_desc(&tmO);
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
   tc_fence_before();
@@ -1016,22 +1024,36 @@ __global__ void __launch_bounds__(kBpThreads, 1)
         par ^= 1;  // (the other half of red: a slower warp may still read this one)
         const float s = block_scale_from_amax(a);
         const float r = 1.0f / s;
-        if (f.ok) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (size_t)row * p.n_out +
-                                                (size_t)d.n * 128 + 64 * hf + wide * h);
+        if (!d.tail && __all_sync(0xffffffffu, f.ok)) {
+          // 32 rows x 64 bytes of a warp by one TMA store, as bp_store_box
+          const int lane_ = tid & 31;
+          const uint32_t buf = sbase + kBpOut + (uint32_t)(tid >> 5) * kBpOutWarp;
+          if (lane_ == 0) bulk_wait_read();
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            if (i < wide / 2) {
-              uint32_t c[4];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                c[j] = pack_e4m3x4(acca[i + 2 * j].x * r, acca[i + 2 * j].y * r, acca[i + 2 * j + 1].x * r,
-                                   acca[i + 2 * j + 1].y * r);
-              dst[i / 8] = make_uint4(c[0], c[1], c[2], c[3]);
-            }
+            for (int j = 0; j < 4; ++j)
+              w[j] = pack_e4m3x4(acca[8 * c + 2 * j].x * r, acca[8 * c + 2 * j].y * r, acca[8 * c + 2 * j + 1].x * r,
+                                 acca[8 * c + 2 * j + 1].y * r);
+            sts_v4(buf + lane_ * 64u + (uint32_t)((c ^ ((lane_ >> 1) & 3)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
           }
-          if (h == 0 && hf == 0) p.out_scale[(size_t)row * (p.n_out / 128) + d.n] = s;
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane_ == 0) {
+            tma_store_2d(&tmO, buf, d.n * 128 + 64 * h, row - lane_);
+            bulk_commit();
+          }
+        } else if (d.tail && f.ok) {
+          uint8_t* dst = static_cast<uint8_t*>(p.out) + (size_t)row * p.n_out + (size_t)d.n * 128 + 64 * hf + 32 * h;
+          uint32_t c[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            c[j] = pack_e4m3x4(acca[2 * j].x * r, acca[2 * j].y * r, acca[2 * j + 1].x * r, acca[2 * j + 1].y * r);
+          st_global_v8(dst, c);
         }
+        if (f.ok && h == 0 && hf == 0) p.out_scale[(size_t)row * (p.n_out / 128) + d.n] = s;
       } else if (p.out_tma) {
         // GEMM2's rows stay in expert order (the combine finds them through the inverse map) and leave as
         // bf16: the outputs of a token's experts are rounded once more before their fp32 sum, about 2^-9 of
@@ -1071,7 +1093,7 @@ __global__ void __launch_bounds__(kBpThreads, 1)
         }
       }
     }
-    if (!G1 && lane == 0) bulk_wait_all();  // no row is on its way when the CTA ends
+    if (lane == 0) bulk_wait_all();  // no row is on its way when the CTA ends
   }
 
   // Both CTAs finish every role (and with it every read of the other CTA's shared memory or tensor
@@ -1170,7 +1192,9 @@ cudaError_t launch_gemm_block(const BlockGemmArgs& a, cudaStream_t s) {
         !make_tensor_map_2d(&mx64, a.x, 1, (uint64_t)a.K, x_rows, 64u))
       return cudaErrorInvalidValue;
     p.pblk = a.pblk;
-    if (a.epi != BG_EPI_G1) {
+    if (a.epi == BG_EPI_G1) {
+      if (!make_tensor_map_2d(&mo, a.out, 1, (uint64_t)a.n_out, x_rows, 32u, 64u)) return cudaErrorInvalidValue;
+    } else {
       p.out_tma = (long)a.n_out * (a.out_bf16 ? 2 : 4) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
       if (!p.out_tma && a.epi == BG_EPI_G2) return cudaErrorInvalidValue;
       if (p.out_tma && !make_tensor_map_2d(&mo, a.out, 2, (uint64_t)a.n_out * (a.out_bf16 ? 1 : 2), x_rows, 32u))
