@@ -14,7 +14,9 @@
 // each (two 16-byte loads of bf16, one 16-byte store, the block's maximum in three shuffles), and every
 // lane loads kUnroll blocks before it works on the first: with 8 elements a lane and one block at a time
 // too few bytes were in flight (8192 x 4096 bf16: 28.9 us, 3.5 TB/s; now 15.4 us, 6.6 TB/s).  The SiLU
-// form is bound by the instructions of its exponential and conversions (4099 x 2048: 8.3 us, 5.1 TB/s).
+// form is bound by the instructions of its exponential and quotient (4099 x 2048: 10.7 us, 3.9 TB/s, 70 %
+// of the issue slots).  An approximate quotient takes 8.3 us and moves four times as many codes that lie
+// on a border as the arithmetic in 32 bits does by itself: not taken.
 #include <algorithm>
 
 #include "moe_align.cuh"
@@ -58,11 +60,6 @@ struct Raw16 {
     return bf16_bits_to_f32((i & 1) ? (u >> 16) : (u & 0xffffu));
   }
 };
-
-// SiLU(g) * u with an approximate quotient (2 ulp, for an e4m3 code of 4 significant bits): the IEEE
-// division took a fifth of the form's time (4099 x 2048: 10.7 us).  Below g = -87.3 it returns 0 for what
-// is less than 2^-119 u.
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
 
 // A lane's 16 values of a block that 8 lanes share: the block's scale and the lane's codes.
 template <typename Get>
@@ -123,7 +120,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_quant_block(const QuantDev p)
       float s;
       const uint4 code = quantise16(
           [&](int j) {
-            if constexpr (SILU) return silu_mul(ra[i].get(j), rb[i].get(j));
+            if constexpr (SILU) return silu(ra[i].get(j)) * rb[i].get(j);
             return ra[i].get(j);
           },
           s);
