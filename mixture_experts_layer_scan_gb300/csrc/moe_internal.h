@@ -71,6 +71,7 @@ cudaError_t launch_quant_x(const void* X, size_t n, const unsigned* amax_bits, u
 cudaError_t launch_quant_act(const float* A, int I, const int32_t* meta, int cap, const unsigned* amax_bits,
                              uint8_t* Aq, cudaStream_t s);
 // out[t] = sum_j w[t][j] * sum_s Y[s][t*k+j]   (Y fp32 or bf16, out fp32 or bf16)
+// inv (bf16 Y without splits): Y is in expert order, inv[t * k + j] the row of a pair, -1 for none
 cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_stride, const float* w, int T, int k,
                            int H, void* out, int out_bf16, cudaStream_t s, const int32_t* inv = nullptr);
 // lanes G that share one output vector in the combine (H % 8 == 0); fixes its addition order
@@ -116,7 +117,7 @@ struct BlockGemmArgs {
   const int32_t* pblk;
   const int32_t* ids;     // swap-AB GEMM1, early: the routing of at most 32 pairs, from which each CTA derives the
                           // tile list (eids and meta are not complete before the dependency wait); else null
-  void* out;
+  void* out;              // GEMM2: rows in pair order; on CTA pairs [cap][n_out] in expert order
   float* out_scale;
   int* status;
   int num_sms;
