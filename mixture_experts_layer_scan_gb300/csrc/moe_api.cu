@@ -706,10 +706,12 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
   if (!(steps & STEPS_COMBINE)) return MOE_OK;
 
 combine_step:
-  // 7. combine
+  // 7. combine.  Only a caller's own routing can hold ids without an expert, whose pairs have no row: the
+  // router's ids are in range, and in a call of several passes (skip_minus_one) every row is some pass's.
   if (o) record(o->stage_begin[MOE_STAGE_COMBINE], s);
   MOE_TRY(launch_combine(y, pl.y_bf16 ? 1 : 0, pl.s2, pl.y_stride, tw, T, topk, H, out, act_dtype == MOE_BF16 ? 1 : 0,
-                         s, pl.path == PATH_BLK && pl.pair ? inv : nullptr));
+                         s, pl.path == PATH_BLK && pl.pair ? inv : nullptr,
+                         tid_in && !skip_minus_one ? tid : nullptr, E));
   if (o) record(o->stage_end[MOE_STAGE_COMBINE], s);
 #undef MOE_TRY
   return MOE_OK;

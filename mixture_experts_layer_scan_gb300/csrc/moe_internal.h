@@ -72,8 +72,10 @@ cudaError_t launch_quant_act(const float* A, int I, const int32_t* meta, int cap
                              uint8_t* Aq, cudaStream_t s);
 // out[t] = sum_j w[t][j] * sum_s Y[s][t*k+j]   (Y fp32 or bf16, out fp32 or bf16)
 // inv (bf16 Y without splits): Y is in expert order, inv[t * k + j] the row of a pair, -1 for none
+// ids [T][k] (nullable, Y in pair order): pairs whose id is outside [0, E) have no row and add nothing
 cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_stride, const float* w, int T, int k,
-                           int H, void* out, int out_bf16, cudaStream_t s, const int32_t* inv = nullptr);
+                           int H, void* out, int out_bf16, cudaStream_t s, const int32_t* inv = nullptr,
+                           const int32_t* ids = nullptr, int E = 0);
 // lanes G that share one output vector in the combine (H % 8 == 0); fixes its addition order
 int combine_lanes(int T, int H, int k);
 

@@ -590,6 +590,10 @@ __global__ void k_quant_act(const float4* __restrict__ A, int vec_per_row, const
 // then the k routed outputs accumulated in j order, fp32, one rounding at the
 // end.  8 consecutive h per thread; the loads of four (j, s) rows are issued
 // before their use so each thread keeps 8 x 16 bytes in flight.
+__device__ __forceinline__ bool pair_kept(const int32_t* __restrict__ ids, size_t f, int E) {
+  return !ids || (unsigned)ids[f] < (unsigned)E;
+}
+
 template <bool Y_BF16>
 __device__ __forceinline__ void load8(const void* Yv, size_t idx, float (&y)[8]) {
   if constexpr (Y_BF16) {
@@ -612,10 +616,13 @@ __device__ __forceinline__ void load8(const void* Yv, size_t idx, float (&y)[8])
 // slots j = g, g+G, ... (each one the sum of its K-split partials, in split
 // order), then the G partial sums are added in a fixed butterfly.  The order of
 // every addition is fixed, so the result is the same on every run.
+// ids (nullable): a routing given by a caller.  A pair whose id is outside [0, E) was dropped from the
+// permutation, nothing wrote its row, and it adds nothing here.  (Its row is loaded all the same: it lies
+// in Y, and the row's load then does not wait for the id's.)
 template <bool Y_BF16, bool OUT_BF16, int G>
 __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, int splits, size_t split_stride,
-                                                 const float* __restrict__ w, int T, int k, int H,
-                                                 void* __restrict__ out) {
+                                                 const float* __restrict__ w, const int32_t* __restrict__ ids,
+                                                 int E, int T, int k, int H, void* __restrict__ out) {
   pdl_enter();
   const int hv = H / 8;
   const size_t total = (size_t)T * hv * G;  // a multiple of G: groups never straddle the tail
@@ -629,11 +636,13 @@ __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, in
     const int rows = ((k - g + G - 1) / G) * splits;
     for (int r0 = 0; r0 < rows; r0 += 4) {
       float y[4][8];
+      bool has[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int r = r0 + q;
         if (r < rows) {
           const int j = g + (r / splits) * G, sp = r % splits;
+          has[q] = pair_kept(ids, (size_t)t * k + j, E);
           load8<Y_BF16>(Yv, (size_t)sp * split_stride + ((size_t)t * k + j) * H + h, y[q]);
         }
       }
@@ -642,9 +651,9 @@ __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, in
         const int r = r0 + q;
         if (r < rows) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) yj[c] += y[q][c];
+          for (int c = 0; c < 8; ++c) yj[c] += has[q] ? y[q][c] : 0.f;
           if (r % splits == splits - 1) {
-            const float wj = w[(size_t)t * k + g + (r / splits) * G];
+            const float wj = has[q] ? w[(size_t)t * k + g + (r / splits) * G] : 0.f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               acc[c] = fmaf(wj, yj[c], acc[c]);
@@ -679,13 +688,14 @@ __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, in
 
 // out[t] = sum_j w[t][j] * Y[t*k + j] for bf16 rows without K splits (the block-scaled expert layer):
 // j in order, fp32, one rounding at the end.  inv (nullable): Y is in expert order, inv[t*k + j] the row, -1
-// for a pair left out.  Bound by HBM (2 k + 2 bytes per output element): each
+// for a pair left out; without it ids (nullable) as in k_combine.  Bound by HBM (2 k + 2 bytes per output element): each
 // thread loads its 8 columns of up to 8 rows before their use, with no index arithmetic between them
 // (the general kernel's per-row divisions made it 209 us for 65536 x 4096 rows).
 constexpr int kCombineRows = 8;
 __global__ void __launch_bounds__(256) k_combine_bf16(const uint4* __restrict__ Y, const float* __restrict__ w,
-                                                      const int32_t* __restrict__ inv, int T, int k, int vec_per_row,
-                                                      uint4* __restrict__ out) {
+                                                      const int32_t* __restrict__ inv,
+                                                      const int32_t* __restrict__ ids, int E, int T, int k,
+                                                      int vec_per_row, uint4* __restrict__ out) {
   pdl_enter();
   const int v = blockIdx.y * 256 + threadIdx.x;
   if (v >= vec_per_row) return;
@@ -699,8 +709,12 @@ __global__ void __launch_bounds__(256) k_combine_bf16(const uint4* __restrict__ 
       for (int j = 0; j < kCombineRows; ++j) {
         const int f = t * k + j0 + j;
         const int row = j0 + j < k ? (inv ? inv[f] : f) : -1;
-        const bool in = row >= 0;
+        bool in = row >= 0;
         u[j] = in ? __ldcs(Y + (size_t)row * vec_per_row + v) : make_uint4(0, 0, 0, 0);
+        if (in && !inv && !pair_kept(ids, f, E)) {
+          in = false;
+          u[j] = make_uint4(0, 0, 0, 0);
+        }
         wj[j] = in ? wt[j0 + j] : 0.0f;
       }
 #pragma unroll
@@ -722,7 +736,8 @@ __global__ void __launch_bounds__(256) k_combine_bf16(const uint4* __restrict__ 
 // Scalar fallback of the combine for H not divisible by 4 (fp32 path only).
 template <bool Y_BF16, bool OUT_BF16>
 __global__ void k_combine_scalar(const void* __restrict__ Yv, int splits, size_t split_stride,
-                                 const float* __restrict__ w, int T, int k, int H, void* __restrict__ out) {
+                                 const float* __restrict__ w, const int32_t* __restrict__ ids, int E, int T, int k,
+                                 int H, void* __restrict__ out) {
   pdl_enter();
   const size_t total = (size_t)T * H;
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (size_t)gridDim.x * blockDim.x) {
@@ -730,6 +745,7 @@ __global__ void k_combine_scalar(const void* __restrict__ Yv, int splits, size_t
     float acc = 0.f;
     for (int j = 0; j < k; ++j) {
       const size_t f = (size_t)t * k + j;
+      if (!pair_kept(ids, f, E)) continue;
       float y = 0.f;
       for (int s = 0; s < splits; ++s) {
         if constexpr (Y_BF16)
@@ -873,37 +889,38 @@ int combine_lanes(int T, int H, int k) {
 }
 
 template <bool YB, bool OB>
-static cudaError_t combine_vec(const void* Y, int splits, size_t split_stride, const float* w, int T, int k, int H,
-                               void* out, cudaStream_t s) {
+static cudaError_t combine_vec(const void* Y, int splits, size_t split_stride, const float* w, const int32_t* ids,
+                               int E, int T, int k, int H, void* out, cudaStream_t s) {
   const int G = combine_lanes(T, H, k);
   const size_t vecs = (size_t)T * (H / 8);
   const int grid = grid_for(vecs * G, 256);
-  if (G == 4) MOE_LAUNCH(k_combine<YB, OB, 4>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, T, k, H, out);
-  else if (G == 2) MOE_LAUNCH(k_combine<YB, OB, 2>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, T, k, H, out);
-  else MOE_LAUNCH(k_combine<YB, OB, 1>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, T, k, H, out);
+  if (G == 4) MOE_LAUNCH(k_combine<YB, OB, 4>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
+  else if (G == 2) MOE_LAUNCH(k_combine<YB, OB, 2>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
+  else MOE_LAUNCH(k_combine<YB, OB, 1>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
   return cudaGetLastError();
 }
 
 cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_stride, const float* w, int T, int k,
-                           int H, void* out, int out_bf16, cudaStream_t s, const int32_t* inv) {
+                           int H, void* out, int out_bf16, cudaStream_t s, const int32_t* inv, const int32_t* ids,
+                           int E) {
   if (inv && !(y_bf16 && out_bf16 && splits == 1 && H % 8 == 0)) return cudaErrorInvalidValue;
   if (y_bf16 && out_bf16 && splits == 1 && H % 8 == 0) {
     const int vpr = H / 8, cols = (vpr + 255) / 256;
     MOE_LAUNCH(k_combine_bf16, dim3(std::min(T, std::max(1, 152 * 16 / cols)), cols), dim3(256), 0, s, (const uint4*)Y, w,
-               inv, T, k, vpr, (uint4*)out);
+               inv, ids, E, T, k, vpr, (uint4*)out);
     return cudaGetLastError();
   }
   if (H % 8 == 0) {
-    if (y_bf16 && out_bf16) return combine_vec<true, true>(Y, splits, split_stride, w, T, k, H, out, s);
-    if (y_bf16) return combine_vec<true, false>(Y, splits, split_stride, w, T, k, H, out, s);
-    if (out_bf16) return combine_vec<false, true>(Y, splits, split_stride, w, T, k, H, out, s);
-    return combine_vec<false, false>(Y, splits, split_stride, w, T, k, H, out, s);
+    if (y_bf16 && out_bf16) return combine_vec<true, true>(Y, splits, split_stride, w, ids, E, T, k, H, out, s);
+    if (y_bf16) return combine_vec<true, false>(Y, splits, split_stride, w, ids, E, T, k, H, out, s);
+    if (out_bf16) return combine_vec<false, true>(Y, splits, split_stride, w, ids, E, T, k, H, out, s);
+    return combine_vec<false, false>(Y, splits, split_stride, w, ids, E, T, k, H, out, s);
   }
   const int grid = grid_for((size_t)T * H, 256);
-  if (y_bf16 && out_bf16) MOE_LAUNCH(k_combine_scalar<true, true>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, T, k, H, out);
-  else if (y_bf16) MOE_LAUNCH(k_combine_scalar<true, false>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, T, k, H, out);
-  else if (out_bf16) MOE_LAUNCH(k_combine_scalar<false, true>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, T, k, H, out);
-  else MOE_LAUNCH(k_combine_scalar<false, false>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, T, k, H, out);
+  if (y_bf16 && out_bf16) MOE_LAUNCH(k_combine_scalar<true, true>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
+  else if (y_bf16) MOE_LAUNCH(k_combine_scalar<true, false>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
+  else if (out_bf16) MOE_LAUNCH(k_combine_scalar<false, true>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
+  else MOE_LAUNCH(k_combine_scalar<false, false>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
   return cudaGetLastError();
 }
 
