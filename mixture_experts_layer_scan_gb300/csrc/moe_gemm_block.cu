@@ -412,6 +412,9 @@ __global__ void __launch_bounds__(kBgThreads, 1)
           }
         }
       }
+      // A wait that gives up does so for each lane by itself.  The stores below shuffle over whole warps, so
+      // a warp stores only if all of its lanes saw every block, and a token's row is stored by one warp.
+      ok = __all_sync(0xffffffffu, ok);
       // transpose through shared memory: thread = weight row -> warp = token
       auto stage_tokens = [&](float* rows, int i0, int n) {  // (i0, n compile-time after unrolling)
 #pragma unroll
