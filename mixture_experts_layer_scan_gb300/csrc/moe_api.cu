@@ -320,6 +320,12 @@ static int make_plan(int T, int H, int I, int E, int topk, moe_dtype act, moe_dt
   return MOE_OK;
 }
 
+// A short batch of block-scaled experts is sorted by the launch that quantises it, and GEMM1's CTAs
+// derive its tiles from the routing.
+static bool align_quantises(const Plan& p, long pairs) {
+  return p.path == PATH_BLK && p.swap && pairs <= kAlignSmallPairs;
+}
+
 static bool misaligned(const void* p, uintptr_t a = 16) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 static int cuda_rc(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -492,9 +498,7 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
   // streams its first weight stages into shared memory while the gather runs.
   const bool g1_prefetch = pl.swap && !gate && (long)T * topk >= 8L * E;
   const bool g1_early = pl.swap && pl.path != PATH_W4 && !pl.gather_in_gemm && !inv && !gate && !g1_prefetch;
-  // a short batch of block-scaled experts is sorted by the launch that quantises it, and GEMM1's CTAs
-  // derive its tiles from the routing
-  const bool align_quant = pl.path == PATH_BLK && pl.swap && n <= kAlignSmallPairs;
+  const bool align_quant = align_quantises(pl, n);
 
   if (!(steps & (STEPS_EXPERTS | STEPS_COMBINE))) return MOE_OK;
   if (!(steps & STEPS_EXPERTS)) goto combine_step;
@@ -761,10 +765,10 @@ int moe_plan_info(int T, int H, int I, int E, int topk, moe_dtype act_dtype, moe
   info->splits_gemm2 = p.s2;
   info->act_split = p.act_split ? 1 : 0;
   // router logits, top-k, align, GEMM1, GEMM2, combine (+ the row gather unless
-  // GEMM1 gathers; + amax and quantisation kernels on the FP8 path; + the
-  // split-K reduction)
+  // GEMM1 gathers or the permutation's launch does; + amax and quantisation kernels
+  // on the FP8 path; + the split-K reduction)
   int n = 6;
-  if (!p.gather_in_gemm) n += 1;            // row gather (FP8: with input quantisation)
+  if (!p.gather_in_gemm && !align_quantises(p, (long)T * topk)) n += 1;  // row gather (FP8: with input quantisation)
   if (p.path == PATH_FP8) n += p.gather_in_gemm ? 3 : 2;  // input amax (+ input quantisation), intermediate quantisation
   if (p.s1 > 1 && !p.fin) n += 1;
   if (p.fused) n = 1;
