@@ -478,16 +478,17 @@ _ROUTED_OPTIONS = moe_options(single_launch=2)  # (the library reads it only)
 def moe_forward_routed(hidden: torch.Tensor, topk_w: torch.Tensor, topk_ids: torch.Tensor, w13: torch.Tensor,
                        w2: torch.Tensor, w13_scale=None, w2_scale=None, out=None, workspace=None, options=None,
                        stream=None, w_format=None):
-    """Steps 3-7 of the layer on a given routing (topk_w fp32 [T,k], topk_ids int32 [T,k]).
+    """Steps 3-7 of the layer on a given routing (topk_w fp32 [T,k], topk_ids int32 [T,k]; buffers of more than T
+    rows and a flat topk_w serve too).
 
     w_format="e4m3_block": e4m3 weights with a scale per 128 x 128 block, as in moe_forward."""
     T, H = hidden.shape
     E, twoI, _ = w13.shape
     I = twoI // 2
     k = topk_ids.shape[1]
-    if topk_ids.dtype != torch.int32 or topk_w.dtype != torch.float32 or topk_ids.shape[0] != T or (
-            topk_w.shape != topk_ids.shape):
-        raise ValueError("topk_w must be float32 and topk_ids int32, both [T, k]")
+    # (any shape with the values of the first T tokens in front: buffers of a larger batch, a flat topk_w)
+    if topk_ids.dtype != torch.int32 or topk_w.dtype != torch.float32 or min(topk_ids.numel(), topk_w.numel()) < T * k:
+        raise ValueError("topk_w must be float32 and topk_ids int32, both with T x k values in front")
     _check_block_scales(w_format, E, H, I, w13, w2, w13_scale, w2_scale)
     act, wdt = _dt(hidden), _w_dtype(w13, w_format)
     if options is None:

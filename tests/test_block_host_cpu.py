@@ -1,6 +1,7 @@
 """Host side of the block-scaled operators and of the calls beside them: what the plan says, and which arguments
 are taken (no call below reaches the device)."""
 import pytest
+import torch
 
 
 @pytest.fixture(scope="module")
@@ -21,3 +22,43 @@ def test_plan_counts_the_launches_of_a_block_scaled_layer(moe, T, k, options, la
     """router, top-k, permutation, quantisation, two products and the combine."""
     p = moe.moe_plan_info(T, 2048, 768, 128, k, moe.MOE_BF16, moe.MOE_E4M3_B128, options)
     assert p["kernel_launches"] == launches
+
+
+class Recorder:
+    """Stands in for the library: keeps the arguments of each call and answers 0."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+
+        return call
+
+
+@pytest.fixture
+def recorded(moe, monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(moe, "_lib", r)
+    return r
+
+
+def test_routings_of_other_shapes(moe, recorded):
+    """What counts is the memory: T x k values in front, in a flat topk_w and in buffers of a larger batch too."""
+    T, H, I, E, k = 5, 256, 128, 4, 2
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    w13, w2 = torch.zeros(E, 2 * I, H, dtype=torch.bfloat16), torch.zeros(E, H, I, dtype=torch.bfloat16)
+    ws = torch.empty(16, dtype=torch.uint8)
+    ids, big = torch.zeros(T, k, dtype=torch.int32), torch.zeros(64, k, dtype=torch.int32)
+    for tw, ti in ((torch.zeros(T, k), ids), (torch.zeros(T * k), ids), (torch.zeros(64, k), big),
+                   (torch.zeros(T, k, 1), big), (torch.zeros(T * k), big)):
+        moe.moe_forward_routed(x, tw, ti, w13, w2, workspace=ws, stream=0)
+        name, args = recorded.calls.pop()
+        assert name == "moe_forward_routed" and args[1:3] == (tw.data_ptr(), ti.data_ptr()) and args[5:10] == (T, H, I, E, k)
+    for tw, ti in ((torch.zeros(T, k - 1), ids), (torch.zeros(T - 1, k), ids), (torch.zeros(T, k), ids[:4]),
+                   (torch.zeros(T, k, dtype=torch.float64), ids), (torch.zeros(T, k), ids.long())):
+        with pytest.raises(ValueError):
+            moe.moe_forward_routed(x, tw, ti, w13, w2, workspace=ws, stream=0)
+    assert not recorded.calls
