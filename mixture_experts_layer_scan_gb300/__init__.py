@@ -357,10 +357,17 @@ def moe_align(topk_ids: torch.Tensor, E: int, block: int, stream=None, with_coun
     return sorted_ids, expert_ids, npp[:1], counts
 
 
+_W_FORMATS = {"int4": MOE_INT4, "e4m3_block": MOE_E4M3_B128}
+# no format beside the tensors' type, and names of that type
+_OWN_FORMATS = (None, "", "f32", "fp32", "float32", "bf16", "bfloat16", "e4m3", "fp8", "float8_e4m3fn")
+
+
 def _w_dtype(w13: torch.Tensor, w_format: Optional[str]) -> int:
-    if w_format is None:
+    if w_format in _OWN_FORMATS:
         return _dt(w13)
-    return {"int4": MOE_INT4, "e4m3_block": MOE_E4M3_B128}[w_format]
+    if w_format not in _W_FORMATS:
+        raise ValueError(f"w_format {w_format!r}: {', '.join(_W_FORMATS)}, or the weights' own type (None)")
+    return _W_FORMATS[w_format]
 
 
 def _check_block_scales(w_format, E, H, I, w13, w2, w13_scale, w2_scale) -> None:

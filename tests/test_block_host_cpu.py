@@ -62,3 +62,22 @@ def test_routings_of_other_shapes(moe, recorded):
         with pytest.raises(ValueError):
             moe.moe_forward_routed(x, tw, ti, w13, w2, workspace=ws, stream=0)
     assert not recorded.calls
+
+
+def test_names_of_weight_formats(moe, recorded):
+    """A name of the weights' own type says nothing new; an unknown name is refused, not guessed."""
+    T, H, I, E, k = 3, 256, 128, 4, 2
+    x, wr = torch.zeros(T, H, dtype=torch.bfloat16), torch.zeros(E, H, dtype=torch.bfloat16)
+    ws = torch.empty(16, dtype=torch.uint8)
+    for dtype, code in ((torch.bfloat16, moe.MOE_BF16), (torch.float8_e4m3fn, moe.MOE_E4M3)):
+        w13, w2 = torch.zeros(E, 2 * I, H, dtype=dtype), torch.zeros(E, H, I, dtype=dtype)
+        for name in (None, "", "bf16", "e4m3", "fp8"):
+            moe.moe_forward(x, wr, w13, w2, k, True, workspace=ws, stream=0, w_format=name)
+            args = [a for n, a in recorded.calls if n == "moe_forward"]
+            assert args and args[-1][11] == code
+            moe.moe_forward_noalloc(x, wr, w13, w2, k, True, stream=0, w_format=name)
+            args = [a for n, a in recorded.calls if n == "moe_forward_noalloc"]
+            assert args and args[-1][11] == code
+        for name in ("int8", "e4m3-block", "E4M3_BLOCK"):
+            with pytest.raises(ValueError):
+                moe.moe_forward(x, wr, w13, w2, k, True, workspace=ws, stream=0, w_format=name)
