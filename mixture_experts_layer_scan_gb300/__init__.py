@@ -9,7 +9,6 @@ no CPU fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional
 
@@ -254,11 +253,12 @@ def moe_topk_from_logits(logits: torch.Tensor, topk: int, renorm: bool, topk_w=N
     return topk_w, topk_ids
 
 
-@functools.lru_cache(maxsize=256)
 def _route_rule(score: str, n_group: int, topk_group: Optional[int], group_sum: int, renorm: bool,
                 scale: float) -> moe_route_rule:
-    return moe_route_rule(SCORES[score], n_group, n_group if topk_group is None else topk_group, group_sum,
-                          int(bool(renorm)), float(scale))
+    if score not in SCORES:
+        raise ValueError(f"score {score!r}: {', '.join(SCORES)}")
+    return moe_route_rule(SCORES[score], int(n_group), int(n_group if topk_group is None else topk_group),
+                          int(group_sum), int(bool(renorm)), float(scale))
 
 
 def moe_topk_grouped(logits: torch.Tensor, topk: int, bias=None, score: str = "sigmoid", n_group: int = 1,

@@ -81,3 +81,19 @@ def test_names_of_weight_formats(moe, recorded):
         for name in ("int8", "e4m3-block", "E4M3_BLOCK"):
             with pytest.raises(ValueError):
                 moe.moe_forward(x, wr, w13, w2, k, True, workspace=ws, stream=0, w_format=name)
+
+
+def test_a_routing_rule_is_its_values(moe, recorded):
+    """The scale may come as a tensor or an array: what it holds at the call counts, not what it held before."""
+    logits = torch.zeros(2, 8)
+    scale = torch.tensor(2.5)
+    seen = []
+    for value in (2.5, 1.0, 16.0):
+        scale.fill_(value)
+        for s in (scale, scale.numpy()):
+            moe.moe_topk_grouped(logits, 2, n_group=4, topk_group=torch.tensor(2), scale=s, stream=0)
+            rule = recorded.calls[-1][1][5]._obj
+            seen.append((rule.scale, rule.n_group, rule.topk_group, rule.score))
+    assert seen == [(v, 4, 2, 1) for v in (2.5, 2.5, 1.0, 1.0, 16.0, 16.0)]
+    with pytest.raises(ValueError):
+        moe.moe_topk_grouped(logits, 2, score="tanh", stream=0)
