@@ -354,8 +354,8 @@ MOE_API int moe_inv_rope_fp8_quant(const void* x, int T, int heads, int head_dim
  * both products and the reciprocal are one fp32 rounding each.  A block holding a NaN
  * or an infinity gets that as its scale, and its codes stand for no finite value.
  *   x [T][K] MOE_F32 or MOE_BF16;  q [T][K] e4m3 codes;  scale [T][ceil(K/128)] fp32
- * K % 16 == 0 (MOE_ERR_UNSUPPORTED otherwise), T * ceil(K/128) < 2^31 - 2^24; scale 4-byte aligned,
- * x and q 16. */
+ * K % 16 == 0 (MOE_ERR_UNSUPPORTED otherwise), K and T * ceil(K/128) below 2^31 - 2^24 (MOE_ERR_ARG
+ * otherwise); scale 4-byte aligned, x and q 16. */
 MOE_API int moe_quant_block(const void* x, int T, int K, moe_dtype x_dtype, uint8_t* q, float* scale,
                             moe_stream_t stream);
 /* The same of h = SiLU(g) * u (fp32, not rounded in between), with gate_up [T][2I] holding the row
@@ -369,8 +369,8 @@ MOE_API int moe_silu_quant_block(const void* gate_up, int T, int I, moe_dtype x_
  * out_dtype.
  *   a [T][K] e4m3, a_scale [T][ceil(K/128)] (moe_quant_block's outputs)
  *   w [N][K] e4m3, w_scale [ceil(N/128)][ceil(K/128)];  out [T][N] MOE_BF16 or MOE_F32
- * Any T >= 0 and N >= 1, K % 16 == 0 (MOE_ERR_UNSUPPORTED otherwise).  No workspace.  Scales 4-byte
- * aligned, the other pointers 16. */
+ * T >= 0, N >= 1, each of T, N and K below 2^31 - 2^24 (MOE_ERR_ARG otherwise), K % 16 == 0
+ * (MOE_ERR_UNSUPPORTED otherwise).  No workspace.  Scales 4-byte aligned, the other pointers 16. */
 MOE_API int moe_gemm_block(const void* a, const float* a_scale, const void* w, const float* w_scale, int T, int N,
                            int K, moe_dtype out_dtype, void* out, moe_stream_t stream);
 

@@ -981,12 +981,16 @@ int moe_inv_rope_fp8_quant(const void* x, int T, int heads, int head_dim, int ro
                                      st, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Largest dimension of the block-scaled operators: their 32-bit tile and block counts round up to a multiple
+// of at most 256, and quantisation steps over blocks by less than 2^24.
+constexpr long long kBlockMaxDim = (1ll << 31) - (1ll << 24);
+
 static int quant_block(const void* x, int T, int K, moe_dtype x_dtype, bool silu_form, uint8_t* q, float* scale,
                        moe_stream_t stream) {
-  if (T < 0 || K < 1) return MOE_ERR_ARG;
+  if (T < 0 || K < 1 || K >= kBlockMaxDim) return MOE_ERR_ARG;
   if (x_dtype != MOE_F32 && x_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (K % 16) return MOE_ERR_UNSUPPORTED;
-  if ((long long)T * ((K + 127) / 128) >= (1ll << 31) - (1ll << 24)) return MOE_ERR_ARG;
+  if ((long long)T * ((K + 127) / 128) >= kBlockMaxDim) return MOE_ERR_ARG;
   if (T == 0) return MOE_OK;
   if (!x || !q || !scale) return MOE_ERR_ARG;
   if (misaligned(x) || misaligned(q) || misaligned(scale, 4)) return MOE_ERR_ALIGNMENT;
@@ -1005,7 +1009,7 @@ int moe_silu_quant_block(const void* gate_up, int T, int I, moe_dtype x_dtype, u
 
 int moe_gemm_block(const void* a, const float* a_scale, const void* w, const float* w_scale, int T, int N, int K,
                    moe_dtype out_dtype, void* out, moe_stream_t stream) {
-  if (T < 0 || N < 1 || K < 1) return MOE_ERR_ARG;
+  if (T < 0 || N < 1 || K < 1 || T >= kBlockMaxDim || N >= kBlockMaxDim || K >= kBlockMaxDim) return MOE_ERR_ARG;
   if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (K % 16) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;

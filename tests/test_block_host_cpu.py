@@ -97,3 +97,14 @@ def test_a_routing_rule_is_its_values(moe, recorded):
     assert seen == [(v, 4, 2, 1) for v in (2.5, 2.5, 1.0, 1.0, 16.0, 16.0)]
     with pytest.raises(ValueError):
         moe.moe_topk_grouped(logits, 2, score="tanh", stream=0)
+
+
+@pytest.mark.parametrize("size", [2 ** 31 - 2 ** 24, 2 ** 31 - 16])
+def test_dimensions_whose_counts_pass_32_bits(moe, size):
+    """The last rows or columns below 2^31 would round up past it: refused before anything is launched."""
+    lib, at = moe.lib(), 0x1000
+    assert lib.moe_gemm_block(at, at, at, at, size, 128, 16, moe.MOE_BF16, at, None) == moe.MOE_ERR_ARG
+    assert lib.moe_gemm_block(at, at, at, at, 4, size, 16, moe.MOE_BF16, at, None) == moe.MOE_ERR_ARG
+    assert lib.moe_gemm_block(at, at, at, at, 4, 128, size, moe.MOE_BF16, at, None) == moe.MOE_ERR_ARG
+    for f in (lib.moe_quant_block, lib.moe_silu_quant_block):
+        assert f(at, 1, size, moe.MOE_BF16, at, at, None) == moe.MOE_ERR_ARG
