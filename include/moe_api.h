@@ -379,8 +379,11 @@ MOE_API int moe_gemm_block(const void* a, const float* a_scale, const void* w, c
  * expert GEMMs and combine as moe_forward, which it matches bit for bit given
  * moe_forward's routing.
  *   topk_w   [T][topk] fp32 routing weights (used as given, no renormalisation)
- *   topk_ids [T][topk] int32 expert ids in [0, E); ids outside are dropped and flagged
- *            MOE_ERR_DEVICE_INDEX
+ *   topk_ids [T][topk] int32 expert ids in [0, E); pairs with ids outside are dropped (they add
+ *            nothing) and flagged MOE_ERR_DEVICE_INDEX.  A token may name an expert more than once;
+ *            in SWAP_AB mode an expert takes at most T pairs rounded up to a multiple of 16 (more
+ *            than distinct ids can give it; MOE_E4M3_B128: any number), and those past that, in
+ *            the order of tokens, are dropped and flagged likewise
  * Other arguments, the workspace (moe_workspace_size with the same E) and the options
  * as moe_forward; the multi-kernel sequence always (single_launch = 1 is refused). */
 MOE_API int moe_forward_routed(const void* hidden, const float* topk_w, const int32_t* topk_ids, const void* w13,

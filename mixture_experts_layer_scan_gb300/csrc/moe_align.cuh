@@ -19,9 +19,9 @@ struct SmallGroup {
 };
 
 // All 32 lanes of a warp; n <= 32.  Ids out of range count as none and are reported to status
-// (nullable).
+// (nullable), and so are an expert's pairs past max_count.
 __device__ __forceinline__ SmallGroup align_small(const int32_t* __restrict__ ids, int n, int E, int B, int* status,
-                                                  int skip_minus_one) {
+                                                  int skip_minus_one, int max_count = 32) {
   const int lane = threadIdx.x & 31;
   SmallGroup g;
   g.e = -1;
@@ -33,7 +33,15 @@ __device__ __forceinline__ SmallGroup align_small(const int32_t* __restrict__ id
     }
   }
   __syncwarp();
-  const unsigned grp = __match_any_sync(0xffffffffu, g.e);
+  unsigned grp = __match_any_sync(0xffffffffu, g.e);
+  if (max_count < n) {
+    if (g.e >= 0 && __popc(grp & ((1u << lane) - 1u)) >= max_count) {
+      if (status) report(status, MOE_ERR_DEVICE_INDEX);
+      g.e = -1;
+    }
+    __syncwarp();
+    grp = __match_any_sync(0xffffffffu, g.e);
+  }
   g.count = __popc(grp);
   g.leader = g.e >= 0 && lane == __ffs(grp) - 1;
   g.leaders = __ballot_sync(0xffffffffu, g.leader);

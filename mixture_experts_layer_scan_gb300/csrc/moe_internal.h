@@ -36,11 +36,12 @@ cudaError_t launch_inject_timeout(const int* flag, int* status, cudaStream_t s);
 // every expert's padded run split into 256-row chunks with a 128-row last chunk where the
 // run has an odd number of blocks: pblk[c] = (first row << 1) | (1 for 128 rows); their
 // count goes to meta[META_NPB].  inv (nullable, T*k words): the sorted row of each
-// pair, -1 for a pair left out.
+// pair, -1 for a pair left out.  max_count: an expert's pairs past this many, in flat order, are dropped
+// and flagged too.
 cudaError_t launch_align(const int32_t* ids, int T, int k, int E, int B, int32_t* sorted, int32_t* eids,
                          int32_t* npp, int32_t* counts, int32_t* meta, int* status, cudaStream_t s,
                          bool skip_minus_one = false, int32_t* pblk = nullptr, unsigned* zero_words = nullptr,
-                         int n_zero = 0, int32_t* inv = nullptr);
+                         int n_zero = 0, int32_t* inv = nullptr, int max_count = INT32_MAX);
 // dst (device) = bytes of page-locked host memory read by the device at src (its device
 // address); a kernel launched like the library's others (bytes and both addresses 16-byte
 // multiples, else cudaErrorInvalidValue)
@@ -72,7 +73,8 @@ cudaError_t launch_quant_act(const float* A, int I, const int32_t* meta, int cap
                              uint8_t* Aq, cudaStream_t s);
 // out[t] = sum_j w[t][j] * sum_s Y[s][t*k+j]   (Y fp32 or bf16, out fp32 or bf16)
 // inv (bf16 Y without splits): Y is in expert order, inv[t * k + j] the row of a pair, -1 for none
-// ids [T][k] (nullable, Y in pair order): pairs whose id is outside [0, E) have no row and add nothing
+// ids [T][k] (nullable, Y in pair order): pairs whose entry is outside [0, E) have no row and add nothing
+// (the routing, or launch_align's inv with E = INT_MAX)
 cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_stride, const float* w, int T, int k,
                            int H, void* out, int out_bf16, cudaStream_t s, const int32_t* inv = nullptr,
                            const int32_t* ids = nullptr, int E = 0);

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kAlignThreads, 1)
     k_align(const int32_t* __restrict__ ids, int T, int k, int E, int B, int32_t* __restrict__ sorted,
             int32_t* __restrict__ eids, int32_t* __restrict__ npp_out, int32_t* __restrict__ counts_out,
             int32_t* __restrict__ meta, int* status, int skip_minus_one, int32_t* __restrict__ pblk,
-            unsigned* __restrict__ zero_words, int n_zero, int32_t* __restrict__ inv) {
+            unsigned* __restrict__ zero_words, int n_zero, int32_t* __restrict__ inv, int max_count) {
   pdl_enter();
   // counters of the next kernels of this call start at zero (e.g. GEMM1's split arrivals)
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_zero; i += gridDim.x * blockDim.x) zero_words[i] = 0u;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kAlignThreads, 1)
       if (r < crank) below += v;
       tot += v;
     }
-    cnt[e] = tot;
+    cnt[e] = min(tot, max_count);
     cbase[e] = below;
   }
   cluster.sync();  // remote reads done: no CTA touches another's shared memory after this
@@ -218,12 +218,14 @@ __global__ void __launch_bounds__(kAlignThreads, 1)
       const int v = end - beg <= 32 * kAlignHeld ? held[j] : look(base + 32 * j);
       const int f = base + 32 * j + lane, e = v & 2047;
       int slot = -1;
-      if (v >= 0) slot = off[e] + cbase[e] + wc[warp * E + e] + (v >> 11 & 31);
-      __syncwarp();
       if (v >= 0) {
-        sorted[slot] = f;
-        if (v >> 16) wc[warp * E + e] += v >> 16;
+        const int r = cbase[e] + wc[warp * E + e] + (v >> 11 & 31);
+        if (r < max_count) slot = off[e] + r;
+        else report(status, MOE_ERR_DEVICE_INDEX);
       }
+      __syncwarp();
+      if (slot >= 0) sorted[slot] = f;
+      if (v >= 0 && v >> 16) wc[warp * E + e] += v >> 16;
       if (inv && f < end) inv[f] = slot;  // pair -> sorted row (-1: left out)
       __syncwarp();
     }
@@ -249,11 +251,11 @@ __global__ void __launch_bounds__(kAlignSmallThreads)
     k_align_small(const int32_t* __restrict__ ids, int n, int E, int B, int32_t* __restrict__ sorted,
                   int32_t* __restrict__ eids, int32_t* __restrict__ npp_out, int32_t* __restrict__ counts_out,
                   int32_t* __restrict__ meta, int* status, int skip_minus_one, unsigned* __restrict__ zero_words,
-                  int n_zero, int32_t* __restrict__ inv) {
+                  int n_zero, int32_t* __restrict__ inv, int max_count) {
   pdl_enter();
   for (int i = threadIdx.x; i < n_zero; i += blockDim.x) zero_words[i] = 0u;
   if (threadIdx.x >= 32) return;
-  const SmallGroup g = align_small(ids, n, E, B, status, skip_minus_one);
+  const SmallGroup g = align_small(ids, n, E, B, status, skip_minus_one, max_count);
   align_small_maps(g, n, E, B, sorted, eids, npp_out, counts_out, meta, inv);
 }
 
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kAlignThreads, 1)
     k_align_mid(const int32_t* __restrict__ ids, int n, int E, int B, int32_t* __restrict__ sorted,
                 int32_t* __restrict__ eids, int32_t* __restrict__ npp_out, int32_t* __restrict__ counts_out,
                 int32_t* __restrict__ meta, int* status, int skip_minus_one, unsigned* __restrict__ zero_words,
-                int n_zero, int32_t* __restrict__ inv) {
+                int n_zero, int32_t* __restrict__ inv, int max_count) {
   pdl_enter();
   for (int i = threadIdx.x; i < n_zero; i += blockDim.x) zero_words[i] = 0u;
   extern __shared__ int sm[];
@@ -298,12 +300,16 @@ __global__ void __launch_bounds__(kAlignThreads, 1)
   int below = 0;  // pairs of my expert in lower warps
   if (e >= 0)
     for (int w = 0; w < warp; ++w) below += wc[w * E + e];
+  if (e >= 0 && below + rank >= max_count) {
+    report(status, MOE_ERR_DEVICE_INDEX);
+    e = -1;
+  }
   if (warp == 0) {
     // offsets: lane l scans experts [l*per, l*per + per) after a warp scan of the lane sums
     const int per = (E + 31) / 32, x0 = min(E, lane * per), x1 = min(E, x0 + per);
     int lp = 0, la = 0;
     for (int x = x0; x < x1; ++x) {
-      const int c = cnt[x];
+      const int c = min(cnt[x], max_count);
       lp += (c + B - 1) / B * B;
       la += c > 0 ? 1 : 0;
     }
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(kAlignThreads, 1)
     const int total = __shfl_sync(0xffffffffu, ip, 31), nact = __shfl_sync(0xffffffffu, ia, 31);
     int rp = ip - lp, ra = ia - la;
     for (int x = x0; x < x1; ++x) {
-      const int c = cnt[x];
+      const int c = min(cnt[x], max_count);
       off[x] = rp;
       if (meta) {
         meta[meta_offsets(E) + x] = rp;
@@ -351,7 +357,7 @@ __global__ void __launch_bounds__(kAlignThreads, 1)
   }
   // block map and sentinel rows, one expert per thread
   for (int x = threadIdx.x; x < E; x += blockDim.x) {
-    const int c = cnt[x];
+    const int c = min(cnt[x], max_count);
     if (c == 0) continue;
     const int o = off[x], pad = (c + B - 1) / B * B;
     for (int b = o / B; b < (o + pad) / B; ++b) eids[b] = x;
@@ -616,9 +622,10 @@ __device__ __forceinline__ void load8(const void* Yv, size_t idx, float (&y)[8])
 // slots j = g, g+G, ... (each one the sum of its K-split partials, in split
 // order), then the G partial sums are added in a fixed butterfly.  The order of
 // every addition is fixed, so the result is the same on every run.
-// ids (nullable): a routing given by a caller.  A pair whose id is outside [0, E) was dropped from the
-// permutation, nothing wrote its row, and it adds nothing here.  (Its row is loaded all the same: it lies
-// in Y, and the row's load then does not wait for the id's.)
+// ids (nullable): a routing given by a caller, or the permutation's inverse map with E = INT_MAX.  A pair
+// whose entry is outside [0, E) was dropped from the permutation, nothing wrote its row, and it adds
+// nothing here.  (Its row is loaded all the same: it lies in Y, and the row's load then does not wait for
+// the entry's.)
 template <bool Y_BF16, bool OUT_BF16, int G>
 __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, int splits, size_t split_stride,
                                                  const float* __restrict__ w, const int32_t* __restrict__ ids,
@@ -773,12 +780,13 @@ int grid_for(size_t work, int threads, int cap_blocks = 152 * 16) {
 
 cudaError_t launch_align(const int32_t* ids, int T, int k, int E, int B, int32_t* sorted, int32_t* eids,
                          int32_t* npp, int32_t* counts, int32_t* meta, int* status, cudaStream_t s,
-                         bool skip_minus_one, int32_t* pblk, unsigned* zero_words, int n_zero, int32_t* inv) {
+                         bool skip_minus_one, int32_t* pblk, unsigned* zero_words, int n_zero, int32_t* inv,
+                         int max_count) {
   if (pblk && B != 128) return cudaErrorInvalidValue;
   if (n_zero > 0 && !zero_words) return cudaErrorInvalidValue;
   if ((long)T * k <= kAlignSmallPairs && !pblk) {
     MOE_LAUNCH(k_align_small, dim3(1), dim3(kAlignSmallThreads), 0, s, ids, T * k, E, B, sorted, eids, npp, counts,
-               meta, status, skip_minus_one ? 1 : 0, zero_words, n_zero, inv);
+               meta, status, skip_minus_one ? 1 : 0, zero_words, n_zero, inv, max_count);
     return cudaGetLastError();
   }
   if ((long)T * k <= kAlignThreads && !pblk) {
@@ -792,7 +800,7 @@ cudaError_t launch_align(const int32_t* ids, int T, int k, int E, int B, int32_t
     }
     const size_t msmem = (size_t)(kAlignWarps * E + 2 * E + 1) * sizeof(int);
     MOE_LAUNCH(k_align_mid, dim3(1), dim3(kAlignThreads), msmem, s, ids, T * k, E, B, sorted, eids, npp, counts, meta,
-               status, skip_minus_one ? 1 : 0, zero_words, n_zero, inv);
+               status, skip_minus_one ? 1 : 0, zero_words, n_zero, inv, max_count);
     return cudaGetLastError();
   }
   const size_t smem = (size_t)(kAlignWarps * E + 4 * E + 1 + 33) * sizeof(int);
@@ -825,7 +833,7 @@ cudaError_t launch_align(const int32_t* ids, int T, int k, int E, int B, int32_t
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k_align, ids, T, k, E, B, sorted, eids, npp, counts, meta, status,
-                            skip_minus_one ? 1 : 0, pblk, zero_words, n_zero, inv);
+                            skip_minus_one ? 1 : 0, pblk, zero_words, n_zero, inv, max_count);
 }
 
 cudaError_t launch_amax_bf16(const void* X, size_t n, unsigned* amax_bits, cudaStream_t s) {
