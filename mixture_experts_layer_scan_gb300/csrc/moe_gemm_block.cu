@@ -623,8 +623,13 @@ __device__ __forceinline__ void bp_fold32(float2* acc, const uint32_t (&r)[32], 
   for (int j = 0; j < 16; ++j) fma2(acc[j], s, s, __uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
 }
 
-// SiLU(g) * u for an intermediate that becomes e4m3 (4 significant bits) right away: the approximate
-// exponential and quotient are within a few 2^-22, and 64 of them per thread stand between two tiles.
+// SiLU(g) * u for an intermediate that becomes e4m3 (4 significant bits) right away.  The quotient is within 2
+// ulp, the exponential within 2 + floor(1.173 |g|) (CUDA's bounds), and for a negative gate e^-g is the whole
+// denominator: about 2^-22 relative near 0, 25 ulp (2^-18.4) at g = -20, 95 ulp (2^-16.4) at -80, and 0 below
+// about -87.  Of the 25 million codes of 4096 tokens through 8 of 128 experts (2048 x 768) 14 differ from the
+// rounded forms'.  64 of these per thread stand between two tiles: with the rounded quotient that layer takes
+// 402 us instead of 275 and 8192 tokens through 64 experts of 4096 x 2048 1866 instead of 1628, with the
+// rounded exponential alone 280 and 1647.
 __device__ __forceinline__ float silu_mul_fast(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // 32 bytes, 32-byte aligned, in one store
@@ -685,7 +690,8 @@ __device__ __forceinline__ void bp_store(const BgDev& p, size_t row, int n, cons
 }
 
 // What a thread keeps for the folds beside its accumulators.  Registers are short (128 sums, 64 loaded
-// columns): a spilled word in the loop costs a tenth of the rate.
+// columns): a spilled word in the loop costs a tenth of the rate.  What the compiler does spill (20 bytes)
+// stays out of it: 8192 x 4096 x 4096 executes 4 local loads per warp and tile, not one per K block.
 struct BpFold {
   uint32_t bars;    // barriers of this CTA (kBpBar)
   uint32_t tmem;    // tensor-memory address of its half in buffer 0 (buffer 1: + 256 columns)
