@@ -81,7 +81,8 @@ enum {
  * take the flexible N slot (page 1, section "Swap-AB pour l'utilisation de
  * WGMMA", Figure 1; re-derived here for tcgen05, whose M slot is 128).
  * TOKEN_MAJOR puts 128 sorted token rows in the M slot (prefill).
- * AUTO picks SWAP_AB for T <= 64 and TOKEN_MAJOR above. */
+ * AUTO picks SWAP_AB for T <= 64 (INT4 weights 128; MOE_E4M3_B128 also up to 32 pairs per expert)
+ * and TOKEN_MAJOR above. */
 typedef enum { MOE_ORIENT_AUTO = 0, MOE_ORIENT_SWAP_AB = 1, MOE_ORIENT_TOKEN_MAJOR = 2 } moe_orientation;
 
 /* Stages of moe_forward, for the optional timing events below. */
@@ -121,7 +122,7 @@ typedef enum {
  * (all-zero struct == defaults).  The same options must be given to
  * moe_workspace_size and to the moe_forward calls that use that workspace. */
 typedef struct {
-  int orientation;    /* moe_orientation; SWAP_AB needs T <= 256 */
+  int orientation;    /* moe_orientation; SWAP_AB needs T <= 256, except with MOE_E4M3_B128 weights */
   int split_k;        /* 0 = automatic; n > 0 forces n K-splits in SWAP_AB mode */
   int inject_timeout; /* test hook: 1 makes the first kernel wait on a device flag that
                          nothing sets, with a ~1 ms bound; the call then reports
@@ -169,7 +170,9 @@ typedef struct {
 MOE_API const char* moe_strerror(int code);
 
 /* Bytes of device workspace moe_forward needs for this shape, dtype pair and
- * options (written to *bytes).  Depends only on its arguments. */
+ * options (written to *bytes).  Depends only on its arguments.  The plan changes with T, and a
+ * longer batch can need less than a shorter one (64 experts of 4096 x 2048 in MOE_E4M3_B128, top-8:
+ * 35.5 MiB at 64 tokens, 31.6 at 65): a workspace for several batch sizes is the largest of theirs. */
 MOE_API int moe_workspace_size(int T, int H, int I, int E, int topk, moe_dtype act_dtype, moe_dtype w_dtype,
                        const moe_options* opts, size_t* bytes);
 
@@ -477,6 +480,8 @@ MOE_API int moe_cache_lru_plan(int E, int n_slots, int n_calls, int pairs, const
  *    one (hidden 2048, 128 experts, FFN 768, top-8: 26.7 MiB) fit; an FP8
  *    layer with hidden 4096, 64 experts, FFN 8192, top-8 at 64 tokens needs
  *    71 MiB and prefill batches need far more -- use moe_forward for those.
+ *    Fitting at one T does not mean fitting at a smaller one: a block-scaled layer of 64
+ *    experts of 4096 x 2048, top-8, fits at 33 and 65 tokens and not at 48, 64 or 80.
  *  - The first call on a device looks up the array's device address
  *    (cudaGetSymbolAddress) and caches it; make that first call before any
  *    stream capture on that device.  cudaDeviceReset() invalidates the cached
