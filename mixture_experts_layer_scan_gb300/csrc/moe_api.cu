@@ -503,9 +503,10 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
   // Only a caller's own routing can hold pairs that are dropped and so have no row in the combine: the
   // router's ids are in range and distinct, and in a call of several passes (skip_minus_one) every row is
   // some pass's.  The combine tells them by the inverse map, which lies where the router's ids would if the
-  // plan has no other use for it.
-  const bool given = tid_in && !skip_minus_one;
-  int32_t* rows = given ? reinterpret_cast<int32_t*>(ws + pl.o_tid) : nullptr;
+  // plan has no other use for it, or (where no map is written) by the ids.
+  const bool given = tid_in && !skip_minus_one, by_expert = pl.path == PATH_BLK && pl.pair;
+  int32_t* rows = inv ? inv : given ? reinterpret_cast<int32_t*>(ws + pl.o_tid) : nullptr;
+  const int32_t* kept = by_expert ? inv : !given ? nullptr : align_quant ? tid : rows;
   // The swap-AB tiles of the formats with one tile for all of an expert's tokens hold xbox rows.  An expert
   // has more pairs only where a caller's routing names it several times for a token: the pairs past the
   // tile are dropped by the permutation (they would be written behind the tile's shared memory).
@@ -523,7 +524,7 @@ static int forward_steps(const Plan& pl, int steps, const void* hidden, const vo
     unsigned* zero_words = pl.fin ? fin : (pl.path == PATH_FP8 ? amax : nullptr);
     const int n_zero = pl.fin ? E * (I / 128) : (pl.path == PATH_FP8 ? 2 : 0);
     MOE_TRY(launch_align(tid, T, topk, E, pl.B, sorted, eids, meta + META_NPP, nullptr, meta, st, s, skip_minus_one,
-                         pblk, zero_words, n_zero, inv ? inv : rows, max_count));
+                         pblk, zero_words, n_zero, rows, max_count));
   }
   if (o) record(o->stage_end[MOE_STAGE_ALIGN], s);
 
@@ -724,8 +725,7 @@ combine_step:
   // 7. combine
   if (o) record(o->stage_begin[MOE_STAGE_COMBINE], s);
   MOE_TRY(launch_combine(y, pl.y_bf16 ? 1 : 0, pl.s2, pl.y_stride, tw, T, topk, H, out, act_dtype == MOE_BF16 ? 1 : 0,
-                         s, pl.path == PATH_BLK && pl.pair ? inv : nullptr,
-                         !given ? nullptr : align_quant ? tid : inv ? inv : rows, align_quant ? E : INT32_MAX));
+                         s, by_expert, kept, kept == tid ? E : INT32_MAX));
   if (o) record(o->stage_end[MOE_STAGE_COMBINE], s);
 #undef MOE_TRY
   return MOE_OK;

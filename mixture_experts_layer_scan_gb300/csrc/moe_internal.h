@@ -72,11 +72,11 @@ cudaError_t launch_quant_x(const void* X, size_t n, const unsigned* amax_bits, u
 cudaError_t launch_quant_act(const float* A, int I, const int32_t* meta, int cap, const unsigned* amax_bits,
                              uint8_t* Aq, cudaStream_t s);
 // out[t] = sum_j w[t][j] * sum_s Y[s][t*k+j]   (Y fp32 or bf16, out fp32 or bf16)
-// inv (bf16 Y without splits): Y is in expert order, inv[t * k + j] the row of a pair, -1 for none
-// ids [T][k] (nullable, Y in pair order): pairs whose entry is outside [0, E) have no row and add nothing
-// (the routing, or launch_align's inv with E = INT_MAX)
+// ids [T][k] (nullable): pairs whose entry is outside [0, E) have no row and add nothing (the routing, or
+// launch_align's inv with E = INT32_MAX; bf16 Y without splits takes the latter alone)
+// by_expert (bf16 Y without splits, with inv): Y is in expert order, inv's entries its rows
 cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_stride, const float* w, int T, int k,
-                           int H, void* out, int out_bf16, cudaStream_t s, const int32_t* inv = nullptr,
+                           int H, void* out, int out_bf16, cudaStream_t s, bool by_expert = false,
                            const int32_t* ids = nullptr, int E = 0);
 // lanes G that share one output vector in the combine (H % 8 == 0); fixes its addition order
 int combine_lanes(int T, int H, int k);

@@ -660,7 +660,8 @@ __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, in
 #pragma unroll
           for (int c = 0; c < 8; ++c) yj[c] += has[q] ? y[q][c] : 0.f;
           if (r % splits == splits - 1) {
-            const float wj = has[q] ? w[(size_t)t * k + g + (r / splits) * G] : 0.f;
+            const float wv = w[(size_t)t * k + g + (r / splits) * G];  // (loaded without waiting for the entry)
+            const float wj = has[q] ? wv : 0.f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               acc[c] = fmaf(wj, yj[c], acc[c]);
@@ -694,14 +695,13 @@ __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, in
 }
 
 // out[t] = sum_j w[t][j] * Y[t*k + j] for bf16 rows without K splits (the block-scaled expert layer):
-// j in order, fp32, one rounding at the end.  inv (nullable): Y is in expert order, inv[t*k + j] the row, -1
-// for a pair left out; without it ids (nullable) as in k_combine.  Bound by HBM (2 k + 2 bytes per output element): each
+// j in order, fp32, one rounding at the end.  inv (nullable): the permutation's inverse map, -1 for a pair left
+// out; by_expert: Y is in expert order, inv[t*k + j] the row.  Bound by HBM (2 k + 2 bytes per output element): each
 // thread loads its 8 columns of up to 8 rows before their use, with no index arithmetic between them
 // (the general kernel's per-row divisions made it 209 us for 65536 x 4096 rows).
 constexpr int kCombineRows = 8;
 __global__ void __launch_bounds__(256) k_combine_bf16(const uint4* __restrict__ Y, const float* __restrict__ w,
-                                                      const int32_t* __restrict__ inv,
-                                                      const int32_t* __restrict__ ids, int E, int T, int k,
+                                                      const int32_t* __restrict__ inv, int by_expert, int T, int k,
                                                       int vec_per_row, uint4* __restrict__ out) {
   pdl_enter();
   const int v = blockIdx.y * 256 + threadIdx.x;
@@ -715,13 +715,10 @@ __global__ void __launch_bounds__(256) k_combine_bf16(const uint4* __restrict__ 
 #pragma unroll
       for (int j = 0; j < kCombineRows; ++j) {
         const int f = t * k + j0 + j;
-        const int row = j0 + j < k ? (inv ? inv[f] : f) : -1;
-        bool in = row >= 0;
+        int row = j0 + j < k ? (inv ? inv[f] : f) : -1;
+        const bool in = row >= 0;
+        if (!by_expert) row = f;
         u[j] = in ? __ldcs(Y + (size_t)row * vec_per_row + v) : make_uint4(0, 0, 0, 0);
-        if (in && !inv && !pair_kept(ids, f, E)) {
-          in = false;
-          u[j] = make_uint4(0, 0, 0, 0);
-        }
         wj[j] = in ? wt[j0 + j] : 0.0f;
       }
 #pragma unroll
@@ -909,13 +906,13 @@ static cudaError_t combine_vec(const void* Y, int splits, size_t split_stride, c
 }
 
 cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_stride, const float* w, int T, int k,
-                           int H, void* out, int out_bf16, cudaStream_t s, const int32_t* inv, const int32_t* ids,
-                           int E) {
-  if (inv && !(y_bf16 && out_bf16 && splits == 1 && H % 8 == 0)) return cudaErrorInvalidValue;
-  if (y_bf16 && out_bf16 && splits == 1 && H % 8 == 0) {
+                           int H, void* out, int out_bf16, cudaStream_t s, bool by_expert, const int32_t* ids, int E) {
+  const bool rows_bf16 = y_bf16 && out_bf16 && splits == 1 && H % 8 == 0;
+  if (by_expert ? !(rows_bf16 && ids) : rows_bf16 && ids && E != INT32_MAX) return cudaErrorInvalidValue;
+  if (rows_bf16) {
     const int vpr = H / 8, cols = (vpr + 255) / 256;
     MOE_LAUNCH(k_combine_bf16, dim3(std::min(T, std::max(1, 152 * 16 / cols)), cols), dim3(256), 0, s, (const uint4*)Y, w,
-               inv, ids, E, T, k, vpr, (uint4*)out);
+               ids, by_expert ? 1 : 0, T, k, vpr, (uint4*)out);
     return cudaGetLastError();
   }
   if (H % 8 == 0) {
