@@ -596,8 +596,9 @@ __global__ void k_quant_act(const float4* __restrict__ A, int vec_per_row, const
 // then the k routed outputs accumulated in j order, fp32, one rounding at the
 // end.  8 consecutive h per thread; the loads of four (j, s) rows are issued
 // before their use so each thread keeps 8 x 16 bytes in flight.
+template <bool GIVEN>
 __device__ __forceinline__ bool pair_kept(const int32_t* __restrict__ ids, size_t f, int E) {
-  return !ids || (unsigned)ids[f] < (unsigned)E;
+  return !GIVEN || (unsigned)ids[f] < (unsigned)E;
 }
 
 template <bool Y_BF16>
@@ -622,11 +623,12 @@ __device__ __forceinline__ void load8(const void* Yv, size_t idx, float (&y)[8])
 // slots j = g, g+G, ... (each one the sum of its K-split partials, in split
 // order), then the G partial sums are added in a fixed butterfly.  The order of
 // every addition is fixed, so the result is the same on every run.
-// ids (nullable): a routing given by a caller, or the permutation's inverse map with E = INT_MAX.  A pair
+// GIVEN: ids is a routing given by a caller, or the permutation's inverse map with E = INT32_MAX.  A pair
 // whose entry is outside [0, E) was dropped from the permutation, nothing wrote its row, and it adds
 // nothing here.  (Its row is loaded all the same: it lies in Y, and the row's load then does not wait for
-// the entry's.)
-template <bool Y_BF16, bool OUT_BF16, int G>
+// the entry's.  The look at the entries takes 0.3 us of a decode batch, which the router's own ids, always in
+// range, do not need.)
+template <bool Y_BF16, bool OUT_BF16, int G, bool GIVEN>
 __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, int splits, size_t split_stride,
                                                  const float* __restrict__ w, const int32_t* __restrict__ ids,
                                                  int E, int T, int k, int H, void* __restrict__ out) {
@@ -649,7 +651,7 @@ __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, in
         const int r = r0 + q;
         if (r < rows) {
           const int j = g + (r / splits) * G, sp = r % splits;
-          has[q] = pair_kept(ids, (size_t)t * k + j, E);
+          has[q] = pair_kept<GIVEN>(ids, (size_t)t * k + j, E);
           load8<Y_BF16>(Yv, (size_t)sp * split_stride + ((size_t)t * k + j) * H + h, y[q]);
         }
       }
@@ -749,7 +751,7 @@ __global__ void k_combine_scalar(const void* __restrict__ Yv, int splits, size_t
     float acc = 0.f;
     for (int j = 0; j < k; ++j) {
       const size_t f = (size_t)t * k + j;
-      if (!pair_kept(ids, f, E)) continue;
+      if (ids && !pair_kept<true>(ids, f, E)) continue;
       float y = 0.f;
       for (int s = 0; s < splits; ++s) {
         if constexpr (Y_BF16)
@@ -893,16 +895,23 @@ int combine_lanes(int T, int H, int k) {
   return vecs >= (size_t)152 * 2048 ? 1 : (k >= 4 ? 4 : (k >= 2 ? 2 : 1));
 }
 
-template <bool YB, bool OB>
+template <bool YB, bool OB, bool GIVEN>
 static cudaError_t combine_vec(const void* Y, int splits, size_t split_stride, const float* w, const int32_t* ids,
                                int E, int T, int k, int H, void* out, cudaStream_t s) {
   const int G = combine_lanes(T, H, k);
   const size_t vecs = (size_t)T * (H / 8);
-  const int grid = grid_for(vecs * G, 256);
-  if (G == 4) MOE_LAUNCH(k_combine<YB, OB, 4>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
-  else if (G == 2) MOE_LAUNCH(k_combine<YB, OB, 2>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
-  else MOE_LAUNCH(k_combine<YB, OB, 1>, dim3(grid), dim3(256), 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
+  const dim3 grid(grid_for(vecs * G, 256)), block(256);
+  if (G == 4) MOE_LAUNCH((k_combine<YB, OB, 4, GIVEN>), grid, block, 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
+  else if (G == 2) MOE_LAUNCH((k_combine<YB, OB, 2, GIVEN>), grid, block, 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
+  else MOE_LAUNCH((k_combine<YB, OB, 1, GIVEN>), grid, block, 0, s, Y, splits, split_stride, w, ids, E, T, k, H, out);
   return cudaGetLastError();
+}
+
+template <bool YB, bool OB>
+static cudaError_t combine_vec(const void* Y, int splits, size_t split_stride, const float* w, const int32_t* ids,
+                               int E, int T, int k, int H, void* out, cudaStream_t s) {
+  return ids ? combine_vec<YB, OB, true>(Y, splits, split_stride, w, ids, E, T, k, H, out, s)
+             : combine_vec<YB, OB, false>(Y, splits, split_stride, w, ids, E, T, k, H, out, s);
 }
 
 cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_stride, const float* w, int T, int k,
