@@ -170,10 +170,27 @@ def _p(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
-def _out(t: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
+def _empty(shape, dtype: torch.dtype, device, stream, zero: bool = False) -> torch.Tensor:
+    """A new tensor for a call on `stream`.
+
+    Beside the current stream its memory is that stream's own, and goes back only after the current stream's
+    work too: torch would else hand it to the current stream's next tensor while the call still runs."""
+    make = torch.zeros if zero else torch.empty
+    if stream is not None and torch.device(device).type == "cuda":
+        handle, current = _stream(stream), torch.cuda.current_stream(device)
+        if handle != current.cuda_stream:
+            side = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+            with torch.cuda.stream(side):
+                t = make(shape, dtype=dtype, device=device)
+            t.record_stream(current)
+            return t
+    return make(shape, dtype=dtype, device=device)
+
+
+def _out(t: Optional[torch.Tensor], shape, dtype, device, stream) -> torch.Tensor:
     """The caller's output tensor, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype, device, stream)
     if t.shape != shape or (t.dtype != dtype and not (dtype == torch.float8_e4m3fn and t.dtype == torch.uint8)):
         raise ValueError(f"an output must be {dtype} {tuple(shape)}")
     return t
@@ -235,9 +252,9 @@ def moe_route(hidden: torch.Tensor, router_w: torch.Tensor, topk: int, renorm: b
     T, H = hidden.shape
     E = router_w.shape[0]
     dev = hidden.device
-    logits = torch.empty(T, E, dtype=torch.float32, device=dev) if logits is None else logits
-    topk_w = torch.empty(T, topk, dtype=torch.float32, device=dev) if topk_w is None else topk_w
-    topk_ids = torch.empty(T, topk, dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
+    logits = _empty((T, E), torch.float32, dev, stream) if logits is None else logits
+    topk_w = _empty((T, topk), torch.float32, dev, stream) if topk_w is None else topk_w
+    topk_ids = _empty((T, topk), torch.int32, dev, stream) if topk_ids is None else topk_ids
     _check(_lib.moe_route(_p(hidden), _p(router_w), T, H, E, topk, int(bool(renorm)), _dt(hidden), _p(logits),
                           _p(topk_w), _p(topk_ids), _stream(stream)), "moe_route")
     return logits, topk_w, topk_ids
@@ -246,8 +263,8 @@ def moe_route(hidden: torch.Tensor, router_w: torch.Tensor, topk: int, renorm: b
 def moe_topk_from_logits(logits: torch.Tensor, topk: int, renorm: bool, topk_w=None, topk_ids=None, stream=None):
     T, E = logits.shape
     dev = logits.device
-    topk_w = torch.empty(T, topk, dtype=torch.float32, device=dev) if topk_w is None else topk_w
-    topk_ids = torch.empty(T, topk, dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
+    topk_w = _empty((T, topk), torch.float32, dev, stream) if topk_w is None else topk_w
+    topk_ids = _empty((T, topk), torch.int32, dev, stream) if topk_ids is None else topk_ids
     _check(_lib.moe_topk_from_logits(_p(logits), T, E, topk, int(bool(renorm)), _p(topk_w), _p(topk_ids),
                                      _stream(stream)), "moe_topk_from_logits")
     return topk_w, topk_ids
@@ -272,8 +289,8 @@ def moe_topk_grouped(logits: torch.Tensor, topk: int, bias=None, score: str = "s
     if logits.dtype != torch.float32 or (bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,))):
         raise ValueError("logits must be float32 [T, E] and bias float32 [E]")
     dev = logits.device
-    topk_w = _out(topk_w, (T, topk), torch.float32, dev)
-    topk_ids = _out(topk_ids, (T, topk), torch.int32, dev)
+    topk_w = _out(topk_w, (T, topk), torch.float32, dev, stream)
+    topk_ids = _out(topk_ids, (T, topk), torch.int32, dev, stream)
     rule = _route_rule(score, n_group, topk_group, group_sum, renorm, scale)
     _check(_lib.moe_topk_grouped(_p(logits), _p(bias), T, E, topk, ctypes.byref(rule), _p(topk_w), _p(topk_ids),
                                  _stream(stream)), "moe_topk_grouped")
@@ -290,9 +307,9 @@ def moe_route_grouped(hidden: torch.Tensor, router_w: torch.Tensor, topk: int, b
             bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,))):
         raise ValueError("router_w must be [E, H] of hidden's type and bias float32 [E]")
     dev = hidden.device
-    logits = _out(logits, (T, E), torch.float32, dev)
-    topk_w = _out(topk_w, (T, topk), torch.float32, dev)
-    topk_ids = _out(topk_ids, (T, topk), torch.int32, dev)
+    logits = _out(logits, (T, E), torch.float32, dev, stream)
+    topk_w = _out(topk_w, (T, topk), torch.float32, dev, stream)
+    topk_ids = _out(topk_ids, (T, topk), torch.int32, dev, stream)
     rule = _route_rule(score, n_group, topk_group, group_sum, renorm, scale)
     _check(_lib.moe_route_grouped(_p(hidden), _p(router_w), _p(bias), T, H, E, topk, ctypes.byref(rule), _dt(hidden),
                                   _p(logits), _p(topk_w), _p(topk_ids), _stream(stream)), "moe_route_grouped")
@@ -302,8 +319,8 @@ def moe_route_grouped(hidden: torch.Tensor, router_w: torch.Tensor, topk: int, b
 def moe_quant_block(x: torch.Tensor, q=None, scale=None, stream=None):
     """e4m3 codes [T,K] (float8_e4m3fn) and float32 scales [T,ceil(K/128)] of x [T,K] by blocks of 128 columns."""
     T, K = x.shape
-    q = _out(q, (T, K), torch.float8_e4m3fn, x.device)
-    scale = _out(scale, (T, (K + 127) // 128), torch.float32, x.device)
+    q = _out(q, (T, K), torch.float8_e4m3fn, x.device, stream)
+    scale = _out(scale, (T, (K + 127) // 128), torch.float32, x.device, stream)
     _check(_lib.moe_quant_block(_p(x), T, K, _dt(x), _p(q), _p(scale), _stream(stream)), "moe_quant_block")
     return q, scale
 
@@ -315,8 +332,8 @@ def moe_silu_quant_block(gate_up: torch.Tensor, q=None, scale=None, stream=None)
         raise ValueError("gate_up must be [T, 2 I]")
     I = two_i // 2
     dev = gate_up.device
-    q = _out(q, (T, I), torch.float8_e4m3fn, dev)
-    scale = _out(scale, (T, (I + 127) // 128), torch.float32, dev)
+    q = _out(q, (T, I), torch.float8_e4m3fn, dev, stream)
+    scale = _out(scale, (T, (I + 127) // 128), torch.float32, dev, stream)
     _check(_lib.moe_silu_quant_block(_p(gate_up), T, I, _dt(gate_up), _p(q), _p(scale), _stream(stream)),
            "moe_silu_quant_block")
     return q, scale
@@ -335,7 +352,7 @@ def moe_gemm_block(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_sc
     if _dt(a) != MOE_E4M3 or _dt(w) != MOE_E4M3 or a_scale.dtype != torch.float32 or w_scale.dtype != torch.float32:
         raise ValueError("a and w must be e4m3 codes with float32 scales")
     if out is None:
-        out = torch.empty(T, N, dtype=out_dtype, device=a.device)
+        out = _empty((T, N), out_dtype, a.device, stream)
     elif out.shape != (T, N):
         raise ValueError("out must be [T, N]")
     _check(_lib.moe_gemm_block(_p(a), _p(a_scale), _p(w), _p(w_scale), T, N, K, _dt(out), _p(out), _stream(stream)),
@@ -348,10 +365,10 @@ def moe_align(topk_ids: torch.Tensor, E: int, block: int, stream=None, with_coun
     T, k = topk_ids.shape
     cap, bcap = moe_align_capacity(T, k, E, block)
     dev = topk_ids.device
-    sorted_ids = torch.empty(max(cap, 1), dtype=torch.int32, device=dev)
-    expert_ids = torch.empty(max(bcap, 1), dtype=torch.int32, device=dev)
-    npp = torch.zeros(4, dtype=torch.int32, device=dev)
-    counts = torch.empty(E, dtype=torch.int32, device=dev) if with_counts else None
+    sorted_ids = _empty(max(cap, 1), torch.int32, dev, stream)
+    expert_ids = _empty(max(bcap, 1), torch.int32, dev, stream)
+    npp = _empty(4, torch.int32, dev, stream, zero=T == 0)  # (an empty batch launches nothing)
+    counts = _empty(E, torch.int32, dev, stream) if with_counts else None
     _check(_lib.moe_align(_p(topk_ids), T, k, E, block, _p(sorted_ids), _p(expert_ids), _p(npp), _p(counts),
                           _stream(stream)), "moe_align")
     return sorted_ids, expert_ids, npp[:1], counts
@@ -400,8 +417,8 @@ def moe_forward(hidden: torch.Tensor, router_w: torch.Tensor, w13: torch.Tensor,
     opts = _opts(options)
     need = moe_workspace_size(T, H, I, E, topk, act, wdt, options)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=hidden.device)
-    out = torch.empty_like(hidden) if out is None else out
+        workspace = _empty(need, torch.uint8, hidden.device, stream)
+    out = _empty(hidden.shape, hidden.dtype, hidden.device, stream) if out is None else out
     _check(_lib.moe_forward(_p(hidden), _p(router_w), _p(w13), _p(w2), T, H, I, E, topk, int(bool(renorm)), act, wdt,
                             _p(w13_scale), _p(w2_scale), _p(out), _p(workspace), workspace.numel(), opts,
                             _stream(stream)), "moe_forward")
@@ -426,8 +443,8 @@ def moe_forward_host(hidden_host: torch.Tensor, router_w: torch.Tensor, w13: tor
     act, wdt = _dt(hidden_host), _w_dtype(w13, w_format)
     need = moe_workspace_size(T, H, I, E, topk, act, wdt, options)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    hidden_dev = torch.empty(hidden_host.shape, dtype=hidden_host.dtype, device=dev) if hidden_dev is None else hidden_dev
+        workspace = _empty(need, torch.uint8, dev, stream)
+    hidden_dev = _empty(hidden_host.shape, hidden_host.dtype, dev, stream) if hidden_dev is None else hidden_dev
     out_host = torch.empty(hidden_host.shape, dtype=hidden_host.dtype).pin_memory() if out_host is None else out_host
     _check(_lib.moe_forward_host(_p(hidden_host), _p(hidden_dev), _p(router_w), _p(w13), _p(w2), T, H, I, E, topk,
                                  int(bool(renorm)), act, wdt, _p(w13_scale), _p(w2_scale), _p(out_host),
@@ -453,7 +470,7 @@ def moe_forward_noalloc(hidden: torch.Tensor, router_w: torch.Tensor, w13: torch
         raise ValueError("inconsistent shapes")
     _check_block_scales(w_format, E, H, I, w13, w2, w13_scale, w2_scale)
     wdt = _w_dtype(w13, w_format)
-    out = torch.empty_like(hidden) if out is None else out
+    out = _empty(hidden.shape, hidden.dtype, hidden.device, stream) if out is None else out
     _check(_lib.moe_forward_noalloc(_p(hidden), _p(router_w), _p(w13), _p(w2), T, H, I, E, topk, int(bool(renorm)),
                                     _dt(hidden), wdt, _p(w13_scale), _p(w2_scale), _p(out), _opts(options),
                                     _stream(stream)), "moe_forward_noalloc")
@@ -471,8 +488,8 @@ def moe_inv_rope_fp8_quant(x: torch.Tensor, positions: torch.Tensor, cos_sin: to
     T, heads, D = x.shape
     assert x.dtype == torch.bfloat16 and x.is_contiguous()
     dev = x.device
-    q_out = torch.empty(T, heads, D, dtype=torch.uint8, device=dev) if q_out is None else q_out
-    scale_out = torch.empty(T, heads, dtype=torch.float32, device=dev) if scale_out is None else scale_out
+    q_out = _empty((T, heads, D), torch.uint8, dev, stream) if q_out is None else q_out
+    scale_out = _empty((T, heads), torch.float32, dev, stream) if scale_out is None else scale_out
     _check(_lib.moe_inv_rope_fp8_quant(_p(x), T, heads, D, int(rot_dim), _p(positions), _p(cos_sin),
                                        cos_sin.shape[0], _p(q_out), _p(scale_out), _stream(stream)),
            "moe_inv_rope_fp8_quant")
@@ -504,9 +521,8 @@ def moe_forward_routed(hidden: torch.Tensor, topk_w: torch.Tensor, topk_ids: tor
         opts = moe_options.from_buffer_copy(options) if isinstance(options, moe_options) else _opts(options)._obj
         opts.single_launch = 2
     if workspace is None:  # (a caller's own is checked by the library)
-        workspace = torch.empty(moe_workspace_size(T, H, I, E, k, act, wdt, opts), dtype=torch.uint8,
-                                device=hidden.device)
-    out = torch.empty_like(hidden) if out is None else out
+        workspace = _empty(moe_workspace_size(T, H, I, E, k, act, wdt, opts), torch.uint8, hidden.device, stream)
+    out = _empty(hidden.shape, hidden.dtype, hidden.device, stream) if out is None else out
     _check(_lib.moe_forward_routed(_p(hidden), _p(topk_w), _p(topk_ids), _p(w13), _p(w2), T, H, I, E, k, act, wdt,
                                    _p(w13_scale), _p(w2_scale), _p(out), _p(workspace), workspace.numel(),
                                    ctypes.byref(opts), _stream(stream)), "moe_forward_routed")
@@ -559,9 +575,8 @@ class ExpertCache:
                 options=None, stream=None) -> torch.Tensor:
         T = hidden.shape[0]
         if workspace is None:
-            workspace = torch.empty(self.workspace_size(T, _dt(hidden), options), dtype=torch.uint8,
-                                    device=hidden.device)
-        out = torch.empty_like(hidden) if out is None else out
+            workspace = _empty(self.workspace_size(T, _dt(hidden), options), torch.uint8, hidden.device, stream)
+        out = _empty(hidden.shape, hidden.dtype, hidden.device, stream) if out is None else out
         _check(_lib.moe_forward_cached(self._h, _p(hidden), _p(router_w), T, int(bool(renorm)), _dt(hidden), _p(out),
                                        _p(workspace), workspace.numel(), _opts(options), _stream(stream)),
                "moe_forward_cached")
