@@ -368,7 +368,7 @@ def moe_align(topk_ids: torch.Tensor, E: int, block: int, stream=None, with_coun
     sorted_ids = _empty(max(cap, 1), torch.int32, dev, stream)
     expert_ids = _empty(max(bcap, 1), torch.int32, dev, stream)
     npp = _empty(4, torch.int32, dev, stream, zero=T == 0)  # (an empty batch launches nothing)
-    counts = _empty(E, torch.int32, dev, stream) if with_counts else None
+    counts = _empty(E, torch.int32, dev, stream, zero=T == 0) if with_counts else None
     _check(_lib.moe_align(_p(topk_ids), T, k, E, block, _p(sorted_ids), _p(expert_ids), _p(npp), _p(counts),
                           _stream(stream)), "moe_align")
     return sorted_ids, expert_ids, npp[:1], counts

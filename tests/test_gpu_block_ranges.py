@@ -61,6 +61,13 @@ def test_permutation_of_many_pairs(moe, T, k, E, block, skew):
     assert np.array_equal(counts.cpu().numpy(), rc)
 
 
+def test_permutation_of_an_empty_batch(moe):
+    junk = torch.full((4096,), 7, dtype=torch.int32, device="cuda")  # (what new memory would hold)
+    del junk
+    _, _, npp, counts = moe.moe_align(torch.empty(0, 2, dtype=torch.int32, device="cuda"), 1024, 16)
+    assert int(npp) == 0 and (counts == 0).all()
+
+
 # ---- expert layer ----------------------------------------------------------------------------------
 
 LAYERS = [
