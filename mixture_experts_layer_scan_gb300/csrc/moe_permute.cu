@@ -698,13 +698,14 @@ __global__ void __launch_bounds__(256) k_combine(const void* __restrict__ Yv, in
 
 // out[t] = sum_j w[t][j] * Y[t*k + j] for bf16 rows without K splits (the block-scaled expert layer):
 // j in order, fp32, one rounding at the end.  inv (nullable): the permutation's inverse map, -1 for a pair left
-// out; by_expert: Y is in expert order, inv[t*k + j] the row.  Bound by HBM (2 k + 2 bytes per output element): each
+// out; BY_EXPERT (with inv): Y is in expert order, inv[t*k + j] the row.  Bound by HBM (2 k + 2 bytes per output element): each
 // thread loads its 8 columns of up to 8 rows before their use, with no index arithmetic between them
 // (the general kernel's per-row divisions made it 209 us for 65536 x 4096 rows).
 constexpr int kCombineRows = 8;
+template <bool BY_EXPERT>
 __global__ void __launch_bounds__(256) k_combine_bf16(const uint4* __restrict__ Y, const float* __restrict__ w,
-                                                      const int32_t* __restrict__ inv, int by_expert, int T, int k,
-                                                      int vec_per_row, uint4* __restrict__ out) {
+                                                      const int32_t* __restrict__ inv, int T, int k, int vec_per_row,
+                                                      uint4* __restrict__ out) {
   pdl_enter();
   const int v = blockIdx.y * 256 + threadIdx.x;
   if (v >= vec_per_row) return;
@@ -717,9 +718,9 @@ __global__ void __launch_bounds__(256) k_combine_bf16(const uint4* __restrict__ 
 #pragma unroll
       for (int j = 0; j < kCombineRows; ++j) {
         const int f = t * k + j0 + j;
-        int row = j0 + j < k ? (inv ? inv[f] : f) : -1;
-        const bool in = row >= 0;
-        if (!by_expert) row = f;
+        const int at = j0 + j < k ? (BY_EXPERT || inv ? inv[f] : f) : -1;
+        const bool in = at >= 0;
+        const int row = BY_EXPERT ? at : f;
         u[j] = in ? __ldcs(Y + (size_t)row * vec_per_row + v) : make_uint4(0, 0, 0, 0);
         wj[j] = in ? wt[j0 + j] : 0.0f;
       }
@@ -920,8 +921,9 @@ cudaError_t launch_combine(const void* Y, int y_bf16, int splits, size_t split_s
   if (by_expert ? !(rows_bf16 && ids) : rows_bf16 && ids && E != INT32_MAX) return cudaErrorInvalidValue;
   if (rows_bf16) {
     const int vpr = H / 8, cols = (vpr + 255) / 256;
-    MOE_LAUNCH(k_combine_bf16, dim3(std::min(T, std::max(1, 152 * 16 / cols)), cols), dim3(256), 0, s, (const uint4*)Y, w,
-               ids, by_expert ? 1 : 0, T, k, vpr, (uint4*)out);
+    const dim3 grid(std::min(T, std::max(1, 152 * 16 / cols)), cols), block(256);
+    if (by_expert) MOE_LAUNCH(k_combine_bf16<true>, grid, block, 0, s, (const uint4*)Y, w, ids, T, k, vpr, (uint4*)out);
+    else MOE_LAUNCH(k_combine_bf16<false>, grid, block, 0, s, (const uint4*)Y, w, ids, T, k, vpr, (uint4*)out);
     return cudaGetLastError();
   }
   if (H % 8 == 0) {
