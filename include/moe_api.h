@@ -377,6 +377,95 @@ MOE_API int moe_silu_quant_block(const void* gate_up, int T, int I, moe_dtype x_
 MOE_API int moe_gemm_block(const void* a, const float* a_scale, const void* w, const float* w_scale, int T, int N,
                            int K, moe_dtype out_dtype, void* out, moe_stream_t stream);
 
+/* Rows of tokens in expert order and back, for experts of the caller's own (moe_forward does the same inside
+ * for its SiLU-gated ones), with gradients.
+ *
+ * moe_permute: moe_align's permutation of topk_ids and the rows in its order:
+ *   rows[row_of[t][j]] = x[t] for every pair with an expert id in [0, E); padding rows (sentinel entries of
+ *   sorted_ids) below *num_post_pad are zero; rows from *num_post_pad on are left as they were.
+ *   row_of [T][topk] int32: the row of each pair, -1 for a pair whose id is out of range (dropped and flagged
+ *   MOE_ERR_DEVICE_INDEX).  rows [sorted_cap][H], the maps and their capacities as moe_align's
+ *   (expert_counts nullable).  A token may name an expert more than once.
+ * moe_unpermute: out[t] = sum_j topk_w[t][j] * rows[row_of[t][j]], summed in fp32 in the order of j and rounded
+ *   once; topk_w null: weights of 1.  rows [n_rows][H]; a pair whose entry of row_of lies outside
+ *   [0, n_rows) has no row and adds nothing.
+ * moe_permute_backward: d_x[t] = sum_j d_rows[row_of[t][j]], likewise.
+ * moe_unpermute_backward: d_rows[row_of[t][j]] = topk_w[t][j] * d_out[t] (rounded once) and
+ *   d_w[t][j] = <d_out[t], rows[row_of[t][j]]> (fp32, 0 for a pair without a row).  d_rows or d_w may be null
+ *   (not computed); rows may be null without d_w.  With sorted_ids and num_post_pad (both or neither) padding
+ *   rows of d_rows below *num_post_pad become zero; other rows that no pair names are left as they were.  The
+ *   entries of row_of in range have to differ.  d_rows may be rows.
+ * x, rows, out, d_x, d_out and d_rows have `dtype` (MOE_F32 or MOE_BF16); weights and d_w are fp32.  Any H >= 1.
+ * topk_w, row_of and d_w 4-byte aligned, the other pointers 16.  Limits as moe_align; n_rows >= 0. */
+MOE_API int moe_permute(const void* x, const int32_t* topk_ids, int T, int H, int E, int topk, int block,
+                        moe_dtype dtype, void* rows, int32_t* row_of, int32_t* sorted_ids, int32_t* expert_ids,
+                        int32_t* num_post_pad, int32_t* expert_counts, moe_stream_t stream);
+MOE_API int moe_unpermute(const void* rows, int n_rows, const int32_t* row_of, const float* topk_w, int T, int H,
+                          int topk, moe_dtype dtype, void* out, moe_stream_t stream);
+MOE_API int moe_permute_backward(const void* d_rows, int n_rows, const int32_t* row_of, int T, int H, int topk,
+                                 moe_dtype dtype, void* d_x, moe_stream_t stream);
+MOE_API int moe_unpermute_backward(const void* d_out, const void* rows, int n_rows, const int32_t* row_of,
+                                   const float* topk_w, const int32_t* sorted_ids, const int32_t* num_post_pad, int T,
+                                   int H, int topk, moe_dtype dtype, void* d_rows, float* d_w, moe_stream_t stream);
+
+/* The norms before and after a block (RMS norms), with the block's gate and residual scale, and their gradients.
+ *
+ * moe_prenorm: h[t] = x[t] * r * w, r = (mean(x[t]^2) + eps)^(-1/2).
+ * moe_postnorm, for a block's output y beside its residual x:
+ *   v = y * r_y * post_w (r_y as r above; post_w null: v = y),  G = gate or sigmoid(gate) (1 without a gate),
+ *   out = res_scale * x + scale * G * v,
+ *   h = out * r_o * next_w, the next block's prenorm, from out before it is rounded (next_w null: no h).
+ *   gate: MOE_GATE_CHANNEL [H], MOE_GATE_TOKEN [T] or MOE_GATE_FULL [T][H], of type gate_dtype.
+ *   out may be x or y, and h the other of them.
+ * Gradients: from d_h [T][H] and d_out [T][H] (either may be null: zero; moe_prenorm_backward needs d_h; d_h
+ * without next_w is refused) the gradients of x, y (required), the weights, and the gate (nullable: not wanted).
+ *   d_w, d_post_w, d_next_w and a channel gate's d_gate are fp32 [H], a token gate's fp32 [T], a full gate's
+ *   [T][H] of gate_dtype.  Sums over tokens are fp32 in a fixed order.  d_x and d_y may take the places of x, y,
+ *   d_out and d_h.  The forward pass is recomputed: nothing has to be kept but its inputs.
+ *   T = 0: the weights' gradients (and a channel gate's) are set to zero.
+ * x, y, out, h, d_* of tokens have `dtype` (MOE_F32 or MOE_BF16); the weights w_dtype, either of the two as well.
+ * Arithmetic is fp32 throughout, every result rounded once.  1 <= H <= 16384 (MOE_ERR_UNSUPPORTED above).
+ * The gradients' workspace: moe_norm_workspace_size bytes, 256-byte aligned, contents ignored (the same for both
+ * calls).  A token gate and its gradient 4-byte aligned, the other pointers 16. */
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 };
+typedef struct {
+  float eps;           /* >= 0 */
+  float scale;         /* of the block's branch */
+  float res_scale;     /* of the residual */
+  int gate;            /* MOE_GATE_*; the gate pointer is null exactly for MOE_GATE_NONE */
+  int gate_sigmoid;
+  moe_dtype gate_dtype;
+  moe_dtype w_dtype;   /* of post_w and next_w */
+} moe_postnorm_rule;
+MOE_API int moe_prenorm(const void* x, const void* w, int T, int H, float eps, moe_dtype dtype, moe_dtype w_dtype,
+                        void* h, moe_stream_t stream);
+MOE_API int moe_norm_workspace_size(int T, int H, size_t* bytes);
+MOE_API int moe_prenorm_backward(const void* d_h, const void* x, const void* w, int T, int H, float eps, moe_dtype dtype,
+                                 moe_dtype w_dtype, void* d_x, float* d_w, void* workspace, size_t workspace_bytes,
+                                 moe_stream_t stream);
+MOE_API int moe_postnorm(const void* x, const void* y, const void* post_w, const void* gate, const void* next_w, int T,
+                         int H, moe_dtype dtype, const moe_postnorm_rule* rule, void* out, void* h,
+                         moe_stream_t stream);
+MOE_API int moe_postnorm_backward(const void* d_out, const void* d_h, const void* x, const void* y, const void* post_w,
+                                  const void* gate, const void* next_w, int T, int H, moe_dtype dtype,
+                                  const moe_postnorm_rule* rule, void* d_x, void* d_y, float* d_post_w, void* d_gate,
+                                  float* d_next_w, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Low-rank adapters of many requests at once, beside a projection that all of them share (moe_gemm_block):
+ *   out[t] = base[t] + scale[l] * b[l] . (a[l] . x[t]),  l = ids[t];  out[t] = base[t] where ids[t] is -1
+ *   x [T][K], a [L][rank][K], b [L][N][rank] bf16;  ids [T] int32, in any order;  scale [L] fp32 (null: 1);
+ *   base [T][N] of out's type, the projection's output (null: 0; may be out itself);  out [T][N] MOE_BF16 or MOE_F32
+ * Sums are fp32, out is rounded once.  An id outside [-1, L) counts as -1 and is flagged MOE_ERR_DEVICE_INDEX.
+ * An adapter of lower rank is padded with zero rows of a and zero columns of b.  An adapter that no token names
+ * is not read.
+ * T >= 0, K, N, rank, L >= 1; rank <= 128 and K, N, rank multiples of 8 (MOE_ERR_UNSUPPORTED otherwise); T, K
+ * and N below 2^31 - 2^24, L <= 1024.  workspace: moe_lora_workspace_size bytes, 256-byte aligned, contents
+ * ignored; ids and scale 4-byte aligned, the other pointers 16.  No gradient: for serving. */
+MOE_API int moe_lora_workspace_size(int T, int K, int N, int rank, int L, size_t* bytes);
+MOE_API int moe_lora(const void* x, const void* a, const void* b, const int32_t* ids, const float* scale,
+                     const void* base, int T, int K, int N, int rank, int L, moe_dtype out_dtype, void* out,
+                     void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /* Steps 3-7 of the layer on a routing the caller provides (its own router, or
  * expert ids remapped to the slots of an expert cache): the same permutation,
  * expert GEMMs and combine as moe_forward, which it matches bit for bit given

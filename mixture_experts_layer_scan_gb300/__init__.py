@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -34,7 +34,9 @@ EXPORTS = ("moe_strerror", "moe_workspace_size", "moe_plan_info", "moe_align_cap
            "moe_version", "moe_inv_rope_fp8_quant", "moe_forward_routed", "moe_cache_create", "moe_cache_destroy",
            "moe_cache_workspace_size", "moe_forward_cached", "moe_cache_stats", "moe_cache_lru_plan",
            "moe_cache_set_copy_mode", "moe_copy_from_host", "moe_forward_host", "moe_topk_grouped",
-           "moe_route_grouped", "moe_quant_block", "moe_silu_quant_block", "moe_gemm_block")
+           "moe_route_grouped", "moe_quant_block", "moe_silu_quant_block", "moe_gemm_block", "moe_permute",
+           "moe_unpermute", "moe_permute_backward", "moe_unpermute_backward", "moe_prenorm", "moe_norm_workspace_size",
+           "moe_prenorm_backward", "moe_postnorm", "moe_postnorm_backward", "moe_lora_workspace_size", "moe_lora")
 NOALLOC_MAX_WORKSPACE = 32 << 20
 
 
@@ -63,6 +65,13 @@ class moe_route_rule(ctypes.Structure):
 
 
 SCORES = {"softmax": 0, "sigmoid": 1}
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+
+
+class moe_postnorm_rule(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("scale", ctypes.c_float), ("res_scale", ctypes.c_float),
+                ("gate", ctypes.c_int), ("gate_sigmoid", ctypes.c_int), ("gate_dtype", ctypes.c_int),
+                ("w_dtype", ctypes.c_int)]
 
 
 class moe_cache_stats_t(ctypes.Structure):
@@ -132,6 +141,20 @@ def _load():
     lib.moe_silu_quant_block.argtypes = [P, i, i, i, P, P, P]
     lib.moe_gemm_block.restype = i
     lib.moe_gemm_block.argtypes = [P, P, P, P, i, i, i, i, P, P]
+    f, rule = ctypes.c_float, ctypes.POINTER(moe_postnorm_rule)
+    for name, args in (("moe_permute", [P, P, i, i, i, i, i, i, P, P, P, P, P, P, P]),
+                       ("moe_unpermute", [P, i, P, P, i, i, i, i, P, P]),
+                       ("moe_permute_backward", [P, i, P, i, i, i, i, P, P]),
+                       ("moe_unpermute_backward", [P, P, i, P, P, P, P, i, i, i, i, P, P, P]),
+                       ("moe_prenorm", [P, P, i, i, f, i, i, P, P]),
+                       ("moe_norm_workspace_size", [i, i, ctypes.POINTER(sz)]),
+                       ("moe_prenorm_backward", [P, P, P, i, i, f, i, i, P, P, P, sz, P]),
+                       ("moe_postnorm", [P, P, P, P, P, i, i, i, rule, P, P, P]),
+                       ("moe_postnorm_backward", [P] * 7 + [i, i, i, rule] + [P] * 6 + [sz, P]),
+                       ("moe_lora_workspace_size", [i, i, i, i, i, ctypes.POINTER(sz)]),
+                       ("moe_lora", [P] * 6 + [i] * 6 + [P, P, sz, P])):
+        getattr(lib, name).restype = i
+        getattr(lib, name).argtypes = args
     return lib
 
 
@@ -372,6 +395,266 @@ def moe_align(topk_ids: torch.Tensor, E: int, block: int, stream=None, with_coun
     _check(_lib.moe_align(_p(topk_ids), T, k, E, block, _p(sorted_ids), _p(expert_ids), _p(npp), _p(counts),
                           _stream(stream)), "moe_align")
     return sorted_ids, expert_ids, npp[:1], counts
+
+
+def _same_device(x: torch.Tensor, *others) -> None:
+    """The arrays of a call lie on the current CUDA device (the library reads their addresses as that device's)."""
+    d = x.get_device()
+    if d < 0 or d != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError("tensors must be on the current CUDA device")
+
+
+_ACTS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _act(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in _ACTS:
+        raise ValueError(f"{what} must be float32 or bfloat16")
+    return _ACTS[t.dtype]
+
+
+def _like(t: Optional[torch.Tensor], shape, dtype, what: str) -> None:
+    """An optional argument's shape and type."""
+    if t is not None and (t.shape != shape or t.dtype != dtype):
+        raise ValueError(f"{what} must be {dtype} {tuple(shape)}")
+
+
+class PermutedRows(NamedTuple):
+    """Rows in expert order (moe_permute): rows [cap,H]; row_of int32 [T,k], the row of each pair (-1: none); and
+    moe_align's maps: sorted_ids [cap], expert_ids [cap/block], num_post_pad [1], expert_counts [E]."""
+    rows: torch.Tensor
+    row_of: torch.Tensor
+    sorted_ids: torch.Tensor
+    expert_ids: torch.Tensor
+    num_post_pad: torch.Tensor
+    expert_counts: torch.Tensor
+
+
+def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, E: int, block: int = 1, rows=None, stream=None) -> PermutedRows:
+    """Rows of x [T,H] (float32 or bfloat16) in expert order, each expert's run padded with zero rows to a multiple of
+    block; rows behind the last run are left as they were (rows=: a buffer of [cap,H], moe_align_capacity's cap)."""
+    T, H = x.shape
+    dt = _act(x, "x")
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T or topk_ids.dtype != torch.int32:
+        raise ValueError("topk_ids must be int32 [T, k]")
+    _same_device(x, topk_ids, rows)
+    k = topk_ids.shape[1]
+    cap, bcap = moe_align_capacity(T, k, E, block)
+    dev = x.device
+    rows = _out(rows, (cap, H), x.dtype, dev, stream)
+    # (one allocation for the maps, each at a multiple of 16 bytes)
+    sizes = [T * k, cap, bcap, 1, E]
+    at, end = [], 0
+    for n in sizes:
+        at.append(end)
+        end += (n + 3) // 4 * 4
+    maps = _empty(end, torch.int32, dev, stream, zero=T == 0)  # (an empty batch launches nothing)
+    row_of, sorted_ids, expert_ids, npp, counts = (maps[a:a + n] for a, n in zip(at, sizes))
+    p = maps.data_ptr()
+    _check(_lib.moe_permute(_p(x), _p(topk_ids), T, H, E, k, block, dt, _p(rows), *(p + 4 * a for a in at),
+                            _stream(stream)), "moe_permute")
+    return PermutedRows(rows, row_of.view(T, k), sorted_ids, expert_ids, npp, counts)
+
+
+def _row_map(row_of: torch.Tensor, rows: torch.Tensor, topk_w=None):
+    if row_of.dim() != 2 or row_of.dtype != torch.int32 or rows.dim() != 2:
+        raise ValueError("row_of must be int32 [T, k] and rows [n, H]")
+    _like(topk_w, row_of.shape, torch.float32, "topk_w")
+    return row_of.shape[0], row_of.shape[1], rows.shape[0], rows.shape[1]
+
+
+def moe_unpermute(rows: torch.Tensor, row_of: torch.Tensor, topk_w: Optional[torch.Tensor] = None, out=None,
+                  stream=None) -> torch.Tensor:
+    """out [T,H] = sum over j of topk_w[t,j] * rows[row_of[t,j]] (topk_w float32 [T,k]; None: weights of 1)."""
+    T, k, n, H = _row_map(row_of, rows, topk_w)
+    dt = _act(rows, "rows")
+    _same_device(rows, row_of, topk_w, out)
+    out = _out(out, (T, H), rows.dtype, rows.device, stream)
+    _check(_lib.moe_unpermute(_p(rows), n, _p(row_of), _p(topk_w), T, H, k, dt, _p(out), _stream(stream)),
+           "moe_unpermute")
+    return out
+
+
+def moe_permute_backward(d_rows: torch.Tensor, row_of: torch.Tensor, d_x=None, stream=None) -> torch.Tensor:
+    """Gradient of moe_permute in x: d_x [T,H] = sum over j of d_rows[row_of[t,j]]."""
+    T, k, n, H = _row_map(row_of, d_rows)
+    dt = _act(d_rows, "d_rows")
+    _same_device(d_rows, row_of, d_x)
+    d_x = _out(d_x, (T, H), d_rows.dtype, d_rows.device, stream)
+    _check(_lib.moe_permute_backward(_p(d_rows), n, _p(row_of), T, H, k, dt, _p(d_x), _stream(stream)),
+           "moe_permute_backward")
+    return d_x
+
+
+def moe_unpermute_backward(d_out: torch.Tensor, rows: torch.Tensor, row_of: torch.Tensor,
+                           topk_w: Optional[torch.Tensor] = None, sorted_ids=None, num_post_pad=None, d_rows=None,
+                           d_w=None, stream=None):
+    """Gradients of moe_unpermute: (d_rows [n,H], d_w float32 [T,k]).
+
+    With the permutation's sorted_ids and num_post_pad its padding rows become zero; rows of d_rows that no pair
+    names are else left as they were."""
+    T, k, n, H = _row_map(row_of, rows, topk_w)
+    dt = _act(rows, "rows")
+    if d_out.shape != (T, H) or d_out.dtype != rows.dtype:
+        raise ValueError("d_out must be [T, H] of rows' type")
+    if (sorted_ids is None) != (num_post_pad is None):
+        raise ValueError("sorted_ids and num_post_pad go together")
+    _like(sorted_ids, (n,), torch.int32, "sorted_ids")
+    _like(num_post_pad, (1,), torch.int32, "num_post_pad")
+    _same_device(d_out, rows, row_of, topk_w, sorted_ids, num_post_pad, d_rows, d_w)
+    d_rows = _out(d_rows, (n, H), rows.dtype, rows.device, stream)
+    d_w = _out(d_w, (T, k), torch.float32, rows.device, stream)
+    _check(_lib.moe_unpermute_backward(_p(d_out), _p(rows), n, _p(row_of), _p(topk_w), _p(sorted_ids), _p(num_post_pad),
+                                       T, H, k, dt, _p(d_rows), _p(d_w), _stream(stream)), "moe_unpermute_backward")
+    return d_rows, d_w
+
+
+def moe_prenorm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, h=None, stream=None) -> torch.Tensor:
+    """RMS norm of the rows of x [T,H] times w [H] (float32 or bfloat16, either with either)."""
+    T, H = x.shape
+    dt, wdt = _act(x, "x"), _act(w, "w")
+    if w.shape != (H,):
+        raise ValueError("w must be [H]")
+    _same_device(x, w, h)
+    h = _out(h, (T, H), x.dtype, x.device, stream)
+    _check(_lib.moe_prenorm(_p(x), _p(w), T, H, eps, dt, wdt, _p(h), _stream(stream)), "moe_prenorm")
+    return h
+
+
+def moe_norm_workspace_size(T: int, H: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_norm_workspace_size(T, H, ctypes.byref(n)), "moe_norm_workspace_size")
+    return int(n.value)
+
+
+def moe_prenorm_backward(d_h: torch.Tensor, x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, d_x=None, d_w=None,
+                         workspace=None, stream=None):
+    """Gradients of moe_prenorm: (d_x [T,H], d_w float32 [H])."""
+    T, H = x.shape
+    dt, wdt = _act(x, "x"), _act(w, "w")
+    if w.shape != (H,) or d_h.shape != (T, H) or d_h.dtype != x.dtype:
+        raise ValueError("w must be [H] and d_h [T, H] of x's type")
+    _same_device(x, d_h, w, d_x, d_w, workspace)
+    d_x = _out(d_x, (T, H), x.dtype, x.device, stream)
+    d_w = _out(d_w, (H,), torch.float32, x.device, stream)
+    if workspace is None:
+        workspace = _empty(moe_norm_workspace_size(T, H), torch.uint8, x.device, stream)
+    _check(_lib.moe_prenorm_backward(_p(d_h), _p(x), _p(w), T, H, eps, dt, wdt, _p(d_x), _p(d_w), _p(workspace),
+                                     workspace.numel(), _stream(stream)), "moe_prenorm_backward")
+    return d_x, d_w
+
+
+def _postnorm(x, y, post_w, gate, sigmoid, scale, res_scale, next_w, eps):
+    """Checked sizes and the rule of a postnorm: (T, H, type, rule)."""
+    T, H = x.shape
+    dt = _act(x, "x")
+    if y.shape != (T, H) or y.dtype != x.dtype:
+        raise ValueError("y must be [T, H] of x's type")
+    w = post_w if post_w is not None else next_w
+    wdt = dt if w is None else _act(w, "weights")
+    for v in (post_w, next_w):
+        if v is not None and (v.shape != (H,) or v.dtype != w.dtype):
+            raise ValueError("post_w and next_w must be [H] of one type")
+    kind, gdt = GATE_NONE, dt
+    if gate is not None:
+        kind = {(H,): GATE_CHANNEL, (T, H): GATE_FULL, (T, 1): GATE_TOKEN}.get(tuple(gate.shape))
+        if kind is None:
+            raise ValueError("gate must be [H], [T, 1] or [T, H]")
+        gdt = _act(gate, "gate")
+    return T, H, dt, moe_postnorm_rule(eps, scale, res_scale, kind, 1 if sigmoid else 0, gdt, wdt)
+
+
+def moe_postnorm(x: torch.Tensor, y: torch.Tensor, post_w=None, gate=None, sigmoid: bool = False, scale: float = 1.0,
+                 res_scale: float = 1.0, next_w=None, eps: float = 1e-6, out=None, h=None, stream=None):
+    """(out, h): out = res_scale * x + scale * gate * norm(y) * post_w and h = norm(out) * next_w.
+
+    x: the residual [T,H]; y: the block's output; post_w [H] (None: y without a norm); gate [H], [T,1] or [T,H] (None:
+    1), through a sigmoid if asked; next_w [H]: the next block's norm (None: h is None).  out may be x or y."""
+    T, H, dt, rule = _postnorm(x, y, post_w, gate, sigmoid, scale, res_scale, next_w, eps)
+    _same_device(x, y, post_w, gate, next_w, out, h)
+    out = _out(out, (T, H), x.dtype, x.device, stream)
+    if next_w is not None:
+        h = _out(h, (T, H), x.dtype, x.device, stream)
+    elif h is not None:
+        raise ValueError("h needs next_w")
+    _check(_lib.moe_postnorm(_p(x), _p(y), _p(post_w), _p(gate), _p(next_w), T, H, dt, ctypes.byref(rule), _p(out),
+                             _p(h), _stream(stream)), "moe_postnorm")
+    return out, h
+
+
+class PostnormGrads(NamedTuple):
+    """Gradients of moe_postnorm (None for what the call has not): weights and a broadcast gate in float32."""
+    d_x: torch.Tensor
+    d_y: torch.Tensor
+    d_post_w: Optional[torch.Tensor]
+    d_gate: Optional[torch.Tensor]
+    d_next_w: Optional[torch.Tensor]
+
+
+def moe_postnorm_backward(d_out: Optional[torch.Tensor], d_h: Optional[torch.Tensor], x: torch.Tensor, y: torch.Tensor,
+                          post_w=None, gate=None, sigmoid: bool = False, scale: float = 1.0, res_scale: float = 1.0,
+                          next_w=None, eps: float = 1e-6, d_x=None, d_y=None, workspace=None,
+                          stream=None) -> PostnormGrads:
+    """Gradients of moe_postnorm from those of out and h (None: zero)."""
+    T, H, dt, rule = _postnorm(x, y, post_w, gate, sigmoid, scale, res_scale, next_w, eps)
+    _like(d_out, (T, H), x.dtype, "d_out")
+    _like(d_h, (T, H), x.dtype, "d_h")
+    if d_h is not None and next_w is None:
+        raise ValueError("d_h needs next_w")
+    _same_device(x, y, post_w, gate, next_w, d_out, d_h, d_x, d_y, workspace)
+    dev = x.device
+    d_x = _out(d_x, (T, H), x.dtype, dev, stream)
+    d_y = _out(d_y, (T, H), x.dtype, dev, stream)
+    d_post_w = None if post_w is None else _empty((H,), torch.float32, dev, stream)
+    d_next_w = None if next_w is None else _empty((H,), torch.float32, dev, stream)
+    d_gate = None
+    if gate is not None:
+        d_gate = _empty(gate.shape, gate.dtype if rule.gate == GATE_FULL else torch.float32, dev, stream)
+    if workspace is None:
+        workspace = _empty(moe_norm_workspace_size(T, H), torch.uint8, dev, stream)
+    _check(_lib.moe_postnorm_backward(_p(d_out), _p(d_h), _p(x), _p(y), _p(post_w), _p(gate), _p(next_w), T, H, dt,
+                                      ctypes.byref(rule), _p(d_x), _p(d_y), _p(d_post_w), _p(d_gate), _p(d_next_w),
+                                      _p(workspace), workspace.numel(), _stream(stream)), "moe_postnorm_backward")
+    return PostnormGrads(d_x, d_y, d_post_w, d_gate, d_next_w)
+
+
+def moe_lora_workspace_size(T: int, K: int, N: int, rank: int, L: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_lora_workspace_size(T, K, N, rank, L, ctypes.byref(n)), "moe_lora_workspace_size")
+    return int(n.value)
+
+
+def moe_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor, scale=None, base=None,
+             out_dtype: torch.dtype = torch.bfloat16, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """out[t] = base[t] + scale[l] * b[l] . (a[l] . x[t]) with l = ids[t] (-1: base alone).
+
+    x bfloat16 [T,K]; a bfloat16 [L,r,K]; b bfloat16 [L,N,r]; ids int32 [T]; scale float32 [L] (None: 1); base [T,N]
+    (None: 0), whose type out then has, and which may be out itself."""
+    T, K = x.shape
+    L, r, Ka = a.shape
+    N = b.shape[1]
+    if Ka != K or b.shape != (L, N, r) or ids.shape != (T,) or (scale is not None and scale.shape != (L,)):
+        raise ValueError("inconsistent shapes")
+    if x.dtype != torch.bfloat16 or a.dtype != torch.bfloat16 or b.dtype != torch.bfloat16 or ids.dtype != torch.int32 or (
+            scale is not None and scale.dtype != torch.float32):
+        raise ValueError("x, a and b must be bfloat16, ids int32 and scale float32")
+    if base is not None:
+        if base.shape != (T, N) or base.dtype not in _ACTS:
+            raise ValueError("base must be float32 or bfloat16 [T, N]")
+        out_dtype = base.dtype
+    elif out is not None:
+        out_dtype = out.dtype
+    _same_device(x, a, b, ids, scale, base, out, workspace)
+    out = _out(out, (T, N), out_dtype, x.device, stream)
+    dt = _act(out, "out")
+    if workspace is None:
+        workspace = _empty(moe_lora_workspace_size(T, K, N, r, L), torch.uint8, x.device, stream)
+    _check(_lib.moe_lora(_p(x), _p(a), _p(b), _p(ids), _p(scale), _p(base), T, K, N, r, L, dt, _p(out), _p(workspace),
+                         workspace.numel(), _stream(stream)), "moe_lora")
+    return out
 
 
 _W_FORMATS = {"int4": MOE_INT4, "e4m3_block": MOE_E4M3_B128}

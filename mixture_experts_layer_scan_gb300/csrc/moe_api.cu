@@ -1060,6 +1060,263 @@ int moe_gemm_block(const void* a, const float* a_scale, const void* w, const flo
   return cuda_rc(launch_gemm_block(g, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+static bool act_type(int d) { return d == MOE_F32 || d == MOE_BF16; }
+
+int moe_permute(const void* x, const int32_t* topk_ids, int T, int H, int E, int topk, int block, moe_dtype dtype,
+                void* rows, int32_t* row_of, int32_t* sorted_ids, int32_t* expert_ids, int32_t* num_post_pad,
+                int32_t* expert_counts, moe_stream_t stream) {
+  if (T < 0 || H < 1 || H >= kBlockMaxDim || topk < 1 || E < 1 || E > 1024 || block < 1 || block > 1024)
+    return MOE_ERR_ARG;
+  if (!act_type(dtype)) return MOE_ERR_UNSUPPORTED;
+  size_t cap = 0, bcap = 0;
+  if (moe_align_capacity(T, topk, E, block, &cap, &bcap) != MOE_OK || cap >= (size_t)kBlockMaxDim) return MOE_ERR_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !topk_ids || !rows || !row_of || !sorted_ids || !expert_ids || !num_post_pad) return MOE_ERR_ARG;
+  if (misaligned(x) || misaligned(topk_ids) || misaligned(rows) || misaligned(row_of, 4) || misaligned(sorted_ids) ||
+      misaligned(expert_ids) || misaligned(num_post_pad) || (expert_counts && misaligned(expert_counts)))
+    return MOE_ERR_ALIGNMENT;
+  int* st = status_word();
+  if (!st) return MOE_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_align(topk_ids, T, topk, E, block, sorted_ids, expert_ids, num_post_pad, expert_counts,
+                               nullptr, st, s, false, nullptr, nullptr, 0, row_of);
+  if (e == cudaSuccess)
+    e = launch_rows_scatter(x, T, H, topk, dtype == MOE_BF16 ? 2 : 4, row_of, sorted_ids, num_post_pad, (int)cap, rows, s);
+  return cuda_rc(e);
+}
+
+static int rows_gather(const void* rows, int n_rows, const int32_t* row_of, const float* w, int T, int H, int topk,
+                       moe_dtype dtype, void* out, moe_stream_t stream) {
+  if (T < 0 || H < 1 || H >= kBlockMaxDim || topk < 1 || n_rows < 0 || (long long)T * topk >= kBlockMaxDim)
+    return MOE_ERR_ARG;
+  if (!act_type(dtype)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if ((!rows && n_rows > 0) || !row_of || !out) return MOE_ERR_ARG;
+  if (misaligned(rows) || misaligned(row_of, 4) || misaligned(w, 4) || misaligned(out)) return MOE_ERR_ALIGNMENT;
+  return cuda_rc(launch_rows_gather(rows, n_rows, row_of, w, T, H, topk, dtype == MOE_BF16, out,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_unpermute(const void* rows, int n_rows, const int32_t* row_of, const float* topk_w, int T, int H, int topk,
+                  moe_dtype dtype, void* out, moe_stream_t stream) {
+  return rows_gather(rows, n_rows, row_of, topk_w, T, H, topk, dtype, out, stream);
+}
+
+int moe_permute_backward(const void* d_rows, int n_rows, const int32_t* row_of, int T, int H, int topk,
+                         moe_dtype dtype, void* d_x, moe_stream_t stream) {
+  return rows_gather(d_rows, n_rows, row_of, nullptr, T, H, topk, dtype, d_x, stream);
+}
+
+int moe_unpermute_backward(const void* d_out, const void* rows, int n_rows, const int32_t* row_of, const float* topk_w,
+                           const int32_t* sorted_ids, const int32_t* num_post_pad, int T, int H, int topk,
+                           moe_dtype dtype, void* d_rows, float* d_w, moe_stream_t stream) {
+  if (T < 0 || H < 1 || H >= kBlockMaxDim || topk < 1 || n_rows < 0 || (long long)T * topk >= kBlockMaxDim)
+    return MOE_ERR_ARG;
+  if (!act_type(dtype)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!d_out || !row_of || (!d_rows && !d_w) || (d_w && !rows && n_rows > 0) || !sorted_ids != !num_post_pad)
+    return MOE_ERR_ARG;
+  if (misaligned(d_out) || misaligned(rows) || misaligned(row_of, 4) || misaligned(topk_w, 4) || misaligned(sorted_ids) ||
+      misaligned(num_post_pad) || misaligned(d_rows) || misaligned(d_w, 4))
+    return MOE_ERR_ALIGNMENT;
+  return cuda_rc(launch_rows_gather_grad(d_out, rows, n_rows, row_of, topk_w, sorted_ids, num_post_pad, T, H, topk,
+                                         dtype == MOE_BF16, d_rows, d_w, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+constexpr int kNormMaxWidth = 16384;
+
+static int norm_size(int T, int H, int dtype, int w_dtype, float eps) {
+  if (T < 0 || H < 1 || !(eps >= 0.0f) || (long long)T >= kBlockMaxDim) return MOE_ERR_ARG;
+  if (!act_type(dtype) || !act_type(w_dtype) || H > kNormMaxWidth) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+static int postnorm_rule(const moe_postnorm_rule* rule, int T, int H, int dtype, const void* gate) {
+  if (!rule || rule->gate < MOE_GATE_NONE || rule->gate > MOE_GATE_FULL) return MOE_ERR_ARG;
+  const int rc = norm_size(T, H, dtype, rule->w_dtype, rule->eps);
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  if ((rule->gate != MOE_GATE_NONE) != (gate != nullptr)) return MOE_ERR_ARG;
+  if (gate && !act_type(rule->gate_dtype)) return MOE_ERR_UNSUPPORTED;
+  if (misaligned(gate, rule->gate == MOE_GATE_TOKEN ? 4 : 16)) return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+int moe_norm_workspace_size(int T, int H, size_t* bytes) {
+  if (T < 0 || H < 1 || !bytes) return MOE_ERR_ARG;
+  if (H > kNormMaxWidth) return MOE_ERR_UNSUPPORTED;
+  *bytes = align_up((size_t)3 * norm_grad_rows(T, H) * H * sizeof(float), 256);
+  return MOE_OK;
+}
+
+int moe_prenorm(const void* x, const void* w, int T, int H, float eps, moe_dtype dtype, moe_dtype w_dtype, void* h,
+                moe_stream_t stream) {
+  const int rc = norm_size(T, H, dtype, w_dtype, eps);
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !h) return MOE_ERR_ARG;
+  if (misaligned(x) || misaligned(w) || misaligned(h)) return MOE_ERR_ALIGNMENT;
+  NormArgs a = {};
+  a.x = x;
+  a.next_w = w;
+  a.T = T;
+  a.H = H;
+  a.bf16 = dtype == MOE_BF16;
+  a.rule.eps = eps;
+  a.rule.w_dtype = w_dtype;
+  a.h = h;
+  return cuda_rc(launch_norm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_prenorm_backward(const void* d_h, const void* x, const void* w, int T, int H, float eps, moe_dtype dtype,
+                         moe_dtype w_dtype, void* d_x, float* d_w, void* workspace, size_t workspace_bytes,
+                         moe_stream_t stream) {
+  int rc = norm_size(T, H, dtype, w_dtype, eps);
+  if (rc) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (misaligned(d_w)) return MOE_ERR_ALIGNMENT;
+  if (T == 0) return d_w ? cuda_rc(cudaMemsetAsync(d_w, 0, (size_t)H * sizeof(float), s)) : MOE_OK;
+  if (!d_h || !x || !w || !d_x || !workspace) return MOE_ERR_ARG;
+  if (misaligned(d_h) || misaligned(x) || misaligned(w) || misaligned(d_x) || misaligned(workspace, 256))
+    return MOE_ERR_ALIGNMENT;
+  size_t need = 0;
+  rc = moe_norm_workspace_size(T, H, &need);
+  if (rc) return rc;
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  NormArgs a = {};
+  a.x = x;
+  a.next_w = w;
+  a.T = T;
+  a.H = H;
+  a.bf16 = dtype == MOE_BF16;
+  a.rule.eps = eps;
+  a.rule.w_dtype = w_dtype;
+  a.d_h = d_h;
+  a.d_x = d_x;
+  a.d_next_w = d_w;
+  a.workspace = workspace;
+  return cuda_rc(launch_norm_grad(a, s));
+}
+
+int moe_postnorm(const void* x, const void* y, const void* post_w, const void* gate, const void* next_w, int T, int H,
+                 moe_dtype dtype, const moe_postnorm_rule* rule, void* out, void* h, moe_stream_t stream) {
+  const int rc = postnorm_rule(rule, T, H, dtype, gate);
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  if (!x || !y || !out || !next_w != !h) return MOE_ERR_ARG;
+  if (misaligned(x) || misaligned(y) || misaligned(post_w) || misaligned(next_w) || misaligned(out) || misaligned(h))
+    return MOE_ERR_ALIGNMENT;
+  NormArgs a = {};
+  a.x = x;
+  a.y = y;
+  a.post_w = post_w;
+  a.gate = gate;
+  a.next_w = next_w;
+  a.T = T;
+  a.H = H;
+  a.bf16 = dtype == MOE_BF16;
+  a.rule = *rule;
+  a.out = out;
+  a.h = h;
+  return cuda_rc(launch_norm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_postnorm_backward(const void* d_out, const void* d_h, const void* x, const void* y, const void* post_w,
+                          const void* gate, const void* next_w, int T, int H, moe_dtype dtype,
+                          const moe_postnorm_rule* rule, void* d_x, void* d_y, float* d_post_w, void* d_gate,
+                          float* d_next_w, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  int rc = postnorm_rule(rule, T, H, dtype, gate);
+  if (rc) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool channel = rule->gate == MOE_GATE_CHANNEL;
+  if (misaligned(d_post_w) || misaligned(d_next_w) || misaligned(d_gate, rule->gate == MOE_GATE_TOKEN ? 4 : 16))
+    return MOE_ERR_ALIGNMENT;
+  if (T == 0) {
+    cudaError_t e = cudaSuccess;
+    for (void* sum : {(void*)d_post_w, (void*)d_next_w, channel ? d_gate : nullptr})
+      if (sum && e == cudaSuccess) e = cudaMemsetAsync(sum, 0, (size_t)H * sizeof(float), s);
+    return cuda_rc(e);
+  }
+  if (!x || !y || !d_x || !d_y || !workspace || (d_h && !next_w) || (d_post_w && !post_w) || (d_next_w && !next_w) ||
+      (d_gate && !gate))
+    return MOE_ERR_ARG;
+  if (misaligned(d_out) || misaligned(d_h) || misaligned(x) || misaligned(y) || misaligned(post_w) ||
+      misaligned(next_w) || misaligned(d_x) || misaligned(d_y) || misaligned(workspace, 256))
+    return MOE_ERR_ALIGNMENT;
+  size_t need = 0;
+  rc = moe_norm_workspace_size(T, H, &need);
+  if (rc) return rc;
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  NormArgs a = {};
+  a.x = x;
+  a.y = y;
+  a.post_w = post_w;
+  a.gate = gate;
+  a.next_w = next_w;
+  a.T = T;
+  a.H = H;
+  a.bf16 = dtype == MOE_BF16;
+  a.rule = *rule;
+  a.d_out = d_out;
+  a.d_h = d_h;
+  a.d_x = d_x;
+  a.d_y = d_y;
+  a.d_gate = d_gate;
+  a.d_post_w = d_post_w;
+  a.d_next_w = d_next_w;
+  a.workspace = workspace;
+  return cuda_rc(launch_norm_grad(a, s));
+}
+
+static int lora_size(int T, int K, int N, int rank, int L) {
+  if (T < 0 || K < 1 || N < 1 || rank < 1 || L < 1 || L > 1024 || T >= kBlockMaxDim || K >= kBlockMaxDim ||
+      N >= kBlockMaxDim)
+    return MOE_ERR_ARG;
+  if (rank > kLoraMaxRank || rank % 8 || K % 8 || N % 8) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int moe_lora_workspace_size(int T, int K, int N, int rank, int L, size_t* bytes) {
+  const int rc = lora_size(T, K, N, rank, L);
+  if (rc) return rc;
+  if (!bytes) return MOE_ERR_ARG;
+  *bytes = lora_workspace_bytes(T, K, N, rank, L);
+  return MOE_OK;
+}
+
+int moe_lora(const void* x, const void* a, const void* b, const int32_t* ids, const float* scale, const void* base,
+             int T, int K, int N, int rank, int L, moe_dtype out_dtype, void* out, void* workspace,
+             size_t workspace_bytes, moe_stream_t stream) {
+  const int rc = lora_size(T, K, N, rank, L);
+  if (rc) return rc;
+  if (!act_type(out_dtype)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !a || !b || !ids || !out || !workspace) return MOE_ERR_ARG;
+  if (misaligned(x) || misaligned(a) || misaligned(b) || misaligned(ids, 4) || misaligned(scale, 4) ||
+      misaligned(base) || misaligned(out) || misaligned(workspace, 256))
+    return MOE_ERR_ALIGNMENT;
+  if (workspace_bytes < lora_workspace_bytes(T, K, N, rank, L)) return MOE_ERR_WORKSPACE;
+  LoraArgs g = {};
+  g.x = x;
+  g.a = a;
+  g.b = b;
+  g.ids = ids;
+  g.scale = scale;
+  g.base = base;
+  g.T = T;
+  g.K = K;
+  g.N = N;
+  g.r = rank;
+  g.L = L;
+  g.out_bf16 = out_dtype == MOE_BF16;
+  g.out = out;
+  g.workspace = workspace;
+  g.status = status_word();
+  g.num_sms = num_sms();
+  if (!g.status || g.num_sms <= 0) return MOE_ERR_CUDA;
+  return cuda_rc(launch_lora(g, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int moe_get_status(moe_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MOE_ERR_CUDA;
   int* st = status_word();

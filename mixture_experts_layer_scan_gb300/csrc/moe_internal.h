@@ -247,6 +247,52 @@ size_t fused_sync_bytes(int T, int H, int I, int E);
 size_t fused_table_bytes(int T, int E, int k);
 cudaError_t launch_decode_fused(const FusedArgs& a, cudaStream_t s);
 
+// ---- rows in expert order and back, with gradients (moe_rows.cu) ------------------------
+// rows[row_of[t][j]] = x[t]; with sorted (launch_align's list, npp its length) padding rows become zero
+cudaError_t launch_rows_scatter(const void* x, int T, int H, int k, int elem_bytes, const int32_t* row_of,
+                                const int32_t* sorted, const int32_t* npp, int n_rows, void* rows, cudaStream_t s);
+// out[t] = sum_j w[t][j] rows[row_of[t][j]] (w null: 1)
+cudaError_t launch_rows_gather(const void* rows, int n_rows, const int32_t* row_of, const float* w, int T, int H, int k,
+                               bool bf16, void* out, cudaStream_t s);
+// d_rows[row_of[t][j]] = w[t][j] d_out[t] (nullable), d_w[t][j] = <d_out[t], rows[row_of[t][j]]> (nullable)
+cudaError_t launch_rows_gather_grad(const void* d_out, const void* rows, int n_rows, const int32_t* row_of,
+                                    const float* w, const int32_t* sorted, const int32_t* npp, int T, int H, int k,
+                                    bool bf16, void* d_rows, float* d_w, cudaStream_t s);
+
+// ---- norms before and after a block (moe_norm.cu) ------------------------------------------
+struct NormArgs {
+  const void *x, *y;                  // y null: prenorm (next_w its weight)
+  const void *post_w, *gate, *next_w; // nullable (next_w: postnorm only)
+  int T, H;
+  bool bf16;
+  moe_postnorm_rule rule;
+  void *out, *h;                      // forward
+  const void *d_out, *d_h;            // gradient (nullable)
+  void *d_x, *d_y, *d_gate;
+  float *d_post_w, *d_next_w;
+  void* workspace;                    // 3 * norm_grad_rows(T, H) * H floats
+};
+int norm_grad_rows(int T, int H);
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_grad(const NormArgs& a, cudaStream_t s);
+
+// ---- low-rank adapters (moe_lora.cu) ---------------------------------------------------------
+constexpr int kLoraMaxRank = 128;
+struct LoraArgs {
+  const void *x, *a, *b;
+  const int32_t* ids;
+  const float* scale;  // nullable
+  const void* base;    // nullable
+  int T, K, N, r, L;
+  bool out_bf16;
+  void* out;
+  void* workspace;
+  int* status;
+  int num_sms;
+};
+size_t lora_workspace_bytes(int T, int K, int N, int r, int L);
+cudaError_t launch_lora(const LoraArgs& a, cudaStream_t s);
+
 // status word of the current device
 int* status_word();
 
