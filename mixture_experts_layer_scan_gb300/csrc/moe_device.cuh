@@ -258,6 +258,12 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // Rank of this CTA in its cluster, and a barrier over every thread of the cluster.
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;

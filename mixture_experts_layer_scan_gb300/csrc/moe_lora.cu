@@ -7,12 +7,13 @@
 //
 // More: the tokens are sorted by adapter (the permutation of the expert layer, an adapter in the place of an
 // expert, blocks of 128 tokens), and both products run on the tensor cores, kind::f16 with fp32 sums:
-//   shrink   a CTA to a block and a run of K: D[128 tokens x r] += X A^T over blocks of 64 K, both operands by
-//            TMA (X as a box where the block's tokens are neighbours, else four rows to a gather); its fp32
-//            sums go to the workspace, one plane for each run
-//   expand   a CTA to a block and every R-th tile of 64 columns: h = s * (the planes' sum, in their order)
-//            becomes the A operand in tensor memory, as bf16 parts that add up to it (2 for a bf16 output: off
-//            by 2^-17 of h at most; 3 for an fp32 one: 2^-25), B's rows come by TMA, and the epilogue adds the base
+//   shrink   a CTA to a block and a run of K: D[128 tokens x r] += X A^T over blocks of 64 K, A by TMA, X's rows by
+//            16-byte asynchronous copies (TMA gathers of four rows of 128 bytes took about 1 us for a block);
+//            its fp32 sums go to the workspace, one plane for each run
+//   expand   persistent over (block, tile of 256 bytes of output columns): h = s * (the planes' sum, in their
+//            order) becomes the A operand in tensor memory, as bf16 parts that add up to it (2 for a bf16
+//            output: off by 2^-17 of h at most; 3 for an fp32 one: 2^-25), B's rows come by TMA, and the
+//            epilogue adds the base
 // A token's row of D depends on that token alone, so what padding rows of a block hold does not matter.
 // Two launches rather than clusters that exchange h: a CTA that holds tensor memory then never waits for
 // another CTA.
@@ -108,29 +109,45 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraDev p) {
 // ---------------------------------------------------------------------------
 constexpr int kBlk = 128;          // tokens of a block
 constexpr int kMaxStages = 6;
-constexpr int kNT = 64;            // output columns of a tile
-constexpr int kMaxBufs = 4;
-constexpr int kShrinkThreads = 192;  // producer, MMA, 4 epilogue warps
+constexpr int kBufs = 2;           // output tiles in tensor memory
+constexpr int kSegBytes = 128;     // of a row of the output tile, half of which a warp takes
+constexpr int kShrinkThreads = 192;  // A's producer, MMA, 4 warps that load x and store the sums
 constexpr int kExpandThreads = 320;  // producer, MMA, 8 epilogue warps
+constexpr int kExpandCols = 512;
+constexpr int kSlots = 152 * 2;    // CTAs of the shrink kernel that are resident together
+constexpr int kMaxSplits = 16;
+constexpr int kBaseStages = 4;     // tiles of base in shared memory
+constexpr int kPieceRow = kSegBytes + 16;  // bytes from row to row of a warp's piece: no bank is met twice
+constexpr int kPieceBytes = 32 * kPieceRow;
 
 struct LoraTcDev {
   int T, K, N, r, L;
   int rn;                 // rank rounded up to 16
-  int nblk_max;           // planes of the partial sums are this many blocks long
-  int splits, kb_total, kb_per;
+  int nblk_max;
+  int kb_total, max_splits;
   int stages;
-  uint32_t stage_bytes, bar_off;
-  int parts, bufs, tmem_cols;
-  int n_tiles, ranges;
-  int wide;               // rows of base and out are whole 32-byte units
-  int copy_ctas;          // grid columns behind the blocks that copy the rows without an adapter
+  uint32_t stage_bytes, bar_off, base_off;
+  int n_tiles;
+  const __nv_bfloat16* x;
   const int32_t *ids, *sorted, *eids, *meta;
   const float* scale;
-  float* part;            // [splits][nblk_max][rn / 4][128] float4
+  float* part;            // [splits][blocks][rn / 4][128] float4
   const void* base;
   void* out;
   int* status;
 };
+
+// K runs of a block and their length in K blocks, from the number of blocks that the routing has
+struct LoraSplit {
+  int n, kb;
+};
+__device__ __forceinline__ LoraSplit lora_split(const LoraTcDev& p, int nblk) {
+  const int want = nblk ? max(1, min(kSlots / nblk, p.max_splits)) : 1;
+  LoraSplit s;
+  s.kb = (p.kb_total + want - 1) / want;
+  s.n = nblk ? (p.kb_total + s.kb - 1) / s.kb : 0;  // (none is empty)
+  return s;
+}
 
 struct TcBars {
   uint32_t full, empty, tfull, tempty, done, drain, exit;
@@ -142,25 +159,25 @@ __device__ __forceinline__ TcBars tc_bars(uint8_t* smem, uint32_t off) {
   b.full = smem_u32(smem) + off;
   b.empty = b.full + 8 * kMaxStages;
   b.tfull = b.empty + 8 * kMaxStages;
-  b.tempty = b.tfull + 8 * kMaxBufs;
-  b.done = b.tempty + 8 * kMaxBufs;
+  b.tempty = b.tfull + 8 * kBufs;
+  b.done = b.tempty + 8 * kBufs;
   b.drain = b.done + 8;
   b.exit = b.drain + 8;
-  b.slot = reinterpret_cast<uint32_t*>(smem + off + 8 * (2 * kMaxStages + 2 * kMaxBufs + 3));
+  b.slot = reinterpret_cast<uint32_t*>(smem + off + 8 * (2 * kMaxStages + 2 * kBufs + 3));
   b.abort = reinterpret_cast<volatile int*>(b.slot + 1);
   return b;
 }
-constexpr uint32_t kBarBytes = 8 * (2 * kMaxStages + 2 * kMaxBufs + 3) + 16;
+constexpr uint32_t kBarBytes = 8 * (2 * kMaxStages + 2 * kBufs + 3) + 16;
 
-// Barriers and tensor memory of a CTA; every thread.  done_count: arrivals of `done`.
-__device__ __forceinline__ uint32_t tc_setup(const TcBars& b, const LoraTcDev& p, int cols, int done_count) {
+// Barriers and tensor memory of a CTA; every thread.  Arrivals of `full` and `done` as given.
+__device__ __forceinline__ uint32_t tc_setup(const TcBars& b, int cols, int full_count, int done_count) {
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(b.full + 8 * s, 1);
+      mbar_init(b.full + 8 * s, full_count);
       mbar_init(b.empty + 8 * s, 1);
     }
-    for (int i = 0; i < kMaxBufs; ++i) {
+    for (int i = 0; i < kBufs; ++i) {
       mbar_init(b.tfull + 8 * i, 1);
       mbar_init(b.tempty + 8 * i, 8);
     }
@@ -192,44 +209,36 @@ __device__ __forceinline__ void tc_finish(const TcBars& b, uint32_t tmem, int co
 
 __device__ __forceinline__ int pow2_cols(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : 128; }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {  // (zeros where !in)
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <int STAGES>
 __global__ void __launch_bounds__(kShrinkThreads)
-    k_lora_shrink_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmX,
-                     const __grid_constant__ CUtensorMap tmXg, const LoraTcDev p) {
+    k_lora_shrink_tc(const __grid_constant__ CUtensorMap tmA, const LoraTcDev p) {
   pdl_wait();
-  const int blk = blockIdx.x, split = blockIdx.y;
-  if (blk >= p.meta[META_NBLK]) return;
+  const int nblk = p.meta[META_NBLK];
+  const LoraSplit runs = lora_split(p, nblk);
+  if ((int)blockIdx.x >= nblk * runs.n) return;
+  const int split = blockIdx.x / nblk, blk = blockIdx.x - split * nblk;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const TcBars b = tc_bars(smem, p.bar_off);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cols = pow2_cols(p.rn);
-  const uint32_t tmem = tc_setup(b, p, cols, 1);
+  const uint32_t tmem = tc_setup(b, cols, 5, 1);
   // Dependents launch once the permutation is complete (this kernel's own wait) and every CTA here holds its
   // tensor memory: the expand kernel's CTAs take theirs before they wait for this kernel.
   pdl_launch_dependents();
-  const int kb0 = split * p.kb_per, kb1 = min(kb0 + p.kb_per, p.kb_total);
+  const int kb0 = split * runs.kb, kb1 = min(kb0 + runs.kb, p.kb_total);
   constexpr uint32_t kXBytes = kBlk * 128;
 
   if (warp == 0) {
     const int l = p.eids[blk];
-    // the block's tokens, four to a lane; padding entries are T or more
-    const int4 s4 = reinterpret_cast<const int4*>(p.sorted + (size_t)blk * kBlk)[lane];
-    int row[4] = {s4.x, s4.y, s4.z, s4.w};
-    int mine = 0;
-    bool near = true;
-    const int first = __shfl_sync(0xffffffffu, row[0], 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = (unsigned)row[i] < (unsigned)p.T;
-      mine += in;
-      near = near && (!in || row[i] == first + 4 * lane + i);
-      if (!in) row[i] = row[0];
-    }
-    const int count = __reduce_add_sync(0xffffffffu, (unsigned)mine);
-    // (a box reads 128 rows whatever their number: only where most of them are wanted)
-    const bool box = __all_sync(0xffffffffu, near) && count > kBlk / 2;
-    const uint32_t xbytes = box ? kXBytes : (uint32_t)((count + 3) / 4) * 512u;
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
@@ -238,26 +247,22 @@ __global__ void __launch_bounds__(kShrinkThreads)
         ok = false;
         break;
       }
-      const uint32_t sx = sbase + stage * p.stage_bytes, fb = b.full + 8 * stage;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(fb, xbytes + (uint32_t)p.r * 128u);
-        tma_load_2d(sx + kXBytes, &tmA, kb * 64, l * p.r, fb);
-        if (box) tma_load_2d(sx, &tmX, kb * 64, first, fb);
+      if (elect_one()) {
+        const uint32_t fb = b.full + 8 * stage;
+        mbar_arrive_expect_tx(fb, (uint32_t)p.r * 128u);
+        tma_load_2d(sbase + stage * p.stage_bytes + kXBytes, &tmA, kb * 64, l * p.r, fb);
       }
       __syncwarp();
-      if (!box && 4 * lane < count)
-        tma_gather4(sx + (uint32_t)lane * 512u, &tmXg, kb * 64, row[0], row[1], row[2], row[3], fb);
-      __syncwarp();
       ++issued;
-      if (++stage == p.stages) {
+      if (++stage == STAGES) {
         stage = 0;
         phase ^= 1u;
       }
     }
     if (!ok && lane == 0) {  // let the copies already in flight land before the CTA exits
-      const uint32_t from = issued > (uint32_t)p.stages ? issued - p.stages : 0u;
+      const uint32_t from = issued > (uint32_t)STAGES ? issued - STAGES : 0u;
       for (uint32_t i = from; i < issued; ++i)
-        mbar_wait_drain(b.full + 8 * (i % p.stages), (i / p.stages) & 1u, 100000000ull);
+        mbar_wait_drain(b.full + 8 * (i % STAGES), (i / STAGES) & 1u, 100000000ull);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
           tc_mma<false>(tmem, sdesc_k_sw128(sx + kk * 32), sdesc_k_sw128(sx + kXBytes + kk * 32), idesc,
                         kb > kb0 || kk > 0);
         tc_commit(b.empty + 8 * stage);
-        if (++stage == p.stages) {
+        if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
         }
@@ -290,11 +295,49 @@ __global__ void __launch_bounds__(kShrinkThreads)
     }
     __syncwarp();
   } else {
-    const int q = warp & 3, row = q * 32 + lane;
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_one(b.done, 0, b.abort, p.status));
+    // x: 8 lanes to the 128 bytes of a row, 16 rows from one of a thread's pieces to the next
+    const int tid = threadIdx.x - 64, r0 = tid >> 3, chunk = tid & 7;
+    const __nv_bfloat16* row[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = p.sorted[(size_t)blk * kBlk + r0 + 16 * i];
+      row[i] = (unsigned)t < (unsigned)p.T ? p.x + (size_t)t * p.K + chunk * 8 : nullptr;
+    }
+    const uint32_t at = sbase + (uint32_t)r0 * 128u + (uint32_t)((chunk ^ (r0 & 7)) * 16);  // 128-byte swizzle
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    // (a stage is handed over while kLag younger ones load; one more may then be with the tensor core)
+    constexpr int kLag = STAGES - 2;
+    const int n = kb1 - kb0;
+    for (int i = 0; i < n + kLag; ++i) {
+      if (i < n) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_one(b.empty + 8 * stage, phase ^ 1u, b.abort, p.status));
+        if (ok) {
+          const int k = (kb0 + i) * 64;
+          const bool in = k + chunk * 8 < p.K;
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (row[c]) cp_async16(at + stage * p.stage_bytes + c * 16 * 128, in ? row[c] + k : row[c], in);
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      cp_async_commit();
+      if (i >= kLag) {  // the oldest stage's copies are there: hand it to the tensor core
+        cp_async_wait<kLag>();
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.full + 8 * ((i - kLag) % STAGES));
+      }
+    }
+    const int q = warp & 3;
+    ok = __all_sync(0xffffffffu, mbar_wait_one(b.done, 0, b.abort, p.status)) && ok;
     tc_fence_after();
     if (ok) {
-      float4* dst = reinterpret_cast<float4*>(p.part) + ((size_t)split * p.nblk_max + blk) * (p.rn / 4) * kBlk + row;
+      float4* dst = reinterpret_cast<float4*>(p.part) + ((size_t)split * nblk + blk) * (p.rn / 4) * kBlk + q * 32 + lane;
       for (int c = 0; c < p.rn; c += 16) {
         float v[16];
         tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
@@ -313,120 +356,51 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                : "memory");
 }
 
-__device__ __forceinline__ void ld_v8(const void* p, uint32_t (&v)[8]) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "l"(p));
-}
-__device__ __forceinline__ void st_v8(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
-// 32 columns of a row of base or out: UNITS times 32 bytes, those within the row
+// Rows of out without an adapter
 template <typename T>
-struct RowPiece {
-  static constexpr int kUnits = 32 * sizeof(T) / 32;
-  static constexpr int kPer = 32 / sizeof(T);  // columns of a unit
-  uint32_t v[kUnits][8];
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = 0;
-  }
-  __device__ __forceinline__ void load(const T* at, int left, bool wide) {
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      if (wide) {
-        if (u * kPer < left) ld_v8(at + u * kPer, v[u]);
-      } else {
-        if (u * kPer < left) {
-          const uint4 a = *reinterpret_cast<const uint4*>(at + u * kPer);
-          v[u][0] = a.x; v[u][1] = a.y; v[u][2] = a.z; v[u][3] = a.w;
-        }
-        if (u * kPer + kPer / 2 < left) {
-          const uint4 a = *reinterpret_cast<const uint4*>(at + u * kPer + kPer / 2);
-          v[u][4] = a.x; v[u][5] = a.y; v[u][6] = a.z; v[u][7] = a.w;
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ void store(T* at, int left, bool wide) const {
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      if (wide) {
-        if (u * kPer < left) st_v8(at + u * kPer, v[u]);
-      } else {
-        if (u * kPer < left) *reinterpret_cast<uint4*>(at + u * kPer) = make_uint4(v[u][0], v[u][1], v[u][2], v[u][3]);
-        if (u * kPer + kPer / 2 < left)
-          *reinterpret_cast<uint4*>(at + u * kPer + kPer / 2) = make_uint4(v[u][4], v[u][5], v[u][6], v[u][7]);
-      }
-    }
-  }
-  // this += f, each sum rounded once
-  __device__ __forceinline__ void add(const uint32_t (&f)[32]) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if constexpr (sizeof(T) == 4) {
-        v[i / 8][i % 8] = __float_as_uint(__uint_as_float(v[i / 8][i % 8]) + __uint_as_float(f[i]));
-      } else if (i % 2 == 0) {
-        uint32_t& w = v[i / 16][i % 16 / 2];
-        w = pack_bf16x2(bf16_bits_to_f32(w & 0xffffu) + __uint_as_float(f[i]),
-                        bf16_bits_to_f32(w >> 16) + __uint_as_float(f[i + 1]));
-      }
-    }
-  }
-};
-
-template <typename T>
-__device__ void lora_copy_rows(const LoraTcDev& p, int cta, int ctas) {
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+__device__ void lora_copy_rows(const LoraTcDev& p, int warp, int warps) {
+  const int lane = threadIdx.x & 31;
   const int vecs = (int)((size_t)p.N * sizeof(T) / 16);
-  for (int t = cta * warps + (threadIdx.x >> 5); t < p.T; t += ctas * warps) {
+  for (int t = warp; t < p.T; t += warps) {
     const int l = p.ids[t];
     if (l >= 0 && l < p.L) continue;
     const uint4* src = static_cast<const uint4*>(p.base) + (size_t)t * vecs;
     uint4* dst = static_cast<uint4*>(p.out) + (size_t)t * vecs;
-#pragma unroll 4
+#pragma unroll 8
     for (int v = lane; v < vecs; v += 32) dst[v] = p.base ? src[v] : make_uint4(0, 0, 0, 0);
   }
 }
 
+// Every CTA takes an equal run of the (block, column tile) pairs.  A warp of the epilogue owns 32 rows x 128 bytes
+// of a tile: it copies that piece of base into shared memory kBaseStages - 1 tiles ahead, adds D there with a
+// row to a thread, and stores it with 8 lanes to a row, all without a barrier beyond its own.
 template <typename T, int PARTS>
 __global__ void __launch_bounds__(kExpandThreads)
     k_lora_expand_tc(const __grid_constant__ CUtensorMap tmB, const LoraTcDev p) {
-  const int blk = blockIdx.x;
-  if (blk >= p.nblk_max) {
-    pdl_wait();
-    pdl_launch_dependents();
-    lora_copy_rows<T>(p, (blk - p.nblk_max) * gridDim.y + blockIdx.y, p.copy_ctas * gridDim.y);
-    return;
-  }
-  // The permutation, base and the weights were complete before the preceding kernel let this one start; only
-  // its sums are not.
-  if (blk >= p.meta[META_NBLK]) {
-    pdl_wait();
-    return;
-  }
+  constexpr int kHalf = kSegBytes / sizeof(T);  // columns of a warp's piece
+  constexpr int kNT = 2 * kHalf;                // columns of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const TcBars b = tc_bars(smem, p.bar_off);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t tmem = tc_setup(b, p, p.tmem_cols, 8);
+  const uint32_t tmem = tc_setup(b, kExpandCols, 1, 8);
+  // The permutation, base and the weights were complete before the preceding kernel let this one start; only
+  // its sums are not.
+  const int nblk = p.meta[META_NBLK];
   const uint32_t hcols = (uint32_t)(p.rn / 2);  // columns of one part of h
-  const uint32_t d0 = tmem, h0 = tmem + (uint32_t)(p.bufs * kNT);
-  const int l = p.eids[blk];
+  const uint32_t h0 = tmem + kBufs * kNT;
   const int kboxes = (p.r + 63) / 64;
   constexpr uint32_t kBoxBytes = kNT * 128;
+  const long total = (long)nblk * p.n_tiles;
+  const int f0 = (int)(total * blockIdx.x / gridDim.x), f1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
 
   if (warp == 0) {
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
-    for (int j = blockIdx.y; j < p.n_tiles; j += p.ranges) {
+    int blk = f0 / p.n_tiles, j = f0 - blk * p.n_tiles, l = f0 < f1 ? p.eids[blk] : 0;
+    for (int f = f0; f < f1; ++f) {
       if (!mbar_wait_all(b.empty + 8 * stage, phase ^ 1u, b.abort, p.status)) {
         ok = false;
         break;
@@ -437,6 +411,10 @@ __global__ void __launch_bounds__(kExpandThreads)
         for (int x = 0; x < kboxes; ++x) tma_load_2d(sw + x * kBoxBytes, &tmB, x * 64, l * p.N + j * kNT, fb);
       }
       __syncwarp();
+      if (++j == p.n_tiles) {
+        j = 0;
+        if (f + 1 < f1) l = p.eids[++blk];
+      }
       ++issued;
       if (++stage == p.stages) {
         stage = 0;
@@ -454,28 +432,32 @@ __global__ void __launch_bounds__(kExpandThreads)
   } else if (warp == 1) {
     if (elect_one()) {
       const uint32_t idesc = idesc_make(kBlk, kNT, false);
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, buf_phase = 0;
-      bool any = false;
-      bool ok = mbar_wait_one(b.done, 0, b.abort, p.status);  // h is in tensor memory
-      for (int j = blockIdx.y; j < p.n_tiles && ok; j += p.ranges) {
-        ok = mbar_wait_one(b.tempty + 8 * buf, buf_phase ^ 1u, b.abort, p.status) &&
+      int stage = 0, buf = 0, j = f0 % p.n_tiles;
+      uint32_t phase = 0, buf_phase = 0, h_phase = 0;
+      bool any = false, ok = true;
+      for (int f = f0; f < f1; ++f) {
+        if (f == f0 || j == 0) {  // this block's h is in tensor memory
+          ok = mbar_wait_one(b.done, h_phase, b.abort, p.status);
+          h_phase ^= 1u;
+        }
+        ok = ok && mbar_wait_one(b.tempty + 8 * buf, buf_phase ^ 1u, b.abort, p.status) &&
              mbar_wait_one(b.full + 8 * stage, phase, b.abort, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t sw = sbase + stage * p.stage_bytes;
         for (int part = 0; part < PARTS; ++part)
           for (int k = 0; k < p.rn / 16; ++k)
-            tc_mma_ts(d0 + buf * kNT, h0 + part * hcols + k * 8,
+            tc_mma_ts(tmem + buf * kNT, h0 + part * hcols + k * 8,
                       sdesc_k_sw128(sw + (k >> 2) * kBoxBytes + (k & 3) * 32), idesc, part > 0 || k > 0);
         tc_commit(b.empty + 8 * stage);
         tc_commit(b.tfull + 8 * buf);
         any = true;
+        if (++j == p.n_tiles) j = 0;
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
         }
-        if (++buf == p.bufs) {
+        if (++buf == kBufs) {
           buf = 0;
           buf_phase ^= 1u;
         }
@@ -487,88 +469,148 @@ __global__ void __launch_bounds__(kExpandThreads)
     }
     __syncwarp();
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2, row = q * 32 + lane;
+    const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    const int t = p.sorted[(size_t)blk * kBlk + row];
-    const bool in = (unsigned)t < (unsigned)p.T;
-    const T* base = p.base && in ? static_cast<const T*>(p.base) + (size_t)t * p.N : nullptr;
-    T* out = in ? static_cast<T*>(p.out) + (size_t)t * p.N : nullptr;
-    RowPiece<T> next;
-    next.zero();
-    auto fetch = [&](int j) {
-      const int n = j * kNT + half * 32;
-      if (base && j < p.n_tiles) next.load(base + n, p.N - n, p.wide);
+    const uint32_t piece = sbase + p.base_off + (uint32_t)(warp - 2) * kPieceBytes;
+    const uint32_t mine = (uint32_t)lane * kPieceRow;               // this thread's row of a piece
+    const int sub = lane >> 3, chunk = lane & 7;                    // its place where 8 lanes share a row
+    const int col = half * kHalf + chunk * (16 / (int)sizeof(T));  // column of its 16 bytes in a tile
+    const uint32_t coal = (uint32_t)sub * kPieceRow + chunk * 16;
+    // the tokens of rows sub, sub + 4, ... of this warp, for the block that is loaded and the one that is stored
+    auto tokens = [&](int blk, int (&tok)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = p.sorted[(size_t)blk * kBlk + q * 32 + sub + 4 * i];
+        tok[i] = (unsigned)t < (unsigned)p.T ? t : -1;
+      }
     };
-    fetch(blockIdx.y);
-    const float s = p.scale ? p.scale[l] : 1.0f;
+    int ltok[8], stok[8];
+    int lblk = f0 / p.n_tiles, lj = f0 - lblk * p.n_tiles, lf = f0;
+    if (f0 < f1) tokens(lblk, ltok);
+    auto load = [&]() {
+      if (lf < f1 && p.base) {
+        const uint32_t dst = piece + (uint32_t)((lf - f0) % kBaseStages) * (8 * kPieceBytes) + coal;
+        const int n = lj * kNT + col;
+        if (n < p.N) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (ltok[i] >= 0) cp_async16(dst + i * 4 * kPieceRow, static_cast<const T*>(p.base) + (size_t)ltok[i] * p.N + n, true);
+        }
+        if (++lj == p.n_tiles) {
+          lj = 0;
+          ++lblk;
+          if (lf + 1 < f1) tokens(lblk, ltok);
+        }
+      }
+      ++lf;
+      cp_async_commit();
+    };
+    for (int i = 0; i < kBaseStages - 1; ++i) load();
     pdl_wait();
-    // h, 16 columns (one MMA step) at a time
-    for (int c = half * 16; c < p.rn; c += 32) {
-      float h[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) h[i] = 0.f;
-      const float4* src = reinterpret_cast<const float4*>(p.part) + ((size_t)blk * (p.rn / 4) + c / 4) * kBlk + row;
-      for (int sp = 0; sp < p.splits; ++sp) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 v = src[((size_t)sp * p.nblk_max * (p.rn / 4) + i) * kBlk];
-          h[4 * i] += v.x; h[4 * i + 1] += v.y; h[4 * i + 2] += v.z; h[4 * i + 3] += v.w;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) h[i] = c + i < p.r ? h[i] * s : 0.f;
-#pragma unroll
-      for (int part = 0; part < PARTS; ++part) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          w[i] = pack_bf16x2(h[2 * i], h[2 * i + 1]);
-          h[2 * i] -= bf16_bits_to_f32(w[i] & 0xffffu);
-          h[2 * i + 1] -= bf16_bits_to_f32(w[i] >> 16);
-        }
-        tmem_st8(h0 + lanes + part * hcols + c / 2, w);
-      }
-    }
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(b.done);
-    int buf = 0;
+    const int splits = lora_split(p, nblk).n;
+    int buf = 0, blk = f0 / p.n_tiles, j = f0 - blk * p.n_tiles;
     uint32_t buf_phase = 0;
-    for (int j = blockIdx.y; j < p.n_tiles; j += p.ranges) {
-      RowPiece<T> cur = next;
-      fetch(j + p.ranges);
-      const bool ok = __all_sync(0xffffffffu, mbar_wait_one(b.tfull + 8 * buf, buf_phase, b.abort, p.status));
-      if (!ok) break;
+    for (int f = f0; f < f1; ++f) {
+      if (f == f0 || j == 0) {
+        // h of this block, 16 columns (one MMA step) at a time.  (The products with the block before have
+        // ended: this warp has seen its last tile.)
+        tokens(blk, stok);
+        const int l = p.eids[blk];
+        const float s = p.scale ? p.scale[l] : 1.0f;
+        for (int c = half * 16; c < p.rn; c += 32) {
+          float h[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) h[i] = 0.f;
+          const float4* src = reinterpret_cast<const float4*>(p.part) + ((size_t)blk * (p.rn / 4) + c / 4) * kBlk + q * 32 + lane;
+#pragma unroll 2
+          for (int sp = 0; sp < splits; ++sp) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 v = src[((size_t)sp * nblk * (p.rn / 4) + i) * kBlk];
+              h[4 * i] += v.x; h[4 * i + 1] += v.y; h[4 * i + 2] += v.z; h[4 * i + 3] += v.w;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) h[i] = c + i < p.r ? h[i] * s : 0.f;
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              w[i] = pack_bf16x2(h[2 * i], h[2 * i + 1]);
+              h[2 * i] -= bf16_bits_to_f32(w[i] & 0xffffu);
+              h[2 * i + 1] -= bf16_bits_to_f32(w[i] >> 16);
+            }
+            tmem_st8(h0 + lanes + part * hcols + c / 2, w);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.done);
+      }
+      load();
+      cp_async_wait<kBaseStages - 1>();
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, mbar_wait_one(b.tfull + 8 * buf, buf_phase, b.abort, p.status))) break;
       tc_fence_after();
-      uint32_t v[32];
-      tmem_ld32_issue(d0 + buf * kNT + lanes + half * 32, v);
-      tmem_wait_ld();
-      tmem_landed(v);
+      const uint32_t at = piece + (uint32_t)((f - f0) % kBaseStages) * (8 * kPieceBytes);
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 32) {
+        uint32_t v[32];
+        tmem_ld32_issue(tmem + buf * kNT + lanes + half * kHalf + c, v);
+        tmem_wait_ld();
+        tmem_landed(v);
+#pragma unroll
+        for (int u = 0; u < 32 * (int)sizeof(T) / 16; ++u) {
+          const uint32_t sa = at + mine + c * (int)sizeof(T) + u * 16;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (p.base) w = lds_v4(sa);
+          uint32_t* e = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4)
+              e[i] = __float_as_uint(__uint_as_float(e[i]) + __uint_as_float(v[4 * u + i]));
+            else
+              e[i] = pack_bf16x2(bf16_bits_to_f32(e[i] & 0xffffu) + __uint_as_float(v[8 * u + 2 * i]),
+                                 bf16_bits_to_f32(e[i] >> 16) + __uint_as_float(v[8 * u + 2 * i + 1]));
+          }
+          sts_v4(sa, w);
+        }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(b.tempty + 8 * buf);
-      if (++buf == p.bufs) {
+      const int n = j * kNT + col;
+      if (n < p.N) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (stok[i] >= 0)
+            *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (size_t)stok[i] * p.N + n) = lds_v4(at + coal + i * 4 * kPieceRow);
+      }
+      __syncwarp();  // (the piece may be loaded again)
+      if (++j == p.n_tiles) {
+        j = 0;
+        ++blk;
+      }
+      if (++buf == kBufs) {
         buf = 0;
         buf_phase ^= 1u;
       }
-      cur.add(v);
-      const int n = j * kNT + half * 32;
-      if (out) cur.store(out + n, p.N - n, p.wide);
     }
+    cp_async_wait<0>();
+    if (p.base != p.out) lora_copy_rows<T>(p, blockIdx.x * 8 + warp - 2, gridDim.x * 8);
   }
-  tc_finish(b, tmem, p.tmem_cols);
+  tc_finish(b, tmem, kExpandCols);
 }
 
 // The tensor-core path's shape for a problem (from its sizes alone).
 struct LoraPlan {
   bool tc;
-  int rn, nblk, splits, kb_total, kb_per, ranges, n_tiles;
+  int rn, nblk, kb_total, max_splits;
   long cap;
   size_t o_sorted, o_eids, o_meta, o_part, total;
 };
-
-constexpr int kSlots = 152 * 2;  // CTAs of either kernel that are resident together
 
 LoraPlan lora_plan(int T, int K, int N, int r, int L) {
   LoraPlan q = {};
@@ -582,16 +624,13 @@ LoraPlan lora_plan(int T, int K, int N, int r, int L) {
   q.cap = (long)T + (long)std::min(L, T) * (kBlk - 1);
   q.nblk = (int)(q.cap / kBlk);
   q.kb_total = (K + 63) / 64;
-  const int want = std::max(1, std::min({kSlots / q.nblk, 8, q.kb_total / 4}));
-  q.kb_per = (q.kb_total + want - 1) / want;
-  q.splits = (q.kb_total + q.kb_per - 1) / q.kb_per;
-  q.n_tiles = (N + kNT - 1) / kNT;
-  q.ranges = std::max(1, std::min(q.n_tiles, (kSlots + q.nblk - 1) / q.nblk));
+  q.max_splits = std::max(1, std::min(kMaxSplits, q.kb_total / 4));  // (4 K blocks at least to a CTA)
   q.o_sorted = 0;
   q.o_eids = up(q.cap * sizeof(int32_t));
   q.o_meta = q.o_eids + up((size_t)q.nblk * sizeof(int32_t));
   q.o_part = q.o_meta + up((size_t)meta_words(L) * sizeof(int32_t));
-  q.total = q.o_part + up((size_t)q.splits * q.nblk * kBlk * q.rn * sizeof(float));
+  // (a plane for each block and run of K: kSlots, or the blocks where they are more)
+  q.total = q.o_part + up((size_t)std::max(q.nblk, kSlots) * kBlk * q.rn * sizeof(float));
   return q;
 }
 
@@ -604,14 +643,37 @@ cudaError_t smem_limit(const void* kernel, bool (&set)[64], size_t bytes) {
   return e;
 }
 
-constexpr size_t kSmemMax = 112 * 1024;  // two CTAs to an SM
+constexpr size_t kSmemHalf = 112 * 1024;  // two CTAs to an SM
+constexpr size_t kSmemMax = 227 * 1024;
 
 template <typename T, int PARTS>
-cudaError_t launch_expand(const CUtensorMap& tmB, const LoraTcDev& p, dim3 grid, size_t smem, cudaStream_t s) {
+cudaError_t launch_expand(const LoraArgs& a, LoraTcDev p, cudaStream_t s) {
+  constexpr int kNT = 2 * kSegBytes / sizeof(T);
+  CUtensorMap tmB;
+  if (!make_tensor_map_2d(&tmB, a.b, 2, a.r, (uint64_t)a.L * a.N, kNT)) return cudaErrorInvalidValue;
+  p.stage_bytes = (uint32_t)((a.r + 63) / 64) * kNT * 128;
+  const uint32_t base_bytes = kBaseStages * 8 * kPieceBytes;
+  p.stages = std::min<int>(kMaxStages, (int)((kSmemMax - 1024 - kBarBytes - base_bytes) / p.stage_bytes));
+  p.base_off = p.stages * p.stage_bytes;
+  p.bar_off = p.base_off + base_bytes;
+  p.n_tiles = (a.N + kNT - 1) / kNT;
   static bool set[64] = {};
   const cudaError_t e = smem_limit(reinterpret_cast<const void*>(k_lora_expand_tc<T, PARTS>), set, kSmemMax);
   if (e != cudaSuccess) return e;
-  MOE_LAUNCH((k_lora_expand_tc<T, PARTS>), grid, dim3(kExpandThreads), smem, s, tmB, p);
+  const int grid = (int)std::min<long>(a.num_sms, (long)p.nblk_max * p.n_tiles);
+  MOE_LAUNCH((k_lora_expand_tc<T, PARTS>), dim3(grid), dim3(kExpandThreads), 1024 + p.bar_off + kBarBytes, s, tmB, p);
+  return cudaGetLastError();
+}
+
+template <int STAGES>
+cudaError_t launch_shrink(const CUtensorMap& tmA, LoraTcDev p, cudaStream_t s) {
+  static bool set[64] = {};
+  const cudaError_t e = smem_limit(reinterpret_cast<const void*>(k_lora_shrink_tc<STAGES>), set, kSmemHalf);
+  if (e != cudaSuccess) return e;
+  p.stage_bytes = kBlk * 128 + (uint32_t)p.rn * 128;
+  p.bar_off = STAGES * p.stage_bytes;
+  MOE_LAUNCH(k_lora_shrink_tc<STAGES>, dim3(std::max(p.nblk_max, kSlots)), dim3(kShrinkThreads),
+             1024 + p.bar_off + kBarBytes, s, tmA, p);
   return cudaGetLastError();
 }
 
@@ -620,11 +682,8 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const LoraPlan& q, cudaStream_t s)
   int32_t* sorted = reinterpret_cast<int32_t*>(ws + q.o_sorted);
   int32_t* eids = reinterpret_cast<int32_t*>(ws + q.o_eids);
   int32_t* meta = reinterpret_cast<int32_t*>(ws + q.o_meta);
-  CUtensorMap tmA, tmX, tmXg, tmB;
-  if (!make_tensor_map_2d(&tmA, a.a, 2, a.K, (uint64_t)a.L * a.r, a.r) ||
-      !make_tensor_map_2d(&tmX, a.x, 2, a.K, a.T, kBlk) || !make_tensor_map_2d(&tmXg, a.x, 2, a.K, a.T, 1) ||
-      !make_tensor_map_2d(&tmB, a.b, 2, a.r, (uint64_t)a.L * a.N, kNT))
-    return cudaErrorInvalidValue;
+  CUtensorMap tmA;
+  if (!make_tensor_map_2d(&tmA, a.a, 2, a.K, (uint64_t)a.L * a.r, a.r)) return cudaErrorInvalidValue;
   cudaError_t e = launch_align(a.ids, a.T, 1, a.L, kBlk, sorted, eids, meta + META_NPP, nullptr, meta, a.status, s, true);
   if (e != cudaSuccess) return e;
   LoraTcDev p = {};
@@ -635,11 +694,9 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const LoraPlan& q, cudaStream_t s)
   p.L = a.L;
   p.rn = q.rn;
   p.nblk_max = q.nblk;
-  p.splits = q.splits;
   p.kb_total = q.kb_total;
-  p.kb_per = q.kb_per;
-  p.n_tiles = q.n_tiles;
-  p.ranges = q.ranges;
+  p.max_splits = q.max_splits;
+  p.x = static_cast<const __nv_bfloat16*>(a.x);
   p.ids = a.ids;
   p.sorted = sorted;
   p.eids = eids;
@@ -649,30 +706,12 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const LoraPlan& q, cudaStream_t s)
   p.base = a.base;
   p.out = a.out;
   p.status = a.status;
-  {
-    static bool set[64] = {};
-    e = smem_limit(reinterpret_cast<const void*>(k_lora_shrink_tc), set, kSmemMax);
-    if (e != cudaSuccess) return e;
-    LoraTcDev d = p;
-    d.stage_bytes = kBlk * 128 + (uint32_t)q.rn * 128;
-    d.stages = std::min<int>(kMaxStages, (kSmemMax - 1024 - kBarBytes) / d.stage_bytes);
-    d.bar_off = d.stages * d.stage_bytes;
-    MOE_LAUNCH(k_lora_shrink_tc, dim3(q.nblk, q.splits), dim3(kShrinkThreads), 1024 + d.bar_off + kBarBytes, s, tmA, tmX,
-               tmXg, d);
-  }
-  p.parts = a.out_bf16 ? 2 : 3;
-  const int hcols = p.parts * q.rn / 2;
-  p.tmem_cols = hcols + 2 * kNT <= 256 ? 256 : 512;
-  p.bufs = std::min(kMaxBufs, (p.tmem_cols - hcols) / kNT);
-  p.stage_bytes = (uint32_t)((a.r + 63) / 64) * kNT * 128;
-  p.stages = kMaxStages;
-  p.bar_off = p.stages * p.stage_bytes;
-  const size_t row = (size_t)a.N * (a.out_bf16 ? 2 : 4);
-  p.wide = row % 32 == 0 && (reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.base)) % 32 == 0;
-  p.copy_ctas = a.base == a.out ? 0 : std::max(1, std::min(a.T / 80, 152) / q.ranges);
-  const dim3 grid(q.nblk + p.copy_ctas, q.ranges);
-  const size_t smem = 1024 + p.bar_off + kBarBytes;
-  return a.out_bf16 ? launch_expand<__nv_bfloat16, 2>(tmB, p, grid, smem, s) : launch_expand<float, 3>(tmB, p, grid, smem, s);
+  e = q.rn <= 16   ? launch_shrink<6>(tmA, p, s)  // (as many stages as leave room for two CTAs)
+      : q.rn <= 32 ? launch_shrink<5>(tmA, p, s)
+      : q.rn <= 64 ? launch_shrink<4>(tmA, p, s)
+                   : launch_shrink<3>(tmA, p, s);
+  if (e != cudaSuccess) return e;
+  return a.out_bf16 ? launch_expand<__nv_bfloat16, 2>(a, p, s) : launch_expand<float, 3>(a, p, s);
 }
 
 }  // namespace
