@@ -112,11 +112,11 @@ constexpr int kMaxStages = 6;
 constexpr int kBufs = 2;           // output tiles in tensor memory
 constexpr int kSegBytes = 128;     // of a row of the output tile, half of which a warp takes
 constexpr int kShrinkThreads = 192;  // A's producer, MMA, 4 warps that load x and store the sums
-constexpr int kExpandThreads = 320;  // producer, MMA, 8 epilogue warps
+constexpr int kExpandThreads = 576;  // producer, MMA, two sets of 8 epilogue warps
 constexpr int kExpandCols = 512;
 constexpr int kSlots = 152 * 2;    // CTAs of the shrink kernel that are resident together
 constexpr int kMaxSplits = 16;
-constexpr int kBaseStages = 4;     // tiles of base in shared memory
+constexpr int kBaseStages = 4;     // tiles of base in shared memory (two of each set of epilogue warps)
 constexpr int kPieceRow = kSegBytes + 16;  // bytes from row to row of a warp's piece: no bank is met twice
 constexpr int kPieceBytes = 32 * kPieceRow;
 
@@ -371,9 +371,10 @@ __device__ void lora_copy_rows(const LoraTcDev& p, int warp, int warps) {
   }
 }
 
-// Every CTA takes an equal run of the (block, column tile) pairs.  A warp of the epilogue owns 32 rows x 128 bytes
-// of a tile: it copies that piece of base into shared memory kBaseStages - 1 tiles ahead, adds D there with a
-// row to a thread, and stores it with 8 lanes to a row, all without a barrier beyond its own.
+// Every CTA takes an equal run of the (block, column tile) pairs; its two sets of epilogue warps take tiles in
+// turn (a warp's way through a tile is a chain of latencies: with one set 91 us for 8192 x 8192 bf16).  A
+// warp owns 32 rows x 128 bytes of a tile: it copies that piece of base into shared memory ahead of time,
+// adds D there with a row to a thread, and stores it with 8 lanes to a row, without a barrier beyond its own.
 template <typename T, int PARTS>
 __global__ void __launch_bounds__(kExpandThreads)
     k_lora_expand_tc(const __grid_constant__ CUtensorMap tmB, const LoraTcDev p) {
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kExpandThreads)
   const uint32_t sbase = smem_u32(smem);
   const TcBars b = tc_bars(smem, p.bar_off);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t tmem = tc_setup(b, kExpandCols, 1, 8);
+  const uint32_t tmem = tc_setup(b, kExpandCols, 1, 16);
   // The permutation, base and the weights were complete before the preceding kernel let this one start; only
   // its sums are not.
   const int nblk = p.meta[META_NBLK];
@@ -469,13 +470,14 @@ __global__ void __launch_bounds__(kExpandThreads)
     }
     __syncwarp();
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int q = warp & 3, group = (warp - 2) >> 2, half = group & 1, set = group >> 1;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    const uint32_t piece = sbase + p.base_off + (uint32_t)(warp - 2) * kPieceBytes;
+    const uint32_t piece = sbase + p.base_off + (uint32_t)(half * 4 + q) * kPieceBytes;
     const uint32_t mine = (uint32_t)lane * kPieceRow;               // this thread's row of a piece
     const int sub = lane >> 3, chunk = lane & 7;                    // its place where 8 lanes share a row
     const int col = half * kHalf + chunk * (16 / (int)sizeof(T));  // column of its 16 bytes in a tile
     const uint32_t coal = (uint32_t)sub * kPieceRow + chunk * 16;
+    const uint32_t row_bytes = (uint32_t)p.N * (uint32_t)sizeof(T);
     // the tokens of rows sub, sub + 4, ... of this warp, for the block that is loaded and the one that is stored
     auto tokens = [&](int blk, int (&tok)[8]) {
 #pragma unroll
@@ -485,61 +487,60 @@ __global__ void __launch_bounds__(kExpandThreads)
       }
     };
     int ltok[8], stok[8];
-    int lblk = f0 / p.n_tiles, lj = f0 - lblk * p.n_tiles, lf = f0;
-    if (f0 < f1) tokens(lblk, ltok);
-    auto load = [&]() {
+    int lf = f0 + set, lblk = -1;
+    auto load = [&]() {  // base of this set's next tile
       if (lf < f1 && p.base) {
+        const int at = lf / p.n_tiles, n = (lf - at * p.n_tiles) * kNT + col;
+        if (at != lblk) {
+          lblk = at;
+          tokens(at, ltok);
+        }
         const uint32_t dst = piece + (uint32_t)((lf - f0) % kBaseStages) * (8 * kPieceBytes) + coal;
-        const int n = lj * kNT + col;
+        const char* src = static_cast<const char*>(p.base) + (size_t)n * sizeof(T);
         if (n < p.N) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (ltok[i] >= 0) cp_async16(dst + i * 4 * kPieceRow, static_cast<const T*>(p.base) + (size_t)ltok[i] * p.N + n, true);
-        }
-        if (++lj == p.n_tiles) {
-          lj = 0;
-          ++lblk;
-          if (lf + 1 < f1) tokens(lblk, ltok);
+            if (ltok[i] >= 0) cp_async16(dst + i * 4 * kPieceRow, src + (uint64_t)(uint32_t)ltok[i] * row_bytes, true);
         }
       }
-      ++lf;
+      lf += 2;
       cp_async_commit();
     };
-    for (int i = 0; i < kBaseStages - 1; ++i) load();
+    load();
     pdl_wait();
     const int splits = lora_split(p, nblk).n;
-    int buf = 0, blk = f0 / p.n_tiles, j = f0 - blk * p.n_tiles;
-    uint32_t buf_phase = 0;
+    int blk = f0 / p.n_tiles, j = f0 - blk * p.n_tiles, sblk = -1;
     for (int f = f0; f < f1; ++f) {
+      const int i = f - f0;
       if (f == f0 || j == 0) {
-        // h of this block, 16 columns (one MMA step) at a time.  (The products with the block before have
-        // ended: this warp has seen its last tile.)
-        tokens(blk, stok);
+        // h of this block, 16 columns (one MMA step) at a time, once the products with the block before have ended
+        if (i && !__all_sync(0xffffffffu, mbar_wait_one(b.tfull + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, b.abort, p.status)))
+          break;
         const int l = p.eids[blk];
         const float s = p.scale ? p.scale[l] : 1.0f;
-        for (int c = half * 16; c < p.rn; c += 32) {
+        for (int c = group * 16; c < p.rn; c += 64) {
           float h[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) h[i] = 0.f;
+          for (int e = 0; e < 16; ++e) h[e] = 0.f;
           const float4* src = reinterpret_cast<const float4*>(p.part) + ((size_t)blk * (p.rn / 4) + c / 4) * kBlk + q * 32 + lane;
-#pragma unroll 2
+#pragma unroll 4
           for (int sp = 0; sp < splits; ++sp) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 v = src[((size_t)sp * nblk * (p.rn / 4) + i) * kBlk];
-              h[4 * i] += v.x; h[4 * i + 1] += v.y; h[4 * i + 2] += v.z; h[4 * i + 3] += v.w;
+            for (int e = 0; e < 4; ++e) {
+              const float4 v = src[((size_t)sp * nblk * (p.rn / 4) + e) * kBlk];
+              h[4 * e] += v.x; h[4 * e + 1] += v.y; h[4 * e + 2] += v.z; h[4 * e + 3] += v.w;
             }
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) h[i] = c + i < p.r ? h[i] * s : 0.f;
+          for (int e = 0; e < 16; ++e) h[e] = c + e < p.r ? h[e] * s : 0.f;
 #pragma unroll
           for (int part = 0; part < PARTS; ++part) {
             uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              w[i] = pack_bf16x2(h[2 * i], h[2 * i + 1]);
-              h[2 * i] -= bf16_bits_to_f32(w[i] & 0xffffu);
-              h[2 * i + 1] -= bf16_bits_to_f32(w[i] >> 16);
+            for (int e = 0; e < 8; ++e) {
+              w[e] = pack_bf16x2(h[2 * e], h[2 * e + 1]);
+              h[2 * e] -= bf16_bits_to_f32(w[e] & 0xffffu);
+              h[2 * e + 1] -= bf16_bits_to_f32(w[e] >> 16);
             }
             tmem_st8(h0 + lanes + part * hcols + c / 2, w);
           }
@@ -549,57 +550,65 @@ __global__ void __launch_bounds__(kExpandThreads)
         __syncwarp();
         if (lane == 0) mbar_arrive(b.done);
       }
-      load();
-      cp_async_wait<kBaseStages - 1>();
-      __syncwarp();
-      if (!__all_sync(0xffffffffu, mbar_wait_one(b.tfull + 8 * buf, buf_phase, b.abort, p.status))) break;
-      tc_fence_after();
-      const uint32_t at = piece + (uint32_t)((f - f0) % kBaseStages) * (8 * kPieceBytes);
-#pragma unroll
-      for (int c = 0; c < kHalf; c += 32) {
-        uint32_t v[32];
-        tmem_ld32_issue(tmem + buf * kNT + lanes + half * kHalf + c, v);
-        tmem_wait_ld();
-        tmem_landed(v);
-#pragma unroll
-        for (int u = 0; u < 32 * (int)sizeof(T) / 16; ++u) {
-          const uint32_t sa = at + mine + c * (int)sizeof(T) + u * 16;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (p.base) w = lds_v4(sa);
-          uint32_t* e = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 4)
-              e[i] = __float_as_uint(__uint_as_float(e[i]) + __uint_as_float(v[4 * u + i]));
-            else
-              e[i] = pack_bf16x2(bf16_bits_to_f32(e[i] & 0xffffu) + __uint_as_float(v[8 * u + 2 * i]),
-                                 bf16_bits_to_f32(e[i] >> 16) + __uint_as_float(v[8 * u + 2 * i + 1]));
-          }
-          sts_v4(sa, w);
+      if ((i & 1) == set) {
+        if (blk != sblk) {
+          sblk = blk;
+          tokens(blk, stok);
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b.tempty + 8 * buf);
-      const int n = j * kNT + col;
-      if (n < p.N) {
+        load();
+        cp_async_wait<1>();
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, mbar_wait_one(b.tfull + 8 * set, (i >> 1) & 1, b.abort, p.status))) break;
+        tc_fence_after();
+        const uint32_t at = piece + (uint32_t)(i % kBaseStages) * (8 * kPieceBytes);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (stok[i] >= 0)
-            *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (size_t)stok[i] * p.N + n) = lds_v4(at + coal + i * 4 * kPieceRow);
+        for (int c = 0; c < kHalf; c += 32) {
+          constexpr int kUnits = 32 * sizeof(T) / 16;
+          uint32_t v[32];
+          uint4 w[kUnits];
+          tmem_ld32_issue(tmem + set * kNT + lanes + half * kHalf + c, v);
+          const uint32_t sa = at + mine + c * (int)sizeof(T);
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) w[u] = p.base ? lds_v4(sa + u * 16) : make_uint4(0, 0, 0, 0);
+          tmem_wait_ld();
+          tmem_landed(v);
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) {
+            uint32_t* e = reinterpret_cast<uint32_t*>(&w[u]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              if constexpr (sizeof(T) == 4)
+                e[x] = __float_as_uint(__uint_as_float(e[x]) + __uint_as_float(v[4 * u + x]));
+              else
+                e[x] = pack_bf16x2(bf16_bits_to_f32(e[x] & 0xffffu) + __uint_as_float(v[8 * u + 2 * x]),
+                                   bf16_bits_to_f32(e[x] >> 16) + __uint_as_float(v[8 * u + 2 * x + 1]));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) sts_v4(sa + u * 16, w[u]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.tempty + 8 * set);
+        const int n = j * kNT + col;
+        if (n < p.N) {
+          char* dst = static_cast<char*>(p.out) + (size_t)n * sizeof(T);
+          uint4 w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = lds_v4(at + coal + e * 4 * kPieceRow);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (stok[e] >= 0) *reinterpret_cast<uint4*>(dst + (uint64_t)(uint32_t)stok[e] * row_bytes) = w[e];
+        }
+        __syncwarp();  // (the piece may be loaded again)
       }
-      __syncwarp();  // (the piece may be loaded again)
       if (++j == p.n_tiles) {
         j = 0;
         ++blk;
       }
-      if (++buf == kBufs) {
-        buf = 0;
-        buf_phase ^= 1u;
-      }
     }
     cp_async_wait<0>();
-    if (p.base != p.out) lora_copy_rows<T>(p, blockIdx.x * 8 + warp - 2, gridDim.x * 8);
+    if (p.base != p.out) lora_copy_rows<T>(p, blockIdx.x * 16 + warp - 2, gridDim.x * 16);
   }
   tc_finish(b, tmem, kExpandCols);
 }
@@ -615,7 +624,7 @@ struct LoraPlan {
 LoraPlan lora_plan(int T, int K, int N, int r, int L) {
   LoraPlan q = {};
   const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  q.tc = T > 64;
+  q.tc = T > 64 && N < (1 << 30);  // (the tensor-core kernels count a row's bytes in 32 bits)
   if (!q.tc) {
     q.total = up((size_t)T * r * sizeof(float));
     return q;
