@@ -41,67 +41,127 @@ struct LoraDev {
   int* status;
 };
 
-__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
-  float fa[8], fb[8];
+// Products of eight bf16 pairs in fp32, added to acc in their order.
+__device__ __forceinline__ float dot8(const uint4& a, const float (&fb)[8], float acc) {
+  float fa[8];
   widen<__nv_bfloat16, 16>(a, fa);
-  widen<__nv_bfloat16, 16>(b, fb);
 #pragma unroll
   for (int c = 0; c < 8; ++c) acc = fmaf(fa[c], fb[c], acc);
   return acc;
 }
 
-// A warp to a token and a row of its A.
+// A CTA to a token and eight rows of its A: a warp takes every eighth run of 256 columns for all of the rows
+// (eight row loads of a lane in flight beside one of x), and the warps' sums meet in shared memory.
+constexpr int kShrinkRows = 8;
 __global__ void __launch_bounds__(256) k_lora_shrink(const LoraDev p) {
   pdl_enter();
-  const int lane = threadIdx.x & 31, i = blockIdx.y * 8 + (threadIdx.x >> 5);
+  __shared__ float s[8][kShrinkRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i0 = blockIdx.y * kShrinkRows;
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
     const int l = p.ids[t];
-    if (l >= p.L || l < -1) {
-      if (threadIdx.x == 0 && blockIdx.y == 0) report(p.status, MOE_ERR_DEVICE_INDEX);
+    if (l >= p.L || l < 0) {
+      if (l != -1 && threadIdx.x == 0 && blockIdx.y == 0) report(p.status, MOE_ERR_DEVICE_INDEX);
       continue;
     }
-    if (l < 0 || i >= p.r) continue;
+    const int vecs = p.K / 8;
     const uint4* xv = reinterpret_cast<const uint4*>(p.x + (size_t)t * p.K);
-    const uint4* av = reinterpret_cast<const uint4*>(p.a + ((size_t)l * p.r + i) * p.K);
-    float acc = 0.f;
-#pragma unroll 4
-    for (int v = lane; v < p.K / 8; v += 32) acc = dot8(xv[v], av[v], acc);
+    const uint4* av = reinterpret_cast<const uint4*>(p.a + ((size_t)l * p.r + i0) * p.K);
+    float acc[kShrinkRows] = {};
+#pragma unroll 2
+    for (int v = warp * 32 + lane; v < vecs; v += 256) {
+      uint4 a[kShrinkRows];
+      const uint4 x = xv[v];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) p.h[(size_t)t * p.r + i] = p.scale ? acc * p.scale[l] : acc;
+      for (int i = 0; i < kShrinkRows; ++i) a[i] = av[(size_t)i * vecs + v];
+      float fx[8];
+      widen<__nv_bfloat16, 16>(x, fx);
+#pragma unroll
+      for (int i = 0; i < kShrinkRows; ++i) acc[i] = dot8(a[i], fx, acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kShrinkRows; ++i)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    __syncthreads();  // (the token before has been read)
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < kShrinkRows; ++i) s[warp][i] = acc[i];
+    __syncthreads();
+    if (threadIdx.x < kShrinkRows) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) sum += s[w][threadIdx.x];
+      p.h[(size_t)t * p.r + i0 + threadIdx.x] = p.scale ? sum * p.scale[l] : sum;
+    }
   }
 }
 
-// A thread to a token and an output column.
-template <typename T>
+// A CTA to a token and a run of output columns: G lanes share a column's row of B (16 bytes each),
+// and a warp walks 32 / G columns at a time, kExpandUnroll steps in flight.
+constexpr int kExpandUnroll = 8;
+template <typename T, int G>
 __global__ void __launch_bounds__(256) k_lora_expand(const LoraDev p) {
   pdl_enter();
-  __shared__ float h[kLoraMaxRank];
-  const int n = blockIdx.y * 256 + threadIdx.x;
+  constexpr int kCols = 32 / G;                      // columns of a warp's step
+  constexpr int kRun = 8 * kCols * kExpandUnroll;    // columns of a CTA's step
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane % G;
+  const int chunks = p.r / 8;
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
     const int l = p.ids[t];
-    const bool on = l >= 0 && l < p.L;
-    __syncthreads();
-    if (on)
-      for (int i = threadIdx.x; i < p.r; i += 256) h[i] = p.h[(size_t)t * p.r + i];
-    __syncthreads();
-    if (n >= p.N) continue;
-    const size_t at = (size_t)t * p.N + n;
-    float acc = p.base ? to_f32(static_cast<const T*>(p.base)[at]) : 0.f;
+    const bool on = l >= 0 && l < p.L && g < chunks;
+    float h[8] = {};
     if (on) {
-      const uint4* bv = reinterpret_cast<const uint4*>(p.b + ((size_t)l * p.N + n) * p.r);
-      float d = 0.f;
-      for (int v = 0; v < p.r / 8; ++v) {
-        float fb[8];
-        widen<__nv_bfloat16, 16>(bv[v], fb);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) d = fmaf(fb[c], h[8 * v + c], d);
-      }
-      acc += d;
+      const float4* hp = reinterpret_cast<const float4*>(p.h + (size_t)t * p.r + g * 8);
+      const float4 a = hp[0], b = hp[1];
+      h[0] = a.x; h[1] = a.y; h[2] = a.z; h[3] = a.w;
+      h[4] = b.x; h[5] = b.y; h[6] = b.z; h[7] = b.w;
     }
-    if constexpr (sizeof(T) == 4) static_cast<float*>(p.out)[at] = acc;
-    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(acc);
+    const uint4* bv = reinterpret_cast<const uint4*>(p.b + (size_t)max(l, 0) * p.N * p.r);
+    for (int n0 = blockIdx.y * kRun + warp * kCols * kExpandUnroll + lane / G; n0 - lane / G < p.N; n0 += gridDim.y * kRun) {
+      uint4 w[kExpandUnroll];
+      float base[kExpandUnroll];
+#pragma unroll
+      for (int u = 0; u < kExpandUnroll; ++u) {
+        const int n = n0 + u * kCols;
+        w[u] = make_uint4(0, 0, 0, 0);
+        base[u] = 0.f;
+        if (n < p.N) {
+          if (on) w[u] = bv[(size_t)n * chunks + g];
+          if (p.base && g == 0) base[u] = to_f32(static_cast<const T*>(p.base)[(size_t)t * p.N + n]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kExpandUnroll; ++u) {
+        float d = dot8(w[u], h, 0.f);
+#pragma unroll
+        for (int o = 1; o < G; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        const int n = n0 + u * kCols;
+        if (g == 0 && n < p.N) {
+          const size_t at = (size_t)t * p.N + n;
+          if constexpr (sizeof(T) == 4) static_cast<float*>(p.out)[at] = base[u] + d;
+          else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(base[u] + d);
+        }
+      }
+    }
   }
+}
+
+template <typename T, int G>
+cudaError_t launch_few(const LoraDev& p, cudaStream_t s) {
+  constexpr int kRun = 8 * (32 / G) * kExpandUnroll;
+  const int rows = std::min(p.T, 1 << 16);
+  MOE_LAUNCH(k_lora_shrink, dim3(rows, p.r / kShrinkRows), dim3(256), 0, s, p);
+  MOE_LAUNCH((k_lora_expand<T, G>), dim3(rows, std::min((p.N + kRun - 1) / kRun, 65535)), dim3(256), 0, s, p);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_few(const LoraDev& p, cudaStream_t s) {
+  const int chunks = p.r / 8;
+  return chunks <= 1   ? launch_few<T, 1>(p, s)
+         : chunks <= 2 ? launch_few<T, 2>(p, s)
+         : chunks <= 4 ? launch_few<T, 4>(p, s)
+         : chunks <= 8 ? launch_few<T, 8>(p, s)
+                       : launch_few<T, 16>(p, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -747,12 +807,7 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t s) {
   p.r = a.r;
   p.L = a.L;
   p.status = a.status;
-  const int rows = std::min(a.T, 1 << 16), cols = (a.N + 255) / 256;
-  if (cols > 65535) return cudaErrorInvalidValue;
-  MOE_LAUNCH(k_lora_shrink, dim3(rows, (a.r + 7) / 8), dim3(256), 0, s, p);
-  if (a.out_bf16) MOE_LAUNCH(k_lora_expand<__nv_bfloat16>, dim3(rows, cols), dim3(256), 0, s, p);
-  else MOE_LAUNCH(k_lora_expand<float>, dim3(rows, cols), dim3(256), 0, s, p);
-  return cudaGetLastError();
+  return a.out_bf16 ? launch_few<__nv_bfloat16>(p, s) : launch_few<float>(p, s);
 }
 
 }  // namespace moe
