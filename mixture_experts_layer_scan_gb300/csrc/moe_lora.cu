@@ -9,14 +9,14 @@
 // expert, blocks of 128 tokens), and both products run on the tensor cores, kind::f16 with fp32 sums:
 //   shrink   a CTA to a block and a run of K: D[128 tokens x r] += X A^T over blocks of 64 K, A by TMA, X's rows by
 //            16-byte asynchronous copies (TMA gathers of four rows of 128 bytes took about 1 us for a block);
-//            its fp32 sums go to the workspace, one plane for each run
-//   expand   persistent over (block, tile of 256 bytes of output columns): h = s * (the planes' sum, in their
-//            order) becomes the A operand in tensor memory, as bf16 parts that add up to it (2 for a bf16
-//            output: off by 2^-17 of h at most; 3 for an fp32 one: 2^-25), B's rows come by TMA, and the
-//            epilogue adds the base
+//            the CTAs of a block are a cluster and add up their fp32 sums in the order of K through distributed
+//            shared memory: h = s A x, as bf16 parts that add up to it (2 for a bf16 output: off by 2^-17 of
+//            h at most; 3 for an fp32 one: 2^-25)
+//   expand   persistent over (block, tile of 256 bytes of output columns): h becomes the A operand in tensor
+//            memory, B's rows come by TMA, and the epilogue adds the base
 // A token's row of D depends on that token alone, so what padding rows of a block hold does not matter.
-// Two launches rather than clusters that exchange h: a CTA that holds tensor memory then never waits for
-// another CTA.
+// Two launches rather than clusters that exchange h: a CTA that holds tensor memory never waits for another
+// CTA, so calls on several streams cannot block one another.
 #include <algorithm>
 #include <type_traits>
 
@@ -175,7 +175,8 @@ constexpr int kShrinkThreads = 192;  // A's producer, MMA, 4 warps that load x a
 constexpr int kExpandThreads = 576;  // producer, MMA, two sets of 8 epilogue warps
 constexpr int kExpandCols = 512;
 constexpr int kSlots = 152 * 2;    // CTAs of the shrink kernel that are resident together
-constexpr int kMaxSplits = 16;
+constexpr int kMaxSplits = 8;
+constexpr int kMaxParts = 3;
 constexpr int kBaseStages = 4;     // tiles of base in shared memory (two of each set of epilogue warps)
 constexpr int kPieceRow = kSegBytes + 16;  // bytes from row to row of a warp's piece: no bank is met twice
 constexpr int kPieceBytes = 32 * kPieceRow;
@@ -184,30 +185,19 @@ struct LoraTcDev {
   int T, K, N, r, L;
   int rn;                 // rank rounded up to 16
   int nblk_max;
-  int kb_total, max_splits;
+  int kb_total, kb_per, splits;
   int stages;
   uint32_t stage_bytes, bar_off, base_off;
   int n_tiles;
   const __nv_bfloat16* x;
   const int32_t *ids, *sorted, *eids, *meta;
   const float* scale;
-  float* part;            // [splits][blocks][rn / 4][128] float4
+  int parts;              // bf16 parts of h
+  uint4* hp;              // h as the expand kernel takes it: [block][part * rn / 8][128 rows], 8 columns each
   const void* base;
   void* out;
   int* status;
 };
-
-// K runs of a block and their length in K blocks, from the number of blocks that the routing has
-struct LoraSplit {
-  int n, kb;
-};
-__device__ __forceinline__ LoraSplit lora_split(const LoraTcDev& p, int nblk) {
-  const int want = nblk ? max(1, min(kSlots / nblk, p.max_splits)) : 1;
-  LoraSplit s;
-  s.kb = (p.kb_total + want - 1) / want;
-  s.n = nblk ? (p.kb_total + s.kb - 1) / s.kb : 0;  // (none is empty)
-  return s;
-}
 
 struct TcBars {
   uint32_t full, empty, tfull, tempty, done, drain, exit;
@@ -276,14 +266,30 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// 8 columns of a row of h from c on, scaled and as `parts` bf16 numbers that add up to each
+__device__ __forceinline__ void lora_store_h(const LoraTcDev& p, int blk, int row, int c, float s, float (&h)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h[e] = c + e < p.r ? h[e] * s : 0.f;
+  uint4* dst = p.hp + ((size_t)blk * p.parts * (p.rn / 8) + c / 8) * kBlk + row;
+  for (int part = 0; part < p.parts; ++part) {
+    uint32_t u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      u[e] = pack_bf16x2(h[2 * e], h[2 * e + 1]);
+      h[2 * e] -= bf16_bits_to_f32(u[e] & 0xffffu);
+      h[2 * e + 1] -= bf16_bits_to_f32(u[e] >> 16);
+    }
+    dst[(size_t)part * (p.rn / 8) * kBlk] = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
 template <int STAGES>
 __global__ void __launch_bounds__(kShrinkThreads)
     k_lora_shrink_tc(const __grid_constant__ CUtensorMap tmA, const LoraTcDev p) {
   pdl_wait();
   const int nblk = p.meta[META_NBLK];
-  const LoraSplit runs = lora_split(p, nblk);
-  if ((int)blockIdx.x >= nblk * runs.n) return;
-  const int split = blockIdx.x / nblk, blk = blockIdx.x - split * nblk;
+  const int blk = blockIdx.x / p.splits, split = blockIdx.x - blk * p.splits;
+  if (blk >= nblk) return;  // (a whole cluster)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   // Dependents launch once the permutation is complete (this kernel's own wait) and every CTA here holds its
   // tensor memory: the expand kernel's CTAs take theirs before they wait for this kernel.
   pdl_launch_dependents();
-  const int kb0 = split * runs.kb, kb1 = min(kb0 + runs.kb, p.kb_total);
+  const int kb0 = split * p.kb_per, kb1 = min(kb0 + p.kb_per, p.kb_total);
   constexpr uint32_t kXBytes = kBlk * 128;
 
   if (warp == 0) {
@@ -396,23 +402,55 @@ __global__ void __launch_bounds__(kShrinkThreads)
     const int q = warp & 3;
     ok = __all_sync(0xffffffffu, mbar_wait_one(b.done, 0, b.abort, p.status)) && ok;
     tc_fence_after();
+    const int me = q * 32 + lane;
+    // (the ring is idle: its memory takes the sums, [rn / 4][128 rows] float4)
     if (ok) {
-      float4* dst = reinterpret_cast<float4*>(p.part) + ((size_t)split * nblk + blk) * (p.rn / 4) * kBlk + q * 32 + lane;
       for (int c = 0; c < p.rn; c += 16) {
         float v[16];
         tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          dst[(size_t)(c / 4 + i) * kBlk] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          sts_v4(sbase + ((uint32_t)(c / 4 + i) * kBlk + me) * 16,
+                 make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                            __float_as_uint(v[4 * i + 3])));
       }
     }
   }
+  // Tensor memory is given back before this CTA waits for others of its cluster: none that needs some ever waits
+  // for one that waits.
   tc_finish(b, tmem, cols);
+  __syncwarp();
+  cluster_sync_all();
+  if (warp >= 2) {
+    const int me = (warp & 3) * 32 + lane;
+    const float scale = p.scale ? p.scale[p.eids[blk]] : 1.0f;
+    for (int c = split * 8; c < p.rn; c += p.splits * 8) {
+      const uint32_t at = sbase + ((uint32_t)(c / 4) * kBlk + me) * 16;
+      float4 u[kMaxSplits], v[kMaxSplits];
+#pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r)
+        if (r < p.splits) {
+          const uint32_t from = mapa_shared(at, r);
+          u[r] = ld_cluster_f32x4(from);
+          v[r] = ld_cluster_f32x4(from + kBlk * 16);
+        }
+      float h[8] = {};
+#pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r)
+        if (r < p.splits) {
+          h[0] += u[r].x; h[1] += u[r].y; h[2] += u[r].z; h[3] += u[r].w;
+          h[4] += v[r].x; h[5] += v[r].y; h[6] += v[r].z; h[7] += v[r].w;
+        }
+      lora_store_h(p, blk, me, c, scale, h);
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();  // (no CTA leaves while another reads its sums)
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
                : "memory");
 }
 
@@ -431,8 +469,30 @@ __device__ void lora_copy_rows(const LoraTcDev& p, int warp, int warps) {
   }
 }
 
-// Every CTA takes an equal run of the (block, column tile) pairs; its two sets of epilogue warps take tiles in
-// turn (a warp's way through a tile is a chain of latencies: with one set 91 us for 8192 x 8192 bf16).  A
+// The tiles of one CTA: an equal run of the (block, tile) pairs.  (Neighbouring tiles to neighbouring CTAs, so that
+// what is in flight lies together in memory, was slower: 120 us instead of 91.)
+struct LoraWalk {
+  int blk, tile, at, end, tiles;
+  __device__ __forceinline__ LoraWalk(const LoraTcDev& p, int nblk) {
+    tiles = p.n_tiles;
+    const long total = (long)nblk * tiles;
+    at = (int)(total * blockIdx.x / gridDim.x);
+    end = (int)(total * (blockIdx.x + 1) / gridDim.x);
+    blk = at / tiles;
+    tile = at - blk * tiles;
+  }
+  __device__ __forceinline__ bool more() const { return at < end; }
+  __device__ __forceinline__ void next() {
+    ++at;
+    if (++tile == tiles) {
+      tile = 0;
+      ++blk;
+    }
+  }
+};
+
+// Persistent; a CTA's two sets of epilogue warps take its tiles in turn (a warp's way through a tile is a chain
+// of latencies: with one set 91 us for 8192 x 8192 bf16).  A
 // warp owns 32 rows x 128 bytes of a tile: it copies that piece of base into shared memory ahead of time,
 // adds D there with a row to a thread, and stores it with 8 lanes to a row, without a barrier beyond its own.
 template <typename T, int PARTS>
@@ -453,29 +513,24 @@ __global__ void __launch_bounds__(kExpandThreads)
   const uint32_t h0 = tmem + kBufs * kNT;
   const int kboxes = (p.r + 63) / 64;
   constexpr uint32_t kBoxBytes = kNT * 128;
-  const long total = (long)nblk * p.n_tiles;
-  const int f0 = (int)(total * blockIdx.x / gridDim.x), f1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
+  LoraWalk w(p, nblk);
 
   if (warp == 0) {
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
-    int blk = f0 / p.n_tiles, j = f0 - blk * p.n_tiles, l = f0 < f1 ? p.eids[blk] : 0;
-    for (int f = f0; f < f1; ++f) {
+    for (; w.more(); w.next()) {
       if (!mbar_wait_all(b.empty + 8 * stage, phase ^ 1u, b.abort, p.status)) {
         ok = false;
         break;
       }
+      const int row = p.eids[w.blk] * p.N + w.tile * kNT;
       if (elect_one()) {
         const uint32_t sw = sbase + stage * p.stage_bytes, fb = b.full + 8 * stage;
         mbar_arrive_expect_tx(fb, (uint32_t)kboxes * kBoxBytes);
-        for (int x = 0; x < kboxes; ++x) tma_load_2d(sw + x * kBoxBytes, &tmB, x * 64, l * p.N + j * kNT, fb);
+        for (int x = 0; x < kboxes; ++x) tma_load_2d(sw + x * kBoxBytes, &tmB, x * 64, row, fb);
       }
       __syncwarp();
-      if (++j == p.n_tiles) {
-        j = 0;
-        if (f + 1 < f1) l = p.eids[++blk];
-      }
       ++issued;
       if (++stage == p.stages) {
         stage = 0;
@@ -493,11 +548,12 @@ __global__ void __launch_bounds__(kExpandThreads)
   } else if (warp == 1) {
     if (elect_one()) {
       const uint32_t idesc = idesc_make(kBlk, kNT, false);
-      int stage = 0, buf = 0, j = f0 % p.n_tiles;
+      int stage = 0, buf = 0, had = -1;
       uint32_t phase = 0, buf_phase = 0, h_phase = 0;
       bool any = false, ok = true;
-      for (int f = f0; f < f1; ++f) {
-        if (f == f0 || j == 0) {  // this block's h is in tensor memory
+      for (; w.more(); w.next()) {
+        if (w.blk != had) {  // this block's h is in tensor memory
+          had = w.blk;
           ok = mbar_wait_one(b.done, h_phase, b.abort, p.status);
           h_phase ^= 1u;
         }
@@ -513,7 +569,6 @@ __global__ void __launch_bounds__(kExpandThreads)
         tc_commit(b.empty + 8 * stage);
         tc_commit(b.tfull + 8 * buf);
         any = true;
-        if (++j == p.n_tiles) j = 0;
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
@@ -547,94 +602,86 @@ __global__ void __launch_bounds__(kExpandThreads)
       }
     };
     int ltok[8], stok[8];
-    int lf = f0 + set, lblk = -1;
+    LoraWalk ld = w;
+    if (set && ld.more()) ld.next();
+    int lblk = -1, li = 0;
     auto load = [&]() {  // base of this set's next tile
-      if (lf < f1 && p.base) {
-        const int at = lf / p.n_tiles, n = (lf - at * p.n_tiles) * kNT + col;
-        if (at != lblk) {
-          lblk = at;
-          tokens(at, ltok);
-        }
-        const uint32_t dst = piece + (uint32_t)((lf - f0) % kBaseStages) * (8 * kPieceBytes) + coal;
-        const char* src = static_cast<const char*>(p.base) + (size_t)n * sizeof(T);
-        if (n < p.N) {
+      if (ld.more()) {
+        const int n = ld.tile * kNT + col;
+        if (p.base) {
+          if (ld.blk != lblk) {
+            lblk = ld.blk;
+            tokens(lblk, ltok);
+          }
+          const uint32_t dst = piece + (uint32_t)(2 * li + set) * (8 * kPieceBytes) + coal;
+          const char* src = static_cast<const char*>(p.base) + (size_t)n * sizeof(T);
+          if (n < p.N) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (ltok[i] >= 0) cp_async16(dst + i * 4 * kPieceRow, src + (uint64_t)(uint32_t)ltok[i] * row_bytes, true);
+            for (int i = 0; i < 8; ++i)
+              if (ltok[i] >= 0) cp_async16(dst + i * 4 * kPieceRow, src + (uint64_t)(uint32_t)ltok[i] * row_bytes, true);
+          }
         }
+        li ^= 1;
+        ld.next();
+        if (ld.more()) ld.next();
       }
-      lf += 2;
       cp_async_commit();
     };
     load();
+    // h of a block: pieces of 8 columns, every fourth to a group of warps; the first kHeld of the next block's are
+    // fetched while this one is at work
+    constexpr int kHeld = 4;
+    const int pieces = PARTS * (p.rn / 8);
+    uint4 held[kHeld];
+    auto fetch = [&](int blk) {
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if (group + 4 * u < pieces) held[u] = __ldcg(p.hp + ((size_t)blk * pieces + group + 4 * u) * kBlk + q * 32 + lane);
+    };
     pdl_wait();
-    const int splits = lora_split(p, nblk).n;
-    int blk = f0 / p.n_tiles, j = f0 - blk * p.n_tiles, sblk = -1;
-    for (int f = f0; f < f1; ++f) {
-      const int i = f - f0;
-      if (f == f0 || j == 0) {
-        // h of this block, 16 columns (one MMA step) at a time, once the products with the block before have ended
+    if (w.more()) fetch(w.blk);
+    const int last_blk = w.more() ? (w.end - 1) / w.tiles : 0;
+    int had = -1, si = 0;
+    for (int i = 0; w.more(); ++i, w.next()) {
+      if (w.blk != had) {
+        // (the products with the block before have to have ended)
         if (i && !__all_sync(0xffffffffu, mbar_wait_one(b.tfull + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, b.abort, p.status)))
           break;
-        const int l = p.eids[blk];
-        const float s = p.scale ? p.scale[l] : 1.0f;
-        for (int c = group * 16; c < p.rn; c += 64) {
-          float h[16];
+        had = w.blk;
+        tokens(had, stok);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) h[e] = 0.f;
-          const float4* src = reinterpret_cast<const float4*>(p.part) + ((size_t)blk * (p.rn / 4) + c / 4) * kBlk + q * 32 + lane;
-#pragma unroll 4
-          for (int sp = 0; sp < splits; ++sp) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 v = src[((size_t)sp * nblk * (p.rn / 4) + e) * kBlk];
-              h[4 * e] += v.x; h[4 * e + 1] += v.y; h[4 * e + 2] += v.z; h[4 * e + 3] += v.w;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) h[e] = c + e < p.r ? h[e] * s : 0.f;
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part) {
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              w[e] = pack_bf16x2(h[2 * e], h[2 * e + 1]);
-              h[2 * e] -= bf16_bits_to_f32(w[e] & 0xffffu);
-              h[2 * e + 1] -= bf16_bits_to_f32(w[e] >> 16);
-            }
-            tmem_st8(h0 + lanes + part * hcols + c / 2, w);
-          }
-        }
+        for (int u = 0; u < kHeld; ++u)
+          if (group + 4 * u < pieces) tmem_st4(h0 + lanes + (group + 4 * u) * 4, held[u]);
+        for (int x = group + 4 * kHeld; x < pieces; x += 4)
+          tmem_st4(h0 + lanes + x * 4, __ldcg(p.hp + ((size_t)had * pieces + x) * kBlk + q * 32 + lane));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b.done);
+        if (had < last_blk) fetch(had + 1);
       }
       if ((i & 1) == set) {
-        if (blk != sblk) {
-          sblk = blk;
-          tokens(blk, stok);
-        }
         load();
         cp_async_wait<1>();
         __syncwarp();
         if (!__all_sync(0xffffffffu, mbar_wait_one(b.tfull + 8 * set, (i >> 1) & 1, b.abort, p.status))) break;
         tc_fence_after();
-        const uint32_t at = piece + (uint32_t)(i % kBaseStages) * (8 * kPieceBytes);
+        const uint32_t at = piece + (uint32_t)(2 * si + set) * (8 * kPieceBytes);
+        si ^= 1;
 #pragma unroll
         for (int c = 0; c < kHalf; c += 32) {
           constexpr int kUnits = 32 * sizeof(T) / 16;
           uint32_t v[32];
-          uint4 w[kUnits];
+          uint4 o[kUnits];
           tmem_ld32_issue(tmem + set * kNT + lanes + half * kHalf + c, v);
           const uint32_t sa = at + mine + c * (int)sizeof(T);
 #pragma unroll
-          for (int u = 0; u < kUnits; ++u) w[u] = p.base ? lds_v4(sa + u * 16) : make_uint4(0, 0, 0, 0);
+          for (int u = 0; u < kUnits; ++u) o[u] = p.base ? lds_v4(sa + u * 16) : make_uint4(0, 0, 0, 0);
           tmem_wait_ld();
           tmem_landed(v);
 #pragma unroll
           for (int u = 0; u < kUnits; ++u) {
-            uint32_t* e = reinterpret_cast<uint32_t*>(&w[u]);
+            uint32_t* e = reinterpret_cast<uint32_t*>(&o[u]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               if constexpr (sizeof(T) == 4)
@@ -645,26 +692,22 @@ __global__ void __launch_bounds__(kExpandThreads)
             }
           }
 #pragma unroll
-          for (int u = 0; u < kUnits; ++u) sts_v4(sa + u * 16, w[u]);
+          for (int u = 0; u < kUnits; ++u) sts_v4(sa + u * 16, o[u]);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b.tempty + 8 * set);
-        const int n = j * kNT + col;
+        const int n = w.tile * kNT + col;
         if (n < p.N) {
           char* dst = static_cast<char*>(p.out) + (size_t)n * sizeof(T);
-          uint4 w[8];
+          uint4 o[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = lds_v4(at + coal + e * 4 * kPieceRow);
+          for (int e = 0; e < 8; ++e) o[e] = lds_v4(at + coal + e * 4 * kPieceRow);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (stok[e] >= 0) *reinterpret_cast<uint4*>(dst + (uint64_t)(uint32_t)stok[e] * row_bytes) = w[e];
+            if (stok[e] >= 0) *reinterpret_cast<uint4*>(dst + (uint64_t)(uint32_t)stok[e] * row_bytes) = o[e];
         }
         __syncwarp();  // (the piece may be loaded again)
-      }
-      if (++j == p.n_tiles) {
-        j = 0;
-        ++blk;
       }
     }
     cp_async_wait<0>();
@@ -676,9 +719,9 @@ __global__ void __launch_bounds__(kExpandThreads)
 // The tensor-core path's shape for a problem (from its sizes alone).
 struct LoraPlan {
   bool tc;
-  int rn, nblk, kb_total, max_splits;
+  int rn, nblk, kb_total, kb_per, splits;
   long cap;
-  size_t o_sorted, o_eids, o_meta, o_part, total;
+  size_t o_sorted, o_eids, o_meta, o_h, total;
 };
 
 LoraPlan lora_plan(int T, int K, int N, int r, int L) {
@@ -693,13 +736,21 @@ LoraPlan lora_plan(int T, int K, int N, int r, int L) {
   q.cap = (long)T + (long)std::min(L, T) * (kBlk - 1);
   q.nblk = (int)(q.cap / kBlk);
   q.kb_total = (K + 63) / 64;
-  q.max_splits = std::max(1, std::min(kMaxSplits, q.kb_total / 4));  // (4 K blocks at least to a CTA)
+  // a cluster shares a block's K where blocks are few: as many runs as keep all CTAs resident (an adapter's last
+  // block is half full on average), of 4 K blocks at least and none of them empty
+  const long blocks = T / kBlk + std::min(L, T) / 2 + 1;
+  int n = 1;
+  while (n < kMaxSplits && blocks * 2 * n <= kSlots && q.kb_total >= 8 * n) n *= 2;
+  for (;; n /= 2) {
+    q.kb_per = (q.kb_total + n - 1) / n;
+    if (q.kb_per * (n - 1) < q.kb_total) break;
+  }
+  q.splits = n;
   q.o_sorted = 0;
   q.o_eids = up(q.cap * sizeof(int32_t));
   q.o_meta = q.o_eids + up((size_t)q.nblk * sizeof(int32_t));
-  q.o_part = q.o_meta + up((size_t)meta_words(L) * sizeof(int32_t));
-  // (a plane for each block and run of K: kSlots, or the blocks where they are more)
-  q.total = q.o_part + up((size_t)std::max(q.nblk, kSlots) * kBlk * q.rn * sizeof(float));
+  q.o_h = q.o_meta + up((size_t)meta_words(L) * sizeof(int32_t));
+  q.total = q.o_h + up((size_t)q.nblk * kBlk * q.rn * kMaxParts * 2);
   return q;
 }
 
@@ -741,9 +792,21 @@ cudaError_t launch_shrink(const CUtensorMap& tmA, LoraTcDev p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   p.stage_bytes = kBlk * 128 + (uint32_t)p.rn * 128;
   p.bar_off = STAGES * p.stage_bytes;
-  MOE_LAUNCH(k_lora_shrink_tc<STAGES>, dim3(std::max(p.nblk_max, kSlots)), dim3(kShrinkThreads),
-             1024 + p.bar_off + kBarBytes, s, tmA, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.nblk_max * p.splits);
+  cfg.blockDim = dim3(kShrinkThreads);
+  cfg.dynamicSmemBytes = 1024 + p.bar_off + kBarBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_lora_shrink_tc<STAGES>, tmA, p);
 }
 
 cudaError_t launch_lora_tc(const LoraArgs& a, const LoraPlan& q, cudaStream_t s) {
@@ -764,14 +827,16 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const LoraPlan& q, cudaStream_t s)
   p.rn = q.rn;
   p.nblk_max = q.nblk;
   p.kb_total = q.kb_total;
-  p.max_splits = q.max_splits;
+  p.kb_per = q.kb_per;
+  p.splits = q.splits;
   p.x = static_cast<const __nv_bfloat16*>(a.x);
   p.ids = a.ids;
   p.sorted = sorted;
   p.eids = eids;
   p.meta = meta;
   p.scale = a.scale;
-  p.part = reinterpret_cast<float*>(ws + q.o_part);
+  p.hp = reinterpret_cast<uint4*>(ws + q.o_h);
+  p.parts = a.out_bf16 ? 2 : kMaxParts;
   p.base = a.base;
   p.out = a.out;
   p.status = a.status;
@@ -780,7 +845,7 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const LoraPlan& q, cudaStream_t s)
       : q.rn <= 64 ? launch_shrink<4>(tmA, p, s)
                    : launch_shrink<3>(tmA, p, s);
   if (e != cudaSuccess) return e;
-  return a.out_bf16 ? launch_expand<__nv_bfloat16, 2>(a, p, s) : launch_expand<float, 3>(a, p, s);
+  return a.out_bf16 ? launch_expand<__nv_bfloat16, 2>(a, p, s) : launch_expand<float, kMaxParts>(a, p, s);
 }
 
 }  // namespace
