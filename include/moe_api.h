@@ -459,7 +459,7 @@ MOE_API int moe_postnorm_backward(const void* d_out, const void* d_h, const void
  * An adapter of lower rank is padded with zero rows of a and zero columns of b.  What an adapter that no
  * token names holds does not matter.
  * T >= 0, K, N, rank, L >= 1; rank <= 128 and K, N, rank multiples of 8 (MOE_ERR_UNSUPPORTED otherwise); T, K
- * and L * N below 2^31 - 2^24, L <= 1024.  workspace: moe_lora_workspace_size bytes, 256-byte aligned, contents
+ * and L * N below 2^31 - 2^24, L <= 1023.  workspace: moe_lora_workspace_size bytes, 256-byte aligned, contents
  * ignored; ids and scale 4-byte aligned, the other pointers 16.  No gradient: for serving. */
 MOE_API int moe_lora_workspace_size(int T, int K, int N, int rank, int L, size_t* bytes);
 MOE_API int moe_lora(const void* x, const void* a, const void* b, const int32_t* ids, const float* scale,

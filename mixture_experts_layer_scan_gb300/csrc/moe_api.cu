@@ -1269,7 +1269,7 @@ int moe_postnorm_backward(const void* d_out, const void* d_h, const void* x, con
 }
 
 static int lora_size(int T, int K, int N, int rank, int L) {
-  if (T < 0 || K < 1 || N < 1 || rank < 1 || L < 1 || L > 1024 || T >= kBlockMaxDim || K >= kBlockMaxDim ||
+  if (T < 0 || K < 1 || N < 1 || rank < 1 || L < 1 || L > 1023 || T >= kBlockMaxDim || K >= kBlockMaxDim ||
       N >= kBlockMaxDim || (long long)L * N >= kBlockMaxDim)
     return MOE_ERR_ARG;
   if (rank > kLoraMaxRank || rank % 8 || K % 8 || N % 8) return MOE_ERR_UNSUPPORTED;

@@ -37,11 +37,12 @@ cudaError_t launch_inject_timeout(const int* flag, int* status, cudaStream_t s);
 // run has an odd number of blocks: pblk[c] = (first row << 1) | (1 for 128 rows); their
 // count goes to meta[META_NPB].  inv (nullable, T*k words): the sorted row of each
 // pair, -1 for a pair left out.  max_count: an expert's pairs past this many, in flat order, are dropped
-// and flagged too.
+// and flagged too.  rest: ids outside [0, E - 1) make up expert E - 1 instead of being dropped (flagged alike).
 cudaError_t launch_align(const int32_t* ids, int T, int k, int E, int B, int32_t* sorted, int32_t* eids,
                          int32_t* npp, int32_t* counts, int32_t* meta, int* status, cudaStream_t s,
                          bool skip_minus_one = false, int32_t* pblk = nullptr, unsigned* zero_words = nullptr,
-                         int n_zero = 0, int32_t* inv = nullptr, int max_count = INT32_MAX);
+                         int n_zero = 0, int32_t* inv = nullptr, int max_count = INT32_MAX,
+                         bool rest = false);
 // dst (device) = bytes of page-locked host memory read by the device at src (its device
 // address); a kernel launched like the library's others (bytes and both addresses 16-byte
 // multiples, else cudaErrorInvalidValue)

@@ -6,7 +6,7 @@
 // token at a time (its adapter's rows come from L2 where tokens share them).
 //
 // More: the tokens are sorted by adapter (the permutation of the expert layer, an adapter in the place of an
-// expert, blocks of 128 tokens), and both products run on the tensor cores, kind::f16 with fp32 sums:
+// expert, blocks of 128 tokens, those without one behind), and both products run on the tensor cores, kind::f16 with fp32 sums:
 //   shrink   a CTA to a block and a run of K: D[128 tokens x r] += X A^T over blocks of 64 K, A by TMA, X's rows by
 //            16-byte asynchronous copies (TMA gathers of four rows of 128 bytes took about 1 us for a block);
 //            the CTAs of a block are a cluster and add up their fp32 sums in the order of K through distributed
@@ -190,7 +190,7 @@ struct LoraTcDev {
   uint32_t stage_bytes, bar_off, base_off;
   int n_tiles;
   const __nv_bfloat16* x;
-  const int32_t *ids, *sorted, *eids, *meta;
+  const int32_t *sorted, *eids, *meta;
   const float* scale;
   int parts;              // bf16 parts of h
   uint4* hp;              // h as the expand kernel takes it: [block][part * rn / 8][128 rows], 8 columns each
@@ -198,6 +198,9 @@ struct LoraTcDev {
   void* out;
   int* status;
 };
+
+// Blocks of tokens with an adapter; those without one are the last group of the permutation.
+__device__ __forceinline__ int lora_blocks(const LoraTcDev& p) { return p.meta[meta_offsets(p.L + 1) + p.L] / kBlk; }
 
 struct TcBars {
   uint32_t full, empty, tfull, tempty, done, drain, exit;
@@ -287,7 +290,7 @@ template <int STAGES>
 __global__ void __launch_bounds__(kShrinkThreads)
     k_lora_shrink_tc(const __grid_constant__ CUtensorMap tmA, const LoraTcDev p) {
   pdl_wait();
-  const int nblk = p.meta[META_NBLK];
+  const int nblk = lora_blocks(p);
   const int blk = blockIdx.x / p.splits, split = blockIdx.x - blk * p.splits;
   if (blk >= nblk) return;  // (a whole cluster)
   extern __shared__ uint8_t smem_raw[];
@@ -454,26 +457,11 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
                : "memory");
 }
 
-// Rows of out without an adapter
-template <typename T>
-__device__ void lora_copy_rows(const LoraTcDev& p, int warp, int warps) {
-  const int lane = threadIdx.x & 31;
-  const int vecs = (int)((size_t)p.N * sizeof(T) / 16);
-  for (int t = warp; t < p.T; t += warps) {
-    const int l = p.ids[t];
-    if (l >= 0 && l < p.L) continue;
-    const uint4* src = static_cast<const uint4*>(p.base) + (size_t)t * vecs;
-    uint4* dst = static_cast<uint4*>(p.out) + (size_t)t * vecs;
-#pragma unroll 8
-    for (int v = lane; v < vecs; v += 32) dst[v] = p.base ? src[v] : make_uint4(0, 0, 0, 0);
-  }
-}
-
 // The tiles of one CTA: an equal run of the (block, tile) pairs.  (Neighbouring tiles to neighbouring CTAs, so that
 // what is in flight lies together in memory, was slower: 120 us instead of 91.)
 struct LoraWalk {
   int blk, tile, at, end, tiles;
-  __device__ __forceinline__ LoraWalk(const LoraTcDev& p, int nblk) {
+  __device__ __forceinline__ LoraWalk(const LoraTcDev& p, int nblk) {  // (of the first nblk blocks)
     tiles = p.n_tiles;
     const long total = (long)nblk * tiles;
     at = (int)(total * blockIdx.x / gridDim.x);
@@ -508,18 +496,18 @@ __global__ void __launch_bounds__(kExpandThreads)
   const uint32_t tmem = tc_setup(b, kExpandCols, 1, 16);
   // The permutation, base and the weights were complete before the preceding kernel let this one start; only
   // its sums are not.
-  const int nblk = p.meta[META_NBLK];
+  const int nblk = lora_blocks(p);
   const uint32_t hcols = (uint32_t)(p.rn / 2);  // columns of one part of h
   const uint32_t h0 = tmem + kBufs * kNT;
   const int kboxes = (p.r + 63) / 64;
   constexpr uint32_t kBoxBytes = kNT * 128;
-  LoraWalk w(p, nblk);
+  LoraWalk w(p, p.base == p.out ? nblk : p.meta[META_NBLK]);  // (in place, rows without an adapter are done)
 
   if (warp == 0) {
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
-    for (; w.more(); w.next()) {
+    for (; w.more() && w.blk < nblk; w.next()) {
       if (!mbar_wait_all(b.empty + 8 * stage, phase ^ 1u, b.abort, p.status)) {
         ok = false;
         break;
@@ -551,7 +539,7 @@ __global__ void __launch_bounds__(kExpandThreads)
       int stage = 0, buf = 0, had = -1;
       uint32_t phase = 0, buf_phase = 0, h_phase = 0;
       bool any = false, ok = true;
-      for (; w.more(); w.next()) {
+      for (; w.more() && w.blk < nblk; w.next()) {
         if (w.blk != had) {  // this block's h is in tensor memory
           had = w.blk;
           ok = mbar_wait_one(b.done, h_phase, b.abort, p.status);
@@ -639,16 +627,20 @@ __global__ void __launch_bounds__(kExpandThreads)
         if (group + 4 * u < pieces) held[u] = __ldcg(p.hp + ((size_t)blk * pieces + group + 4 * u) * kBlk + q * 32 + lane);
     };
     pdl_wait();
-    if (w.more()) fetch(w.blk);
-    const int last_blk = w.more() ? (w.end - 1) / w.tiles : 0;
-    int had = -1, si = 0;
+    if (w.more() && w.blk < nblk) fetch(w.blk);
+    const int last_blk = w.more() ? min(nblk - 1, (w.end - 1) / w.tiles) : 0;
+    int had = -1, with_h = -1, si = 0;
     for (int i = 0; w.more(); ++i, w.next()) {
+      const bool adapter = w.blk < nblk;
       if (w.blk != had) {
+        had = w.blk;
+        tokens(had, stok);
+      }
+      if (adapter && w.blk != with_h) {
         // (the products with the block before have to have ended)
         if (i && !__all_sync(0xffffffffu, mbar_wait_one(b.tfull + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, b.abort, p.status)))
           break;
-        had = w.blk;
-        tokens(had, stok);
+        with_h = w.blk;
 #pragma unroll
         for (int u = 0; u < kHeld; ++u)
           if (group + 4 * u < pieces) tmem_st4(h0 + lanes + (group + 4 * u) * 4, held[u]);
@@ -664,8 +656,10 @@ __global__ void __launch_bounds__(kExpandThreads)
         load();
         cp_async_wait<1>();
         __syncwarp();
-        if (!__all_sync(0xffffffffu, mbar_wait_one(b.tfull + 8 * set, (i >> 1) & 1, b.abort, p.status))) break;
-        tc_fence_after();
+        if (adapter) {
+          if (!__all_sync(0xffffffffu, mbar_wait_one(b.tfull + 8 * set, (i >> 1) & 1, b.abort, p.status))) break;
+          tc_fence_after();
+        }
         const uint32_t at = piece + (uint32_t)(2 * si + set) * (8 * kPieceBytes);
         si ^= 1;
 #pragma unroll
@@ -673,7 +667,12 @@ __global__ void __launch_bounds__(kExpandThreads)
           constexpr int kUnits = 32 * sizeof(T) / 16;
           uint32_t v[32];
           uint4 o[kUnits];
-          tmem_ld32_issue(tmem + set * kNT + lanes + half * kHalf + c, v);
+          if (adapter) {
+            tmem_ld32_issue(tmem + set * kNT + lanes + half * kHalf + c, v);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) v[u] = 0;
+          }
           const uint32_t sa = at + mine + c * (int)sizeof(T);
 #pragma unroll
           for (int u = 0; u < kUnits; ++u) o[u] = p.base ? lds_v4(sa + u * 16) : make_uint4(0, 0, 0, 0);
@@ -696,7 +695,7 @@ __global__ void __launch_bounds__(kExpandThreads)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b.tempty + 8 * set);
+        if (adapter && lane == 0) mbar_arrive(b.tempty + 8 * set);
         const int n = w.tile * kNT + col;
         if (n < p.N) {
           char* dst = static_cast<char*>(p.out) + (size_t)n * sizeof(T);
@@ -711,7 +710,6 @@ __global__ void __launch_bounds__(kExpandThreads)
       }
     }
     cp_async_wait<0>();
-    if (p.base != p.out) lora_copy_rows<T>(p, blockIdx.x * 16 + warp - 2, gridDim.x * 16);
   }
   tc_finish(b, tmem, kExpandCols);
 }
@@ -733,12 +731,12 @@ LoraPlan lora_plan(int T, int K, int N, int r, int L) {
     return q;
   }
   q.rn = (r + 15) / 16 * 16;
-  q.cap = (long)T + (long)std::min(L, T) * (kBlk - 1);
+  q.cap = (long)T + (long)std::min(L + 1, T) * (kBlk - 1);  // (an adapter's tokens, and those without one, to whole blocks)
   q.nblk = (int)(q.cap / kBlk);
   q.kb_total = (K + 63) / 64;
-  // a cluster shares a block's K where blocks are few: as many runs as keep all CTAs resident (an adapter's last
-  // block is half full on average), of 4 K blocks at least and none of them empty
-  const long blocks = T / kBlk + std::min(L, T) / 2 + 1;
+  // a cluster shares a block's K where blocks are few: as many runs as keep all CTAs resident (a block to each
+  // adapter, the last one of each half full on average), of 4 K blocks at least and none of them empty
+  const long blocks = std::max(std::min(L, T), T / kBlk + std::min(L, T) / 2 + 1);
   int n = 1;
   while (n < kMaxSplits && blocks * 2 * n <= kSlots && q.kb_total >= 8 * n) n *= 2;
   for (;; n /= 2) {
@@ -749,7 +747,7 @@ LoraPlan lora_plan(int T, int K, int N, int r, int L) {
   q.o_sorted = 0;
   q.o_eids = up(q.cap * sizeof(int32_t));
   q.o_meta = q.o_eids + up((size_t)q.nblk * sizeof(int32_t));
-  q.o_h = q.o_meta + up((size_t)meta_words(L) * sizeof(int32_t));
+  q.o_h = q.o_meta + up((size_t)meta_words(L + 1) * sizeof(int32_t));
   q.total = q.o_h + up((size_t)q.nblk * kBlk * q.rn * kMaxParts * 2);
   return q;
 }
@@ -816,7 +814,8 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const LoraPlan& q, cudaStream_t s)
   int32_t* meta = reinterpret_cast<int32_t*>(ws + q.o_meta);
   CUtensorMap tmA;
   if (!make_tensor_map_2d(&tmA, a.a, 2, a.K, (uint64_t)a.L * a.r, a.r)) return cudaErrorInvalidValue;
-  cudaError_t e = launch_align(a.ids, a.T, 1, a.L, kBlk, sorted, eids, meta + META_NPP, nullptr, meta, a.status, s, true);
+  cudaError_t e = launch_align(a.ids, a.T, 1, a.L + 1, kBlk, sorted, eids, meta + META_NPP, nullptr, meta, a.status, s, true,
+                               nullptr, nullptr, 0, nullptr, INT32_MAX, true);
   if (e != cudaSuccess) return e;
   LoraTcDev p = {};
   p.T = a.T;
@@ -830,7 +829,6 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const LoraPlan& q, cudaStream_t s)
   p.kb_per = q.kb_per;
   p.splits = q.splits;
   p.x = static_cast<const __nv_bfloat16*>(a.x);
-  p.ids = a.ids;
   p.sorted = sorted;
   p.eids = eids;
   p.meta = meta;

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kAlignThreads, 1)
     k_align(const int32_t* __restrict__ ids, int T, int k, int E, int B, int32_t* __restrict__ sorted,
             int32_t* __restrict__ eids, int32_t* __restrict__ npp_out, int32_t* __restrict__ counts_out,
             int32_t* __restrict__ meta, int* status, int skip_minus_one, int32_t* __restrict__ pblk,
-            unsigned* __restrict__ zero_words, int n_zero, int32_t* __restrict__ inv, int max_count) {
+            unsigned* __restrict__ zero_words, int n_zero, int32_t* __restrict__ inv, int max_count, int rest) {
   pdl_enter();
   // counters of the next kernels of this call start at zero (e.g. GEMM1's split arrivals)
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_zero; i += gridDim.x * blockDim.x) zero_words[i] = 0u;
@@ -117,8 +117,8 @@ __global__ void __launch_bounds__(kAlignThreads, 1)
     int e = -1;
     if (f < end) {
       e = ids[f];
-      // -1 marks a pair another pass handles (skip_minus_one): dropped without a flag
-      if (e < 0 || e >= E) { bad = bad || !(skip_minus_one && e == -1); e = -1; }
+      // -1 marks a pair another pass handles (skip_minus_one): dropped without a flag, or one of the last group
+      if (e < 0 || e >= E - rest) { bad = bad || !(skip_minus_one && e == -1); e = rest ? E - 1 : -1; }
     }
     const unsigned grp = E < 128 ? same_expert<7>(e) : E < 512 ? same_expert<9>(e) : same_expert<11>(e);
     const int rank = __popc(grp & ((1u << lane) - 1u));
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kAlignThreads, 1)
     k_align_mid(const int32_t* __restrict__ ids, int n, int E, int B, int32_t* __restrict__ sorted,
                 int32_t* __restrict__ eids, int32_t* __restrict__ npp_out, int32_t* __restrict__ counts_out,
                 int32_t* __restrict__ meta, int* status, int skip_minus_one, unsigned* __restrict__ zero_words,
-                int n_zero, int32_t* __restrict__ inv, int max_count) {
+                int n_zero, int32_t* __restrict__ inv, int max_count, int rest) {
   pdl_enter();
   for (int i = threadIdx.x; i < n_zero; i += blockDim.x) zero_words[i] = 0u;
   extern __shared__ int sm[];
@@ -284,9 +284,9 @@ __global__ void __launch_bounds__(kAlignThreads, 1)
   int e = -1;
   if (f < n) {
     e = ids[f];
-    if (e < 0 || e >= E) {
+    if (e < 0 || e >= E - rest) {
       if (!(skip_minus_one && e == -1)) report(status, MOE_ERR_DEVICE_INDEX);
-      e = -1;
+      e = rest ? E - 1 : -1;
     }
   }
   __syncthreads();
@@ -782,10 +782,10 @@ int grid_for(size_t work, int threads, int cap_blocks = 152 * 16) {
 cudaError_t launch_align(const int32_t* ids, int T, int k, int E, int B, int32_t* sorted, int32_t* eids,
                          int32_t* npp, int32_t* counts, int32_t* meta, int* status, cudaStream_t s,
                          bool skip_minus_one, int32_t* pblk, unsigned* zero_words, int n_zero, int32_t* inv,
-                         int max_count) {
+                         int max_count, bool rest) {
   if (pblk && B != 128) return cudaErrorInvalidValue;
   if (n_zero > 0 && !zero_words) return cudaErrorInvalidValue;
-  if ((long)T * k <= kAlignSmallPairs && !pblk) {
+  if ((long)T * k <= kAlignSmallPairs && !pblk && !rest) {
     MOE_LAUNCH(k_align_small, dim3(1), dim3(kAlignSmallThreads), 0, s, ids, T * k, E, B, sorted, eids, npp, counts,
                meta, status, skip_minus_one ? 1 : 0, zero_words, n_zero, inv, max_count);
     return cudaGetLastError();
@@ -801,7 +801,7 @@ cudaError_t launch_align(const int32_t* ids, int T, int k, int E, int B, int32_t
     }
     const size_t msmem = (size_t)(kAlignWarps * E + 2 * E + 1) * sizeof(int);
     MOE_LAUNCH(k_align_mid, dim3(1), dim3(kAlignThreads), msmem, s, ids, T * k, E, B, sorted, eids, npp, counts, meta,
-               status, skip_minus_one ? 1 : 0, zero_words, n_zero, inv, max_count);
+               status, skip_minus_one ? 1 : 0, zero_words, n_zero, inv, max_count, rest ? 1 : 0);
     return cudaGetLastError();
   }
   const size_t smem = (size_t)(kAlignWarps * E + 4 * E + 1 + 33) * sizeof(int);
@@ -834,7 +834,7 @@ cudaError_t launch_align(const int32_t* ids, int T, int k, int E, int B, int32_t
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k_align, ids, T, k, E, B, sorted, eids, npp, counts, meta, status,
-                            skip_minus_one ? 1 : 0, pblk, zero_words, n_zero, inv, max_count);
+                            skip_minus_one ? 1 : 0, pblk, zero_words, n_zero, inv, max_count, rest ? 1 : 0);
 }
 
 cudaError_t launch_amax_bf16(const void* X, size_t n, unsigned* amax_bits, cudaStream_t s) {

@@ -108,7 +108,7 @@ def test_lora(moe):
     f = moe.lib().moe_lora
     need = moe.moe_lora_workspace_size(4, 64, 72, 16, 3)
     args = [P, P, P, P, P, P, 4, 64, 72, 16, 3, 1, P, P, need, None]
-    each_refused(f, args, [(6, -1), (7, 0), (8, 0), (9, 0), (10, 0), (10, 1025), (6, BIG), (7, BIG), (8, BIG)] +
+    each_refused(f, args, [(6, -1), (7, 0), (8, 0), (9, 0), (10, 0), (10, 1024), (6, BIG), (7, BIG), (8, BIG)] +
                  [(i, None) for i in (0, 1, 2, 3, 12, 13)], moe.MOE_ERR_ARG)
     each_refused(f, args, [(7, 60), (8, 70), (9, 12), (9, 136), (11, 2)], moe.MOE_ERR_UNSUPPORTED)
     each_refused(f, args, [(i, ODD4) for i in (0, 1, 2, 5, 12, 13)] + [(3, ODD2), (4, ODD2)], moe.MOE_ERR_ALIGNMENT)
