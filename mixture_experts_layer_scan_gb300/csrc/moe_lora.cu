@@ -2,10 +2,10 @@
 //
 //   out[t] = base[t] + s[l] B_l (A_l x_t),  l = ids[t];  out[t] = base[t] where ids[t] = -1
 //
-// Few tokens: two launches on the CUDA cores, h = s A x (fp32, in the workspace), then out = base + B h, a
+// Little work (lora_plan says how much): two launches on the CUDA cores, h = s A x (fp32, in the workspace), then out = base + B h, a
 // token at a time (its adapter's rows come from L2 where tokens share them).
 //
-// More: the tokens are sorted by adapter (the permutation of the expert layer, an adapter in the place of an
+// More work: the tokens are sorted by adapter (the permutation of the expert layer, an adapter in the place of an
 // expert, blocks of 128 tokens, those without one behind), and both products run on the tensor cores, kind::f16 with fp32 sums:
 //   shrink   a CTA to a block and a run of K: D[128 tokens x r] += X A^T over blocks of 64 K, A by TMA, X's rows by
 //            16-byte asynchronous copies (TMA gathers of four rows of 128 bytes took about 1 us for a block);
@@ -725,7 +725,15 @@ struct LoraPlan {
 LoraPlan lora_plan(int T, int K, int N, int r, int L) {
   LoraPlan q = {};
   const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  q.tc = T > 64 && N < (1 << 30);  // (the tensor-core kernels count a row's bytes in 32 bits)
+  // Which path, by what each was measured to cost (us).  A token at a time: 5, and the adapters' rows of every
+  // token at 9 TB/s (mostly from L2: 512 tokens of rank 8 through 4096 x 4096 12.2, 256 of rank 64 35, 1024 of rank
+  // 16 42, 256 of rank 128 through 8192 x 8192 119).  Tensor cores: 13, every adapter's rows once from memory, and
+  // 0.009 for each output tile of a block, however few its tokens (the same four: 18.6, 21.2, 36, 33).
+  const long named = std::min(L, T), blocks = std::max(named, T / kBlk + named / 2 + 1);  // (as far as T and L tell)
+  const double adapter = 2.0 * r * ((double)K + N);
+  const double one_by_one = 5.0 + T * adapter / 9e6;
+  const double sorted = 13.0 + named * adapter / 6.5e6 + 0.009 * blocks * ((N + 127) / 128);
+  q.tc = one_by_one > sorted && N < (1 << 30);  // (the tensor-core kernels count a row's bytes in 32 bits)
   if (!q.tc) {
     q.total = up((size_t)T * r * sizeof(float));
     return q;
@@ -736,7 +744,6 @@ LoraPlan lora_plan(int T, int K, int N, int r, int L) {
   q.kb_total = (K + 63) / 64;
   // a cluster shares a block's K where blocks are few: as many runs as keep all CTAs resident (a block to each
   // adapter, the last one of each half full on average), of 4 K blocks at least and none of them empty
-  const long blocks = std::max(std::min(L, T), T / kBlk + std::min(L, T) / 2 + 1);
   int n = 1;
   while (n < kMaxSplits && blocks * 2 * n <= kSlots && q.kb_total >= 8 * n) n *= 2;
   for (;; n /= 2) {

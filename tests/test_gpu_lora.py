@@ -73,10 +73,34 @@ def test_sizes(moe, size, out_t):
     check(moe, make(*size, seed=sum(size)), out_t)
 
 
-@pytest.mark.parametrize("T", [2, 40, 500])
-def test_forms(moe, T):
+def sorts(moe, T, K, N, r, L):
+    """Whether a call sorts its tokens by adapter (tensor cores): its workspace is then more than h [T,r] in fp32."""
+    return moe.moe_lora_workspace_size(T, K, N, r, L) > -(-T * r * 4 // 256) * 256
+
+
+# the same for what the tensor cores take: odd lengths of K, N and rank, a block of one token, adapters in one block
+# each and in many, K in one piece and shared by clusters of 2, 4 and 8
+LARGE = [(120000, 72, 40, 8, 3), (9000, 136, 264, 24, 5), (100001, 64, 8, 16, 1), (300, 2040, 4104, 128, 3),
+         (129, 8192, 8200, 120, 1), (1000, 1032, 2056, 64, 40), (2500, 520, 1000, 40, 7), (30000, 8, 72, 32, 300),
+         (900, 4096, 136, 72, 2)]
+
+
+@pytest.mark.parametrize("out_t", ["bf16", "f32"])
+@pytest.mark.parametrize("size", LARGE)
+def test_tensor_core_sizes(moe, size, out_t):
+    assert sorts(moe, *size)
+    check(moe, make(*size, seed=sum(size), runs=size[0] % 2 == 0), out_t)
+
+
+FORMS = [(2, 264, 520, 16, 6), (40, 264, 520, 16, 6), (3000, 264, 1032, 64, 6)]
+
+
+@pytest.mark.parametrize("size", FORMS)
+def test_forms(moe, size):
     """Without a base, without scales, one adapter for all, none at all, in place."""
-    d = make(T, 264, 520, 16, 6, T)
+    assert sorts(moe, *size) == (size[0] == 3000)
+    T = size[0]
+    d = make(*size, T)
     for out_t in ("bf16", "f32"):
         check(moe, d, out_t, base=False)
         check(moe, d, out_t, scale=False)
@@ -92,7 +116,7 @@ def test_forms(moe, T):
     assert got is buf and torch.equal(buf, ref)
 
 
-@pytest.mark.parametrize("T", [7, 300])
+@pytest.mark.parametrize("T", [7, 300, 12000])
 def test_runs_and_single_tokens(moe, T):
     """Tokens of a request side by side, a request with one token, adapters that no token names (NaN there is not
     read into any result)."""
@@ -103,7 +127,7 @@ def test_runs_and_single_tokens(moe, T):
     check(moe, d)
 
 
-@pytest.mark.parametrize("T", [5, 400])
+@pytest.mark.parametrize("T", [5, 400, 12000])
 def test_ids_out_of_range(moe, T):
     d = make(T, 136, 264, 16, 4, T)
     ids = d["ids"].clone()
@@ -118,7 +142,7 @@ def test_ids_out_of_range(moe, T):
 
 def test_special_values(moe):
     """A NaN or an infinity in a token's input or base stays in that token's row."""
-    for T in (9, 300):
+    for T in (9, 300, 12000):
         d = make(T, 136, 264, 16, 4, T, none=0.0)
         c = {n: v.cuda() for n, v in d.items()}
         ref = moe.moe_lora(c["x"], c["a"], c["b"], c["ids"], base=c["base"])
@@ -136,9 +160,11 @@ def test_stale_workspace_graph_and_stream(moe):
     """A workspace with anything in it, shared by calls of other sizes; a captured call on new ids; another stream."""
     ws = torch.empty(max(moe.moe_lora_workspace_size(T, 520, 1032, 64, 8) for T in range(1, 601)), dtype=torch.uint8,
                      device="cuda").fill_(255)
-    for T in (600, 3, 200, 64):
+    assert sorts(moe, 600, 520, 1032, 64, 8) and not sorts(moe, 200, 520, 1032, 64, 8)
+    for T in (600, 3, 500, 200, 64, 601):
         check(moe, make(T, 520, 1032, 64, 8, T), ws=ws)
-    for T in (20, 500):
+    assert sorts(moe, 9000, 264, 520, 16, 6)
+    for T in (20, 500, 9000):
         sets = [{n: v.cuda() for n, v in make(T, 264, 520, 16, 6, s).items()} for s in range(3)]
         one = {n: v.clone() for n, v in sets[0].items()}
         call = lambda c, **k: moe.moe_lora(c["x"], c["a"], c["b"], c["ids"], scale=c["scale"], base=c["base"], **k)  # noqa: E731
