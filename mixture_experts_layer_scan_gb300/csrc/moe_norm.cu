@@ -49,7 +49,13 @@ __device__ __forceinline__ float load_one(const void* w, bool f32, size_t i) {
   return f32 ? static_cast<const float*>(w)[i] : bf16_bits_to_f32(static_cast<const uint16_t*>(w)[i]);
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+// bf16 rows take the approximate exponential and quotient (off by some 2^-21, far below a step of theirs): with the
+// rounded ones a full gate of 16384 x 4096 was bound by their instructions.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float z) {
+  if constexpr (sizeof(T) == 2) return __fdividef(1.0f, 1.0f + __expf(-z));
+  return 1.0f / (1.0f + expf(-z));
+}
 
 // Sums of two values over the CTA, in every thread (fixed order).  `s` is not reused before a barrier.
 __device__ __forceinline__ float2 block_sum2(float a, float b, float2* s) {
@@ -85,78 +91,94 @@ struct NormDev {
 };
 
 // The gate of N elements of row t (1 without a gate).
-template <int N>
+template <typename T, int N>
 __device__ __forceinline__ void load_gate(const NormDev& p, int t, int i, float token, float (&g)[N]) {
   if (p.gate_kind == MOE_GATE_CHANNEL || p.gate_kind == MOE_GATE_FULL) {
     load_w<N>(p.gate, p.gate_f32, (p.gate_kind == MOE_GATE_FULL ? (size_t)t * p.H : 0) + i, g);
     if (p.sigmoid) {
 #pragma unroll
-      for (int c = 0; c < N; ++c) g[c] = sigmoid(g[c]);
+      for (int c = 0; c < N; ++c) g[c] = sigmoid<T>(g[c]);
     }
   } else {
 #pragma unroll
     for (int c = 0; c < N; ++c) g[c] = token;
   }
 }
+template <typename T>
 __device__ __forceinline__ float token_gate(const NormDev& p, int t) {
   if (p.gate_kind != MOE_GATE_TOKEN) return 1.0f;
   const float g = load_one(p.gate, p.gate_f32, t);
-  return p.sigmoid ? sigmoid(g) : g;
+  return p.sigmoid ? sigmoid<T>(g) : g;
 }
 
-// A CTA to a row; thread i holds vectors i, i + blockDim, ... (NV of them).
+// Persistent: a CTA takes every gridDim-th row and holds the next one's loads while it is at work on this one.
+// Thread i holds vectors i, i + blockDim, ... (NV of them).  The sums' shared memory alternates from row to row: what a
+// row wrote is overwritten two barriers later.  Measured, 16384 x 4096 bf16 with a token gate (us): a CTA to a row
+// with 8 elements a thread 164, with 16 107.
 template <typename T, int W, int NV, bool POST>
-__global__ void __launch_bounds__(1024) k_norm(const NormDev p) {
+__global__ void __launch_bounds__(512) k_norm(const NormDev p) {
   pdl_enter();
   using V = typename Word<W>::type;
   constexpr int N = W / sizeof(T);
-  __shared__ float2 s1[32], s2[32];
+  __shared__ float2 sums[2][2][32];
   const int vpr = p.H / N;
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+  V xv[NV], yv[POST ? NV : 1];
+  auto fetch = [&](int t) {
     const V* xr = reinterpret_cast<const V*>(static_cast<const T*>(p.x) + (size_t)t * p.H);
-    V xv[NV], yv[POST ? NV : 1];
+    const V* yr = reinterpret_cast<const V*>(static_cast<const T*>(p.y) + (size_t)t * p.H);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      zero_word(xv[i]);
-      if (v < vpr) xv[i] = xr[v];
-      if constexpr (POST) {
-        zero_word(yv[i]);
-        if (v < vpr) yv[i] = reinterpret_cast<const V*>(static_cast<const T*>(p.y) + (size_t)t * p.H)[v];
+      if (v < vpr) {
+        xv[i] = xr[v];
+        if constexpr (POST) yv[i] = yr[v];
       }
     }
-    float o[NV][N];
+  };
 #pragma unroll
-    for (int i = 0; i < NV; ++i) widen<T, W>(xv[i], o[i]);
+  for (int i = 0; i < NV; ++i) {
+    zero_word(xv[i]);
+    if constexpr (POST) zero_word(yv[i]);
+  }
+  if ((int)blockIdx.x < p.T) fetch(blockIdx.x);
+  int par = 0;
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x, par ^= 1) {
+    float o[NV][N], y[POST ? NV : 1][N];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      widen<T, W>(xv[i], o[i]);
+      if constexpr (POST) widen<T, W>(yv[i], y[i]);
+    }
+    if (t + (int)gridDim.x < p.T) fetch(t + gridDim.x);
     if constexpr (POST) {
       float ry = 1.0f;
       if (p.post_w) {
         float a = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          float y[N];
-          widen<T, W>(yv[i], y);
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int c = 0; c < N; ++c) a = fmaf(y[c], y[c], a);
-        }
-        ry = rsqrtf(block_sum2(a, 0.f, s1).x * p.inv_h + p.eps);
+          for (int c = 0; c < N; ++c) a = fmaf(y[i][c], y[i][c], a);
+        ry = rsqrtf(block_sum2(a, 0.f, sums[par][0]).x * p.inv_h + p.eps);
       }
-      const float tok = token_gate(p, t);
+      const float tok = p.scale * token_gate<T>(p, t);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v >= vpr) break;
-        float y[N], g[N];
-        widen<T, W>(yv[i], y);
+        float g[N];
         if (p.post_w) {
           float w[N];
           load_w<N>(p.post_w, p.w_f32, (size_t)v * N, w);
 #pragma unroll
-          for (int c = 0; c < N; ++c) y[c] *= ry * w[c];
+          for (int c = 0; c < N; ++c) y[i][c] *= ry * w[c];
         }
-        load_gate<N>(p, t, v * N, tok, g);
+        if (p.gate_kind == MOE_GATE_CHANNEL || p.gate_kind == MOE_GATE_FULL) {
+          load_gate<T, N>(p, t, v * N, 1.0f, g);
 #pragma unroll
-        for (int c = 0; c < N; ++c) o[i][c] = fmaf(p.res_scale, o[i][c], p.scale * g[c] * y[c]);
+          for (int c = 0; c < N; ++c) y[i][c] *= g[c];
+        }
+#pragma unroll
+        for (int c = 0; c < N; ++c) o[i][c] = fmaf(p.res_scale, o[i][c], tok * y[i][c]);
         reinterpret_cast<V*>(static_cast<T*>(p.out) + (size_t)t * p.H)[v] = narrow<T, W>(o[i]);
       }
     }
@@ -167,7 +189,7 @@ __global__ void __launch_bounds__(1024) k_norm(const NormDev p) {
 #pragma unroll
         for (int c = 0; c < N; ++c) a = fmaf(o[i][c], o[i][c], a);
       }
-      const float r = rsqrtf(block_sum2(a, 0.f, s2).x * p.inv_h + p.eps);
+      const float r = rsqrtf(block_sum2(a, 0.f, sums[par][1]).x * p.inv_h + p.eps);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
@@ -179,7 +201,6 @@ __global__ void __launch_bounds__(1024) k_norm(const NormDev p) {
         reinterpret_cast<V*>(static_cast<T*>(p.h) + (size_t)t * p.H)[v] = narrow<T, W>(o[i]);
       }
     }
-    if (t + (int)gridDim.x < p.T) __syncthreads();  // (the sums' shared memory is free again)
   }
 }
 
@@ -229,7 +250,7 @@ __global__ void __launch_bounds__(NV * (W / (int)sizeof(T)) > 8 ? 1024 : 512) k_
         }
         ry = rsqrtf(block_sum2(a, 0.f, s1).x * p.inv_h + p.eps);
       }
-      tok = token_gate(p, t);
+      tok = token_gate<T>(p, t);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
@@ -241,7 +262,7 @@ __global__ void __launch_bounds__(NV * (W / (int)sizeof(T)) > 8 ? 1024 : 512) k_
 #pragma unroll
         for (int c = 0; c < N; ++c) w[c] = 1.f;
         if (p.post_w) load_w<N>(p.post_w, p.w_f32, (size_t)v * N, w);
-        load_gate<N>(p, t, v * N, tok, g);
+        load_gate<T, N>(p, t, v * N, tok, g);
 #pragma unroll
         for (int c = 0; c < N; ++c) o[i][c] = fmaf(p.res_scale, o[i][c], p.scale * g[c] * (n[i][c] * w[c]));
       }
@@ -310,7 +331,7 @@ __global__ void __launch_bounds__(NV * (W / (int)sizeof(T)) > 8 ? 1024 : 512) k_
         }
         reinterpret_cast<V*>(static_cast<T*>(p.d_x) + at)[v] = narrow<T, W>(dx);
         if (p.post_w) load_w<N>(p.post_w, p.w_f32, (size_t)v * N, w);
-        load_gate<N>(p, t, v * N, tok, g);
+        load_gate<T, N>(p, t, v * N, tok, g);
 #pragma unroll
         for (int c = 0; c < N; ++c) {
           const float z = p.scale * D[i][c];
@@ -397,24 +418,53 @@ __global__ void __launch_bounds__(256) k_sum_rows(const SumDev p) {
   }
 }
 
-// Elements of a thread: 8, or 16 for rows that 512 threads do not hold with 8.
+// Elements of a thread of the gradients: 8, or 16 for rows that 512 threads do not hold with 8.
 int threads_for(int H, int per) { return std::max(32, ((H + per - 1) / per + 31) / 32 * 32); }
 bool wide_row(int H) { return H > 8 * 512; }
 
+// CTAs of a forward kernel that are resident together
 template <typename T, int W, int NV, bool POST>
-cudaError_t launch_one(const NormDev& p, bool grad, int grid, cudaStream_t s) {
-  const dim3 block(threads_for(p.H, NV * (W / (int)sizeof(T))));
-  if (grad) MOE_LAUNCH((k_norm_grad<T, W, NV, POST>), dim3(grid), block, 0, s, p);
-  else MOE_LAUNCH((k_norm<T, W, NV, POST>), dim3(grid), block, 0, s, p);
+int resident(int threads) {
+  static int known[64][17] = {};  // (by device and warps; racing threads write the same)
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int* at = dev >= 0 && dev < 64 && threads <= 512 ? &known[dev][threads / 32] : nullptr;
+  if (at && *at) return *at;
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_norm<T, W, NV, POST>, threads, 0) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = 1;
+  }
+  if (at) *at = n * 152;
+  return n * 152;
+}
+
+template <typename T, int W, int NV, bool POST>
+cudaError_t launch_forward(const NormDev& p, cudaStream_t s) {
+  const int threads = threads_for(p.H, NV * (W / (int)sizeof(T)));
+  const int grid = std::min(p.T, resident<T, W, NV, POST>(threads));
+  MOE_LAUNCH((k_norm<T, W, NV, POST>), dim3(grid), dim3(threads), 0, s, p);
   return cudaGetLastError();
 }
 
+template <typename T, int W, int NV, bool POST>
+cudaError_t launch_gradient(const NormDev& p, int grid, cudaStream_t s) {
+  MOE_LAUNCH((k_norm_grad<T, W, NV, POST>), dim3(grid), dim3(threads_for(p.H, NV * (W / (int)sizeof(T)))), 0, s, p);
+  return cudaGetLastError();
+}
+
+template <typename T, int W, bool POST>
+cudaError_t launch_width(const NormDev& p, bool grad, int grid, cudaStream_t s) {
+  constexpr int N = W / sizeof(T);
+  if (grad) return wide_row(p.H) ? launch_gradient<T, W, 16 / N, POST>(p, grid, s) : launch_gradient<T, W, 8 / N, POST>(p, grid, s);
+  // elements of a thread: 16; few rows 8 (a row is over sooner: one of 4096 1.6 us instead of 1.8); long ones 32
+  if (p.H > 512 * 16) return launch_forward<T, W, 32 / N, POST>(p, s);
+  if (p.T <= 304 && p.H <= 512 * 8) return launch_forward<T, W, 8 / N, POST>(p, s);
+  return launch_forward<T, W, 16 / N, POST>(p, s);
+}
 template <typename T, int W>
 cudaError_t launch_width(const NormDev& p, bool post, bool grad, int grid, cudaStream_t s) {
-  constexpr int N = W / sizeof(T);
-  if (wide_row(p.H))
-    return post ? launch_one<T, W, 16 / N, true>(p, grad, grid, s) : launch_one<T, W, 16 / N, false>(p, grad, grid, s);
-  return post ? launch_one<T, W, 8 / N, true>(p, grad, grid, s) : launch_one<T, W, 8 / N, false>(p, grad, grid, s);
+  return post ? launch_width<T, W, true>(p, grad, grid, s) : launch_width<T, W, false>(p, grad, grid, s);
 }
 
 cudaError_t launch_typed(const NormDev& p, bool bf16, bool post, bool grad, int grid, cudaStream_t s) {
@@ -459,7 +509,7 @@ int norm_grad_rows(int T, int H) { return std::min(T, 152 * std::max(1, 512 / th
 
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
   const NormDev p = make_dev(a);
-  return launch_typed(p, a.bf16, a.y != nullptr, false, std::min(a.T, 1 << 20), s);
+  return launch_typed(p, a.bf16, a.y != nullptr, false, 0, s);
 }
 
 cudaError_t launch_norm_grad(const NormArgs& a, cudaStream_t s) {
