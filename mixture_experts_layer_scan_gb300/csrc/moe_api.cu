@@ -1165,6 +1165,8 @@ int moe_prenorm(const void* x, const void* w, int T, int H, float eps, moe_dtype
   a.rule.eps = eps;
   a.rule.w_dtype = w_dtype;
   a.h = h;
+  a.status = status_word();
+  if (!a.status) return MOE_ERR_CUDA;
   return cuda_rc(launch_norm(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1195,6 +1197,8 @@ int moe_prenorm_backward(const void* d_h, const void* x, const void* w, int T, i
   a.d_x = d_x;
   a.d_next_w = d_w;
   a.workspace = workspace;
+  a.status = status_word();
+  if (!a.status) return MOE_ERR_CUDA;
   return cuda_rc(launch_norm_grad(a, s));
 }
 
@@ -1218,6 +1222,8 @@ int moe_postnorm(const void* x, const void* y, const void* post_w, const void* g
   a.rule = *rule;
   a.out = out;
   a.h = h;
+  a.status = status_word();
+  if (!a.status) return MOE_ERR_CUDA;
   return cuda_rc(launch_norm(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1265,6 +1271,8 @@ int moe_postnorm_backward(const void* d_out, const void* d_h, const void* x, con
   a.d_post_w = d_post_w;
   a.d_next_w = d_next_w;
   a.workspace = workspace;
+  a.status = status_word();
+  if (!a.status) return MOE_ERR_CUDA;
   return cuda_rc(launch_norm_grad(a, s));
 }
 

@@ -272,6 +272,7 @@ struct NormArgs {
   void *d_x, *d_y, *d_gate;
   float *d_post_w, *d_next_w;
   void* workspace;                    // 3 * norm_grad_rows(T, H) * H floats
+  int* status;
 };
 int norm_grad_rows(int T, int H);
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);

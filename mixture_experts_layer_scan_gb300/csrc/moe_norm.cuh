@@ -1,0 +1,396 @@
+// Norms before and after a block, with the block's gate and residual scale, and their gradients.
+//
+//   prenorm    h = x r w,  r = (mean x^2 + eps)^-1/2
+//   postnorm   n = y r_y,  v = n post_w (v = y without a norm),  out = res_scale x + scale G v,
+//              h = out r_o next_w (the next block's prenorm, from the unrounded out)
+//   gradients  of a norm n = x r with d_n = g:  d_x = r (g - n mean(g n))
+//              D = d_out + that of h at out;  d_x = res_scale D,  d_v = scale G D,  d_G = scale D v,
+//              d_post_w = sum_t d_v n,  d_next_w = sum_t d_h out r_o,  d_y from d_v post_w
+//
+// Everything is fp32 between the loads and the one rounding of each result.  The gradients recompute the
+// forward pass from x and y: statistics kept by the forward pass would save no bytes, and a rounded out
+// would not be the one that the norm saw.
+//
+// Bound by HBM.  The CTAs are persistent and take every gridDim-th row; a ring of rows in shared memory is filled by
+// bulk copies several rows ahead, so that the sums over a row (two in the forward pass, three in the gradients, each
+// a barrier) wait for no load.  The rows are read from there again after each sum.  The weights' gradients are
+// sums over rows: a CTA keeps those of its rows in registers, writes one fp32 row of partial sums, and a second
+// kernel adds the CTAs' rows in their order.
+// Beside the bytes, instructions bound it: with the weights loaded and widened in every row and the calls' forms
+// told apart there, 16384 x 4096 took 35 of them for an element.  So a thread keeps its columns' weights in
+// registers (the norm's after the block times a gate by channels as one factor), works on pairs (f32x2), and
+// the gradients of that norm's weight and of such a gate are one sum times the other factor.
+// Rows that are no whole 16 bytes are copied with the neighbours' bytes around them (the last one without what
+// would lie behind the tensor).  Where two rows do not fit, they are read from memory each time.
+#pragma once
+#include <algorithm>
+
+#include "moe_device.cuh"
+#include "moe_internal.h"
+#include "moe_vec.cuh"
+
+namespace moe {
+
+// N consecutive values of a weight (or gate) vector of fp32 or bf16
+template <int N>
+__device__ __forceinline__ void load_w(const void* w, bool f32, size_t i, float (&f)[N]) {
+  constexpr int WB = N * 2;  // bytes of N bf16
+  if (f32) {
+    constexpr int WF = N * 4 >= 16 ? 16 : N * 4;
+    using V = typename Word<WF>::type;
+    constexpr int per = WF / 4;
+#pragma unroll
+    for (int q = 0; q < N / per; ++q) {
+      float g[per];
+      widen<float, WF>(reinterpret_cast<const V*>(static_cast<const float*>(w) + i)[q], g);
+#pragma unroll
+      for (int c = 0; c < per; ++c) f[q * per + c] = g[c];
+    }
+  } else {
+    using V = typename Word<WB>::type;
+    widen<__nv_bfloat16, WB>(*reinterpret_cast<const V*>(static_cast<const uint16_t*>(w) + i), f);
+  }
+}
+
+__device__ __forceinline__ float load_one(const void* w, bool f32, size_t i) {
+  return f32 ? static_cast<const float*>(w)[i] : bf16_bits_to_f32(static_cast<const uint16_t*>(w)[i]);
+}
+
+// bf16 rows take the approximate exponential and quotient (off by some 2^-21, far below a step of theirs): with the
+// rounded ones a full gate of 16384 x 4096 was bound by their instructions.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float z) {
+  if constexpr (sizeof(T) == 2) return __fdividef(1.0f, 1.0f + __expf(-z));
+  return 1.0f / (1.0f + expf(-z));
+}
+
+// Sums over the CTA, in every thread, in a fixed order: a butterfly in each warp, then the warps' sums in turn.
+// s: a value for each warp, in whole float4s and zero behind the last warp.
+constexpr int kMaxWarps = 32;
+__device__ __forceinline__ float block_sum(float2 p, float* s) {
+  float a = p.x + p.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return a;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = a;
+  __syncthreads();
+  a = 0.f;
+  for (int i = 0; i < warps; i += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(s + i);
+    a += (v.x + v.y) + (v.z + v.w);
+  }
+  return a;
+}
+__device__ __forceinline__ float2 block_sum2(float2 p, float2 q, float* s) {  // (2 floats a warp)
+  float2 a = make_float2(p.x + p.y, q.x + q.y);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+    a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+  }
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return a;
+  if ((threadIdx.x & 31) == 0) reinterpret_cast<float2*>(s)[threadIdx.x >> 5] = a;
+  __syncthreads();
+  a = make_float2(0.f, 0.f);
+  for (int i = 0; i < warps; i += 2) {
+    const float4 v = *reinterpret_cast<const float4*>(s + 2 * i);
+    a.x += v.x + v.z;
+    a.y += v.y + v.w;
+  }
+  return a;
+}
+
+enum { S_X = 0, S_Y, S_DOUT, S_DH, S_GATE, S_MAX };
+
+struct NormDev {
+  const void* stream[S_MAX];  // [T][H], of the activations' type but for the gate (null: none)
+  const void *post_w, *gate, *next_w;
+  void *out, *h;
+  void *d_x, *d_y, *d_gate;
+  float* part;       // partial sums: [3][gridDim.x][H] of d_post_w, d_next_w, d_gate
+  int T, H;
+  float inv_h, eps, scale, res_scale;
+  int gate_kind;     // MOE_GATE_*
+  bool sigmoid, w_f32, gate_f32;
+  bool sum_post, sum_next, sum_gate;
+  bool gate_ring;    // a full gate of the activations' type: comes through the ring too
+  int stages;        // rows of the ring
+  uint32_t pitch;    // bytes of a stream's row in it
+  int streams;
+  int* status;
+};
+
+// The rows of a CTA, in turn, NV vectors of W bytes to a thread (vectors i, i + blockDim, ...): from a ring in shared
+// memory (RING) or from memory.  A thread's E elements are E / 2 pairs; those behind the row's end are 0.
+template <typename T, int W, int NV, bool RING>
+struct Rows {
+  using V = typename Word<W>::type;
+  static constexpr int N = W / sizeof(T), E = NV * N;
+  static_assert(E % 2 == 0, "pairs");
+  const NormDev& p;
+  uint32_t buf, bars;
+  volatile int* abort;
+  int vpr, k, stage;             // vectors of a row; rows so far; the present one's place
+  uint32_t phase, shift, whole;  // shift: of the row in its copy; whole: bytes of the copy
+  size_t at;                     // element offset of the present row
+  bool ok, refilled, tail;       // tail: the copy leaves out the row's end
+  float token;                   // the next row's gate
+  int place[S_MAX];              // of a stream among those of a stage
+
+  __device__ __forceinline__ Rows(const NormDev& q, uint8_t* smem)
+      : p(q), vpr(q.H / N), k(0), stage(0), phase(0), shift(0), whole(0), at(0), ok(true), refilled(false),
+        tail(false), token(1.0f) {
+    if constexpr (RING) {
+      abort = reinterpret_cast<volatile int*>(smem);
+      bars = smem_u32(smem) + 16;
+      buf = smem_u32(smem) + 128;
+      int n = 0;
+#pragma unroll
+      for (int s = 0; s < S_MAX; ++s) place[s] = p.stream[s] && (s != S_GATE || p.gate_ring) ? n++ : 0;
+      if (threadIdx.x == 0) {
+        *abort = 0;
+        for (int i = 0; i < p.stages; ++i) mbar_init(bars + 8 * i, 1);
+        fence_barrier_init();
+      }
+    }
+  }
+  __device__ __forceinline__ int vec(int i) const { return threadIdx.x + i * blockDim.x; }
+  __device__ __forceinline__ bool has(int i) const { return vec(i) < vpr; }
+  // The 16-byte units around row t: first byte and their number of bytes.
+  __device__ __forceinline__ void extent(int t, size_t& from, uint32_t& n) const {
+    const size_t row = (size_t)p.H * sizeof(T), begin = (size_t)t * row, end = begin + row;
+    from = begin & ~(size_t)15;
+    const size_t up = (end + 15) & ~(size_t)15;
+    // (nothing behind the tensor is read: a row whose end the copy leaves out comes from memory)
+    const size_t till = W == 16 || up <= (size_t)p.T * row ? up : end & ~(size_t)15;
+    n = till > from ? (uint32_t)(till - from) : 0;
+  }
+  __device__ __forceinline__ void issue(int t, int s) {  // (one thread)
+    size_t from;
+    uint32_t n;
+    extent(t, from, n);
+    const uint32_t bar = bars + 8 * s;
+    mbar_arrive_expect_tx(bar, n * p.streams);
+    if (!n) return;
+#pragma unroll
+    for (int i = 0; i < S_MAX; ++i)
+      if (p.stream[i] && (i != S_GATE || p.gate_ring))
+        bulk_g2s(buf + (uint32_t)(s * p.streams + place[i]) * p.pitch, static_cast<const uint8_t*>(p.stream[i]) + from, n, bar);
+  }
+  __device__ __forceinline__ void start() {  // behind a barrier after the constructor
+    if (RING && threadIdx.x == 0)
+      for (int s = 0; s < p.stages; ++s) {
+        const long t = blockIdx.x + (long)s * gridDim.x;
+        if (t < p.T) issue((int)t, s);
+      }
+  }
+  __device__ __forceinline__ void open(int t) {
+    at = (size_t)t * p.H;
+    if constexpr (RING) {
+      refilled = false;
+      if (ok) ok = mbar_wait_one(bars + 8 * stage, phase, abort, p.status);
+      if (W < 16) {
+        size_t from;
+        extent(t, from, whole);
+        shift = (uint32_t)(at * sizeof(T) - from);
+        tail = shift + (uint32_t)p.H * sizeof(T) > whole;
+      }
+    }
+  }
+  // Called behind a barrier in every row: the row before has been read by all.
+  __device__ __forceinline__ void refill(int t) {
+    if constexpr (RING) {
+      if (refilled) return;
+      refilled = true;
+      if (threadIdx.x == 0 && k > 0) {
+        const long next = t + (long)(p.stages - 1) * gridDim.x;
+        if (next < p.T) issue((int)next, stage == 0 ? p.stages - 1 : stage - 1);
+      }
+    }
+  }
+  __device__ __forceinline__ void close(int t) {
+    if constexpr (RING) {
+      if (!refilled) {  // (a row without a sum)
+        __syncthreads();
+        refill(t);
+      }
+      ++k;
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    } else {
+      ++k;
+    }
+  }
+  __device__ __forceinline__ void drain() {  // a wait gave up: let the copies in flight land before the CTA ends
+    if (RING && !ok && threadIdx.x == 0)
+      for (int i = 0; i < p.stages; ++i) {
+        mbar_wait_drain(bars + 8 * i, 0, 50000000ull);
+        mbar_wait_drain(bars + 8 * i, 1, 50000000ull);
+      }
+  }
+  __device__ __forceinline__ V from_memory(int s, int i) const {
+    return reinterpret_cast<const V*>(static_cast<const T*>(p.stream[s]) + at)[vec(i)];
+  }
+  __device__ __forceinline__ V from_ring(int s, int i) const {
+    const uint32_t from = buf + (uint32_t)(stage * p.streams + place[s]) * p.pitch + (W < 16 ? shift : 0u) + (uint32_t)vec(i) * W;
+    V v;
+    if constexpr (W == 16) v = lds_v4(from);
+    else if constexpr (W == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(from) : "memory");
+    else asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(from) : "memory");
+    return v;
+  }
+  __device__ __forceinline__ static void put(float2 (&f)[E / 2], int e, float v) {  // (e known at compile time)
+    if (e & 1) f[e / 2].y = v;
+    else f[e / 2].x = v;
+  }
+  __device__ __forceinline__ static float pick(const float2 (&f)[E / 2], int e) { return e & 1 ? f[e / 2].y : f[e / 2].x; }
+  __device__ __forceinline__ void load(int s, float2 (&f)[E / 2]) const {
+    V v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) zero_word(v[i]);
+    if (RING && (W == 16 || !tail)) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (has(i)) v[i] = from_ring(s, i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (has(i)) v[i] = from_memory(s, i);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float g[N];
+      widen<T, W>(v[i], g);
+#pragma unroll
+      for (int c = 0; c < N; ++c) put(f, i * N + c, g[c]);
+    }
+  }
+  __device__ __forceinline__ void store(void* base, const float2 (&f)[E / 2]) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!has(i)) break;
+      float g[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) g[c] = pick(f, i * N + c);
+      reinterpret_cast<V*>(static_cast<T*>(base) + at)[vec(i)] = narrow<T, W>(g);
+    }
+  }
+  // A weight (or gate) of the thread's columns, from element `from` on.
+  __device__ __forceinline__ void weight(const void* w, bool f32, size_t from, float2 (&f)[E / 2]) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float g[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) g[c] = 0.f;
+      if (has(i)) load_w<N>(w, f32, from + (size_t)vec(i) * N, g);
+#pragma unroll
+      for (int c = 0; c < N; ++c) put(f, i * N + c, g[c]);
+    }
+  }
+  // The factor of the columns after the block: post_w times a gate by channels (1 where there is neither).
+  __device__ __forceinline__ void channel_gate(float2 (&g)[E / 2]) const {
+    weight(p.gate, p.gate_f32, 0, g);
+    if (p.sigmoid)
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) g[e] = make_float2(sigmoid<T>(g[e].x), sigmoid<T>(g[e].y));
+  }
+  __device__ __forceinline__ void factor(float2 (&f)[E / 2]) const {
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) f[e] = both(1.f);
+    if (p.post_w) weight(p.post_w, p.w_f32, 0, f);
+    if (p.gate_kind == MOE_GATE_CHANNEL) {
+      float2 g[E / 2];
+      channel_gate(g);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) f[e] = mul2(f[e], g[e]);
+    }
+  }
+  __device__ __forceinline__ void full_gate(float2 (&g)[E / 2]) const {
+    if (p.gate_ring) load(S_GATE, g);
+    else weight(p.stream[S_GATE], p.gate_f32, at, g);
+    if (p.sigmoid)
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) g[e] = make_float2(sigmoid<T>(g[e].x), sigmoid<T>(g[e].y));
+  }
+  // A token's gate, loaded a row ahead.
+  __device__ __forceinline__ void fetch_token(long t) {
+    if (p.gate_kind == MOE_GATE_TOKEN && t < p.T) token = load_one(p.gate, p.gate_f32, t);
+  }
+  __device__ __forceinline__ float token_gate(int t) {
+    if (p.gate_kind != MOE_GATE_TOKEN) return 1.0f;
+    const float g = token;
+    fetch_token((long)t + gridDim.x);
+    return p.sigmoid ? sigmoid<T>(g) : g;
+  }
+};
+
+// What a kernel does: the prenorm, the postnorm, the postnorm with a gate of [T][H].
+enum { N_PRE = 0, N_POST, N_FULL };
+
+// Elements of a thread: 16; for few forward rows 8 (a row is over sooner: one of 4096 1.6 us instead of 1.8).
+constexpr int kElems = 16;
+inline int norm_threads(int H, int per) { return std::max(32, ((H + per - 1) / per + 31) / 32 * 32); }
+// CTAs of an SM that `regs` registers a thread leave room for
+inline int norm_ctas(int threads, int regs) { return std::max(1, std::min(16, 65536 / ((regs + 7) / 8 * 8 * threads))); }
+
+constexpr int kMaxStages = 8;
+constexpr size_t kSmemSm = 226 * 1024;
+
+// Rows of the ring of one of `ctas` CTAs, and its bytes
+inline int ring_stages(size_t row, int ctas, size_t* bytes) {
+  const size_t room = kSmemSm / ctas - 3 * 1024;  // (static shared memory and what the system takes)
+  const int n = (int)std::min<size_t>(kMaxStages, (room - 128) / row);
+  *bytes = n < 2 ? 0 : 128 + n * row;
+  return n < 2 ? 0 : n;
+}
+
+// Sizes of a launch: ring, CTAs and threads.
+struct NormShape {
+  int threads, grid;
+  size_t smem;
+};
+template <typename T, int W>
+NormShape norm_shape(NormDev& p, int regs, int per, int most, bool ring) {
+  NormShape q;
+  q.threads = norm_threads(p.H, per);
+  int ctas = norm_ctas(q.threads, regs);
+  q.smem = 0;
+  p.gate_ring = p.gate_ring && ring;
+  p.streams = 0;
+  for (int i = 0; i < S_MAX; ++i) p.streams += p.stream[i] && (i != S_GATE || p.gate_ring);
+  const size_t row = (size_t)p.H * sizeof(T);
+  p.pitch = (uint32_t)(W == 16 ? row : (row + 30) / 16 * 16);
+  p.stages = 0;
+  // (few CTAs with a ring rather than many without; rows that come about one to a CTA need none)
+  if (ring && p.T > 152 * ctas)
+    for (int c = ctas;; c /= 2) {
+      p.stages = ring_stages((size_t)p.pitch * p.streams, c, &q.smem);
+      if (p.stages) ctas = c;
+      if (p.stages || c == 1) break;
+    }
+  q.grid = std::min(std::min(p.T, most), 152 * ctas);
+  return q;
+}
+// Registers of a kernel, and its shared memory raised, once for each device.
+template <typename K>
+int norm_regs(K kernel, int (&known)[64]) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && known[dev]) return known[dev];
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemSm - 3 * 1024) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev >= 0 && dev < 64) known[dev] = a.numRegs;
+  return a.numRegs;
+}
+
+NormDev norm_dev(const NormArgs& a);
+
+}  // namespace moe

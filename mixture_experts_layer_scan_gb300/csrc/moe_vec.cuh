@@ -57,6 +57,52 @@ __device__ __forceinline__ typename Word<W>::type narrow(const float (&f)[W / si
   return v;
 }
 
+// Pairs of fp32 in one packed instruction, each half one rounding.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t x, y, z;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(z) : "l"(x), "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(c.x), "=f"(c.y) : "l"(z));
+  return c;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t x, y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(x));
+  return a;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t x, y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(x));
+  return a;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// A vector of W bytes as pairs of fp32 (a single element: the pair's second is 0).
+template <typename T, int W>
+__device__ __forceinline__ void widen2(const typename Word<W>::type& v, float2 (&f)[(W / sizeof(T) + 1) / 2]) {
+  constexpr int N = W / sizeof(T);
+  float g[N];
+  widen<T, W>(v, g);
+#pragma unroll
+  for (int i = 0; i < (N + 1) / 2; ++i) f[i] = make_float2(g[2 * i], 2 * i + 1 < N ? g[2 * i + 1 < N ? 2 * i + 1 : 0] : 0.0f);
+}
+template <typename T, int W>
+__device__ __forceinline__ typename Word<W>::type narrow2(const float2 (&f)[(W / sizeof(T) + 1) / 2]) {
+  constexpr int N = W / sizeof(T);
+  float g[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) g[i] = i % 2 ? f[i / 2].y : f[i / 2].x;
+  return narrow<T, W>(g);
+}
+
 // widest vector (bytes) that divides a row
 inline int row_word(long row_bytes) {
   return row_bytes % 16 == 0 ? 16 : row_bytes % 8 == 0 ? 8 : row_bytes % 4 == 0 ? 4 : 2;
