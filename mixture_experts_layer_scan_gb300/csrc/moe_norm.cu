@@ -5,69 +5,92 @@ namespace moe {
 
 namespace {
 
-// The sums' shared memory alternates from row to row: what a row wrote is overwritten two barriers later.
+// The sums' shared memory alternates from row to row: what a row wrote is overwritten behind the next row's barrier.
 template <typename T, int W, int NV, int KIND, bool RING, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ NormDev p) {
   pdl_enter();
   using R = Rows<T, W, NV, RING>;
-  constexpr int E2 = R::E / 2;
+  constexpr int C2 = R::C2, CH = R::CHUNKS;
   constexpr bool POST = KIND != N_PRE, HOLD = THREADS <= 512;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ __align__(16) float sums[2][2][kMaxWarps];
-  for (int i = threadIdx.x; i < 4 * kMaxWarps; i += blockDim.x) (&sums[0][0][0])[i] = 0.f;
+  __shared__ float sums[2][2][THREADS / 4];
   R rows(p, smem);
   __syncthreads();
   rows.start();
   if constexpr (POST) rows.fetch_token(blockIdx.x);
-  float2 cw[POST ? E2 : 1], nw[E2];
+  float2 cw[HOLD && POST ? CH : 1][C2], nw[HOLD ? CH : 1][C2];
   if constexpr (HOLD) {
-    if constexpr (POST) rows.factor(cw);
-    if (p.next_w) rows.weight(p.next_w, p.w_f32, 0, nw);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if constexpr (POST) rows.factor(c, cw[c]);
+      if (p.next_w) rows.weight(p.next_w, p.w_f32, 0, c, nw[c]);
+    }
   }
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
     rows.open(t);
-    float (&s2)[2][kMaxWarps] = sums[rows.k & 1];
-    float2 o[E2];
-    rows.load(S_X, o);
+    float (&s2)[2][THREADS / 4] = sums[rows.k & 1];
+    float2 o[CH][C2], y[POST ? CH : 1][C2];
+    float2 a0 = both(0.f), a1 = a0, a2 = a0, a3 = a0;  // x^2, y^2, x c, c^2
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      rows.load(S_X, c, o[c]);
+      if constexpr (POST) {
+        if constexpr (!HOLD) rows.factor(c, cw[0]);
+        float2 g[C2];
+        rows.load(S_Y, c, y[c]);
+        if constexpr (KIND == N_FULL) rows.full_gate(c, g);
+#pragma unroll
+        for (int e = 0; e < C2; ++e) {
+          a1 = fma2(y[c][e], y[c][e], a1);
+          y[c][e] = mul2(y[c][e], cw[HOLD ? c : 0][e]);
+          if constexpr (KIND == N_FULL) y[c][e] = mul2(y[c][e], g[e]);
+          a2 = fma2(o[c][e], y[c][e], a2);
+          a3 = fma2(y[c][e], y[c][e], a3);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < C2; ++e) a0 = fma2(o[c][e], o[c][e], a0);
+    }
+    float r = 0.f, b = 0.f;
     if constexpr (POST) {
-      // out = res_scale x + (scale r_y G) (y post_w gate): what does not need r_y comes before its sum is there
-      float2 y[E2], a = both(0.f);
-      rows.load(S_Y, y);
-      if constexpr (!HOLD) rows.factor(cw);
+      float v[4] = {flat(a0), flat(a1), flat(a2), flat(a3)};
+      block_sums(v, s2[0]);
+      rows.refill(t);
+      b = p.scale * rows.token_gate(t);
+      if (p.post_w) b *= rsqrtf(v[1] * p.inv_h + p.eps);
+      const float pp = p.res_scale * p.res_scale * v[0], qq = b * b * v[3], ee = pp + qq + 2.f * p.res_scale * b * v[2];
+      r = ee;
 #pragma unroll
-      for (int e = 0; e < E2; ++e) {
-        a = fma2(y[e], y[e], a);
-        y[e] = mul2(y[e], cw[e]);
-        o[e] = mul2(o[e], both(p.res_scale));
-      }
-      if constexpr (KIND == N_FULL) {
-        float2 g[E2];
-        rows.full_gate(g);
+      for (int c = 0; c < CH; ++c) {
 #pragma unroll
-        for (int e = 0; e < E2; ++e) y[e] = mul2(y[e], g[e]);
+        for (int e = 0; e < C2; ++e) o[c][e] = fma2(both(b), y[c][e], mul2(both(p.res_scale), o[c][e]));
+        rows.store(p.out, c, o[c]);
       }
-      float s = p.scale * rows.token_gate(t);
-      if (p.post_w) {
-        s *= rsqrtf(block_sum(a, s2[0]) * p.inv_h + p.eps);
-        rows.refill(t);
-      }
+      if (p.next_w && parts_cancel(pp, qq, ee)) {
+        a0 = both(0.f);
 #pragma unroll
-      for (int e = 0; e < E2; ++e) o[e] = fma2(both(s), y[e], o[e]);
-      rows.store(p.out, o);
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int e = 0; e < C2; ++e) a0 = fma2(o[c][e], o[c][e], a0);
+        float u[1] = {flat(a0)};
+        block_sums(u, s2[1]);
+        r = u[0];
+      }
+    } else {
+      float v[1] = {flat(a0)};
+      block_sums(v, s2[0]);
+      rows.refill(t);
+      r = v[0];
     }
     if (!POST || p.next_w) {
-      float2 a = both(0.f);
-      if constexpr (!HOLD) rows.weight(p.next_w, p.w_f32, 0, nw);
+      r = rsqrtf(r * p.inv_h + p.eps);
 #pragma unroll
-      for (int e = 0; e < E2; ++e) {
-        a = fma2(o[e], o[e], a);
-        o[e] = mul2(o[e], nw[e]);
+      for (int c = 0; c < CH; ++c) {
+        if constexpr (!HOLD) rows.weight(p.next_w, p.w_f32, 0, c, nw[0]);
+#pragma unroll
+        for (int e = 0; e < C2; ++e) o[c][e] = mul2(mul2(o[c][e], both(r)), nw[HOLD ? c : 0][e]);
+        rows.store(p.h, c, o[c]);
       }
-      const float2 r = both(rsqrtf(block_sum(a, s2[1]) * p.inv_h + p.eps));
-      rows.refill(t);
-#pragma unroll
-      for (int e = 0; e < E2; ++e) o[e] = mul2(o[e], r);
-      rows.store(p.h, o);
     }
     rows.close(t);
   }

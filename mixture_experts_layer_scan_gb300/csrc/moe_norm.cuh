@@ -12,8 +12,13 @@
 // would not be the one that the norm saw.
 //
 // Bound by HBM.  The CTAs are persistent and take every gridDim-th row; a ring of rows in shared memory is filled by
-// bulk copies several rows ahead, so that the sums over a row (two in the forward pass, three in the gradients, each
-// a barrier) wait for no load.  The rows are read from there again after each sum.  The weights' gradients are
+// bulk copies several rows ahead, so that the sums over a row wait for no load.  A row is looked at twice, with one
+// barrier between: every sum that it needs follows from sums of products of its inputs.  With c = y post_w gate,
+// e = d_h next_w, b = scale r_y (times a token's gate):
+//   sum out^2 = res^2 sum x^2 + 2 res b sum x c + b^2 sum c^2,   sum out e = res sum x e + b sum c e,
+//   sum g n (for d_y) = scale r_y (sum d_out c + r_o sum e c - r_o^2 m sum out c),  m = mean(e out r_o)
+// (A row whose residual and branch cancel, so that the first of these lost digits, is summed again from out.)
+// The weights' gradients are
 // sums over rows: a CTA keeps those of its rows in registers, writes one fp32 row of partial sums, and a second
 // kernel adds the CTAs' rows in their order.
 // Beside the bytes, instructions bound it: with the weights loaded and widened in every row and the calls' forms
@@ -64,43 +69,34 @@ __device__ __forceinline__ float sigmoid(float z) {
   return 1.0f / (1.0f + expf(-z));
 }
 
-// Sums over the CTA, in every thread, in a fixed order: a butterfly in each warp, then the warps' sums in turn.
-// s: a value for each warp, in whole float4s and zero behind the last warp.
-constexpr int kMaxWarps = 32;
-__device__ __forceinline__ float block_sum(float2 p, float* s) {
-  float a = p.x + p.y;
+// The sums of K <= 8 values over the CTA, in every thread, in a fixed order.  s: 8 floats a warp.
+template <int K>
+__device__ __forceinline__ void block_sums(float (&v)[K], float* s) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return a;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = a;
-  __syncthreads();
-  a = 0.f;
-  for (int i = 0; i < warps; i += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(s + i);
-    a += (v.x + v.y) + (v.z + v.w);
-  }
-  return a;
-}
-__device__ __forceinline__ float2 block_sum2(float2 p, float2 q, float* s) {  // (2 floats a warp)
-  float2 a = make_float2(p.x + p.y, q.x + q.y);
+  for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
-    a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (warps == 1) return;
+  if (lane == 0) {
+    float* at = s + (threadIdx.x >> 5) * 8;
+#pragma unroll
+    for (int k = 0; k < K; ++k) at[k] = v[k];
   }
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return a;
-  if ((threadIdx.x & 31) == 0) reinterpret_cast<float2*>(s)[threadIdx.x >> 5] = a;
   __syncthreads();
-  a = make_float2(0.f, 0.f);
-  for (int i = 0; i < warps; i += 2) {
-    const float4 v = *reinterpret_cast<const float4*>(s + 2 * i);
-    a.x += v.x + v.z;
-    a.y += v.y + v.w;
-  }
-  return a;
+  // lane l: value l % 8 of every fourth warp
+  float a = 0.f;
+  for (int w = lane >> 3; w < warps; w += 4) a += s[w * 8 + (lane & 7)];
+  a += __shfl_xor_sync(0xffffffffu, a, 8);
+  a += __shfl_xor_sync(0xffffffffu, a, 16);
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, a, k);
 }
+__device__ __forceinline__ float flat(float2 a) { return a.x + a.y; }
+
+// 1 / rms of a row whose sum of squares is known in parts, and whether that sum is trusted: E = p + q + 2 c with p, q >= 0;
+// each part is off by some 2^-22 of p + q, which an E of an eighth of it turns into 2^-19 at most.
+__device__ __forceinline__ bool parts_cancel(float p, float q, float e) { return !(e >= 0.125f * (p + q)); }
 
 enum { S_X = 0, S_Y, S_DOUT, S_DH, S_GATE, S_MAX };
 
@@ -128,7 +124,8 @@ template <typename T, int W, int NV, bool RING>
 struct Rows {
   using V = typename Word<W>::type;
   static constexpr int N = W / sizeof(T), E = NV * N;
-  static_assert(E % 2 == 0, "pairs");
+  static constexpr int CV = N == 1 ? 8 : 1, CE = CV * N, C2 = CE / 2, CHUNKS = NV / CV;  // vectors, elements, pairs
+  static_assert(CE % 2 == 0 && NV % CV == 0, "whole chunks of pairs");
   const NormDev& p;
   uint32_t buf, bars;
   volatile int* abort;
@@ -243,78 +240,79 @@ struct Rows {
     else asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(from) : "memory");
     return v;
   }
-  __device__ __forceinline__ static void put(float2 (&f)[E / 2], int e, float v) {  // (e known at compile time)
+  __device__ __forceinline__ static void put(float2 (&f)[C2], int e, float v) {  // (e known at compile time)
     if (e & 1) f[e / 2].y = v;
     else f[e / 2].x = v;
   }
-  __device__ __forceinline__ static float pick(const float2 (&f)[E / 2], int e) { return e & 1 ? f[e / 2].y : f[e / 2].x; }
-  __device__ __forceinline__ void load(int s, float2 (&f)[E / 2]) const {
-    V v[NV];
+  __device__ __forceinline__ static float pick(const float2 (&f)[C2], int e) { return e & 1 ? f[e / 2].y : f[e / 2].x; }
+  __device__ __forceinline__ void load(int s, int chunk, float2 (&f)[C2]) const {
+    V v[CV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) zero_word(v[i]);
+    for (int i = 0; i < CV; ++i) zero_word(v[i]);
     if (RING && (W == 16 || !tail)) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (has(i)) v[i] = from_ring(s, i);
+      for (int i = 0; i < CV; ++i)
+        if (has(chunk * CV + i)) v[i] = from_ring(s, chunk * CV + i);
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (has(i)) v[i] = from_memory(s, i);
+      for (int i = 0; i < CV; ++i)
+        if (has(chunk * CV + i)) v[i] = from_memory(s, chunk * CV + i);
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < CV; ++i) {
       float g[N];
       widen<T, W>(v[i], g);
 #pragma unroll
       for (int c = 0; c < N; ++c) put(f, i * N + c, g[c]);
     }
   }
-  __device__ __forceinline__ void store(void* base, const float2 (&f)[E / 2]) const {
+  __device__ __forceinline__ void store(void* base, int chunk, const float2 (&f)[C2]) const {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!has(i)) break;
+    for (int i = 0; i < CV; ++i) {
+      if (!has(chunk * CV + i)) break;
       float g[N];
 #pragma unroll
       for (int c = 0; c < N; ++c) g[c] = pick(f, i * N + c);
-      reinterpret_cast<V*>(static_cast<T*>(base) + at)[vec(i)] = narrow<T, W>(g);
+      reinterpret_cast<V*>(static_cast<T*>(base) + at)[vec(chunk * CV + i)] = narrow<T, W>(g);
     }
   }
   // A weight (or gate) of the thread's columns, from element `from` on.
-  __device__ __forceinline__ void weight(const void* w, bool f32, size_t from, float2 (&f)[E / 2]) const {
+  __device__ __forceinline__ void weight(const void* w, bool f32, size_t from, int chunk, float2 (&f)[C2]) const {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < CV; ++i) {
       float g[N];
 #pragma unroll
       for (int c = 0; c < N; ++c) g[c] = 0.f;
-      if (has(i)) load_w<N>(w, f32, from + (size_t)vec(i) * N, g);
+      if (has(chunk * CV + i)) load_w<N>(w, f32, from + (size_t)vec(chunk * CV + i) * N, g);
 #pragma unroll
       for (int c = 0; c < N; ++c) put(f, i * N + c, g[c]);
     }
   }
-  // The factor of the columns after the block: post_w times a gate by channels (1 where there is neither).
-  __device__ __forceinline__ void channel_gate(float2 (&g)[E / 2]) const {
-    weight(p.gate, p.gate_f32, 0, g);
+  __device__ __forceinline__ void squash(float2 (&g)[C2]) const {
     if (p.sigmoid)
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) g[e] = make_float2(sigmoid<T>(g[e].x), sigmoid<T>(g[e].y));
+      for (int e = 0; e < C2; ++e) g[e] = make_float2(sigmoid<T>(g[e].x), sigmoid<T>(g[e].y));
   }
-  __device__ __forceinline__ void factor(float2 (&f)[E / 2]) const {
+  __device__ __forceinline__ void channel_gate(int chunk, float2 (&g)[C2]) const {
+    weight(p.gate, p.gate_f32, 0, chunk, g);
+    squash(g);
+  }
+  // The factor of the columns after the block: post_w times a gate by channels (1 where there is neither).
+  __device__ __forceinline__ void factor(int chunk, float2 (&f)[C2]) const {
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) f[e] = both(1.f);
-    if (p.post_w) weight(p.post_w, p.w_f32, 0, f);
+    for (int e = 0; e < C2; ++e) f[e] = both(1.f);
+    if (p.post_w) weight(p.post_w, p.w_f32, 0, chunk, f);
     if (p.gate_kind == MOE_GATE_CHANNEL) {
-      float2 g[E / 2];
-      channel_gate(g);
+      float2 g[C2];
+      channel_gate(chunk, g);
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) f[e] = mul2(f[e], g[e]);
+      for (int e = 0; e < C2; ++e) f[e] = mul2(f[e], g[e]);
     }
   }
-  __device__ __forceinline__ void full_gate(float2 (&g)[E / 2]) const {
-    if (p.gate_ring) load(S_GATE, g);
-    else weight(p.stream[S_GATE], p.gate_f32, at, g);
-    if (p.sigmoid)
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) g[e] = make_float2(sigmoid<T>(g[e].x), sigmoid<T>(g[e].y));
+  __device__ __forceinline__ void full_gate(int chunk, float2 (&g)[C2]) const {
+    if (p.gate_ring) load(S_GATE, chunk, g);
+    else weight(p.stream[S_GATE], p.gate_f32, at, chunk, g);
+    squash(g);
   }
   // A token's gate, loaded a row ahead.
   __device__ __forceinline__ void fetch_token(long t) {
@@ -342,7 +340,7 @@ constexpr size_t kSmemSm = 226 * 1024;
 
 // Rows of the ring of one of `ctas` CTAs, and its bytes
 inline int ring_stages(size_t row, int ctas, size_t* bytes) {
-  const size_t room = kSmemSm / ctas - 3 * 1024;  // (static shared memory and what the system takes)
+  const size_t room = kSmemSm / ctas - 4 * 1024;  // (static shared memory and what the system takes)
   const int n = (int)std::min<size_t>(kMaxStages, (room - 128) / row);
   *bytes = n < 2 ? 0 : 128 + n * row;
   return n < 2 ? 0 : n;
@@ -383,7 +381,7 @@ int norm_regs(K kernel, int (&known)[64]) {
   if (dev >= 0 && dev < 64 && known[dev]) return known[dev];
   cudaFuncAttributes a;
   if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess ||
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemSm - 3 * 1024) != cudaSuccess) {
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemSm - 4 * 1024) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }

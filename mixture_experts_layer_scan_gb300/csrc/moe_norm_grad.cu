@@ -5,134 +5,183 @@ namespace moe {
 
 namespace {
 
-// With u = scale D (n post_w gate) = z n cw, z = scale D and cw the columns' factor (a token's or a full gate apart):
-//   d_post_w = sum_t z G n,  d_gate = sum z n post_w:  for a gate by channels both are sum_t z n times the other
-//   factor, and one sum is kept;  the sum over a row of z cw n is a token gate's gradient and, times G, what d_y needs.
+// With z = scale G D (G a token's gate) and cw the columns' factor: d_post_w = sum_t z gate n and d_gate = sum_t z n post_w.
+// For a gate by channels both are sum_t z n times the other factor, and one sum is kept.
 template <typename T, int W, int NV, int KIND, bool RING, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant__ NormDev p) {
   pdl_enter();
   using R = Rows<T, W, NV, RING>;
-  constexpr int N = R::N, E2 = R::E / 2;
+  constexpr int N = R::N, C2 = R::C2, CH = R::CHUNKS, CP = KIND != N_PRE ? CH : 1;
   constexpr bool POST = KIND != N_PRE, FULL = KIND == N_FULL, HOLD = THREADS <= 512;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ __align__(16) float sums[2][3][2 * kMaxWarps];
-  for (int i = threadIdx.x; i < 12 * kMaxWarps; i += blockDim.x) (&sums[0][0][0])[i] = 0.f;
+  __shared__ float sums[2][2][THREADS / 4];
   R rows(p, smem);
   __syncthreads();
   rows.start();
   if constexpr (POST) rows.fetch_token(blockIdx.x);
   const bool dh = p.stream[S_DH] != nullptr, dout = p.stream[S_DOUT] != nullptr;
-  float2 cw[POST ? E2 : 1], nw[E2], acc_n[E2], acc_s[POST ? E2 : 1];
+  float2 cw[HOLD ? CP : 1][C2], nw[HOLD ? CH : 1][C2], acc_n[CH][C2], acc_s[CP][C2];
 #pragma unroll
-  for (int e = 0; e < E2; ++e) {
-    acc_n[e] = nw[e] = both(0.f);
-    if constexpr (POST) acc_s[e] = both(0.f);
-  }
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int e = 0; e < C2; ++e) {
+      acc_n[c][e] = both(0.f);
+      if constexpr (POST) acc_s[c][e] = both(0.f);
+    }
+  auto weights = [&](int c, float2 (&f)[C2], float2 (&n)[C2]) {
+    if constexpr (POST) rows.factor(c, f);
+    if (dh) {
+      rows.weight(p.next_w, p.w_f32, 0, c, n);
+    } else {
+#pragma unroll
+      for (int e = 0; e < C2; ++e) n[e] = both(0.f);
+    }
+  };
   if constexpr (HOLD) {
-    if constexpr (POST) rows.factor(cw);
-    if (dh) rows.weight(p.next_w, p.w_f32, 0, nw);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) weights(c, cw[POST ? c : 0], nw[c]);
   }
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
     rows.open(t);
-    float (&s3)[3][2 * kMaxWarps] = sums[rows.k & 1];
-    float ry = 1.0f, tok = 1.0f;
-    if constexpr (POST) {
-      if (p.post_w) {
-        float2 y[E2], a = both(0.f);
-        rows.load(S_Y, y);
-#pragma unroll
-        for (int e = 0; e < E2; ++e) a = fma2(y[e], y[e], a);
-        ry = rsqrtf(block_sum(a, s3[0]) * p.inv_h + p.eps);
-        rows.refill(t);
-      }
-      tok = rows.token_gate(t);
-      if constexpr (!HOLD) rows.factor(cw);
-    }
-    if constexpr (!HOLD)
-      if (dh) rows.weight(p.next_w, p.w_f32, 0, nw);
-    const float sy = p.scale * tok * ry;
-    float r = 0.f, m = 0.f;  // 1 / rms of out, mean(g n) of the next norm
-    auto forward = [&](float2 (&o)[E2], float2 (&y)[POST ? E2 : 1], float2 (&g)[FULL ? E2 : 1]) {
-      rows.load(S_X, o);
+    float (&s2)[2][THREADS / 4] = sums[rows.k & 1];
+    // x, c = y post_w gate and e = d_h next_w of a chunk
+    auto inputs = [&](int c, float2 (&x)[C2], float2 (&y)[C2], float2 (&yc)[C2], float2 (&d)[C2], float2 (&e)[C2], float2 (&g)[C2]) {
+      if constexpr (!HOLD) weights(c, cw[0], nw[0]);
+      rows.load(S_X, c, x);
       if constexpr (POST) {
-        rows.load(S_Y, y);
-        if constexpr (FULL) rows.full_gate(g);
+        rows.load(S_Y, c, y);
+        if constexpr (FULL) rows.full_gate(c, g);
 #pragma unroll
-        for (int e = 0; e < E2; ++e) {
-          float2 b = mul2(y[e], cw[e]);
-          if constexpr (FULL) b = mul2(b, g[e]);
-          o[e] = fma2(both(sy), b, mul2(both(p.res_scale), o[e]));
+        for (int i = 0; i < C2; ++i) {
+          yc[i] = mul2(y[i], cw[HOLD ? c : 0][i]);
+          if constexpr (FULL) yc[i] = mul2(yc[i], g[i]);
         }
-      }
-    };
-    if (dh) {
-      float2 o[E2], y[POST ? E2 : 1], g[FULL ? E2 : 1], d[E2], a = both(0.f), b = both(0.f);
-      forward(o, y, g);
-      rows.load(S_DH, d);
-#pragma unroll
-      for (int e = 0; e < E2; ++e) {
-        a = fma2(o[e], o[e], a);
-        b = fma2(o[e], mul2(d[e], nw[e]), b);
-      }
-      const float2 s = block_sum2(a, b, s3[1]);
-      rows.refill(t);
-      r = rsqrtf(s.x * p.inv_h + p.eps);
-      m = s.y * r * p.inv_h;
-    }
-    float2 gn[E2];  // D, then the gradient in n (but for a token's gate)
-    float2 a = both(0.f);
-    {
-      float2 o[E2], y[POST ? E2 : 1], g[FULL ? E2 : 1], d[E2];
-      forward(o, y, g);
-      if (POST && dout) {
-        rows.load(S_DOUT, gn);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E2; ++e) gn[e] = both(0.f);
       }
       if (dh) {
-        rows.load(S_DH, d);
-#pragma unroll
-        for (int e = 0; e < E2; ++e) {
-          const float2 nn = mul2(o[e], both(r));
-          acc_n[e] = fma2(d[e], nn, acc_n[e]);
-          gn[e] = fma2(both(r), fma2(nn, both(-m), mul2(d[e], nw[e])), gn[e]);
-        }
-      }
-      if constexpr (!POST) {
-        rows.store(p.d_x, gn);
+        rows.load(S_DH, c, d);
       } else {
 #pragma unroll
-        for (int e = 0; e < E2; ++e) o[e] = mul2(gn[e], both(p.res_scale));
-        rows.store(p.d_x, o);
+        for (int i = 0; i < C2; ++i) d[i] = both(0.f);
+      }
 #pragma unroll
-        for (int e = 0; e < E2; ++e) {
-          const float2 z = mul2(gn[e], both(p.scale)), n = mul2(y[e], both(ry));
-          const float2 zc = mul2(z, cw[e]), u = mul2(zc, n);
-          if constexpr (FULL) {
-            gn[e] = mul2(zc, g[e]);
-            acc_s[e] = fma2(mul2(z, g[e]), n, acc_s[e]);
-            a = fma2(u, g[e], a);
-            // d_gate, in place of out
-            o[e] = p.sigmoid ? mul2(u, make_float2(g[e].x * (1.0f - g[e].x), g[e].y * (1.0f - g[e].y))) : u;
-          } else {
-            gn[e] = zc;
-            acc_s[e] = fma2(mul2(z, both(tok)), n, acc_s[e]);
-            a = add2(u, a);
+      for (int i = 0; i < C2; ++i) e[i] = mul2(d[i], nw[HOLD ? c : 0][i]);
+    };
+    float2 xx = both(0.f), yy = xx, xc = xx, cc = xx, xe = xx, ce = xx, dc = xx;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float2 x[C2], y[C2], yc[C2], d[C2], e[C2], g[C2];
+      inputs(c, x, y, yc, d, e, g);
+#pragma unroll
+      for (int i = 0; i < C2; ++i) {
+        xx = fma2(x[i], x[i], xx);
+        xe = fma2(x[i], e[i], xe);
+        if constexpr (POST) {
+          yy = fma2(y[i], y[i], yy);
+          xc = fma2(x[i], yc[i], xc);
+          cc = fma2(yc[i], yc[i], cc);
+          ce = fma2(yc[i], e[i], ce);
+        }
+      }
+      if constexpr (POST) {
+        if (dout) {
+          rows.load(S_DOUT, c, d);
+#pragma unroll
+          for (int i = 0; i < C2; ++i) dc = fma2(d[i], yc[i], dc);
+        }
+      }
+    }
+    float ry = 1.f, tok = 1.f, b = 0.f, r, m, mean = 0.f;  // r: 1 / rms of out; m: mean(e out r)
+    if constexpr (POST) {
+      float v[7] = {flat(xx), flat(yy), flat(xc), flat(cc), flat(xe), flat(ce), flat(dc)};
+      block_sums(v, s2[0]);
+      rows.refill(t);
+      tok = rows.token_gate(t);
+      if (p.post_w) ry = rsqrtf(v[1] * p.inv_h + p.eps);
+      b = p.scale * tok * ry;
+      const float pp = p.res_scale * p.res_scale * v[0], qq = b * b * v[3];
+      float ee = pp + qq + 2.f * p.res_scale * b * v[2], oe = p.res_scale * v[4] + b * v[5];
+      if (dh && parts_cancel(pp, qq, ee)) {
+        float2 a0 = both(0.f), a1 = a0;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          float2 x[C2], y[C2], yc[C2], d[C2], e[C2], g[C2];
+          inputs(c, x, y, yc, d, e, g);
+#pragma unroll
+          for (int i = 0; i < C2; ++i) {
+            x[i] = fma2(both(b), yc[i], mul2(both(p.res_scale), x[i]));
+            a0 = fma2(x[i], x[i], a0);
+            a1 = fma2(x[i], e[i], a1);
           }
         }
+        float u[2] = {flat(a0), flat(a1)};
+        block_sums(u, s2[1]);
+        ee = u[0];
+        oe = u[1];
+      }
+      r = dh ? rsqrtf(ee * p.inv_h + p.eps) : 0.f;
+      m = oe * r * p.inv_h;
+      // sum over the row of scale D c, which is a token gate's gradient times r_y's inverse
+      const float u = p.scale * ry * (v[6] + r * v[5] - r * r * m * (p.res_scale * v[2] + b * v[3]));
+      mean = u * p.inv_h;
+      if (p.gate_kind == MOE_GATE_TOKEN && p.d_gate && threadIdx.x == 0)
+        static_cast<float*>(p.d_gate)[t] = p.sigmoid ? u * tok * (1.0f - tok) : u;
+    } else {
+      float v[2] = {flat(xx), flat(xe)};
+      block_sums(v, s2[0]);
+      rows.refill(t);
+      r = rsqrtf(v[0] * p.inv_h + p.eps);
+      m = v[1] * r * p.inv_h;
+    }
+    const float2 r2 = both(r), rm = both(-r * r * m), z2 = both(p.scale * tok), ry2 = both(ry);
+    const float2 c1 = both(p.post_w ? -mean * tok * ry * ry : 0.f);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float2 x[C2], y[C2], yc[C2], d[C2], e[C2], g[C2], D[C2];
+      inputs(c, x, y, yc, d, e, g);
+      if (POST && dout) {
+        rows.load(S_DOUT, c, D);
+      } else {
+#pragma unroll
+        for (int i = 0; i < C2; ++i) D[i] = both(0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < C2; ++i) {
+        if constexpr (POST) x[i] = fma2(both(b), yc[i], mul2(both(p.res_scale), x[i]));  // out
+        acc_n[c][i] = fma2(d[i], mul2(x[i], r2), acc_n[c][i]);
+        D[i] = fma2(r2, e[i], fma2(rm, x[i], D[i]));
+      }
+      if constexpr (!POST) {
+        rows.store(p.d_x, c, D);
+      } else {
+#pragma unroll
+        for (int i = 0; i < C2; ++i) x[i] = mul2(D[i], both(p.res_scale));
+        rows.store(p.d_x, c, x);
+#pragma unroll
+        for (int i = 0; i < C2; ++i) {
+          float2 z = mul2(D[i], z2);
+          const float2 n = mul2(y[i], ry2);
+          if constexpr (FULL) {  // d_gate, in place of out
+            const float2 u = mul2(mul2(z, cw[HOLD ? c : 0][i]), n);
+            x[i] = p.sigmoid ? mul2(u, make_float2(g[i].x * (1.0f - g[i].x), g[i].y * (1.0f - g[i].y))) : u;
+            z = mul2(z, g[i]);
+          }
+          acc_s[c][i] = fma2(z, n, acc_s[c][i]);
+          z = mul2(z, cw[HOLD ? c : 0][i]);
+          D[i] = fma2(c1, y[i], mul2(ry2, z));  // d_y
+        }
+        rows.store(p.d_y, c, D);
         if constexpr (FULL) {
           if (p.d_gate) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-              if (!rows.has(i)) break;
+            for (int i = 0; i < R::CV; ++i) {
+              if (!rows.has(c * R::CV + i)) break;
               float f[N];
 #pragma unroll
-              for (int c = 0; c < N; ++c) f[c] = R::pick(o, i * N + c);
-              const size_t to = rows.at + (size_t)rows.vec(i) * N;
+              for (int k = 0; k < N; ++k) f[k] = R::pick(x, i * N + k);
+              const size_t to = rows.at + (size_t)rows.vec(c * R::CV + i) * N;
               if (p.gate_f32) {
 #pragma unroll
-                for (int c = 0; c < N; ++c) static_cast<float*>(p.d_gate)[to + c] = f[c];
+                for (int k = 0; k < N; ++k) static_cast<float*>(p.d_gate)[to + k] = f[k];
               } else {
                 using G = typename Word<N * 2>::type;
                 *reinterpret_cast<G*>(static_cast<uint16_t*>(p.d_gate) + to) = narrow<__nv_bfloat16, N * 2>(f);
@@ -142,65 +191,42 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
         }
       }
     }
-    if constexpr (POST) {
-      float mean = 0.f;
-      if (p.post_w || p.gate_kind == MOE_GATE_TOKEN) {
-        const float s = block_sum(a, s3[2]);
-        rows.refill(t);
-        mean = s * p.inv_h;
-        if (p.gate_kind == MOE_GATE_TOKEN && p.d_gate && threadIdx.x == 0)
-          static_cast<float*>(p.d_gate)[t] = p.sigmoid ? s * tok * (1.0f - tok) : s;
-      }
-      if (p.post_w) {
-        float2 y[E2];
-        rows.load(S_Y, y);
-        const float2 c0 = both(tok * ry), c1 = both(-mean * ry);
-#pragma unroll
-        for (int e = 0; e < E2; ++e) gn[e] = mul2(c0, fma2(c1, y[e], gn[e]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < E2; ++e) gn[e] = mul2(both(tok), gn[e]);
-      }
-      rows.store(p.d_y, gn);
-    }
     rows.close(t);
   }
   rows.drain();
   // partial sums
   const size_t plane = (size_t)gridDim.x * p.H;
   float* part = p.part + (size_t)blockIdx.x * p.H;
-  auto store = [&](float* to, const float2 (&f)[E2]) {
+  auto store = [&](float* to, int c, const float2 (&f)[C2]) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!rows.has(i)) break;
+    for (int i = 0; i < R::CV; ++i) {
+      if (!rows.has(c * R::CV + i)) break;
 #pragma unroll
-      for (int c = 0; c < N; ++c) to[(size_t)rows.vec(i) * N + c] = R::pick(f, i * N + c);
+      for (int k = 0; k < N; ++k) to[(size_t)rows.vec(c * R::CV + i) * N + k] = R::pick(f, i * N + k);
     }
   };
-  if (p.sum_next) store(part + plane, acc_n);
-  if constexpr (POST) {
-    float2 f[E2], g[E2];
-    if (p.sum_gate) {
-      rows.channel_gate(g);
 #pragma unroll
-      for (int e = 0; e < E2; ++e) f[e] = both(1.f);
-      if (p.post_w) rows.weight(p.post_w, p.w_f32, 0, f);
+  for (int c = 0; c < CH; ++c) {
+    if (p.sum_next) store(part + plane, c, acc_n[c]);
+    if constexpr (POST) {
+      float2 f[C2], g[C2];
+      if (p.gate_kind == MOE_GATE_CHANNEL) rows.channel_gate(c, g);
+      if (p.sum_gate) {
 #pragma unroll
-      for (int e = 0; e < E2; ++e) {
-        f[e] = mul2(f[e], acc_s[e]);
-        if (p.sigmoid) f[e] = mul2(f[e], make_float2(g[e].x * (1.0f - g[e].x), g[e].y * (1.0f - g[e].y)));
+        for (int i = 0; i < C2; ++i) f[i] = both(1.f);
+        if (p.post_w) rows.weight(p.post_w, p.w_f32, 0, c, f);
+#pragma unroll
+        for (int i = 0; i < C2; ++i) {
+          f[i] = mul2(f[i], acc_s[c][i]);
+          if (p.sigmoid) f[i] = mul2(f[i], make_float2(g[i].x * (1.0f - g[i].x), g[i].y * (1.0f - g[i].y)));
+        }
+        store(part + 2 * plane, c, f);
       }
-      store(part + 2 * plane, f);
-    }
-    if (p.sum_post) {
+      if (p.sum_post) {
 #pragma unroll
-      for (int e = 0; e < E2; ++e) f[e] = acc_s[e];
-      if (p.gate_kind == MOE_GATE_CHANNEL) {
-        rows.channel_gate(g);
-#pragma unroll
-        for (int e = 0; e < E2; ++e) f[e] = mul2(f[e], g[e]);
+        for (int i = 0; i < C2; ++i) f[i] = p.gate_kind == MOE_GATE_CHANNEL ? mul2(acc_s[c][i], g[i]) : acc_s[c][i];
+        store(part, c, f);
       }
-      store(part, f);
     }
   }
 }
