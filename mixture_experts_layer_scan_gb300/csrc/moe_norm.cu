@@ -6,12 +6,14 @@ namespace moe {
 namespace {
 
 // The sums' shared memory alternates from row to row: what a row wrote is overwritten behind the next row's barrier.
-template <typename T, int W, int NV, int KIND, bool RING, int THREADS>
+// FAST: whole vectors in every thread, and both norms: nothing is asked for each vector.
+template <typename T, int W, int NV, int KIND, bool RING, int THREADS, bool FAST>
 __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ NormDev p) {
   pdl_enter();
-  using R = Rows<T, W, NV, RING>;
+  using R = Rows<T, W, NV, RING, FAST>;
   constexpr int C2 = R::C2, CH = R::CHUNKS;
   constexpr bool POST = KIND != N_PRE, HOLD = THREADS <= 512;
+  const bool post = FAST || p.post_w, next = !POST || FAST || p.next_w;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float sums[2][2][THREADS / 4];
   R rows(p, smem);
@@ -23,7 +25,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if constexpr (POST) rows.factor(c, cw[c]);
-      if (p.next_w) rows.weight(p.next_w, p.w_f32, 0, c, nw[c]);
+      if (next) rows.weight(p.next_w, p.w_f32, 0, c, nw[c]);
     }
   }
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
@@ -57,7 +59,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
       block_sums(v, s2[0]);
       rows.refill(t);
       b = p.scale * rows.token_gate(t);
-      if (p.post_w) b *= rsqrtf(v[1] * p.inv_h + p.eps);
+      if (post) b *= rsqrtf(v[1] * p.inv_h + p.eps);
       const float pp = p.res_scale * p.res_scale * v[0], qq = b * b * v[3], ee = pp + qq + 2.f * p.res_scale * b * v[2];
       r = ee;
 #pragma unroll
@@ -66,7 +68,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
         for (int e = 0; e < C2; ++e) o[c][e] = fma2(both(b), y[c][e], mul2(both(p.res_scale), o[c][e]));
         rows.store(p.out, c, o[c]);
       }
-      if (p.next_w && parts_cancel(pp, qq, ee)) {
+      if (next && parts_cancel(pp, qq, ee)) {
         a0 = both(0.f);
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
       rows.refill(t);
       r = v[0];
     }
-    if (!POST || p.next_w) {
+    if (next) {
       r = rsqrtf(r * p.inv_h + p.eps);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -98,10 +100,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
 }
 
 // (the ring's kernel, or the one without where rows do not fit or are few; the ring's registers decide for both)
-template <typename T, int W, int NV, int KIND, bool RING, int THREADS>
+template <typename T, int W, int NV, int KIND, bool RING, int THREADS, bool FAST = false>
 cudaError_t launch_one(NormDev p, cudaStream_t s) {
+  if constexpr (W == 16 && RING && !FAST)
+    if (p.H % (32 * kElems) == 0 && (KIND == N_PRE || (p.post_w && p.next_w)))
+      return launch_one<T, W, NV, KIND, RING, THREADS, true>(p, s);
   static int known[64] = {};
-  auto kernel = k_norm<T, W, NV, KIND, RING, THREADS>;
+  auto kernel = k_norm<T, W, NV, KIND, RING, THREADS, FAST>;
   const int regs = norm_regs(kernel, known);
   if (!regs) return cudaErrorInvalidValue;
   const NormShape q = norm_shape<T, W>(p, regs, NV * (W / (int)sizeof(T)), p.T, RING);

@@ -119,8 +119,8 @@ struct NormDev {
 };
 
 // The rows of a CTA, in turn, NV vectors of W bytes to a thread (vectors i, i + blockDim, ...): from a ring in shared
-// memory (RING) or from memory.  A thread's E elements are E / 2 pairs; those behind the row's end are 0.
-template <typename T, int W, int NV, bool RING>
+// memory (RING) or from memory.  A thread's E elements are E / 2 pairs; those behind the row's end are 0.  FULL_ROWS: every thread has all of its vectors.
+template <typename T, int W, int NV, bool RING, bool FULL_ROWS>
 struct Rows {
   using V = typename Word<W>::type;
   static constexpr int N = W / sizeof(T), E = NV * N;
@@ -135,6 +135,7 @@ struct Rows {
   bool ok, refilled, tail;       // tail: the copy leaves out the row's end
   float token;                   // the next row's gate
   int place[S_MAX];              // of a stream among those of a stage
+  uint32_t first;                // this thread's first vector in the present stage
 
   __device__ __forceinline__ Rows(const NormDev& q, uint8_t* smem)
       : p(q), vpr(q.H / N), k(0), stage(0), phase(0), shift(0), whole(0), at(0), ok(true), refilled(false),
@@ -154,7 +155,7 @@ struct Rows {
     }
   }
   __device__ __forceinline__ int vec(int i) const { return threadIdx.x + i * blockDim.x; }
-  __device__ __forceinline__ bool has(int i) const { return vec(i) < vpr; }
+  __device__ __forceinline__ bool has(int i) const { return FULL_ROWS || vec(i) < vpr; }
   // The 16-byte units around row t: first byte and their number of bytes.
   __device__ __forceinline__ void extent(int t, size_t& from, uint32_t& n) const {
     const size_t row = (size_t)p.H * sizeof(T), begin = (size_t)t * row, end = begin + row;
@@ -188,6 +189,7 @@ struct Rows {
     if constexpr (RING) {
       refilled = false;
       if (ok) ok = mbar_wait_one(bars + 8 * stage, phase, abort, p.status);
+      first = buf + (uint32_t)(stage * p.streams) * p.pitch + threadIdx.x * W;
       if (W < 16) {
         size_t from;
         extent(t, from, whole);
@@ -233,7 +235,7 @@ struct Rows {
     return reinterpret_cast<const V*>(static_cast<const T*>(p.stream[s]) + at)[vec(i)];
   }
   __device__ __forceinline__ V from_ring(int s, int i) const {
-    const uint32_t from = buf + (uint32_t)(stage * p.streams + place[s]) * p.pitch + (W < 16 ? shift : 0u) + (uint32_t)vec(i) * W;
+    const uint32_t from = first + (uint32_t)place[s] * p.pitch + (W < 16 ? shift : 0u) + (uint32_t)(i * blockDim.x) * W;
     V v;
     if constexpr (W == 16) v = lds_v4(from);
     else if constexpr (W == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(from) : "memory");

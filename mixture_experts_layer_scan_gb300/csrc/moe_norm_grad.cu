@@ -7,10 +7,11 @@ namespace {
 
 // With z = scale G D (G a token's gate) and cw the columns' factor: d_post_w = sum_t z gate n and d_gate = sum_t z n post_w.
 // For a gate by channels both are sum_t z n times the other factor, and one sum is kept.
-template <typename T, int W, int NV, int KIND, bool RING, int THREADS>
+// FAST: whole vectors in every thread, both norms and both incoming gradients: nothing is asked for each vector.
+template <typename T, int W, int NV, int KIND, bool RING, int THREADS, bool FAST>
 __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant__ NormDev p) {
   pdl_enter();
-  using R = Rows<T, W, NV, RING>;
+  using R = Rows<T, W, NV, RING, FAST>;
   constexpr int N = R::N, C2 = R::C2, CH = R::CHUNKS, CP = KIND != N_PRE ? CH : 1;
   constexpr bool POST = KIND != N_PRE, FULL = KIND == N_FULL, HOLD = THREADS <= 512;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -19,7 +20,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
   __syncthreads();
   rows.start();
   if constexpr (POST) rows.fetch_token(blockIdx.x);
-  const bool dh = p.stream[S_DH] != nullptr, dout = p.stream[S_DOUT] != nullptr;
+  const bool dh = FAST || p.stream[S_DH], dout = FAST || p.stream[S_DOUT], post = FAST || p.post_w;
   float2 cw[HOLD ? CP : 1][C2], nw[HOLD ? CH : 1][C2], acc_n[CH][C2], acc_s[CP][C2];
 #pragma unroll
   for (int c = 0; c < CH; ++c)
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
       block_sums(v, s2[0]);
       rows.refill(t);
       tok = rows.token_gate(t);
-      if (p.post_w) ry = rsqrtf(v[1] * p.inv_h + p.eps);
+      if (post) ry = rsqrtf(v[1] * p.inv_h + p.eps);
       b = p.scale * tok * ry;
       const float pp = p.res_scale * p.res_scale * v[0], qq = b * b * v[3];
       float ee = pp + qq + 2.f * p.res_scale * b * v[2], oe = p.res_scale * v[4] + b * v[5];
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
       m = v[1] * r * p.inv_h;
     }
     const float2 r2 = both(r), rm = both(-r * r * m), z2 = both(p.scale * tok), ry2 = both(ry);
-    const float2 c1 = both(p.post_w ? -mean * tok * ry * ry : 0.f);
+    const float2 c1 = both(post ? -mean * tok * ry * ry : 0.f);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       float2 x[C2], y[C2], yc[C2], d[C2], e[C2], g[C2], D[C2];
@@ -261,10 +262,13 @@ __global__ void __launch_bounds__(32 * kSumWarps) k_sum_rows(const SumDev p) {
   }
 }
 
-template <typename T, int W, int NV, int KIND, bool RING, int THREADS>
+template <typename T, int W, int NV, int KIND, bool RING, int THREADS, bool FAST = false>
 cudaError_t launch_one(NormDev p, int most, int* grid, cudaStream_t s) {
+  if constexpr (W == 16 && RING && !FAST)
+    if (p.H % (32 * kElems) == 0 && p.stream[S_DH] && (KIND == N_PRE || (p.post_w && p.stream[S_DOUT])))
+      return launch_one<T, W, NV, KIND, RING, THREADS, true>(p, most, grid, s);
   static int known[64] = {};
-  auto kernel = k_norm_grad<T, W, NV, KIND, RING, THREADS>;
+  auto kernel = k_norm_grad<T, W, NV, KIND, RING, THREADS, FAST>;
   const int regs = norm_regs(kernel, known);
   if (!regs) return cudaErrorInvalidValue;
   const NormShape q = norm_shape<T, W>(p, regs, kElems, most, RING);

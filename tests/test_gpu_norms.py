@@ -267,3 +267,36 @@ def test_other_stream(moe):
     with torch.cuda.stream(side):
         assert all(bool(torch.equal(a, b)) for a, b in zip(got, ref))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(6000, 512), (700, 1024), (500, 4096), (400, 8192), (700, 2047), (2500, 33), (6000, 8), (450, 4160)])
+def test_rows_through_the_ring(moe, T, H, dtype, gate):
+    """More rows than CTAs: rows that every thread holds whole vectors of, and others; rows that begin off a
+    16-byte boundary; the last rows of a tensor."""
+    g = torch.Generator().manual_seed(T + H)
+    d = inputs(T, H, DT[dtype], torch.float32, g, True, gate, True)
+    check_all(moe, d, gate == "full", 0.5, 1.25, f"{T} x {H} {dtype} {gate}", T)
+    x, w, dh = d["x"].cuda(), d["next_w"].cuda(), d["d_h"].cuda()
+    r = rstd(d["x"].double())
+    n, gg = d["x"].double() * r, d["d_h"].double() * d["next_w"].double()
+    within(moe.moe_prenorm(x, w, EPS), n * d["next_w"].double(), (half(DT[dtype]) + FUZZ) * (n * d["next_w"].double()).abs(), "h")
+    d_x, d_w = moe.moe_prenorm_backward(dh, x, w, EPS)
+    ref = r * (gg - n * mean(gg * n))
+    within(d_x, ref, half(DT[dtype]) * ref.abs() + FUZZ * r * (gg.abs() + n.abs() * mean((gg * n).abs())), "d_x")
+    within(d_w, (d["d_h"].double() * n).sum(0), (FUZZ + T * 2.0 ** -24) * (d["d_h"].double() * n).abs().sum(0), "d_w")
+
+
+@pytest.mark.parametrize("T,H", [(3, 256), (900, 2048)])
+def test_residual_that_cancels(moe, T, H):
+    """Rows whose residual and branch nearly cancel: out is small beside them, and so is the sum of its squares."""
+    g = torch.Generator().manual_seed(T)
+    for small in (1e-1, 1e-3):
+        d = inputs(T, H, torch.float32, torch.float32, g, False, "none", True)
+        d["x"] = small * d["x"] - 0.5 * d["y"]
+        check_all(moe, d, False, 0.5, 1.0, f"{small}", T, eps=EPS)
+        d = inputs(T, H, torch.float32, torch.float32, g, True, "token", True)
+        n = d["y"].double() * rstd(d["y"].double()) * d["post_w"].double()
+        d["x"] = (small * d["x"].double() - d["gate"].double() * n).float()
+        check_all(moe, d, False, 1.0, 1.0, f"normed {small}", T, eps=EPS)
