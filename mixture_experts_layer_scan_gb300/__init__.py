@@ -397,14 +397,23 @@ def moe_align(topk_ids: torch.Tensor, E: int, block: int, stream=None, with_coun
     return sorted_ids, expert_ids, npp[:1], counts
 
 
-def _same_device(x: torch.Tensor, *others) -> None:
-    """The arrays of a call lie on the current CUDA device (the library reads their addresses as that device's)."""
+def _begin(stream, x: torch.Tensor, *others) -> int:
+    """The handle of a call's stream.  Its arrays have to lie on the current CUDA device (the library reads their
+    addresses as that device's)."""
     d = x.get_device()
-    if d < 0 or d != torch.cuda.current_device():
+    if d < 0 or d != torch._C._cuda_getDevice():
         raise ValueError("tensors must be on the current CUDA device")
     for t in others:
         if t is not None and t.get_device() != d:
             raise ValueError("tensors must be on the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(d) if stream is None else _stream(stream)
+
+
+def _out_like(t: Optional[torch.Tensor], x: torch.Tensor, stream) -> torch.Tensor:
+    """The caller's output of x's shape and type, checked, or a new one."""
+    if t is None and stream is None:
+        return torch.empty_like(x)  # (cheaper on the host than a new shape)
+    return _out(t, x.shape, x.dtype, x.device, stream)
 
 
 _ACTS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
@@ -422,15 +431,23 @@ def _like(t: Optional[torch.Tensor], shape, dtype, what: str) -> None:
         raise ValueError(f"{what} must be {dtype} {tuple(shape)}")
 
 
-class PermutedRows(NamedTuple):
+class PermutedRows:
     """Rows in expert order (moe_permute): rows [cap,H]; row_of int32 [T,k], the row of each pair (-1: none); and
-    moe_align's maps: sorted_ids [cap], expert_ids [cap/block], num_post_pad [1], expert_counts [E]."""
-    rows: torch.Tensor
-    row_of: torch.Tensor
-    sorted_ids: torch.Tensor
-    expert_ids: torch.Tensor
-    num_post_pad: torch.Tensor
-    expert_counts: torch.Tensor
+    moe_align's maps: sorted_ids [cap], expert_ids [cap/block], num_post_pad [1], expert_counts [E].  The maps are views
+    of one tensor."""
+    __slots__ = ("rows", "_maps", "_at", "_shape")
+
+    def __init__(self, rows: torch.Tensor, maps: torch.Tensor, at, shape):
+        self.rows, self._maps, self._at, self._shape = rows, maps, at, shape
+
+    def _view(self, i: int) -> torch.Tensor:
+        return self._maps[self._at[i][0]:self._at[i][1]]
+
+    row_of = property(lambda self: self._view(0).view(self._shape))
+    sorted_ids = property(lambda self: self._view(1))
+    expert_ids = property(lambda self: self._view(2))
+    num_post_pad = property(lambda self: self._view(3))
+    expert_counts = property(lambda self: self._view(4))
 
 
 def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, E: int, block: int = 1, rows=None, stream=None) -> PermutedRows:
@@ -440,23 +457,23 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, E: int, block: int = 1,
     dt = _act(x, "x")
     if topk_ids.dim() != 2 or topk_ids.shape[0] != T or topk_ids.dtype != torch.int32:
         raise ValueError("topk_ids must be int32 [T, k]")
-    _same_device(x, topk_ids, rows)
+    handle = _begin(stream, x, topk_ids, rows)
     k = topk_ids.shape[1]
-    cap, bcap = moe_align_capacity(T, k, E, block)
-    dev = x.device
-    rows = _out(rows, (cap, H), x.dtype, dev, stream)
+    n = T * k
+    if min(E, block, k) < 1:
+        raise MoeError(MOE_ERR_ARG, "moe_permute")
+    cap = n + min(E, n) * (block - 1)  # (moe_align_capacity)
+    rows = _out(rows, (cap, H), x.dtype, x.device, stream)
     # (one allocation for the maps, each at a multiple of 16 bytes)
-    sizes = [T * k, cap, bcap, 1, E]
     at, end = [], 0
-    for n in sizes:
-        at.append(end)
-        end += (n + 3) // 4 * 4
-    maps = _empty(end, torch.int32, dev, stream, zero=T == 0)  # (an empty batch launches nothing)
-    row_of, sorted_ids, expert_ids, npp, counts = (maps[a:a + n] for a, n in zip(at, sizes))
+    for size in (n, cap, cap // block, 1, E):
+        at.append((end, end + size))
+        end += (size + 3) & -4
+    maps = _empty(end, torch.int32, x.device, stream, zero=T == 0)  # (an empty batch launches nothing)
     p = maps.data_ptr()
-    _check(_lib.moe_permute(_p(x), _p(topk_ids), T, H, E, k, block, dt, _p(rows), *(p + 4 * a for a in at),
-                            _stream(stream)), "moe_permute")
-    return PermutedRows(rows, row_of.view(T, k), sorted_ids, expert_ids, npp, counts)
+    _check(_lib.moe_permute(_p(x), _p(topk_ids), T, H, E, k, block, dt, _p(rows), p, p + 4 * at[1][0], p + 4 * at[2][0],
+                            p + 4 * at[3][0], p + 4 * at[4][0], handle), "moe_permute")
+    return PermutedRows(rows, maps, at, (T, k))
 
 
 def _row_map(row_of: torch.Tensor, rows: torch.Tensor, topk_w=None):
@@ -471,10 +488,9 @@ def moe_unpermute(rows: torch.Tensor, row_of: torch.Tensor, topk_w: Optional[tor
     """out [T,H] = sum over j of topk_w[t,j] * rows[row_of[t,j]] (topk_w float32 [T,k]; None: weights of 1)."""
     T, k, n, H = _row_map(row_of, rows, topk_w)
     dt = _act(rows, "rows")
-    _same_device(rows, row_of, topk_w, out)
+    handle = _begin(stream, rows, row_of, topk_w, out)
     out = _out(out, (T, H), rows.dtype, rows.device, stream)
-    _check(_lib.moe_unpermute(_p(rows), n, _p(row_of), _p(topk_w), T, H, k, dt, _p(out), _stream(stream)),
-           "moe_unpermute")
+    _check(_lib.moe_unpermute(_p(rows), n, _p(row_of), _p(topk_w), T, H, k, dt, _p(out), handle), "moe_unpermute")
     return out
 
 
@@ -482,10 +498,9 @@ def moe_permute_backward(d_rows: torch.Tensor, row_of: torch.Tensor, d_x=None, s
     """Gradient of moe_permute in x: d_x [T,H] = sum over j of d_rows[row_of[t,j]]."""
     T, k, n, H = _row_map(row_of, d_rows)
     dt = _act(d_rows, "d_rows")
-    _same_device(d_rows, row_of, d_x)
+    handle = _begin(stream, d_rows, row_of, d_x)
     d_x = _out(d_x, (T, H), d_rows.dtype, d_rows.device, stream)
-    _check(_lib.moe_permute_backward(_p(d_rows), n, _p(row_of), T, H, k, dt, _p(d_x), _stream(stream)),
-           "moe_permute_backward")
+    _check(_lib.moe_permute_backward(_p(d_rows), n, _p(row_of), T, H, k, dt, _p(d_x), handle), "moe_permute_backward")
     return d_x
 
 
@@ -504,11 +519,11 @@ def moe_unpermute_backward(d_out: torch.Tensor, rows: torch.Tensor, row_of: torc
         raise ValueError("sorted_ids and num_post_pad go together")
     _like(sorted_ids, (n,), torch.int32, "sorted_ids")
     _like(num_post_pad, (1,), torch.int32, "num_post_pad")
-    _same_device(d_out, rows, row_of, topk_w, sorted_ids, num_post_pad, d_rows, d_w)
-    d_rows = _out(d_rows, (n, H), rows.dtype, rows.device, stream)
+    handle = _begin(stream, d_out, rows, row_of, topk_w, sorted_ids, num_post_pad, d_rows, d_w)
+    d_rows = _out_like(d_rows, rows, stream)
     d_w = _out(d_w, (T, k), torch.float32, rows.device, stream)
     _check(_lib.moe_unpermute_backward(_p(d_out), _p(rows), n, _p(row_of), _p(topk_w), _p(sorted_ids), _p(num_post_pad),
-                                       T, H, k, dt, _p(d_rows), _p(d_w), _stream(stream)), "moe_unpermute_backward")
+                                       T, H, k, dt, _p(d_rows), _p(d_w), handle), "moe_unpermute_backward")
     return d_rows, d_w
 
 
@@ -518,9 +533,9 @@ def moe_prenorm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, h=None, str
     dt, wdt = _act(x, "x"), _act(w, "w")
     if w.shape != (H,):
         raise ValueError("w must be [H]")
-    _same_device(x, w, h)
-    h = _out(h, (T, H), x.dtype, x.device, stream)
-    _check(_lib.moe_prenorm(_p(x), _p(w), T, H, eps, dt, wdt, _p(h), _stream(stream)), "moe_prenorm")
+    handle = _begin(stream, x, w, h)
+    h = _out_like(h, x, stream)
+    _check(_lib.moe_prenorm(_p(x), _p(w), T, H, eps, dt, wdt, _p(h), handle), "moe_prenorm")
     return h
 
 
@@ -537,18 +552,21 @@ def moe_prenorm_backward(d_h: torch.Tensor, x: torch.Tensor, w: torch.Tensor, ep
     dt, wdt = _act(x, "x"), _act(w, "w")
     if w.shape != (H,) or d_h.shape != (T, H) or d_h.dtype != x.dtype:
         raise ValueError("w must be [H] and d_h [T, H] of x's type")
-    _same_device(x, d_h, w, d_x, d_w, workspace)
-    d_x = _out(d_x, (T, H), x.dtype, x.device, stream)
+    handle = _begin(stream, x, d_h, w, d_x, d_w, workspace)
+    d_x = _out_like(d_x, x, stream)
     d_w = _out(d_w, (H,), torch.float32, x.device, stream)
     if workspace is None:
         workspace = _empty(moe_norm_workspace_size(T, H), torch.uint8, x.device, stream)
     _check(_lib.moe_prenorm_backward(_p(d_h), _p(x), _p(w), T, H, eps, dt, wdt, _p(d_x), _p(d_w), _p(workspace),
-                                     workspace.numel(), _stream(stream)), "moe_prenorm_backward")
+                                     workspace.numel(), handle), "moe_prenorm_backward")
     return d_x, d_w
 
 
+_POSTNORM_RULES: dict = {}  # (the library reads them only)
+
+
 def _postnorm(x, y, post_w, gate, sigmoid, scale, res_scale, next_w, eps):
-    """Checked sizes and the rule of a postnorm: (T, H, type, rule)."""
+    """Checked sizes and the rule of a postnorm, by reference: (T, H, type, kind of gate, rule)."""
     T, H = x.shape
     dt = _act(x, "x")
     if y.shape != (T, H) or y.dtype != x.dtype:
@@ -564,7 +582,13 @@ def _postnorm(x, y, post_w, gate, sigmoid, scale, res_scale, next_w, eps):
         if kind is None:
             raise ValueError("gate must be [H], [T, 1] or [T, H]")
         gdt = _act(gate, "gate")
-    return T, H, dt, moe_postnorm_rule(eps, scale, res_scale, kind, 1 if sigmoid else 0, gdt, wdt)
+    key = (eps, scale, res_scale, kind, bool(sigmoid), gdt, wdt)
+    rule = _POSTNORM_RULES.get(key)
+    if rule is None:
+        if len(_POSTNORM_RULES) >= 256:  # (scales that change from call to call)
+            _POSTNORM_RULES.clear()
+        rule = _POSTNORM_RULES[key] = ctypes.byref(moe_postnorm_rule(*key))
+    return T, H, dt, kind, rule
 
 
 def moe_postnorm(x: torch.Tensor, y: torch.Tensor, post_w=None, gate=None, sigmoid: bool = False, scale: float = 1.0,
@@ -573,15 +597,15 @@ def moe_postnorm(x: torch.Tensor, y: torch.Tensor, post_w=None, gate=None, sigmo
 
     x: the residual [T,H]; y: the block's output; post_w [H] (None: y without a norm); gate [H], [T,1] or [T,H] (None:
     1), through a sigmoid if asked; next_w [H]: the next block's norm (None: h is None).  out may be x or y."""
-    T, H, dt, rule = _postnorm(x, y, post_w, gate, sigmoid, scale, res_scale, next_w, eps)
-    _same_device(x, y, post_w, gate, next_w, out, h)
-    out = _out(out, (T, H), x.dtype, x.device, stream)
+    T, H, dt, _, rule = _postnorm(x, y, post_w, gate, sigmoid, scale, res_scale, next_w, eps)
+    handle = _begin(stream, x, y, post_w, gate, next_w, out, h)
+    out = _out_like(out, x, stream)
     if next_w is not None:
-        h = _out(h, (T, H), x.dtype, x.device, stream)
+        h = _out_like(h, x, stream)
     elif h is not None:
         raise ValueError("h needs next_w")
-    _check(_lib.moe_postnorm(_p(x), _p(y), _p(post_w), _p(gate), _p(next_w), T, H, dt, ctypes.byref(rule), _p(out),
-                             _p(h), _stream(stream)), "moe_postnorm")
+    _check(_lib.moe_postnorm(_p(x), _p(y), _p(post_w), _p(gate), _p(next_w), T, H, dt, rule, _p(out),
+                             _p(h), handle), "moe_postnorm")
     return out, h
 
 
@@ -599,25 +623,25 @@ def moe_postnorm_backward(d_out: Optional[torch.Tensor], d_h: Optional[torch.Ten
                           next_w=None, eps: float = 1e-6, d_x=None, d_y=None, workspace=None,
                           stream=None) -> PostnormGrads:
     """Gradients of moe_postnorm from those of out and h (None: zero)."""
-    T, H, dt, rule = _postnorm(x, y, post_w, gate, sigmoid, scale, res_scale, next_w, eps)
+    T, H, dt, kind, rule = _postnorm(x, y, post_w, gate, sigmoid, scale, res_scale, next_w, eps)
     _like(d_out, (T, H), x.dtype, "d_out")
     _like(d_h, (T, H), x.dtype, "d_h")
     if d_h is not None and next_w is None:
         raise ValueError("d_h needs next_w")
-    _same_device(x, y, post_w, gate, next_w, d_out, d_h, d_x, d_y, workspace)
+    handle = _begin(stream, x, y, post_w, gate, next_w, d_out, d_h, d_x, d_y, workspace)
     dev = x.device
-    d_x = _out(d_x, (T, H), x.dtype, dev, stream)
-    d_y = _out(d_y, (T, H), x.dtype, dev, stream)
+    d_x = _out_like(d_x, x, stream)
+    d_y = _out_like(d_y, x, stream)
     d_post_w = None if post_w is None else _empty((H,), torch.float32, dev, stream)
     d_next_w = None if next_w is None else _empty((H,), torch.float32, dev, stream)
     d_gate = None
     if gate is not None:
-        d_gate = _empty(gate.shape, gate.dtype if rule.gate == GATE_FULL else torch.float32, dev, stream)
+        d_gate = _empty(gate.shape, gate.dtype if kind == GATE_FULL else torch.float32, dev, stream)
     if workspace is None:
         workspace = _empty(moe_norm_workspace_size(T, H), torch.uint8, dev, stream)
     _check(_lib.moe_postnorm_backward(_p(d_out), _p(d_h), _p(x), _p(y), _p(post_w), _p(gate), _p(next_w), T, H, dt,
-                                      ctypes.byref(rule), _p(d_x), _p(d_y), _p(d_post_w), _p(d_gate), _p(d_next_w),
-                                      _p(workspace), workspace.numel(), _stream(stream)), "moe_postnorm_backward")
+                                      rule, _p(d_x), _p(d_y), _p(d_post_w), _p(d_gate), _p(d_next_w),
+                                      _p(workspace), workspace.numel(), handle), "moe_postnorm_backward")
     return PostnormGrads(d_x, d_y, d_post_w, d_gate, d_next_w)
 
 
@@ -647,13 +671,13 @@ def moe_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tenso
         out_dtype = base.dtype
     elif out is not None:
         out_dtype = out.dtype
-    _same_device(x, a, b, ids, scale, base, out, workspace)
-    out = _out(out, (T, N), out_dtype, x.device, stream)
+    handle = _begin(stream, x, a, b, ids, scale, base, out, workspace)
+    out = _out(out, (T, N), out_dtype, x.device, stream) if base is None else _out_like(out, base, stream)
     dt = _act(out, "out")
     if workspace is None:
         workspace = _empty(moe_lora_workspace_size(T, K, N, r, L), torch.uint8, x.device, stream)
     _check(_lib.moe_lora(_p(x), _p(a), _p(b), _p(ids), _p(scale), _p(base), T, K, N, r, L, dt, _p(out), _p(workspace),
-                         workspace.numel(), _stream(stream)), "moe_lora")
+                         workspace.numel(), handle), "moe_lora")
     return out
 
 
