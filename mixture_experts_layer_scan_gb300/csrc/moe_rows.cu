@@ -9,8 +9,10 @@
 // butterfly), each result rounded once.  A pair whose row is outside [0, n_rows) has none: it adds nothing
 // and its weight's gradient is 0.
 //
-// All four are bound by HBM: nothing is read twice.  The scatter reads a token's row once for its k stores.
-// Rows move as vectors of the widest power of two (16 bytes at most) that divides a row.
+// All four are bound by HBM: nothing is read twice from there.  The scatter reads a token's row once for its k stores.
+// Rows of whole 16-byte units move as those.  Other rows begin anywhere: there a thread takes an aligned unit of the row
+// that is written, puts the other row's bytes for it together from the two units that hold them, and goes by
+// elements only at the row's ends (by elements throughout, 9218 x 3 rows of 2475 bf16 took 131 us to sum).
 #include <algorithm>
 
 #include "moe_device.cuh"
@@ -31,16 +33,18 @@ struct RowsDev {
   void* out;
   float* dw;
   int T, k, n_rows;
-  int vpr;                 // vectors per row
+  int vpr;                 // 16-byte vectors per row
   int chunks;              // scatter: runs of 32 * U vectors per row
 };
+
+constexpr int kRowsThreads = 256;
+constexpr int kPadCtas = 152;  // CTAs of a launch that fill the padding
 
 // Rows that hold no pair (sorted[r] >= n_pairs).  A warp looks at up to 32 entries of the list at a time, and at fewer
 // where that spreads the rows over more warps (a decode batch over many experts is mostly padding: 64 tokens of
 // top-8 over 128 experts in blocks of 16 took 15.4 us with 32).
-template <int W>
-__device__ __forceinline__ void zero_padding(const RowsDev& p, int unit, int n_units) {
-  using V = typename Word<W>::type;
+template <typename Zero>
+__device__ __forceinline__ void zero_padding(const RowsDev& p, int unit, int n_units, Zero zero) {
   const int lane = threadIdx.x & 31, npp = min(*p.npp, p.n_rows), n = p.T * p.k;
   const int per = min(32, (npp + n_units - 1) / n_units);
   for (long r0 = (long)unit * per; r0 < npp; r0 += (long)n_units * per) {
@@ -49,29 +53,31 @@ __device__ __forceinline__ void zero_padding(const RowsDev& p, int unit, int n_u
     while (pad) {
       const int b = __ffs(pad) - 1;
       pad &= pad - 1;
-      V z;
-      zero_word(z);
-      V* dst = static_cast<V*>(p.out) + (size_t)(r0 + b) * p.vpr;
-      for (int v = lane; v < p.vpr; v += 32) dst[v] = z;
+      zero((size_t)(r0 + b));
     }
   }
 }
+// The padding's share of a launch's first CTAs, rows of whole units.
+__device__ __forceinline__ bool pad_cta(const RowsDev& p) {
+  const int ctas = p.sorted ? kPadCtas : 0, warps = blockDim.x >> 5;
+  if ((int)blockIdx.x >= ctas) return false;
+  zero_padding(p, blockIdx.x * warps + (threadIdx.x >> 5), ctas * warps, [&](size_t row) {
+    uint4* dst = static_cast<uint4*>(p.out) + row * p.vpr;
+    for (int v = threadIdx.x & 31; v < p.vpr; v += 32) dst[v] = make_uint4(0, 0, 0, 0);
+  });
+  return true;
+}
 
-constexpr int kRowsThreads = 256;
-constexpr int kPadCtas = 152;  // CTAs of a launch that fill the padding
 
 // A warp holds U vectors a lane of one token's row and stores them at the rows of its k pairs.
-template <int W, int U>
+template <int U>
 __global__ void __launch_bounds__(kRowsThreads) k_rows_scatter(const RowsDev p) {
   pdl_enter();
-  using V = typename Word<W>::type;
+  using V = uint4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int warps = kRowsThreads / 32;
+  if (pad_cta(p)) return;
   const int pad_ctas = p.sorted ? kPadCtas : 0;
-  if ((int)blockIdx.x < pad_ctas) {
-    zero_padding<W>(p, blockIdx.x * warps + warp, pad_ctas * warps);
-    return;
-  }
   const long units = (long)p.T * p.chunks;
   for (long u = (long)(blockIdx.x - pad_ctas) * warps + warp; u < units; u += (long)(gridDim.x - pad_ctas) * warps) {
     const int t = (int)(u / p.chunks), v0 = (int)(u % p.chunks) * (32 * U) + lane;
@@ -97,11 +103,11 @@ __global__ void __launch_bounds__(kRowsThreads) k_rows_scatter(const RowsDev p) 
 
 // A thread sums one vector of a token over its rows, kGatherRows of them in flight.
 constexpr int kGatherRows = 8;
-template <typename T, int W>
+template <typename T>
 __global__ void __launch_bounds__(kRowsThreads) k_rows_gather(const RowsDev p) {
   pdl_enter();
-  using V = typename Word<W>::type;
-  constexpr int N = W / sizeof(T);
+  using V = uint4;
+  constexpr int N = 16 / sizeof(T);
   const V* rows = static_cast<const V*>(p.x);
   const int v = blockIdx.y * kRowsThreads + threadIdx.x;
   if (v >= p.vpr) return;
@@ -123,28 +129,25 @@ __global__ void __launch_bounds__(kRowsThreads) k_rows_gather(const RowsDev p) {
       for (int j = 0; j < kGatherRows; ++j) {
         if (j0 + j >= p.k) break;
         float f[N];
-        widen<T, W>(u[j], f);
+        widen<T, 16>(u[j], f);
 #pragma unroll
         for (int c = 0; c < N; ++c) acc[c] = fmaf(wj[j], f[c], acc[c]);
       }
     }
-    static_cast<V*>(p.out)[(size_t)t * p.vpr + v] = narrow<T, W>(acc);
+    static_cast<V*>(p.out)[(size_t)t * p.vpr + v] = narrow<T, 16>(acc);
   }
 }
 
 // Gradient of the weighted sum: a CTA per token, a warp per pair (the pairs' reads of d_out meet in L1).
 constexpr int kGradUnroll = 4;
-template <typename T, int W>
+template <typename T>
 __global__ void __launch_bounds__(kRowsThreads) k_rows_gather_grad(const RowsDev p) {
   pdl_enter();
-  using V = typename Word<W>::type;
-  constexpr int N = W / sizeof(T);
+  using V = uint4;
+  constexpr int N = 16 / sizeof(T);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (pad_cta(p)) return;
   const int pad_ctas = p.sorted ? kPadCtas : 0;
-  if ((int)blockIdx.x < pad_ctas) {
-    zero_padding<W>(p, blockIdx.x * warps + warp, pad_ctas * warps);
-    return;
-  }
   for (int t = blockIdx.x - pad_ctas; t < p.T; t += gridDim.x - pad_ctas) {
     const V* d = static_cast<const V*>(p.x) + (size_t)t * p.vpr;
     for (int j = warp; j < p.k; j += warps) {
@@ -175,14 +178,14 @@ __global__ void __launch_bounds__(kRowsThreads) k_rows_gather_grad(const RowsDev
         for (int i = 0; i < kGradUnroll; ++i) {
           const int v = v0 + 32 * i;
           float fa[N], fb[N];
-          widen<T, W>(a[i], fa);
-          widen<T, W>(b[i], fb);
+          widen<T, 16>(a[i], fa);
+          widen<T, 16>(b[i], fb);
 #pragma unroll
           for (int c = 0; c < N; ++c) {
             dot = fmaf(fa[c], fb[c], dot);
             fa[c] *= wj;
           }
-          if (dst && v < p.vpr) dst[v] = narrow<T, W>(fa);
+          if (dst && v < p.vpr) dst[v] = narrow<T, 16>(fa);
         }
       }
       if (p.dw) {
@@ -194,9 +197,247 @@ __global__ void __launch_bounds__(kRowsThreads) k_rows_gather_grad(const RowsDev
   }
 }
 
-template <int W>
+// ---- rows that are no whole 16-byte units --------------------------------------------------------------
+// The aligned units of a row of a tensor: byte of the first, their number, bytes of the first before the row.
+struct Units {
+  int n, lead, bytes;
+  __device__ __forceinline__ Units(size_t row, size_t row_bytes) : lead((int)((row * row_bytes) & 15)), bytes((int)row_bytes) {
+    n = (lead + bytes + 15) / 16;
+  }
+  __device__ __forceinline__ int from(int u) const { return u * 16 - lead; }  // byte of the row at which unit u begins
+  __device__ __forceinline__ bool whole(int u) const { return from(u) >= 0 && from(u) + 16 <= bytes; }
+};
+
+// Another row's bytes in the units of a row: unit u is 16 bytes from `at` + 16 u on, `sh` bytes further.
+// near_end: some of what those units hold lies outside the tensor, and units are put together by elements.
+template <int E>
+struct Source {
+  const uint8_t *row, *at;
+  uint32_t sh;
+  bool near_end;
+  __device__ __forceinline__ Source(const void* tensor, size_t rows, size_t r, const Units& q) {
+    const uint8_t* begin = static_cast<const uint8_t*>(tensor);
+    row = begin + r * (size_t)q.bytes;
+    const size_t off = r * (size_t)q.bytes + 16;  // (of unit 0, 16 bytes further: not negative)
+    const size_t unit = off - q.lead;
+    sh = (uint32_t)(unit & 15);
+    at = begin + (unit - sh) - 16;
+    near_end = unit - sh < 16 || unit - sh - 16 + 16 * (size_t)(q.n + 1) > rows * (size_t)q.bytes;
+  }
+  // Unit u; what lies outside the row is anything (0 near the tensor's ends).
+  __device__ __forceinline__ uint4 load(const Units& q, int u) const {
+    if (near_end) return by_elements(q, u);
+    const uint4* from = reinterpret_cast<const uint4*>(at) + u;
+    const uint4 a = __ldg(from);
+    if (sh == 0) return a;
+    const uint4 b = __ldg(from + 1);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (sh & 4)
+#pragma unroll
+      for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
+    if (sh & 8)
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 2];
+    if (E == 2 && (sh & 2))
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __noinline__ uint4 by_elements(const Units& q, int u) const {
+    uint32_t w[4] = {0, 0, 0, 0};
+    for (int i = 0; i < 16 / E; ++i) {
+      const int b = q.from(u) + i * E;
+      if (b < 0 || b >= q.bytes) continue;
+      const uint32_t v = *reinterpret_cast<const typename Word<E>::type*>(row + b);
+      const int k = i * E / 4;
+      const uint32_t bits = E == 2 ? v << (16 * (i & 1)) : v;
+      if (k == 0) w[0] |= bits;
+      else if (k == 1) w[1] |= bits;
+      else if (k == 2) w[2] |= bits;
+      else w[3] |= bits;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+template <int E>
+__device__ __forceinline__ void store_unit(uint8_t* row, const Units& q, int u, const uint4& v) {
+  if (q.whole(u)) {
+    *reinterpret_cast<uint4*>(row + q.from(u)) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 16 / E; ++i) {
+    const int b = q.from(u) + i * E;
+    if (b < 0 || b >= q.bytes) continue;
+    *reinterpret_cast<typename Word<E>::type*>(row + b) =
+        (typename Word<E>::type)(E == 2 ? w[i / 2] >> (16 * (i & 1)) : w[i]);
+  }
+}
+
+template <int E>
+__device__ __forceinline__ bool pad_cta_odd(const RowsDev& p, size_t row_bytes) {
+  const int ctas = p.sorted ? kPadCtas : 0, warps = blockDim.x >> 5;
+  if ((int)blockIdx.x >= ctas) return false;
+  zero_padding(p, blockIdx.x * warps + (threadIdx.x >> 5), ctas * warps, [&](size_t row) {
+    const Units q(row, row_bytes);
+    uint8_t* dst = static_cast<uint8_t*>(p.out) + row * row_bytes;
+    for (int u = threadIdx.x & 31; u < q.n; u += 32) store_unit<E>(dst, q, u, make_uint4(0, 0, 0, 0));
+  });
+  return true;
+}
+
+// A warp to a pair.
+template <int E>
+__global__ void __launch_bounds__(kRowsThreads) k_rows_scatter_odd(const RowsDev p, size_t row_bytes) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int warps = kRowsThreads / 32;
+  if (pad_cta_odd<E>(p, row_bytes)) return;
+  const int pad_ctas = p.sorted ? kPadCtas : 0;
+  const long pairs = (long)p.T * p.k;
+  for (long f = (long)(blockIdx.x - pad_ctas) * warps + warp; f < pairs; f += (long)(gridDim.x - pad_ctas) * warps) {
+    const int r = p.row_of[f];
+    if ((unsigned)r >= (unsigned)p.n_rows) continue;
+    const Units q(r, row_bytes);
+    const Source<E> src(p.x, p.T, f / p.k, q);
+    uint8_t* dst = static_cast<uint8_t*>(p.out) + (size_t)r * row_bytes;
+    for (int u0 = lane; u0 < q.n; u0 += 32 * 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (u0 + 32 * i < q.n) v[i] = src.load(q, u0 + 32 * i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (u0 + 32 * i < q.n) store_unit<E>(dst, q, u0 + 32 * i, v[i]);
+    }
+  }
+}
+
+// A thread sums one unit of a token over its rows, four of them in flight.
+template <typename T>
+__global__ void __launch_bounds__(kRowsThreads) k_rows_gather_odd(const RowsDev p, size_t row_bytes) {
+  pdl_enter();
+  constexpr int N = 16 / sizeof(T), kFlight = 4;
+  const int u = blockIdx.y * blockDim.x + threadIdx.x;
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    const Units q(t, row_bytes);
+    if (u >= q.n) continue;
+    const size_t f0 = (size_t)t * p.k;
+    float acc[N] = {};
+    for (int j0 = 0; j0 < p.k; j0 += kFlight) {
+      uint4 y[kFlight];
+      float w[kFlight];
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j) {
+        const int at = j0 + j < p.k ? p.row_of[f0 + j0 + j] : -1;
+        const bool in = (unsigned)at < (unsigned)p.n_rows;
+        w[j] = !in ? 0.f : p.w ? p.w[f0 + j0 + j] : 1.f;
+        y[j] = make_uint4(0, 0, 0, 0);
+        if (in) y[j] = Source<sizeof(T)>(p.x, p.n_rows, at, q).load(q, u);
+      }
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j) {
+        if (j0 + j >= p.k) break;
+        float f[N];
+        widen<T, 16>(y[j], f);
+#pragma unroll
+        for (int c = 0; c < N; ++c) acc[c] = fmaf(w[j], f[c], acc[c]);
+      }
+    }
+    store_unit<sizeof(T)>(static_cast<uint8_t*>(p.out) + (size_t)t * row_bytes, q, u, narrow<T, 16>(acc));
+  }
+}
+
+// A CTA to a token, a warp to a pair, as k_rows_gather_grad.
+template <typename T>
+__global__ void __launch_bounds__(kRowsThreads) k_rows_gather_grad_odd(const RowsDev p, size_t row_bytes) {
+  pdl_enter();
+  constexpr int N = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (pad_cta_odd<sizeof(T)>(p, row_bytes)) return;
+  const int pad_ctas = p.sorted ? kPadCtas : 0;
+  for (int t = blockIdx.x - pad_ctas; t < p.T; t += gridDim.x - pad_ctas) {
+    for (int j = warp; j < p.k; j += warps) {
+      const size_t f = (size_t)t * p.k + j;
+      const int r = p.row_of[f];
+      if ((unsigned)r >= (unsigned)p.n_rows) {
+        if (p.dw && lane == 0) p.dw[f] = 0.f;
+        continue;
+      }
+      const float wj = p.w ? p.w[f] : 1.f;
+      const Units q(r, row_bytes);
+      const Source<sizeof(T)> d(p.x, p.T, t, q), src(p.dw ? p.rows : p.x, p.n_rows, r, q);
+      uint8_t* dst = static_cast<uint8_t*>(p.out) + (size_t)r * row_bytes;
+      float dot = 0.f;
+      for (int u0 = lane; u0 < q.n; u0 += 32 * 2) {
+        uint4 va[2], vb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int u = u0 + 32 * i;
+          va[i] = vb[i] = make_uint4(0, 0, 0, 0);
+          if (u < q.n) {
+            va[i] = d.load(q, u);
+            if (p.dw) vb[i] = src.load(q, u);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int u = u0 + 32 * i;
+          if (u >= q.n) break;
+          float a[N], b[N];
+          widen<T, 16>(va[i], a);
+          widen<T, 16>(vb[i], b);
+          if (!q.whole(u))
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+              const int at = q.from(u) + c * (int)sizeof(T);
+              if (at < 0 || at >= q.bytes) a[c] = b[c] = 0.f;
+            }
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            dot = fmaf(a[c], b[c], dot);
+            a[c] *= wj;
+          }
+          if (p.out) store_unit<sizeof(T)>(dst, q, u, narrow<T, 16>(a));
+        }
+      }
+      if (p.dw) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) p.dw[f] = dot;
+      }
+    }
+  }
+}
+
+cudaError_t scatter_odd(RowsDev& p, size_t row_bytes, int elem, cudaStream_t s) {
+  const long pairs = (long)p.T * p.k;
+  const int ctas = (int)std::min<long>((pairs + 7) / 8, 1 << 20) + (p.sorted ? kPadCtas : 0);
+  if (elem == 2) MOE_LAUNCH(k_rows_scatter_odd<2>, dim3(ctas), dim3(kRowsThreads), 0, s, p, row_bytes);
+  else MOE_LAUNCH(k_rows_scatter_odd<4>, dim3(ctas), dim3(kRowsThreads), 0, s, p, row_bytes);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t gather_odd(RowsDev& p, size_t row_bytes, cudaStream_t s) {
+  const int units = (int)(row_bytes / 16) + 2, cols = (units + kRowsThreads - 1) / kRowsThreads;
+  if (cols > 65535) return cudaErrorInvalidValue;
+  const int threads = ((units + cols - 1) / cols + 31) / 32 * 32;  // (no column of CTAs that is nearly empty)
+  const dim3 grid(std::min(p.T, std::max(1, 152 * 4096 / (threads * cols))), cols);
+  MOE_LAUNCH(k_rows_gather_odd<T>, grid, dim3(threads), 0, s, p, row_bytes);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t gather_grad_odd(RowsDev& p, size_t row_bytes, cudaStream_t s) {
+  const int warps = std::min(p.k, kRowsThreads / 32);
+  const int ctas = std::min(p.T, 1 << 20) + (p.sorted ? kPadCtas : 0);
+  MOE_LAUNCH(k_rows_gather_grad_odd<T>, dim3(ctas), dim3(32 * warps), 0, s, p, row_bytes);
+  return cudaGetLastError();
+}
+
 cudaError_t scatter(RowsDev& p, long row_bytes, cudaStream_t s) {
-  p.vpr = (int)(row_bytes / W);
+  p.vpr = (int)(row_bytes / 16);
   // few rows: one vector a lane, so that they spread over more warps
   const long units4 = (long)p.T * ((p.vpr + 127) / 128);
   const bool few = units4 < 152 * 16;
@@ -204,27 +445,27 @@ cudaError_t scatter(RowsDev& p, long row_bytes, cudaStream_t s) {
   p.chunks = (p.vpr + per - 1) / per;
   const long units = (long)p.T * p.chunks;
   const int ctas = (int)std::min<long>((units + 7) / 8, 1 << 20) + (p.sorted ? kPadCtas : 0);
-  if (few) MOE_LAUNCH((k_rows_scatter<W, 1>), dim3(ctas), dim3(kRowsThreads), 0, s, p);
-  else MOE_LAUNCH((k_rows_scatter<W, 4>), dim3(ctas), dim3(kRowsThreads), 0, s, p);
+  if (few) MOE_LAUNCH((k_rows_scatter<1>), dim3(ctas), dim3(kRowsThreads), 0, s, p);
+  else MOE_LAUNCH((k_rows_scatter<4>), dim3(ctas), dim3(kRowsThreads), 0, s, p);
   return cudaGetLastError();
 }
 
-template <typename T, int W>
+template <typename T>
 cudaError_t gather(RowsDev& p, long row_bytes, cudaStream_t s) {
-  p.vpr = (int)(row_bytes / W);
+  p.vpr = (int)(row_bytes / 16);
   const int cols = (p.vpr + kRowsThreads - 1) / kRowsThreads;
   if (cols > 65535) return cudaErrorInvalidValue;
   const dim3 grid(std::min(p.T, std::max(1, 152 * 16 / cols)), cols);
-  MOE_LAUNCH((k_rows_gather<T, W>), grid, dim3(kRowsThreads), 0, s, p);
+  MOE_LAUNCH((k_rows_gather<T>), grid, dim3(kRowsThreads), 0, s, p);
   return cudaGetLastError();
 }
 
-template <typename T, int W>
+template <typename T>
 cudaError_t gather_grad(RowsDev& p, long row_bytes, cudaStream_t s) {
-  p.vpr = (int)(row_bytes / W);
+  p.vpr = (int)(row_bytes / 16);
   const int warps = std::min(p.k, kRowsThreads / 32);
   const int ctas = std::min(p.T, 1 << 20) + (p.sorted ? kPadCtas : 0);
-  MOE_LAUNCH((k_rows_gather_grad<T, W>), dim3(ctas), dim3(32 * warps), 0, s, p);
+  MOE_LAUNCH((k_rows_gather_grad<T>), dim3(ctas), dim3(32 * warps), 0, s, p);
   return cudaGetLastError();
 }
 
@@ -242,12 +483,7 @@ cudaError_t launch_rows_scatter(const void* x, int T, int H, int k, int elem_byt
   p.k = k;
   p.n_rows = n_rows;
   const long b = (long)H * elem_bytes;
-  switch (row_word(b)) {
-    case 16: return scatter<16>(p, b, s);
-    case 8: return scatter<8>(p, b, s);
-    case 4: return scatter<4>(p, b, s);
-    default: return scatter<2>(p, b, s);
-  }
+  return b % 16 == 0 ? scatter(p, b, s) : scatter_odd(p, b, elem_bytes, s);
 }
 
 cudaError_t launch_rows_gather(const void* rows, int n_rows, const int32_t* row_of, const float* w, int T, int H, int k,
@@ -261,12 +497,8 @@ cudaError_t launch_rows_gather(const void* rows, int n_rows, const int32_t* row_
   p.k = k;
   p.n_rows = n_rows;
   const long b = (long)H * (bf16 ? 2 : 4);
-  switch (row_word(b)) {
-    case 16: return bf16 ? gather<__nv_bfloat16, 16>(p, b, s) : gather<float, 16>(p, b, s);
-    case 8: return bf16 ? gather<__nv_bfloat16, 8>(p, b, s) : gather<float, 8>(p, b, s);
-    case 4: return bf16 ? gather<__nv_bfloat16, 4>(p, b, s) : gather<float, 4>(p, b, s);
-    default: return gather<__nv_bfloat16, 2>(p, b, s);
-  }
+  if (b % 16 == 0) return bf16 ? gather<__nv_bfloat16>(p, b, s) : gather<float>(p, b, s);
+  return bf16 ? gather_odd<__nv_bfloat16>(p, b, s) : gather_odd<float>(p, b, s);
 }
 
 cudaError_t launch_rows_gather_grad(const void* d_out, const void* rows, int n_rows, const int32_t* row_of,
@@ -285,12 +517,8 @@ cudaError_t launch_rows_gather_grad(const void* d_out, const void* rows, int n_r
   p.k = k;
   p.n_rows = n_rows;
   const long b = (long)H * (bf16 ? 2 : 4);
-  switch (row_word(b)) {
-    case 16: return bf16 ? gather_grad<__nv_bfloat16, 16>(p, b, s) : gather_grad<float, 16>(p, b, s);
-    case 8: return bf16 ? gather_grad<__nv_bfloat16, 8>(p, b, s) : gather_grad<float, 8>(p, b, s);
-    case 4: return bf16 ? gather_grad<__nv_bfloat16, 4>(p, b, s) : gather_grad<float, 4>(p, b, s);
-    default: return gather_grad<__nv_bfloat16, 2>(p, b, s);
-  }
+  if (b % 16 == 0) return bf16 ? gather_grad<__nv_bfloat16>(p, b, s) : gather_grad<float>(p, b, s);
+  return bf16 ? gather_grad_odd<__nv_bfloat16>(p, b, s) : gather_grad_odd<float>(p, b, s);
 }
 
 }  // namespace moe

@@ -103,9 +103,4 @@ __device__ __forceinline__ typename Word<W>::type narrow2(const float2 (&f)[(W /
   return narrow<T, W>(g);
 }
 
-// widest vector (bytes) that divides a row
-inline int row_word(long row_bytes) {
-  return row_bytes % 16 == 0 ? 16 : row_bytes % 8 == 0 ? 8 : row_bytes % 4 == 0 ? 4 : 2;
-}
-
 }  // namespace moe
