@@ -202,8 +202,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
 #pragma unroll
     for (int i = 0; i < R::CV; ++i) {
       if (!rows.has(c * R::CV + i)) break;
+      float* at = to + (size_t)rows.vec(c * R::CV + i) * N;
+      if constexpr (N >= 4) {  // (W = 16: H is a multiple of 4)
 #pragma unroll
-      for (int k = 0; k < N; ++k) to[(size_t)rows.vec(c * R::CV + i) * N + k] = R::pick(f, i * N + k);
+        for (int k = 0; k < N; k += 4)
+          *reinterpret_cast<float4*>(at + k) = make_float4(f[(i * N + k) / 2].x, f[(i * N + k) / 2].y, f[(i * N + k) / 2 + 1].x, f[(i * N + k) / 2 + 1].y);
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) at[k] = R::pick(f, i * N + k);
+      }
     }
   };
 #pragma unroll
@@ -232,21 +239,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
   }
 }
 
-// out[z][c] = sum_g part[z][g][c], 32 columns to a CTA, its warps' runs of rows added in their order
+// out[z][c] = sum_g part[z][g][c]: 32 columns to a CTA, the runs of rows of its WARPS warps added in their order.
 struct SumDev {
-  const float* part;
+  const float* part[3];
   float* out[3];
   int rows, H;
 };
-constexpr int kSumWarps = 32;
-__global__ void __launch_bounds__(32 * kSumWarps) k_sum_rows(const SumDev p) {
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) k_sum_rows(const SumDev p) {
   pdl_enter();
-  __shared__ float s[kSumWarps][32];
-  float* out = p.out[blockIdx.y];
-  if (!out) return;
+  __shared__ float s[WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  const float* part = p.part + (size_t)blockIdx.y * p.rows * p.H + c;
-  const int per = (p.rows + kSumWarps - 1) / kSumWarps, g0 = min(p.rows, warp * per), g1 = min(p.rows, g0 + per);
+  const float* part = p.part[blockIdx.y] + c;
+  const int per = (p.rows + WARPS - 1) / WARPS, g0 = min(p.rows, warp * per), g1 = min(p.rows, g0 + per);
   float a = 0.f;
   if (c < p.H) {
 #pragma unroll 16
@@ -257,8 +262,8 @@ __global__ void __launch_bounds__(32 * kSumWarps) k_sum_rows(const SumDev p) {
   if (warp == 0 && c < p.H) {
     a = 0.f;
 #pragma unroll
-    for (int w = 0; w < kSumWarps; ++w) a += s[w][lane];
-    out[c] = a;
+    for (int w = 0; w < WARPS; ++w) a += s[w][lane];
+    p.out[blockIdx.y][c] = a;
   }
 }
 
@@ -312,13 +317,19 @@ cudaError_t launch_norm_grad(const NormArgs& a, cudaStream_t s) {
   else e = vec ? launch_width<float, 16>(p, kind, most, &rows, s) : launch_width<float, 4>(p, kind, most, &rows, s);
   if (e != cudaSuccess || !(p.sum_post || p.sum_next || p.sum_gate)) return e;
   SumDev q = {};
-  q.part = p.part;
-  q.out[0] = a.d_post_w;
-  q.out[1] = a.d_next_w;
-  q.out[2] = p.sum_gate ? static_cast<float*>(a.d_gate) : nullptr;
+  int sums = 0;
+  const size_t plane = (size_t)rows * a.H;
+  float* const out[3] = {a.d_post_w, a.d_next_w, p.sum_gate ? static_cast<float*>(a.d_gate) : nullptr};
+  for (int i = 0; i < 3; ++i)
+    if (out[i]) {
+      q.part[sums] = p.part + i * plane;
+      q.out[sums++] = out[i];
+    }
   q.rows = rows;
   q.H = a.H;
-  MOE_LAUNCH(k_sum_rows, dim3((a.H + 31) / 32, 3), dim3(32 * kSumWarps), 0, s, q);
+  const dim3 grid((a.H + 31) / 32, sums);
+  if (rows <= 64) MOE_LAUNCH(k_sum_rows<4>, grid, dim3(128), 0, s, q);
+  else MOE_LAUNCH(k_sum_rows<16>, grid, dim3(512), 0, s, q);
   return cudaGetLastError();
 }
 
