@@ -7,11 +7,11 @@ namespace {
 
 // The sums' shared memory alternates from row to row: what a row wrote is overwritten behind the next row's barrier.
 // FAST: whole vectors in every thread, and both norms: nothing is asked for each vector.
-template <typename T, int W, int NV, int KIND, bool RING, int THREADS, bool FAST>
+template <typename T, int NV, int KIND, bool RING, int THREADS, bool FAST, bool ODD>
 __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ NormDev p) {
   pdl_enter();
-  using R = Rows<T, W, NV, RING, FAST>;
-  constexpr int C2 = R::C2, CH = R::CHUNKS;
+  using R = Rows<T, NV, RING, FAST, ODD>;
+  constexpr int C2 = R::C2, CH = NV;
   constexpr bool POST = KIND != N_PRE, HOLD = THREADS <= 512;
   const bool post = FAST || p.post_w, next = !POST || FAST || p.next_w;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -100,35 +100,36 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
 }
 
 // (the ring's kernel, or the one without where rows do not fit or are few; the ring's registers decide for both)
-template <typename T, int W, int NV, int KIND, bool RING, int THREADS, bool FAST = false>
+template <typename T, int NV, int KIND, bool RING, int THREADS, bool ODD, bool FAST = false>
 cudaError_t launch_one(NormDev p, cudaStream_t s) {
-  if constexpr (W == 16 && RING && !FAST)
+  if constexpr (RING && !FAST && !ODD)
     if (p.H % (32 * kElems) == 0 && (KIND == N_PRE || (p.post_w && p.next_w)))
-      return launch_one<T, W, NV, KIND, RING, THREADS, true>(p, s);
+      return launch_one<T, NV, KIND, RING, THREADS, ODD, true>(p, s);
   static int known[64] = {};
-  auto kernel = k_norm<T, W, NV, KIND, RING, THREADS, FAST>;
+  auto kernel = k_norm<T, NV, KIND, RING, THREADS, FAST, ODD>;
   const int regs = norm_regs(kernel, known);
   if (!regs) return cudaErrorInvalidValue;
-  const NormShape q = norm_shape<T, W>(p, regs, NV * (W / (int)sizeof(T)), p.T, RING);
+  const NormShape q = norm_shape<T>(p, regs, NV * (16 / (int)sizeof(T)), p.T, RING);
   if constexpr (RING)
-    if (!p.stages) return launch_one<T, W, NV, KIND, false, THREADS>(p, s);
+    if (!p.stages) return launch_one<T, NV, KIND, false, THREADS, ODD>(p, s);
   MOE_LAUNCH(kernel, dim3(q.grid), dim3(q.threads), q.smem, s, p);
   return cudaGetLastError();
 }
 
-template <typename T, int W, int KIND>
+template <typename T, int KIND, bool ODD>
 cudaError_t launch_kind(const NormDev& p, cudaStream_t s) {
-  constexpr int N = W / sizeof(T);
-  if constexpr (W == 16)
-    if (p.T <= 304 && p.H <= 512 * 8) return launch_one<T, W, 8 / N, KIND, false, 512>(p, s);
-  return p.H > 512 * kElems ? launch_one<T, W, kElems / N, KIND, false, 1024>(p, s)
-                            : launch_one<T, W, kElems / N, KIND, true, 512>(p, s);
+  constexpr int N = 16 / sizeof(T);
+  const int elems = norm_elems(p.H, N);
+  if constexpr (!ODD)
+    if (p.T <= 304 && elems <= 512 * 8) return launch_one<T, 8 / N, KIND, false, 512, ODD>(p, s);
+  return elems > 512 * kElems ? launch_one<T, long_elems(ODD) / N, KIND, false, long_threads(ODD), ODD>(p, s)
+                              : launch_one<T, kElems / N, KIND, true, 512, ODD>(p, s);
 }
-template <typename T, int W>
+template <typename T, bool ODD>
 cudaError_t launch_width(const NormDev& p, int kind, cudaStream_t s) {
-  return kind == N_PRE ? launch_kind<T, W, N_PRE>(p, s)
-         : kind == N_POST ? launch_kind<T, W, N_POST>(p, s)
-                          : launch_kind<T, W, N_FULL>(p, s);
+  return kind == N_PRE ? launch_kind<T, N_PRE, ODD>(p, s)
+         : kind == N_POST ? launch_kind<T, N_POST, ODD>(p, s)
+                          : launch_kind<T, N_FULL, ODD>(p, s);
 }
 
 }  // namespace
@@ -168,9 +169,9 @@ NormDev norm_dev(const NormArgs& a) {
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
   const NormDev p = norm_dev(a);
   const int kind = !a.y ? N_PRE : a.rule.gate == MOE_GATE_FULL ? N_FULL : N_POST;
-  const bool vec = (long)a.H * (a.bf16 ? 2 : 4) % 16 == 0;
-  if (a.bf16) return vec ? launch_width<__nv_bfloat16, 16>(p, kind, s) : launch_width<__nv_bfloat16, 2>(p, kind, s);
-  return vec ? launch_width<float, 16>(p, kind, s) : launch_width<float, 4>(p, kind, s);
+  const bool odd = (long)a.H * (a.bf16 ? 2 : 4) % 16 != 0;
+  if (a.bf16) return odd ? launch_width<__nv_bfloat16, true>(p, kind, s) : launch_width<__nv_bfloat16, false>(p, kind, s);
+  return odd ? launch_width<float, true>(p, kind, s) : launch_width<float, false>(p, kind, s);
 }
 
 }  // namespace moe

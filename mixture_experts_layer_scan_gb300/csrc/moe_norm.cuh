@@ -25,8 +25,9 @@
 // told apart there, 16384 x 4096 took 35 of them for an element.  So a thread keeps its columns' weights in
 // registers (the norm's after the block times a gate by channels as one factor), works on pairs (f32x2), and
 // the gradients of that norm's weight and of such a gate are one sum times the other factor.
-// Rows that are no whole 16 bytes are copied with the neighbours' bytes around them (the last one without what
-// would lie behind the tensor).  Where two rows do not fit, they are read from memory each time.
+// Rows that are no whole 16-byte units are taken in the aligned units that hold them, which every stream and result of
+// a row share; a CTA's rows all begin at the same place in a unit (the grid is a multiple of 8), so that a
+// thread's columns stay the same.  Where two rows do not fit into a ring, they are read from memory each time.
 #pragma once
 #include <algorithm>
 
@@ -118,28 +119,26 @@ struct NormDev {
   int* status;
 };
 
-// The rows of a CTA, in turn, NV vectors of W bytes to a thread (vectors i, i + blockDim, ...): from a ring in shared
-// memory (RING) or from memory.  A thread's E elements are E / 2 pairs; those behind the row's end are 0.  FULL_ROWS: every thread has all of its vectors.
-template <typename T, int W, int NV, bool RING, bool FULL_ROWS>
+// The rows of a CTA, in turn, NV units of 16 bytes to a thread (units i, i + blockDim, ...): from a ring in shared
+// memory (RING) or from memory.  A unit is N elements, C2 pairs; elements outside the row are 0.  FULL_ROWS: every
+// thread has all of its units.  ODD: rows begin `lead` elements into their first unit.
+template <typename T, int NV, bool RING, bool FULL_ROWS, bool ODD>
 struct Rows {
-  using V = typename Word<W>::type;
-  static constexpr int N = W / sizeof(T), E = NV * N;
-  static constexpr int CV = N == 1 ? 8 : 1, CE = CV * N, C2 = CE / 2, CHUNKS = NV / CV;  // vectors, elements, pairs
-  static_assert(CE % 2 == 0 && NV % CV == 0, "whole chunks of pairs");
+  static constexpr int N = 16 / sizeof(T), C2 = N / 2;
   const NormDev& p;
   uint32_t buf, bars;
   volatile int* abort;
-  int vpr, k, stage;             // vectors of a row; rows so far; the present one's place
-  uint32_t phase, shift, whole;  // shift: of the row in its copy; whole: bytes of the copy
+  int lead, units, k, stage;     // units of a row; rows so far; the present one's place
+  uint32_t phase, first;         // first: this thread's first unit in the present stage
   size_t at;                     // element offset of the present row
-  bool ok, refilled, tail;       // tail: the copy leaves out the row's end
+  bool ok, refilled, tail;       // tail: the copy leaves out the row's last unit
   float token;                   // the next row's gate
   int place[S_MAX];              // of a stream among those of a stage
-  uint32_t first;                // this thread's first vector in the present stage
 
   __device__ __forceinline__ Rows(const NormDev& q, uint8_t* smem)
-      : p(q), vpr(q.H / N), k(0), stage(0), phase(0), shift(0), whole(0), at(0), ok(true), refilled(false),
-        tail(false), token(1.0f) {
+      : p(q), lead(0), k(0), stage(0), phase(0), first(0), at(0), ok(true), refilled(false), tail(false), token(1.0f) {
+    if (ODD) lead = (int)((size_t)blockIdx.x * p.H % N);
+    units = (lead + p.H + N - 1) / N;
     if constexpr (RING) {
       abort = reinterpret_cast<volatile int*>(smem);
       bars = smem_u32(smem) + 16;
@@ -154,15 +153,18 @@ struct Rows {
       }
     }
   }
-  __device__ __forceinline__ int vec(int i) const { return threadIdx.x + i * blockDim.x; }
-  __device__ __forceinline__ bool has(int i) const { return FULL_ROWS || vec(i) < vpr; }
-  // The 16-byte units around row t: first byte and their number of bytes.
+  __device__ __forceinline__ int unit(int i) const { return threadIdx.x + i * blockDim.x; }
+  __device__ __forceinline__ bool has(int i) const { return FULL_ROWS || unit(i) < units; }
+  __device__ __forceinline__ int column(int i) const { return unit(i) * N - lead; }  // of a unit's first element
+  __device__ __forceinline__ bool inside(int i, int c) const { return !ODD || (unsigned)(column(i) + c) < (unsigned)p.H; }
+  __device__ __forceinline__ bool whole(int i) const { return !ODD || (column(i) >= 0 && column(i) + N <= p.H); }
+  // The units of row t that a copy takes: first byte and their bytes.
   __device__ __forceinline__ void extent(int t, size_t& from, uint32_t& n) const {
     const size_t row = (size_t)p.H * sizeof(T), begin = (size_t)t * row, end = begin + row;
     from = begin & ~(size_t)15;
     const size_t up = (end + 15) & ~(size_t)15;
     // (nothing behind the tensor is read: a row whose end the copy leaves out comes from memory)
-    const size_t till = W == 16 || up <= (size_t)p.T * row ? up : end & ~(size_t)15;
+    const size_t till = !ODD || up <= (size_t)p.T * row ? up : end & ~(size_t)15;
     n = till > from ? (uint32_t)(till - from) : 0;
   }
   __device__ __forceinline__ void issue(int t, int s) {  // (one thread)
@@ -189,12 +191,12 @@ struct Rows {
     if constexpr (RING) {
       refilled = false;
       if (ok) ok = mbar_wait_one(bars + 8 * stage, phase, abort, p.status);
-      first = buf + (uint32_t)(stage * p.streams) * p.pitch + threadIdx.x * W;
-      if (W < 16) {
+      first = buf + (uint32_t)(stage * p.streams) * p.pitch + threadIdx.x * 16;
+      if (ODD) {
         size_t from;
-        extent(t, from, whole);
-        shift = (uint32_t)(at * sizeof(T) - from);
-        tail = shift + (uint32_t)p.H * sizeof(T) > whole;
+        uint32_t n;
+        extent(t, from, n);
+        tail = n < (uint32_t)units * 16;
       }
     }
   }
@@ -231,89 +233,109 @@ struct Rows {
         mbar_wait_drain(bars + 8 * i, 1, 50000000ull);
       }
   }
-  __device__ __forceinline__ V from_memory(int s, int i) const {
-    return reinterpret_cast<const V*>(static_cast<const T*>(p.stream[s]) + at)[vec(i)];
-  }
-  __device__ __forceinline__ V from_ring(int s, int i) const {
-    const uint32_t from = first + (uint32_t)place[s] * p.pitch + (W < 16 ? shift : 0u) + (uint32_t)(i * blockDim.x) * W;
-    V v;
-    if constexpr (W == 16) v = lds_v4(from);
-    else if constexpr (W == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(from) : "memory");
-    else asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(from) : "memory");
-    return v;
+  __device__ __forceinline__ uint4 from_memory(int s, int i) const {
+    const T* base = static_cast<const T*>(p.stream[s]);
+    if (!ODD || at - lead + (size_t)(unit(i) + 1) * N <= (size_t)p.T * p.H)
+      return *reinterpret_cast<const uint4*>(base + (at - lead) + (size_t)unit(i) * N);
+    float f[N];  // (the tensor ends in this unit)
+#pragma unroll
+    for (int c = 0; c < N; ++c) f[c] = inside(i, c) ? to_f32(base[at + column(i) + c]) : 0.f;
+    return narrow<T, 16>(f);
   }
   __device__ __forceinline__ static void put(float2 (&f)[C2], int e, float v) {  // (e known at compile time)
     if (e & 1) f[e / 2].y = v;
     else f[e / 2].x = v;
   }
   __device__ __forceinline__ static float pick(const float2 (&f)[C2], int e) { return e & 1 ? f[e / 2].y : f[e / 2].x; }
-  __device__ __forceinline__ void load(int s, int chunk, float2 (&f)[C2]) const {
-    V v[CV];
+  __device__ __forceinline__ void load(int s, int i, float2 (&f)[C2]) const {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (RING && !(ODD && tail)) {
+      if (has(i)) v = lds_v4(first + (uint32_t)place[s] * p.pitch + (uint32_t)(i * blockDim.x) * 16);
+    } else {
+      if (has(i)) v = from_memory(s, i);
+    }
+    float g[N];
+    widen<T, 16>(v, g);
 #pragma unroll
-    for (int i = 0; i < CV; ++i) zero_word(v[i]);
-    if (RING && (W == 16 || !tail)) {
+    for (int c = 0; c < N; ++c) put(f, c, g[c]);
+    if constexpr (ODD)
+      if (!whole(i)) {
 #pragma unroll
-      for (int i = 0; i < CV; ++i)
-        if (has(chunk * CV + i)) v[i] = from_ring(s, chunk * CV + i);
+        for (int c = 0; c < N; ++c)
+          if (!inside(i, c)) put(f, c, 0.f);
+      }
+  }
+  __device__ __forceinline__ void store(void* base, int i, const float2 (&f)[C2]) const {
+    if (!has(i)) return;
+    float g[N];
+#pragma unroll
+    for (int c = 0; c < N; ++c) g[c] = pick(f, c);
+    T* to = static_cast<T*>(base) + at;
+    if (whole(i)) {
+      *reinterpret_cast<uint4*>(to + column(i)) = narrow<T, 16>(g);
     } else {
 #pragma unroll
-      for (int i = 0; i < CV; ++i)
-        if (has(chunk * CV + i)) v[i] = from_memory(s, chunk * CV + i);
-    }
-#pragma unroll
-    for (int i = 0; i < CV; ++i) {
-      float g[N];
-      widen<T, W>(v[i], g);
-#pragma unroll
-      for (int c = 0; c < N; ++c) put(f, i * N + c, g[c]);
+      for (int c = 0; c < N; ++c)
+        if (inside(i, c)) {
+          if constexpr (sizeof(T) == 4) to[column(i) + c] = g[c];
+          else to[column(i) + c] = __float2bfloat16_rn(g[c]);
+        }
     }
   }
-  __device__ __forceinline__ void store(void* base, int chunk, const float2 (&f)[C2]) const {
+  // N fp32 values of the unit's columns
+  __device__ __forceinline__ void store_f32(float* to, int i, const float2 (&f)[C2]) const {
+    if (!has(i)) return;
+    if constexpr (!ODD) {
 #pragma unroll
-    for (int i = 0; i < CV; ++i) {
-      if (!has(chunk * CV + i)) break;
-      float g[N];
+      for (int c = 0; c < N; c += 4)
+        *reinterpret_cast<float4*>(to + column(i) + c) = make_float4(f[c / 2].x, f[c / 2].y, f[c / 2 + 1].x, f[c / 2 + 1].y);
+    } else {
 #pragma unroll
-      for (int c = 0; c < N; ++c) g[c] = pick(f, i * N + c);
-      reinterpret_cast<V*>(static_cast<T*>(base) + at)[vec(chunk * CV + i)] = narrow<T, W>(g);
+      for (int c = 0; c < N; ++c)
+        if (inside(i, c)) to[column(i) + c] = pick(f, c);
     }
   }
-  // A weight (or gate) of the thread's columns, from element `from` on.
-  __device__ __forceinline__ void weight(const void* w, bool f32, size_t from, int chunk, float2 (&f)[C2]) const {
+  // A weight (or gate) of the unit's columns, from element `from` on.
+  __device__ __forceinline__ void weight(const void* w, bool f32, size_t from, int i, float2 (&f)[C2]) const {
+    float g[N];
 #pragma unroll
-    for (int i = 0; i < CV; ++i) {
-      float g[N];
+    for (int c = 0; c < N; ++c) g[c] = 0.f;
+    if (has(i)) {
+      if constexpr (!ODD) {
+        load_w<N>(w, f32, from + column(i), g);
+      } else {
 #pragma unroll
-      for (int c = 0; c < N; ++c) g[c] = 0.f;
-      if (has(chunk * CV + i)) load_w<N>(w, f32, from + (size_t)vec(chunk * CV + i) * N, g);
-#pragma unroll
-      for (int c = 0; c < N; ++c) put(f, i * N + c, g[c]);
+        for (int c = 0; c < N; ++c)
+          if (inside(i, c)) g[c] = load_one(w, f32, from + column(i) + c);
+      }
     }
+#pragma unroll
+    for (int c = 0; c < N; ++c) put(f, c, g[c]);
   }
   __device__ __forceinline__ void squash(float2 (&g)[C2]) const {
     if (p.sigmoid)
 #pragma unroll
       for (int e = 0; e < C2; ++e) g[e] = make_float2(sigmoid<T>(g[e].x), sigmoid<T>(g[e].y));
   }
-  __device__ __forceinline__ void channel_gate(int chunk, float2 (&g)[C2]) const {
-    weight(p.gate, p.gate_f32, 0, chunk, g);
+  __device__ __forceinline__ void channel_gate(int i, float2 (&g)[C2]) const {
+    weight(p.gate, p.gate_f32, 0, i, g);
     squash(g);
   }
   // The factor of the columns after the block: post_w times a gate by channels (1 where there is neither).
-  __device__ __forceinline__ void factor(int chunk, float2 (&f)[C2]) const {
+  __device__ __forceinline__ void factor(int i, float2 (&f)[C2]) const {
 #pragma unroll
     for (int e = 0; e < C2; ++e) f[e] = both(1.f);
-    if (p.post_w) weight(p.post_w, p.w_f32, 0, chunk, f);
+    if (p.post_w) weight(p.post_w, p.w_f32, 0, i, f);
     if (p.gate_kind == MOE_GATE_CHANNEL) {
       float2 g[C2];
-      channel_gate(chunk, g);
+      channel_gate(i, g);
 #pragma unroll
       for (int e = 0; e < C2; ++e) f[e] = mul2(f[e], g[e]);
     }
   }
-  __device__ __forceinline__ void full_gate(int chunk, float2 (&g)[C2]) const {
-    if (p.gate_ring) load(S_GATE, chunk, g);
-    else weight(p.stream[S_GATE], p.gate_f32, at, chunk, g);
+  __device__ __forceinline__ void full_gate(int i, float2 (&g)[C2]) const {
+    if (p.gate_ring) load(S_GATE, i, g);
+    else weight(p.stream[S_GATE], p.gate_f32, at, i, g);
     squash(g);
   }
   // A token's gate, loaded a row ahead.
@@ -333,7 +355,12 @@ enum { N_PRE = 0, N_POST, N_FULL };
 
 // Elements of a thread: 16; for few forward rows 8 (a row is over sooner: one of 4096 1.6 us instead of 1.8).
 constexpr int kElems = 16;
-inline int norm_threads(int H, int per) { return std::max(32, ((H + per - 1) / per + 31) / 32 * 32); }
+// ... and threads of a row that 512 of them do not hold (1024 of 16 would not hold the units of 16383 elements).
+constexpr int long_elems(bool odd) { return odd ? 24 : kElems; }
+constexpr int long_threads(bool odd) { return odd ? 704 : 1024; }
+inline int norm_threads(int elems, int per) { return std::max(32, ((elems + per - 1) / per + 31) / 32 * 32); }
+// Elements of the units that may hold a row
+inline int norm_elems(int H, int n) { return H % n ? H + 2 * n - 2 : H; }
 // CTAs of an SM that `regs` registers a thread leave room for
 inline int norm_ctas(int threads, int regs) { return std::max(1, std::min(16, 65536 / ((regs + 7) / 8 * 8 * threads))); }
 
@@ -353,17 +380,17 @@ struct NormShape {
   int threads, grid;
   size_t smem;
 };
-template <typename T, int W>
+template <typename T>
 NormShape norm_shape(NormDev& p, int regs, int per, int most, bool ring) {
+  constexpr int N = 16 / sizeof(T);
   NormShape q;
-  q.threads = norm_threads(p.H, per);
+  q.threads = norm_threads(norm_elems(p.H, N), per);
   int ctas = norm_ctas(q.threads, regs);
   q.smem = 0;
   p.gate_ring = p.gate_ring && ring;
   p.streams = 0;
   for (int i = 0; i < S_MAX; ++i) p.streams += p.stream[i] && (i != S_GATE || p.gate_ring);
-  const size_t row = (size_t)p.H * sizeof(T);
-  p.pitch = (uint32_t)(W == 16 ? row : (row + 30) / 16 * 16);
+  p.pitch = (uint32_t)((norm_elems(p.H, N) + N - 1) / N * 16);
   p.stages = 0;
   // (few CTAs with a ring rather than many without; rows that come about one to a CTA need none)
   if (ring && p.T > 152 * ctas)
@@ -373,6 +400,7 @@ NormShape norm_shape(NormDev& p, int regs, int per, int most, bool ring) {
       if (p.stages || c == 1) break;
     }
   q.grid = std::min(std::min(p.T, most), 152 * ctas);
+  if (q.grid < p.T && q.grid >= 8) q.grid &= ~7;  // (a CTA's rows begin at the same place in a unit)
   return q;
 }
 // Registers of a kernel, and its shared memory raised, once for each device.

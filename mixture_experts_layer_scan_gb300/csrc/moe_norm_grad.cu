@@ -8,11 +8,11 @@ namespace {
 // With z = scale G D (G a token's gate) and cw the columns' factor: d_post_w = sum_t z gate n and d_gate = sum_t z n post_w.
 // For a gate by channels both are sum_t z n times the other factor, and one sum is kept.
 // FAST: whole vectors in every thread, both norms and both incoming gradients: nothing is asked for each vector.
-template <typename T, int W, int NV, int KIND, bool RING, int THREADS, bool FAST>
+template <typename T, int NV, int KIND, bool RING, int THREADS, bool FAST, bool ODD>
 __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant__ NormDev p) {
   pdl_enter();
-  using R = Rows<T, W, NV, RING, FAST>;
-  constexpr int N = R::N, C2 = R::C2, CH = R::CHUNKS, CP = KIND != N_PRE ? CH : 1;
+  using R = Rows<T, NV, RING, FAST, ODD>;
+  constexpr int N = R::N, C2 = R::C2, CH = NV, CP = KIND != N_PRE ? CH : 1;
   constexpr bool POST = KIND != N_PRE, FULL = KIND == N_FULL, HOLD = THREADS <= 512;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float sums[2][2][THREADS / 4];
@@ -173,19 +173,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
         rows.store(p.d_y, c, D);
         if constexpr (FULL) {
           if (p.d_gate) {
+            if (p.gate_f32 == (sizeof(T) == 4)) {
+              rows.store(p.d_gate, c, x);
+            } else if (rows.has(c)) {  // (a gate of the other type)
 #pragma unroll
-            for (int i = 0; i < R::CV; ++i) {
-              if (!rows.has(c * R::CV + i)) break;
-              float f[N];
-#pragma unroll
-              for (int k = 0; k < N; ++k) f[k] = R::pick(x, i * N + k);
-              const size_t to = rows.at + (size_t)rows.vec(c * R::CV + i) * N;
-              if (p.gate_f32) {
-#pragma unroll
-                for (int k = 0; k < N; ++k) static_cast<float*>(p.d_gate)[to + k] = f[k];
-              } else {
-                using G = typename Word<N * 2>::type;
-                *reinterpret_cast<G*>(static_cast<uint16_t*>(p.d_gate) + to) = narrow<__nv_bfloat16, N * 2>(f);
+              for (int k = 0; k < N; ++k) {
+                if (!rows.inside(c, k)) continue;
+                const size_t to = rows.at + rows.column(c) + k;
+                if (p.gate_f32) static_cast<float*>(p.d_gate)[to] = R::pick(x, k);
+                else static_cast<__nv_bfloat16*>(p.d_gate)[to] = __float2bfloat16_rn(R::pick(x, k));
               }
             }
           }
@@ -198,24 +194,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
   // partial sums
   const size_t plane = (size_t)gridDim.x * p.H;
   float* part = p.part + (size_t)blockIdx.x * p.H;
-  auto store = [&](float* to, int c, const float2 (&f)[C2]) {
-#pragma unroll
-    for (int i = 0; i < R::CV; ++i) {
-      if (!rows.has(c * R::CV + i)) break;
-      float* at = to + (size_t)rows.vec(c * R::CV + i) * N;
-      if constexpr (N >= 4) {  // (W = 16: H is a multiple of 4)
-#pragma unroll
-        for (int k = 0; k < N; k += 4)
-          *reinterpret_cast<float4*>(at + k) = make_float4(f[(i * N + k) / 2].x, f[(i * N + k) / 2].y, f[(i * N + k) / 2 + 1].x, f[(i * N + k) / 2 + 1].y);
-      } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) at[k] = R::pick(f, i * N + k);
-      }
-    }
-  };
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    if (p.sum_next) store(part + plane, c, acc_n[c]);
+    if (p.sum_next) rows.store_f32(part + plane, c, acc_n[c]);
     if constexpr (POST) {
       float2 f[C2], g[C2];
       if (p.gate_kind == MOE_GATE_CHANNEL) rows.channel_gate(c, g);
@@ -228,12 +209,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
           f[i] = mul2(f[i], acc_s[c][i]);
           if (p.sigmoid) f[i] = mul2(f[i], make_float2(g[i].x * (1.0f - g[i].x), g[i].y * (1.0f - g[i].y)));
         }
-        store(part + 2 * plane, c, f);
+        rows.store_f32(part + 2 * plane, c, f);
       }
       if (p.sum_post) {
 #pragma unroll
         for (int i = 0; i < C2; ++i) f[i] = p.gate_kind == MOE_GATE_CHANNEL ? mul2(acc_s[c][i], g[i]) : acc_s[c][i];
-        store(part, c, f);
+        rows.store_f32(part, c, f);
       }
     }
   }
@@ -267,34 +248,35 @@ __global__ void __launch_bounds__(32 * WARPS) k_sum_rows(const SumDev p) {
   }
 }
 
-template <typename T, int W, int NV, int KIND, bool RING, int THREADS, bool FAST = false>
+template <typename T, int NV, int KIND, bool RING, int THREADS, bool ODD, bool FAST = false>
 cudaError_t launch_one(NormDev p, int most, int* grid, cudaStream_t s) {
-  if constexpr (W == 16 && RING && !FAST)
+  if constexpr (RING && !FAST && !ODD)
     if (p.H % (32 * kElems) == 0 && p.stream[S_DH] && (KIND == N_PRE || (p.post_w && p.stream[S_DOUT])))
-      return launch_one<T, W, NV, KIND, RING, THREADS, true>(p, most, grid, s);
+      return launch_one<T, NV, KIND, RING, THREADS, ODD, true>(p, most, grid, s);
   static int known[64] = {};
-  auto kernel = k_norm_grad<T, W, NV, KIND, RING, THREADS, FAST>;
+  auto kernel = k_norm_grad<T, NV, KIND, RING, THREADS, FAST, ODD>;
   const int regs = norm_regs(kernel, known);
   if (!regs) return cudaErrorInvalidValue;
-  const NormShape q = norm_shape<T, W>(p, regs, kElems, most, RING);
+  const NormShape q = norm_shape<T>(p, regs, NV * (16 / (int)sizeof(T)), most, RING);
   if constexpr (RING)
-    if (!p.stages) return launch_one<T, W, NV, KIND, false, THREADS>(p, most, grid, s);
+    if (!p.stages) return launch_one<T, NV, KIND, false, THREADS, ODD>(p, most, grid, s);
   *grid = q.grid;
   MOE_LAUNCH(kernel, dim3(q.grid), dim3(q.threads), q.smem, s, p);
   return cudaGetLastError();
 }
 
-template <typename T, int W, int KIND>
+template <typename T, int KIND, bool ODD>
 cudaError_t launch_kind(const NormDev& p, int most, int* grid, cudaStream_t s) {
-  constexpr int NV = kElems / (W / sizeof(T));
-  return p.H > 512 * kElems ? launch_one<T, W, NV, KIND, false, 1024>(p, most, grid, s)
-                            : launch_one<T, W, NV, KIND, true, 512>(p, most, grid, s);
+  constexpr int N = 16 / sizeof(T), NV = kElems / N;
+  const int elems = norm_elems(p.H, N);
+  return elems > 512 * kElems ? launch_one<T, long_elems(ODD) / N, KIND, false, long_threads(ODD), ODD>(p, most, grid, s)
+                              : launch_one<T, NV, KIND, true, 512, ODD>(p, most, grid, s);
 }
-template <typename T, int W>
+template <typename T, bool ODD>
 cudaError_t launch_width(const NormDev& p, int kind, int most, int* grid, cudaStream_t s) {
-  return kind == N_PRE ? launch_kind<T, W, N_PRE>(p, most, grid, s)
-         : kind == N_POST ? launch_kind<T, W, N_POST>(p, most, grid, s)
-                          : launch_kind<T, W, N_FULL>(p, most, grid, s);
+  return kind == N_PRE ? launch_kind<T, N_PRE, ODD>(p, most, grid, s)
+         : kind == N_POST ? launch_kind<T, N_POST, ODD>(p, most, grid, s)
+                          : launch_kind<T, N_FULL, ODD>(p, most, grid, s);
 }
 
 }  // namespace
@@ -309,12 +291,12 @@ cudaError_t launch_norm_grad(const NormArgs& a, cudaStream_t s) {
   p.sum_next = a.d_next_w != nullptr;
   p.sum_gate = a.rule.gate == MOE_GATE_CHANNEL && a.d_gate;
   const int kind = !a.y ? N_PRE : a.rule.gate == MOE_GATE_FULL ? N_FULL : N_POST;
-  const bool vec = (long)a.H * (a.bf16 ? 2 : 4) % 16 == 0;
+  const bool odd = (long)a.H * (a.bf16 ? 2 : 4) % 16 != 0;
   const int most = norm_grad_rows(a.T, a.H);
   int rows = 0;
   cudaError_t e;
-  if (a.bf16) e = vec ? launch_width<__nv_bfloat16, 16>(p, kind, most, &rows, s) : launch_width<__nv_bfloat16, 2>(p, kind, most, &rows, s);
-  else e = vec ? launch_width<float, 16>(p, kind, most, &rows, s) : launch_width<float, 4>(p, kind, most, &rows, s);
+  if (a.bf16) e = odd ? launch_width<__nv_bfloat16, true>(p, kind, most, &rows, s) : launch_width<__nv_bfloat16, false>(p, kind, most, &rows, s);
+  else e = odd ? launch_width<float, true>(p, kind, most, &rows, s) : launch_width<float, false>(p, kind, most, &rows, s);
   if (e != cudaSuccess || !(p.sum_post || p.sum_next || p.sum_gate)) return e;
   SumDev q = {};
   int sums = 0;

@@ -300,3 +300,35 @@ def test_residual_that_cancels(moe, T, H):
         n = d["y"].double() * rstd(d["y"].double()) * d["post_w"].double()
         d["x"] = (small * d["x"].double() - d["gate"].double() * n).float()
         check_all(moe, d, False, 1.0, 1.0, f"normed {small}", T, eps=EPS)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(9, 16383), (170, 8190), (9, 8187), (330, 8179), (350, 4093), (5000, 5), (13, 3)])
+def test_rows_that_share_units(moe, T, H, dtype):
+    """Rows that begin and end inside a 16-byte unit, with the neighbours' elements around them: the longest, those at
+    the turn from one form to the next, and rows of less than one unit."""
+    g = torch.Generator().manual_seed(T + H)
+    for gate in ("channel", "full"):
+        check_all(moe, inputs(T, H, DT[dtype], torch.float32, g, True, gate, True), gate == "full", 0.5, 1.25, f"{T} x {H} {gate}", T)
+
+
+@pytest.mark.parametrize("T,H", [(11, 1023), (700, 2045), (3000, 6)])
+def test_bad_values_stay_in_their_row(moe, T, H):
+    """NaN and infinities in every third row reach no other row's results."""
+    g = torch.Generator().manual_seed(T)
+    d = {n: cuda(v) for n, v in inputs(T, H, torch.bfloat16, torch.float32, g, True, "full", True).items()}
+    kw = dict(post_w=d["post_w"], sigmoid=True, next_w=d["next_w"], eps=EPS)
+    bad = {n: d[n].clone() for n in ("x", "y", "gate", "d_out", "d_h")}
+    for i, n in enumerate(("x", "y", "d_out", "d_h")):
+        bad[n][i % 3::3] = float("nan") if i % 2 else float("inf")
+        keep = torch.ones(T, dtype=torch.bool, device="cuda")
+        keep[i % 3::3] = False
+        new = {**{k: d[k] for k in bad}, n: bad[n]}
+        for a, b in zip(moe.moe_postnorm(d["x"], d["y"], gate=d["gate"], **kw),
+                        moe.moe_postnorm(new["x"], new["y"], gate=new["gate"], **kw)):
+            assert torch.equal(a[keep], b[keep])
+        ga = moe.moe_postnorm_backward(d["d_out"], d["d_h"], d["x"], d["y"], gate=d["gate"], **kw)
+        gb = moe.moe_postnorm_backward(new["d_out"], new["d_h"], new["x"], new["y"], gate=new["gate"], **kw)
+        for k in ("d_x", "d_y", "d_gate"):
+            assert torch.equal(getattr(ga, k)[keep], getattr(gb, k)[keep]), (n, k)
+    assert moe.moe_get_status() == 0
