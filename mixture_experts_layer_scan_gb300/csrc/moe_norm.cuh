@@ -128,17 +128,31 @@ struct Rows {
   const NormDev& p;
   uint32_t buf, bars;
   volatile int* abort;
-  int lead, units, k, stage;     // units of a row; rows so far; the present one's place
+  int lead, units, behind;       // units of a row, elements of its last unit behind it
+  int k, stage;                  // rows so far; the present one's place
   uint32_t phase, first;         // first: this thread's first unit in the present stage
   size_t at;                     // element offset of the present row
   bool ok, refilled, tail;       // tail: the copy leaves out the row's last unit
   float token;                   // the next row's gate
   int place[S_MAX];              // of a stream among those of a stage
+  uint32_t mask[ODD ? NV : 1][4];  // the bits of a unit that are in the row: the same in every row, so found once
 
   __device__ __forceinline__ Rows(const NormDev& q, uint8_t* smem)
-      : p(q), lead(0), k(0), stage(0), phase(0), first(0), at(0), ok(true), refilled(false), tail(false), token(1.0f) {
+      : p(q), lead(0), behind(0), k(0), stage(0), phase(0), first(0), at(0), ok(true), refilled(false), tail(false), token(1.0f) {
     if (ODD) lead = (int)((size_t)blockIdx.x * p.H % N);
     units = (lead + p.H + N - 1) / N;
+    if constexpr (ODD) {
+      behind = units * N - lead - p.H;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          mask[i][w] = 0;
+#pragma unroll
+          for (int c = 0; c < N / 4; ++c)
+            if (inside(i, w * (N / 4) + c)) mask[i][w] |= N == 4 ? 0xffffffffu : 0xffffu << (16 * c);
+        }
+    }
     if constexpr (RING) {
       abort = reinterpret_cast<volatile int*>(smem);
       bars = smem_u32(smem) + 16;
@@ -192,12 +206,7 @@ struct Rows {
       refilled = false;
       if (ok) ok = mbar_wait_one(bars + 8 * stage, phase, abort, p.status);
       first = buf + (uint32_t)(stage * p.streams) * p.pitch + threadIdx.x * 16;
-      if (ODD) {
-        size_t from;
-        uint32_t n;
-        extent(t, from, n);
-        tail = n < (uint32_t)units * 16;
-      }
+      if (ODD) tail = min(p.T - 1 - t, N) * p.H < behind;
     }
   }
   // Called behind a barrier in every row: the row before has been read by all.
@@ -254,16 +263,16 @@ struct Rows {
     } else {
       if (has(i)) v = from_memory(s, i);
     }
+    if constexpr (ODD) {
+      v.x &= mask[i][0];
+      v.y &= mask[i][1];
+      v.z &= mask[i][2];
+      v.w &= mask[i][3];
+    }
     float g[N];
     widen<T, 16>(v, g);
 #pragma unroll
     for (int c = 0; c < N; ++c) put(f, c, g[c]);
-    if constexpr (ODD)
-      if (!whole(i)) {
-#pragma unroll
-        for (int c = 0; c < N; ++c)
-          if (!inside(i, c)) put(f, c, 0.f);
-      }
   }
   __device__ __forceinline__ void store(void* base, int i, const float2 (&f)[C2]) const {
     if (!has(i)) return;
