@@ -1145,7 +1145,7 @@ static int postnorm_rule(const moe_postnorm_rule* rule, int T, int H, int dtype,
 int moe_norm_workspace_size(int T, int H, size_t* bytes) {
   if (T < 0 || H < 1 || !bytes) return MOE_ERR_ARG;
   if (H > kNormMaxWidth) return MOE_ERR_UNSUPPORTED;
-  *bytes = align_up((size_t)3 * norm_grad_rows(T, H) * H * sizeof(float), 256);
+  *bytes = align_up((size_t)3 * norm_grad_rows(T, H) * norm_pitch(H) * sizeof(float), 256);
   return MOE_OK;
 }
 

@@ -271,10 +271,12 @@ struct NormArgs {
   const void *d_out, *d_h;            // gradient (nullable)
   void *d_x, *d_y, *d_gate;
   float *d_post_w, *d_next_w;
-  void* workspace;                    // 3 * norm_grad_rows(T, H) * H floats
+  void* workspace;                    // 3 * norm_grad_rows(T, H) * norm_pitch(H) floats
   int* status;
 };
 int norm_grad_rows(int T, int H);
+// Floats of a row of partial sums: the 16-byte units, of 8 or 4 elements, that may hold a row of H.
+__host__ __device__ constexpr int norm_pitch(int H) { return H % 8 ? (H + 14) / 8 * 8 : H; }
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_norm_grad(const NormArgs& a, cudaStream_t s);
 

@@ -106,7 +106,7 @@ struct NormDev {
   const void *post_w, *gate, *next_w;
   void *out, *h;
   void *d_x, *d_y, *d_gate;
-  float* part;       // partial sums: [3][gridDim.x][H] of d_post_w, d_next_w, d_gate
+  float* part;       // partial sums: [3][gridDim.x][norm_pitch(H)] of d_post_w, d_next_w, d_gate
   int T, H;
   float inv_h, eps, scale, res_scale;
   int gate_kind;     // MOE_GATE_*
@@ -291,18 +291,12 @@ struct Rows {
         }
     }
   }
-  // N fp32 values of the unit's columns
-  __device__ __forceinline__ void store_f32(float* to, int i, const float2 (&f)[C2]) const {
+  // N partial sums of the unit's columns, in a row of them that begins at the row's first unit
+  __device__ __forceinline__ void store_part(float* to, int i, const float2 (&f)[C2]) const {
     if (!has(i)) return;
-    if constexpr (!ODD) {
 #pragma unroll
-      for (int c = 0; c < N; c += 4)
-        *reinterpret_cast<float4*>(to + column(i) + c) = make_float4(f[c / 2].x, f[c / 2].y, f[c / 2 + 1].x, f[c / 2 + 1].y);
-    } else {
-#pragma unroll
-      for (int c = 0; c < N; ++c)
-        if (inside(i, c)) to[column(i) + c] = pick(f, c);
-    }
+    for (int c = 0; c < N; c += 4)
+      *reinterpret_cast<float4*>(to + unit(i) * N + c) = make_float4(f[c / 2].x, f[c / 2].y, f[c / 2 + 1].x, f[c / 2 + 1].y);
   }
   // A weight (or gate) of the unit's columns, from element `from` on.
   __device__ __forceinline__ void weight(const void* w, bool f32, size_t from, int i, float2 (&f)[C2]) const {

@@ -192,11 +192,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
   }
   rows.drain();
   // partial sums
-  const size_t plane = (size_t)gridDim.x * p.H;
-  float* part = p.part + (size_t)blockIdx.x * p.H;
+  const size_t plane = (size_t)gridDim.x * norm_pitch(p.H);
+  float* part = p.part + (size_t)blockIdx.x * norm_pitch(p.H);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    if (p.sum_next) rows.store_f32(part + plane, c, acc_n[c]);
+    if (p.sum_next) rows.store_part(part + plane, c, acc_n[c]);
     if constexpr (POST) {
       float2 f[C2], g[C2];
       if (p.gate_kind == MOE_GATE_CHANNEL) rows.channel_gate(c, g);
@@ -209,35 +209,42 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
           f[i] = mul2(f[i], acc_s[c][i]);
           if (p.sigmoid) f[i] = mul2(f[i], make_float2(g[i].x * (1.0f - g[i].x), g[i].y * (1.0f - g[i].y)));
         }
-        rows.store_f32(part + 2 * plane, c, f);
+        rows.store_part(part + 2 * plane, c, f);
       }
       if (p.sum_post) {
 #pragma unroll
         for (int i = 0; i < C2; ++i) f[i] = p.gate_kind == MOE_GATE_CHANNEL ? mul2(acc_s[c][i], g[i]) : acc_s[c][i];
-        rows.store_f32(part, c, f);
+        rows.store_part(part, c, f);
       }
     }
   }
 }
 
-// out[z][c] = sum_g part[z][g][c]: COLS columns to a CTA, the runs of rows of its threads added in their order.
+// out[z][c] = sum_g part[z][g][lead(g) + c]: COLS columns to a CTA, the runs of rows of its threads added in their
+// order.  lead(g) is where row g of the tensors begins in its first unit of n elements.
 struct SumDev {
   const float* part[3];
   float* out[3];
-  int rows, H;
+  int rows, H, n;
 };
-template <int THREADS, int COLS>
+template <int THREADS, int COLS, bool ODD>
 __global__ void __launch_bounds__(THREADS) k_sum_rows(const SumDev p) {
   pdl_enter();
   constexpr int RUNS = THREADS / COLS;
   __shared__ float s[RUNS][COLS];
   const int col = threadIdx.x % COLS, run = threadIdx.x / COLS, c = blockIdx.x * COLS + col;
-  const float* part = p.part[blockIdx.y] + c;
   const int per = (p.rows + RUNS - 1) / RUNS, g0 = min(p.rows, run * per), g1 = min(p.rows, g0 + per);
   float a = 0.f;
   if (c < p.H) {
+    const int pitch = norm_pitch(p.H);
+    const float* part = p.part[blockIdx.y] + (size_t)g0 * pitch + c;
+    int lead = ODD ? g0 * p.H & (p.n - 1) : 0;
 #pragma unroll 16
-    for (int g = g0; g < g1; ++g) a += part[(size_t)g * p.H];
+    for (int g = g0; g < g1; ++g) {
+      a += part[lead];
+      part += pitch;
+      if (ODD) lead = (lead + p.H) & (p.n - 1);
+    }
   }
   s[run][col] = a;
   __syncthreads();
@@ -247,6 +254,16 @@ __global__ void __launch_bounds__(THREADS) k_sum_rows(const SumDev p) {
     for (int w = 0; w < RUNS; ++w) a += s[w][col];
     p.out[blockIdx.y][c] = a;
   }
+}
+
+// (half the columns to a CTA where SMs would have none otherwise: the prenorm's 4096 x 2048 17.1 -> 16.1 us)
+template <bool ODD>
+cudaError_t launch_sums(const SumDev& q, int sums, cudaStream_t s) {
+  const int groups = (q.H + 31) / 32;
+  if (q.rows <= 64) MOE_LAUNCH((k_sum_rows<128, 32, ODD>), dim3(groups, sums), dim3(128), 0, s, q);
+  else if (groups * sums >= 152) MOE_LAUNCH((k_sum_rows<512, 32, ODD>), dim3(groups, sums), dim3(512), 0, s, q);
+  else MOE_LAUNCH((k_sum_rows<512, 16, ODD>), dim3((q.H + 15) / 16, sums), dim3(512), 0, s, q);
+  return cudaGetLastError();
 }
 
 template <typename T, int NV, int KIND, bool RING, int THREADS, bool ODD, bool FAST = false>
@@ -301,7 +318,7 @@ cudaError_t launch_norm_grad(const NormArgs& a, cudaStream_t s) {
   if (e != cudaSuccess || !(p.sum_post || p.sum_next || p.sum_gate)) return e;
   SumDev q = {};
   int sums = 0;
-  const size_t plane = (size_t)rows * a.H;
+  const size_t plane = (size_t)rows * norm_pitch(a.H);
   float* const out[3] = {a.d_post_w, a.d_next_w, p.sum_gate ? static_cast<float*>(a.d_gate) : nullptr};
   for (int i = 0; i < 3; ++i)
     if (out[i]) {
@@ -310,12 +327,8 @@ cudaError_t launch_norm_grad(const NormArgs& a, cudaStream_t s) {
     }
   q.rows = rows;
   q.H = a.H;
-  // (half the columns to a CTA where SMs would have none otherwise: the prenorm's 4096 x 2048 17.1 -> 16.1 us)
-  const int groups = (a.H + 31) / 32;
-  if (rows <= 64) MOE_LAUNCH((k_sum_rows<128, 32>), dim3(groups, sums), dim3(128), 0, s, q);
-  else if (groups * sums >= 152) MOE_LAUNCH((k_sum_rows<512, 32>), dim3(groups, sums), dim3(512), 0, s, q);
-  else MOE_LAUNCH((k_sum_rows<512, 16>), dim3((a.H + 15) / 16, sums), dim3(512), 0, s, q);
-  return cudaGetLastError();
+  q.n = a.bf16 ? 8 : 4;
+  return odd ? launch_sums<true>(q, sums, s) : launch_sums<false>(q, sums, s);
 }
 
 }  // namespace moe
