@@ -256,12 +256,14 @@ struct Rows {
     else f[e / 2].x = v;
   }
   __device__ __forceinline__ static float pick(const float2 (&f)[C2], int e) { return e & 1 ? f[e / 2].y : f[e / 2].x; }
-  __device__ __forceinline__ void load(int s, int i, float2 (&f)[C2]) const {
+  // (there: false of a stream that the call does not have: zeros, by a predicate rather than by a branch that the
+  // loads would wait behind)
+  __device__ __forceinline__ void load(int s, int i, float2 (&f)[C2], bool there = true) const {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (RING && !(ODD && tail)) {
-      if (has(i)) v = lds_v4(first + (uint32_t)place[s] * p.pitch + (uint32_t)(i * blockDim.x) * 16);
+      if (there && has(i)) v = lds_v4(first + (uint32_t)place[s] * p.pitch + (uint32_t)(i * blockDim.x) * 16);
     } else {
-      if (has(i)) v = from_memory(s, i);
+      if (there && has(i)) v = from_memory(s, i);
     }
     if constexpr (ODD) {
       v.x &= mask[i][0];

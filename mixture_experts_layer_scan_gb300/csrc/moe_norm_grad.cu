@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
   __syncthreads();
   rows.start();
   if constexpr (POST) rows.fetch_token(blockIdx.x);
-  const bool dh = FAST || p.stream[S_DH], dout = FAST || p.stream[S_DOUT], post = FAST || p.post_w;
+  const bool dh = FAST || !POST || p.stream[S_DH], dout = FAST || p.stream[S_DOUT], post = FAST || p.post_w;
   float2 cw[HOLD ? CP : 1][C2], nw[HOLD ? CH : 1][C2], acc_n[CH][C2], acc_s[CP][C2];
 #pragma unroll
   for (int c = 0; c < CH; ++c)
@@ -58,12 +58,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
           if constexpr (FULL) yc[i] = mul2(yc[i], g[i]);
         }
       }
-      if (dh) {
-        rows.load(S_DH, c, d);
-      } else {
-#pragma unroll
-        for (int i = 0; i < C2; ++i) d[i] = both(0.f);
-      }
+      rows.load(S_DH, c, d, dh);
 #pragma unroll
       for (int i = 0; i < C2; ++i) e[i] = mul2(d[i], nw[HOLD ? c : 0][i]);
     };
@@ -84,11 +79,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
         }
       }
       if constexpr (POST) {
-        if (dout) {
-          rows.load(S_DOUT, c, d);
+        rows.load(S_DOUT, c, d, dout);
 #pragma unroll
-          for (int i = 0; i < C2; ++i) dc = fma2(d[i], yc[i], dc);
-        }
+        for (int i = 0; i < C2; ++i) dc = fma2(d[i], yc[i], dc);
       }
     }
     float ry = 1.f, tok = 1.f, b = 0.f, r, m, mean = 0.f;  // r: 1 / rms of out; m: mean(e out r)
@@ -139,8 +132,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
     for (int c = 0; c < CH; ++c) {
       float2 x[C2], y[C2], yc[C2], d[C2], e[C2], g[C2], D[C2];
       inputs(c, x, y, yc, d, e, g);
-      if (POST && dout) {
-        rows.load(S_DOUT, c, D);
+      if constexpr (POST) {
+        rows.load(S_DOUT, c, D, dout);
       } else {
 #pragma unroll
         for (int i = 0; i < C2; ++i) D[i] = both(0.f);
