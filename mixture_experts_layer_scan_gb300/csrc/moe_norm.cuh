@@ -58,6 +58,11 @@ __device__ __forceinline__ void load_w(const void* w, bool f32, size_t i, float 
   }
 }
 
+__device__ __forceinline__ void sts_one(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+__device__ __forceinline__ void sts_one(uint32_t a, __nv_bfloat16 v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(__bfloat16_as_ushort(v)) : "memory");
+}
+
 __device__ __forceinline__ float load_one(const void* w, bool f32, size_t i) {
   return f32 ? static_cast<const float*>(w)[i] : bf16_bits_to_f32(static_cast<const uint16_t*>(w)[i]);
 }
@@ -132,26 +137,24 @@ struct Rows {
   int k, stage;                  // rows so far; the present one's place
   uint32_t phase, first;         // first: this thread's first unit in the present stage
   size_t at;                     // element offset of the present row
-  bool ok, refilled, tail;       // tail: the copy leaves out the row's last unit
+  bool ok, refilled;
   float token;                   // the next row's gate
   int place[S_MAX];              // of a stream among those of a stage
-  uint32_t mask[ODD ? NV : 1][4];  // the bits of a unit that are in the row: the same in every row, so found once
+  uint32_t in[ODD ? NV : 1];     // which elements of a unit are in the row: the same in every row, so found once
 
   __device__ __forceinline__ Rows(const NormDev& q, uint8_t* smem)
-      : p(q), lead(0), behind(0), k(0), stage(0), phase(0), first(0), at(0), ok(true), refilled(false), tail(false), token(1.0f) {
+      : p(q), lead(0), behind(0), k(0), stage(0), phase(0), first(0), at(0), ok(true), refilled(false), token(1.0f) {
     if (ODD) lead = (int)((size_t)blockIdx.x * p.H % N);
     units = (lead + p.H + N - 1) / N;
     if constexpr (ODD) {
       behind = units * N - lead - p.H;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        in[i] = 0;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          mask[i][w] = 0;
-#pragma unroll
-          for (int c = 0; c < N / 4; ++c)
-            if (inside(i, w * (N / 4) + c)) mask[i][w] |= N == 4 ? 0xffffffffu : 0xffffu << (16 * c);
-        }
+        for (int c = 0; c < N; ++c)
+          if (inside(i, c)) in[i] |= 1u << c;
+      }
     }
     if constexpr (RING) {
       abort = reinterpret_cast<volatile int*>(smem);
@@ -171,13 +174,13 @@ struct Rows {
   __device__ __forceinline__ bool has(int i) const { return FULL_ROWS || unit(i) < units; }
   __device__ __forceinline__ int column(int i) const { return unit(i) * N - lead; }  // of a unit's first element
   __device__ __forceinline__ bool inside(int i, int c) const { return !ODD || (unsigned)(column(i) + c) < (unsigned)p.H; }
-  __device__ __forceinline__ bool whole(int i) const { return !ODD || (column(i) >= 0 && column(i) + N <= p.H); }
+  __device__ __forceinline__ bool whole(int i) const { return !ODD || in[ODD ? i : 0] == (1u << N) - 1; }
   // The units of row t that a copy takes: first byte and their bytes.
   __device__ __forceinline__ void extent(int t, size_t& from, uint32_t& n) const {
     const size_t row = (size_t)p.H * sizeof(T), begin = (size_t)t * row, end = begin + row;
     from = begin & ~(size_t)15;
     const size_t up = (end + 15) & ~(size_t)15;
-    // (nothing behind the tensor is read: a row whose end the copy leaves out comes from memory)
+    // (nothing behind the tensor is read: last_unit puts in what the copy leaves out)
     const size_t till = !ODD || up <= (size_t)p.T * row ? up : end & ~(size_t)15;
     n = till > from ? (uint32_t)(till - from) : 0;
   }
@@ -206,7 +209,19 @@ struct Rows {
       refilled = false;
       if (ok) ok = mbar_wait_one(bars + 8 * stage, phase, abort, p.status);
       first = buf + (uint32_t)(stage * p.streams) * p.pitch + threadIdx.x * 16;
-      if (ODD) tail = min(p.T - 1 - t, N) * p.H < behind;
+      if (ODD && min(p.T - 1 - t, N) * p.H < behind) last_unit();
+    }
+  }
+  // The last rows of a tensor that ends inside a unit: the copy left that unit out, and the thread that looks at
+  // it puts it into the ring (the stage is not filled again: the grid has more rows than a unit has elements).
+  __device__ __forceinline__ void last_unit() {
+    const int u = units - 1;
+    if ((int)threadIdx.x != u % (int)blockDim.x) return;
+    for (int s = 0, n = 0; s < S_MAX; ++s) {
+      if (!p.stream[s] || (s == S_GATE && !p.gate_ring)) continue;
+      const uint32_t to = buf + (uint32_t)(stage * p.streams + n++) * p.pitch + u * 16;
+      const T* base = static_cast<const T*>(p.stream[s]) + at;
+      for (int c = max(0, u * N - lead); c < p.H; ++c) sts_one(to + (c - (u * N - lead)) * (int)sizeof(T), base[c]);
     }
   }
   // Called behind a barrier in every row: the row before has been read by all.
@@ -260,16 +275,24 @@ struct Rows {
   // loads would wait behind)
   __device__ __forceinline__ void load(int s, int i, float2 (&f)[C2], bool there = true) const {
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (RING && !(ODD && tail)) {
+    if constexpr (RING) {
       if (there && has(i)) v = lds_v4(first + (uint32_t)place[s] * p.pitch + (uint32_t)(i * blockDim.x) * 16);
     } else {
       if (there && has(i)) v = from_memory(s, i);
     }
     if constexpr (ODD) {
-      v.x &= mask[i][0];
-      v.y &= mask[i][1];
-      v.z &= mask[i][2];
-      v.w &= mask[i][3];
+      if (!whole(i)) {  // (few threads)
+        uint32_t m[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if constexpr (N == 4) m[w] = 0u - (in[i] >> w & 1u);
+          else m[w] = (in[i] >> (2 * w) & 1u) * 0xffffu | (in[i] >> (2 * w + 1) & 1u) * 0xffff0000u;
+        }
+        v.x &= m[0];
+        v.y &= m[1];
+        v.z &= m[2];
+        v.w &= m[3];
+      }
     }
     float g[N];
     widen<T, 16>(v, g);
