@@ -222,7 +222,7 @@ struct SumDev {
 };
 template <int THREADS, int COLS, bool ODD>
 __global__ void __launch_bounds__(THREADS) k_sum_rows(const SumDev p) {
-  pdl_enter();
+  pdl_wait();
   constexpr int RUNS = THREADS / COLS;
   __shared__ float s[RUNS][COLS];
   const int col = threadIdx.x % COLS, run = threadIdx.x / COLS, c = blockIdx.x * COLS + col;
@@ -247,6 +247,8 @@ __global__ void __launch_bounds__(THREADS) k_sum_rows(const SumDev p) {
     for (int w = 0; w < RUNS; ++w) a += s[w][col];
     p.out[blockIdx.y][c] = a;
   }
+  // (not sooner: CTAs of the next call's kernel that come while these hold registers do not all find their place)
+  pdl_launch_dependents();
 }
 
 // (half the columns to a CTA where SMs would have none otherwise: the prenorm's 4096 x 2048 17.1 -> 16.1 us)
