@@ -582,7 +582,8 @@ def _postnorm(x, y, post_w, gate, sigmoid, scale, res_scale, next_w, eps):
         if kind is None:
             raise ValueError("gate must be [H], [T, 1] or [T, H]")
         gdt = _act(gate, "gate")
-    key = (eps, scale, res_scale, kind, bool(sigmoid), gdt, wdt)
+    # (numbers, not objects that hold one and may change)
+    key = (float(eps), float(scale), float(res_scale), kind, bool(sigmoid), gdt, wdt)
     rule = _POSTNORM_RULES.get(key)
     if rule is None:
         if len(_POSTNORM_RULES) >= 256:  # (scales that change from call to call)

@@ -1060,12 +1060,15 @@ int moe_gemm_block(const void* a, const float* a_scale, const void* w, const flo
   return cuda_rc(launch_gemm_block(g, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Rows of calls that move them: a row has fewer than 2^16 columns of CTAs.
+constexpr int kRowsMaxWidth = 1 << 25;
+
 static bool act_type(int d) { return d == MOE_F32 || d == MOE_BF16; }
 
 int moe_permute(const void* x, const int32_t* topk_ids, int T, int H, int E, int topk, int block, moe_dtype dtype,
                 void* rows, int32_t* row_of, int32_t* sorted_ids, int32_t* expert_ids, int32_t* num_post_pad,
                 int32_t* expert_counts, moe_stream_t stream) {
-  if (T < 0 || H < 1 || H >= kBlockMaxDim || topk < 1 || E < 1 || E > 1024 || block < 1 || block > 1024)
+  if (T < 0 || H < 1 || H >= kRowsMaxWidth || topk < 1 || E < 1 || E > 1024 || block < 1 || block > 1024)
     return MOE_ERR_ARG;
   if (!act_type(dtype)) return MOE_ERR_UNSUPPORTED;
   size_t cap = 0, bcap = 0;
@@ -1087,7 +1090,7 @@ int moe_permute(const void* x, const int32_t* topk_ids, int T, int H, int E, int
 
 static int rows_gather(const void* rows, int n_rows, const int32_t* row_of, const float* w, int T, int H, int topk,
                        moe_dtype dtype, void* out, moe_stream_t stream) {
-  if (T < 0 || H < 1 || H >= kBlockMaxDim || topk < 1 || n_rows < 0 || (long long)T * topk >= kBlockMaxDim)
+  if (T < 0 || H < 1 || H >= kRowsMaxWidth || topk < 1 || n_rows < 0 || (long long)T * topk >= kBlockMaxDim)
     return MOE_ERR_ARG;
   if (!act_type(dtype)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
@@ -1110,7 +1113,7 @@ int moe_permute_backward(const void* d_rows, int n_rows, const int32_t* row_of, 
 int moe_unpermute_backward(const void* d_out, const void* rows, int n_rows, const int32_t* row_of, const float* topk_w,
                            const int32_t* sorted_ids, const int32_t* num_post_pad, int T, int H, int topk,
                            moe_dtype dtype, void* d_rows, float* d_w, moe_stream_t stream) {
-  if (T < 0 || H < 1 || H >= kBlockMaxDim || topk < 1 || n_rows < 0 || (long long)T * topk >= kBlockMaxDim)
+  if (T < 0 || H < 1 || H >= kRowsMaxWidth || topk < 1 || n_rows < 0 || (long long)T * topk >= kBlockMaxDim)
     return MOE_ERR_ARG;
   if (!act_type(dtype)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;

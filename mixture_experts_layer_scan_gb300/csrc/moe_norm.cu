@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
         for (int e = 0; e < C2; ++e) o[c][e] = fma2(both(b), y[c][e], mul2(both(p.res_scale), o[c][e]));
         rows.store(p.out, c, o[c]);
       }
-      if (next && parts_cancel(pp, qq, ee)) {
+      if (next && parts_fail(pp, qq, ee, b, v[3])) {
         a0 = both(0.f);
 #pragma unroll
         for (int c = 0; c < CH; ++c)

@@ -17,7 +17,7 @@
 // e = d_h next_w, b = scale r_y (times a token's gate):
 //   sum out^2 = res^2 sum x^2 + 2 res b sum x c + b^2 sum c^2,   sum out e = res sum x e + b sum c e,
 //   sum g n (for d_y) = scale r_y (sum d_out c + r_o sum e c - r_o^2 m sum out c),  m = mean(e out r_o)
-// (A row whose residual and branch cancel, so that the first of these lost digits, is summed again from out.)
+// (A row whose residual and branch cancel, so that the first of these lost digits, is summed again from out: parts_fail.)
 // The weights' gradients are
 // sums over rows: a CTA keeps those of its rows in registers, writes one fp32 row of partial sums, and a second
 // kernel adds the CTAs' rows in their order.
@@ -100,9 +100,12 @@ __device__ __forceinline__ void block_sums(float (&v)[K], float* s) {
 }
 __device__ __forceinline__ float flat(float2 a) { return a.x + a.y; }
 
-// 1 / rms of a row whose sum of squares is known in parts, and whether that sum is trusted: E = p + q + 2 c with p, q >= 0;
-// each part is off by some 2^-22 of p + q, which an E of an eighth of it turns into 2^-19 at most.
-__device__ __forceinline__ bool parts_cancel(float p, float q, float e) { return !(e >= 0.125f * (p + q)); }
+// Whether a row's sums in parts are not to be trusted, and it is summed again from out.  E = p + q + 2 c with p, q >= 0
+// and q = b^2 cc: each part is off by some 2^-22 of p + q, which an E of an eighth of it turns into 2^-19 at most.
+// Nor are they where y post_w gate, without r_y, left the range whose squares fp32 holds, although out did not.
+__device__ __forceinline__ bool parts_fail(float p, float q, float e, float b, float cc) {
+  return !(e >= 0.125f * (p + q) && p + q < 1e38f) || (cc < 1e-30f && b * b > 1e8f);
+}
 
 enum { S_X = 0, S_Y, S_DOUT, S_DH, S_GATE, S_MAX };
 

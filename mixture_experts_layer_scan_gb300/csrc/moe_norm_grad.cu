@@ -94,28 +94,42 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm_grad(const __grid_constant_
       b = p.scale * tok * ry;
       const float pp = p.res_scale * p.res_scale * v[0], qq = b * b * v[3];
       float ee = pp + qq + 2.f * p.res_scale * b * v[2], oe = p.res_scale * v[4] + b * v[5];
-      if (dh && parts_cancel(pp, qq, ee)) {
-        float2 a0 = both(0.f), a1 = a0;
+      // sums over the row of c d_out, c e and c out
+      float sd = v[6], se = v[5], so = p.res_scale * v[2] + b * v[3];
+      if (dh && parts_fail(pp, qq, ee, b, v[3])) {
+        float2 a[5] = {};
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           float2 x[C2], y[C2], yc[C2], d[C2], e[C2], g[C2];
           inputs(c, x, y, yc, d, e, g);
+          rows.load(S_DOUT, c, d, dout);
 #pragma unroll
           for (int i = 0; i < C2; ++i) {
             x[i] = fma2(both(b), yc[i], mul2(both(p.res_scale), x[i]));
-            a0 = fma2(x[i], x[i], a0);
-            a1 = fma2(x[i], e[i], a1);
+            yc[i] = mul2(yc[i], both(ry));  // (so that its products stay in range)
+            a[0] = fma2(x[i], x[i], a[0]);
+            a[1] = fma2(x[i], e[i], a[1]);
+            a[2] = fma2(yc[i], d[i], a[2]);
+            a[3] = fma2(yc[i], e[i], a[3]);
+            a[4] = fma2(yc[i], x[i], a[4]);
           }
         }
-        float u[2] = {flat(a0), flat(a1)};
+        float u[5] = {flat(a[0]), flat(a[1]), flat(a[2]), flat(a[3]), flat(a[4])};
         block_sums(u, s2[1]);
         ee = u[0];
         oe = u[1];
+        sd = u[2];
+        se = u[3];
+        so = u[4];
+      } else {
+        sd *= ry;
+        se *= ry;
+        so *= ry;
       }
       r = dh ? rsqrtf(ee * p.inv_h + p.eps) : 0.f;
       m = oe * r * p.inv_h;
       // sum over the row of scale D c, which is a token gate's gradient times r_y's inverse
-      const float u = p.scale * ry * (v[6] + r * v[5] - r * r * m * (p.res_scale * v[2] + b * v[3]));
+      const float u = p.scale * (dh ? sd + r * se - r * r * m * so : sd);
       mean = u * p.inv_h;
       if (p.gate_kind == MOE_GATE_TOKEN && p.d_gate && threadIdx.x == 0)
         static_cast<float*>(p.d_gate)[t] = p.sigmoid ? u * tok * (1.0f - tok) : u;

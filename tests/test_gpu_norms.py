@@ -332,3 +332,25 @@ def test_bad_values_stay_in_their_row(moe, T, H):
         for k in ("d_x", "d_y", "d_gate"):
             assert torch.equal(getattr(ga, k)[keep], getattr(gb, k)[keep]), (n, k)
     assert moe.moe_get_status() == 0
+
+
+@pytest.mark.parametrize("T,H", [(3, 512), (400, 4096), (330, 2047)])
+def test_block_output_of_any_size(moe, T, H):
+    """out is of ordinary size, but y post_w gate, before its norm, is not: its squares leave fp32's range."""
+    g = torch.Generator().manual_seed(T)
+    d = inputs(T, H, torch.float32, torch.float32, g, True, "channel", True)
+    d["y"], d["post_w"], d["gate"] = d["y"] * 2.0 ** 50, d["post_w"] * 2.0 ** 10, d["gate"] * 2.0 ** 10
+    check_all(moe, d, False, 2.0 ** -20, 1.25, "large", T)
+    # a norm without eps of a small output: squares below fp32's range (2^-149) where its own are not
+    d = inputs(T, H, torch.float32, torch.float32, g, True, "channel", True)
+    d["y"], d["post_w"] = d["y"] * 2.0 ** -56, d["post_w"] * 2.0 ** -30
+    d["x"] = d["x"] * 2.0 ** -30
+    out, h = moe.moe_postnorm(*(cuda(d[n]) for n in ("x", "y", "post_w", "gate")), next_w=cuda(d["next_w"]), eps=0.0)
+    x, y = d["x"].double(), d["y"].double()
+    branch = d["gate"].double() * d["post_w"].double() * y * rstd(y, 0.0)
+    ref = x + branch
+    mag = x.abs() + branch.abs()
+    within(out, ref, half(torch.float32) * ref.abs() + FUZZ * mag, "small out")
+    r = rstd(ref, 0.0) * d["next_w"].double()
+    # (1 / rms moves with the sum of out^2: by its relative error, FUZZ times mean(mag^2) / mean(out^2))
+    within(h, ref * r, half(torch.float32) * (ref * r).abs() + FUZZ * (mag * r.abs() + (ref * r).abs() * mean(mag * mag) / mean(ref * ref)), "small h")

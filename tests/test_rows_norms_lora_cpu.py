@@ -148,3 +148,22 @@ def test_python_checks(moe):
     for call in calls:
         with pytest.raises(ValueError):
             call()
+
+
+def test_row_widths(moe):
+    """Rows too wide for the kernels' 32-bit offsets in a row."""
+    wide = 1 << 25
+    for f, args, at in ((moe.lib().moe_permute, [P, P, 1, 64, 8, 2, 16, 1, P, P, P, P, P, P, None], 3),
+                        (moe.lib().moe_unpermute, [P, 8, P, P, 1, 64, 2, 1, P, None], 5),
+                        (moe.lib().moe_permute_backward, [P, 8, P, 1, 64, 2, 1, P, None], 4),
+                        (moe.lib().moe_unpermute_backward, [P, P, 8, P, P, P, P, 1, 64, 2, 1, P, P, None], 8)):
+        each_refused(f, args, [(at, wide), (at, wide + 1)], moe.MOE_ERR_ARG)
+
+
+def test_postnorm_rule_follows_its_numbers(moe):
+    """A scale that is a tensor: its present value counts, not its identity."""
+    x, scale = torch.zeros(4, 64), torch.tensor(0.5)
+    rule = lambda: moe._postnorm(x, x, None, None, False, scale, 1.0, None, 1e-6)[-1]._obj.scale  # noqa: E731
+    assert rule() == 0.5
+    scale.fill_(2.0)
+    assert rule() == 2.0
