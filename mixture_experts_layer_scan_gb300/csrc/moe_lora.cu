@@ -279,8 +279,9 @@ __device__ __forceinline__ void lora_store_h(const LoraTcDev& p, int blk, int ro
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       u[e] = pack_bf16x2(h[2 * e], h[2 * e + 1]);
-      h[2 * e] -= bf16_bits_to_f32(u[e] & 0xffffu);
-      h[2 * e + 1] -= bf16_bits_to_f32(u[e] >> 16);
+      const float lo = bf16_bits_to_f32(u[e] & 0xffffu), hi = bf16_bits_to_f32(u[e] >> 16);
+      h[2 * e] = isinf(lo) ? 0.f : h[2 * e] - lo;  // (an infinite h is its first part alone, not inf - inf)
+      h[2 * e + 1] = isinf(hi) ? 0.f : h[2 * e + 1] - hi;
     }
     dst[(size_t)part * (p.rn / 8) * kBlk] = make_uint4(u[0], u[1], u[2], u[3]);
   }

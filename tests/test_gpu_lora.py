@@ -192,3 +192,21 @@ def test_stale_workspace_graph_and_stream(moe):
 def test_empty(moe):
     d = {n: v.cuda() for n, v in make(4, 64, 72, 8, 2, 1).items()}
     assert moe.moe_lora(d["x"][:0], d["a"], d["b"], d["ids"][:0]).shape == (0, 72)
+
+
+@pytest.mark.parametrize("out_t", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [5, 1030])
+def test_product_that_overflows(moe, T, out_t):
+    """A x beyond fp32 is infinite, and so is what it gives, with the formula's signs; other tokens are as they were."""
+    d = make(T, 1024, 768, 16, 3, T)
+    d["x"][::3] = d["x"][::3].abs() * 2.0 ** 66
+    d["a"][:, 0] = 2.0 ** 66
+    d["a"][:, 1:] = 0
+    d["b"][:, :, 0] = torch.where(d["b"][:, :, 0] < 0, -1.0, 1.0)
+    got = moe.moe_lora(*(d[n].cuda() for n in ("x", "a", "b", "ids")), out_dtype=DT[out_t]).cpu()
+    on = (d["ids"] >= 0) & (torch.arange(T) % 3 == 0)
+    sign = d["b"][d["ids"].clamp(min=0).long(), :, 0].float()
+    assert torch.equal(got[on].float(), sign[on] * float("inf"))
+    assert bool((got[d["ids"] < 0] == 0).all())
+    rest = (d["ids"] >= 0) & (torch.arange(T) % 3 != 0)
+    assert bool(got[rest].isfinite().all())
