@@ -35,10 +35,18 @@ struct RowsDev {
   int T, k, n_rows;
   int vpr;                 // 16-byte vectors per row
   int chunks;              // scatter: runs of 32 * U vectors per row
+  int pad_ctas;            // the launch's first CTAs, which fill the padding
 };
 
 constexpr int kRowsThreads = 256;
-constexpr int kPadCtas = 152;  // CTAs of a launch that fill the padding
+// CTAs that fill the padding: a warp to each row that may be padding, from 8 warps of an SM on to 32.  (A few tokens
+// over many experts are mostly padding: 200 x 3 rows of 2968 fp32 over 256 experts in blocks of 64, with 456 warps, took
+// 70 us.)
+int pad_ctas(const RowsDev& p, int threads) {
+  if (!p.sorted) return 0;
+  const long rows = std::max(0l, (long)p.n_rows - (long)p.T * p.k), warps = threads / 32;
+  return (int)((std::min(std::max(rows, 152l * 8), 152l * 32) + warps - 1) / warps);
+}
 
 // Rows that hold no pair (sorted[r] >= n_pairs).  A warp looks at up to 32 entries of the list at a time, and at fewer
 // where that spreads the rows over more warps (a decode batch over many experts is mostly padding: 64 tokens of
@@ -59,7 +67,7 @@ __device__ __forceinline__ void zero_padding(const RowsDev& p, int unit, int n_u
 }
 // The padding's share of a launch's first CTAs, rows of whole units.
 __device__ __forceinline__ bool pad_cta(const RowsDev& p) {
-  const int ctas = p.sorted ? kPadCtas : 0, warps = blockDim.x >> 5;
+  const int ctas = p.pad_ctas, warps = blockDim.x >> 5;
   if ((int)blockIdx.x >= ctas) return false;
   zero_padding(p, blockIdx.x * warps + (threadIdx.x >> 5), ctas * warps, [&](size_t row) {
     uint4* dst = static_cast<uint4*>(p.out) + row * p.vpr;
@@ -77,9 +85,8 @@ __global__ void __launch_bounds__(kRowsThreads) k_rows_scatter(const RowsDev p) 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int warps = kRowsThreads / 32;
   if (pad_cta(p)) return;
-  const int pad_ctas = p.sorted ? kPadCtas : 0;
   const long units = (long)p.T * p.chunks;
-  for (long u = (long)(blockIdx.x - pad_ctas) * warps + warp; u < units; u += (long)(gridDim.x - pad_ctas) * warps) {
+  for (long u = (long)(blockIdx.x - p.pad_ctas) * warps + warp; u < units; u += (long)(gridDim.x - p.pad_ctas) * warps) {
     const int t = (int)(u / p.chunks), v0 = (int)(u % p.chunks) * (32 * U) + lane;
     const V* src = static_cast<const V*>(p.x) + (size_t)t * p.vpr;
     V buf[U];
@@ -141,62 +148,90 @@ __global__ void __launch_bounds__(kRowsThreads) k_rows_gather(const RowsDev p) {
 
 // Gradient of the weighted sum: a CTA per token, a warp per pair (the pairs' reads of d_out meet in L1).  8192 tokens of
 // 8 rows of 4096 bf16: 174 us, 6.5 TB/s, 97 % of a copy's rate.
+// WIDE, for few pairs: a CTA per pair (a warp's way through a long row is a chain of memory's latencies: 56 x 8 rows of
+// 5185 fp32 took 50 us).
 constexpr int kGradUnroll = 4;
-template <typename T>
+constexpr long kWidePairs = 152 * 8;   // at most
+constexpr long kWideBytes = 4096;      // of a row at least
+
+// The pairs of a CTA, pair(t, j); then the sum of a pair's products over its warp or CTA, in a fixed order.
+template <bool WIDE, typename F>
+__device__ __forceinline__ void each_pair(const RowsDev& p, F pair) {
+  const long at = blockIdx.x - p.pad_ctas, step = gridDim.x - p.pad_ctas;
+  if constexpr (WIDE) {
+    for (long f = at; f < (long)p.T * p.k; f += step) pair((int)(f / p.k), (int)(f % p.k));
+  } else {
+    for (long t = at; t < p.T; t += step)
+      for (int j = threadIdx.x >> 5; j < p.k; j += blockDim.x >> 5) pair((int)t, j);
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ float pair_sum(float dot) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+  if constexpr (WIDE) {
+    __shared__ float s[kRowsThreads / 32];
+    __syncthreads();  // (the pair before has been read)
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = dot;
+    __syncthreads();
+    dot = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRowsThreads / 32; ++w) dot += s[w];
+  }
+  return dot;
+}
+
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(kRowsThreads) k_rows_gather_grad(const RowsDev p) {
   pdl_enter();
   using V = uint4;
   constexpr int N = 16 / sizeof(T);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (pad_cta(p)) return;
-  const int pad_ctas = p.sorted ? kPadCtas : 0;
-  for (int t = blockIdx.x - pad_ctas; t < p.T; t += gridDim.x - pad_ctas) {
+  const int me = WIDE ? threadIdx.x : threadIdx.x & 31, team = WIDE ? kRowsThreads : 32;
+  each_pair<WIDE>(p, [&](int t, int j) {
     const V* d = static_cast<const V*>(p.x) + (size_t)t * p.vpr;
-    for (int j = warp; j < p.k; j += warps) {
-      const size_t f = (size_t)t * p.k + j;
-      const int r = p.row_of[f];
-      const bool in = (unsigned)r < (unsigned)p.n_rows;
-      if (!in) {
-        if (p.dw && lane == 0) p.dw[f] = 0.f;
-        continue;
-      }
-      const float wj = p.w ? p.w[f] : 1.f;
-      const V* src = p.dw ? static_cast<const V*>(p.rows) + (size_t)r * p.vpr : nullptr;
-      V* dst = p.out ? static_cast<V*>(p.out) + (size_t)r * p.vpr : nullptr;
-      float dot = 0.f;
-      for (int v0 = lane; v0 < p.vpr; v0 += 32 * kGradUnroll) {
-        V a[kGradUnroll], b[kGradUnroll];
+    const size_t f = (size_t)t * p.k + j;
+    const int r = p.row_of[f];
+    const bool in = (unsigned)r < (unsigned)p.n_rows;
+    if (!in) {
+      if (p.dw && me == 0) p.dw[f] = 0.f;
+      return;
+    }
+    const float wj = p.w ? p.w[f] : 1.f;
+    const V* src = p.dw ? static_cast<const V*>(p.rows) + (size_t)r * p.vpr : nullptr;
+    V* dst = p.out ? static_cast<V*>(p.out) + (size_t)r * p.vpr : nullptr;
+    float dot = 0.f;
+    for (int v0 = me; v0 < p.vpr; v0 += team * kGradUnroll) {
+      V a[kGradUnroll], b[kGradUnroll];
 #pragma unroll
-        for (int i = 0; i < kGradUnroll; ++i) {
-          const int v = v0 + 32 * i;
-          zero_word(a[i]);
-          zero_word(b[i]);
-          if (v < p.vpr) {
-            a[i] = d[v];
-            if (src) b[i] = __ldcs(src + v);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kGradUnroll; ++i) {
-          const int v = v0 + 32 * i;
-          float fa[N], fb[N];
-          widen<T, 16>(a[i], fa);
-          widen<T, 16>(b[i], fb);
-#pragma unroll
-          for (int c = 0; c < N; ++c) {
-            dot = fmaf(fa[c], fb[c], dot);
-            fa[c] *= wj;
-          }
-          if (dst && v < p.vpr) dst[v] = narrow<T, 16>(fa);
+      for (int i = 0; i < kGradUnroll; ++i) {
+        const int v = v0 + team * i;
+        zero_word(a[i]);
+        zero_word(b[i]);
+        if (v < p.vpr) {
+          a[i] = d[v];
+          if (src) b[i] = __ldcs(src + v);
         }
       }
-      if (p.dw) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) p.dw[f] = dot;
+      for (int i = 0; i < kGradUnroll; ++i) {
+        const int v = v0 + team * i;
+        float fa[N], fb[N];
+        widen<T, 16>(a[i], fa);
+        widen<T, 16>(b[i], fb);
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          dot = fmaf(fa[c], fb[c], dot);
+          fa[c] *= wj;
+        }
+        if (dst && v < p.vpr) dst[v] = narrow<T, 16>(fa);
       }
     }
-  }
+    if (p.dw) {
+      dot = pair_sum<WIDE>(dot);
+      if (me == 0) p.dw[f] = dot;
+    }
+  });
 }
 
 // ---- rows that are no whole 16-byte units --------------------------------------------------------------
@@ -280,7 +315,7 @@ __device__ __forceinline__ void store_unit(uint8_t* row, const Units& q, int u, 
 
 template <int E>
 __device__ __forceinline__ bool pad_cta_odd(const RowsDev& p, size_t row_bytes) {
-  const int ctas = p.sorted ? kPadCtas : 0, warps = blockDim.x >> 5;
+  const int ctas = p.pad_ctas, warps = blockDim.x >> 5;
   if ((int)blockIdx.x >= ctas) return false;
   zero_padding(p, blockIdx.x * warps + (threadIdx.x >> 5), ctas * warps, [&](size_t row) {
     const Units q(row, row_bytes);
@@ -297,9 +332,8 @@ __global__ void __launch_bounds__(kRowsThreads) k_rows_scatter_odd(const RowsDev
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int warps = kRowsThreads / 32;
   if (pad_cta_odd<E>(p, row_bytes)) return;
-  const int pad_ctas = p.sorted ? kPadCtas : 0;
   const long pairs = (long)p.T * p.k;
-  for (long f = (long)(blockIdx.x - pad_ctas) * warps + warp; f < pairs; f += (long)(gridDim.x - pad_ctas) * warps) {
+  for (long f = (long)(blockIdx.x - p.pad_ctas) * warps + warp; f < pairs; f += (long)(gridDim.x - p.pad_ctas) * warps) {
     const int r = p.row_of[f];
     if ((unsigned)r >= (unsigned)p.n_rows) continue;
     const Units q(r, row_bytes);
@@ -352,71 +386,68 @@ __global__ void __launch_bounds__(kRowsThreads) k_rows_gather_odd(const RowsDev 
   }
 }
 
-// A CTA to a token, a warp to a pair, as k_rows_gather_grad.
-template <typename T>
+// Pairs as k_rows_gather_grad's.
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(kRowsThreads) k_rows_gather_grad_odd(const RowsDev p, size_t row_bytes) {
   pdl_enter();
   constexpr int N = 16 / sizeof(T);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (pad_cta_odd<sizeof(T)>(p, row_bytes)) return;
-  const int pad_ctas = p.sorted ? kPadCtas : 0;
-  for (int t = blockIdx.x - pad_ctas; t < p.T; t += gridDim.x - pad_ctas) {
-    for (int j = warp; j < p.k; j += warps) {
-      const size_t f = (size_t)t * p.k + j;
-      const int r = p.row_of[f];
-      if ((unsigned)r >= (unsigned)p.n_rows) {
-        if (p.dw && lane == 0) p.dw[f] = 0.f;
-        continue;
-      }
-      const float wj = p.w ? p.w[f] : 1.f;
-      const Units q(r, row_bytes);
-      const Source<sizeof(T)> d(p.x, p.T, t, q), src(p.dw ? p.rows : p.x, p.n_rows, r, q);
-      uint8_t* dst = static_cast<uint8_t*>(p.out) + (size_t)r * row_bytes;
-      float dot = 0.f;
-      for (int u0 = lane; u0 < q.n; u0 += 32 * 2) {
-        uint4 va[2], vb[2];
+  const int me = WIDE ? threadIdx.x : threadIdx.x & 31, team = WIDE ? kRowsThreads : 32;
+  each_pair<WIDE>(p, [&](int t, int j) {
+    const size_t f = (size_t)t * p.k + j;
+    const int r = p.row_of[f];
+    if ((unsigned)r >= (unsigned)p.n_rows) {
+      if (p.dw && me == 0) p.dw[f] = 0.f;
+      return;
+    }
+    const float wj = p.w ? p.w[f] : 1.f;
+    const Units q(r, row_bytes);
+    const Source<sizeof(T)> d(p.x, p.T, t, q), src(p.dw ? p.rows : p.x, p.n_rows, r, q);
+    uint8_t* dst = static_cast<uint8_t*>(p.out) + (size_t)r * row_bytes;
+    float dot = 0.f;
+    for (int u0 = me; u0 < q.n; u0 += team * 2) {
+      uint4 va[2], vb[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int u = u0 + 32 * i;
-          va[i] = vb[i] = make_uint4(0, 0, 0, 0);
-          if (u < q.n) {
-            va[i] = d.load(q, u);
-            if (p.dw) vb[i] = src.load(q, u);
-          }
+      for (int i = 0; i < 2; ++i) {
+        const int u = u0 + team * i;
+        va[i] = vb[i] = make_uint4(0, 0, 0, 0);
+        if (u < q.n) {
+          va[i] = d.load(q, u);
+          if (p.dw) vb[i] = src.load(q, u);
         }
+      }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int u = u0 + 32 * i;
-          if (u >= q.n) break;
-          float a[N], b[N];
-          widen<T, 16>(va[i], a);
-          widen<T, 16>(vb[i], b);
-          if (!q.whole(u))
-#pragma unroll
-            for (int c = 0; c < N; ++c) {
-              const int at = q.from(u) + c * (int)sizeof(T);
-              if (at < 0 || at >= q.bytes) a[c] = b[c] = 0.f;
-            }
+      for (int i = 0; i < 2; ++i) {
+        const int u = u0 + team * i;
+        if (u >= q.n) break;
+        float a[N], b[N];
+        widen<T, 16>(va[i], a);
+        widen<T, 16>(vb[i], b);
+        if (!q.whole(u))
 #pragma unroll
           for (int c = 0; c < N; ++c) {
-            dot = fmaf(a[c], b[c], dot);
-            a[c] *= wj;
+            const int at = q.from(u) + c * (int)sizeof(T);
+            if (at < 0 || at >= q.bytes) a[c] = b[c] = 0.f;
           }
-          if (p.out) store_unit<sizeof(T)>(dst, q, u, narrow<T, 16>(a));
-        }
-      }
-      if (p.dw) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) p.dw[f] = dot;
+        for (int c = 0; c < N; ++c) {
+          dot = fmaf(a[c], b[c], dot);
+          a[c] *= wj;
+        }
+        if (p.out) store_unit<sizeof(T)>(dst, q, u, narrow<T, 16>(a));
       }
     }
-  }
+    if (p.dw) {
+      dot = pair_sum<WIDE>(dot);
+      if (me == 0) p.dw[f] = dot;
+    }
+  });
 }
 
 cudaError_t scatter_odd(RowsDev& p, size_t row_bytes, int elem, cudaStream_t s) {
   const long pairs = (long)p.T * p.k;
-  const int ctas = (int)std::min<long>((pairs + 7) / 8, 1 << 20) + (p.sorted ? kPadCtas : 0);
+  p.pad_ctas = pad_ctas(p, kRowsThreads);
+  const int ctas = (int)std::min<long>((pairs + 7) / 8, 1 << 20) + p.pad_ctas;
   if (elem == 2) MOE_LAUNCH(k_rows_scatter_odd<2>, dim3(ctas), dim3(kRowsThreads), 0, s, p, row_bytes);
   else MOE_LAUNCH(k_rows_scatter_odd<4>, dim3(ctas), dim3(kRowsThreads), 0, s, p, row_bytes);
   return cudaGetLastError();
@@ -430,11 +461,25 @@ cudaError_t gather_odd(RowsDev& p, size_t row_bytes, cudaStream_t s) {
   MOE_LAUNCH(k_rows_gather_odd<T>, grid, dim3(threads), 0, s, p, row_bytes);
   return cudaGetLastError();
 }
+// A launch of a gradient: threads, and CTAs with those that fill the padding.
+struct GradShape {
+  bool wide;
+  int threads, ctas;
+};
+GradShape grad_shape(RowsDev& p, long row_bytes) {
+  GradShape q;
+  const long pairs = (long)p.T * p.k;
+  q.wide = pairs <= kWidePairs && row_bytes >= kWideBytes;
+  q.threads = q.wide ? kRowsThreads : 32 * std::min(p.k, kRowsThreads / 32);
+  p.pad_ctas = pad_ctas(p, q.threads);
+  q.ctas = (int)std::min<long>(q.wide ? pairs : p.T, 1 << 20) + p.pad_ctas;
+  return q;
+}
 template <typename T>
 cudaError_t gather_grad_odd(RowsDev& p, size_t row_bytes, cudaStream_t s) {
-  const int warps = std::min(p.k, kRowsThreads / 32);
-  const int ctas = std::min(p.T, 1 << 20) + (p.sorted ? kPadCtas : 0);
-  MOE_LAUNCH(k_rows_gather_grad_odd<T>, dim3(ctas), dim3(32 * warps), 0, s, p, row_bytes);
+  const GradShape q = grad_shape(p, (long)row_bytes);
+  if (q.wide) MOE_LAUNCH((k_rows_gather_grad_odd<T, true>), dim3(q.ctas), dim3(q.threads), 0, s, p, row_bytes);
+  else MOE_LAUNCH((k_rows_gather_grad_odd<T, false>), dim3(q.ctas), dim3(q.threads), 0, s, p, row_bytes);
   return cudaGetLastError();
 }
 
@@ -446,7 +491,8 @@ cudaError_t scatter(RowsDev& p, long row_bytes, cudaStream_t s) {
   const int per = few ? 32 : 128;
   p.chunks = (p.vpr + per - 1) / per;
   const long units = (long)p.T * p.chunks;
-  const int ctas = (int)std::min<long>((units + 7) / 8, 1 << 20) + (p.sorted ? kPadCtas : 0);
+  p.pad_ctas = pad_ctas(p, kRowsThreads);
+  const int ctas = (int)std::min<long>((units + 7) / 8, 1 << 20) + p.pad_ctas;
   if (few) MOE_LAUNCH((k_rows_scatter<1>), dim3(ctas), dim3(kRowsThreads), 0, s, p);
   else MOE_LAUNCH((k_rows_scatter<4>), dim3(ctas), dim3(kRowsThreads), 0, s, p);
   return cudaGetLastError();
@@ -465,9 +511,9 @@ cudaError_t gather(RowsDev& p, long row_bytes, cudaStream_t s) {
 template <typename T>
 cudaError_t gather_grad(RowsDev& p, long row_bytes, cudaStream_t s) {
   p.vpr = (int)(row_bytes / 16);
-  const int warps = std::min(p.k, kRowsThreads / 32);
-  const int ctas = std::min(p.T, 1 << 20) + (p.sorted ? kPadCtas : 0);
-  MOE_LAUNCH((k_rows_gather_grad<T>), dim3(ctas), dim3(32 * warps), 0, s, p);
+  const GradShape q = grad_shape(p, row_bytes);
+  if (q.wide) MOE_LAUNCH((k_rows_gather_grad<T, true>), dim3(q.ctas), dim3(q.threads), 0, s, p);
+  else MOE_LAUNCH((k_rows_gather_grad<T, false>), dim3(q.ctas), dim3(q.threads), 0, s, p);
   return cudaGetLastError();
 }
 
