@@ -261,3 +261,15 @@ def test_graph_replay_and_side_stream(moe):
     out = moe.moe_unpermute(p.rows, p.row_of, w, stream=side)
     side.synchronize()
     assert torch.equal(out, refs[1][0]) and moe.moe_get_status() == 0
+
+
+# short rows off the 16-byte grid in great number; few pairs of long rows; padding in plenty
+MORE = [(900, 13, 16, 3, 4), (1300, 109, 64, 2, 16), (700, 235, 8, 4, 1), (2500, 1, 4, 1, 1), (30, 2056, 8, 4, 1),
+        (9, 4133, 300, 8, 16), (1, 8195, 4, 1, 64), (20, 1028, 200, 3, 64)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", MORE)
+def test_forms_by_size(moe, shape, dtype):
+    test_permute(moe, shape, dtype)
+    test_back_and_gradients(moe, shape, dtype, True)
