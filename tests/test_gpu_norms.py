@@ -354,3 +354,18 @@ def test_block_output_of_any_size(moe, T, H):
     r = rstd(ref, 0.0) * d["next_w"].double()
     # (1 / rms moves with the sum of out^2: by its relative error, FUZZ times mean(mag^2) / mean(out^2))
     within(h, ref * r, half(torch.float32) * (ref * r).abs() + FUZZ * (mag * r.abs() + (ref * r).abs() * mean(mag * mag) / mean(ref * ref)), "small h")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(700, 5120), (400, 4104), (9, 5112), (330, 4128)])
+def test_prenorm_gradient_of_two_ctas(moe, T, H, dtype):
+    """Widths at which the prenorm's gradient holds its registers to two CTAs of an SM."""
+    g = torch.Generator().manual_seed(T + H)
+    x, w, dh = torch.randn(T, H, generator=g).to(DT[dtype]), 1 + torch.randn(H, generator=g) / 4, torch.randn(T, H, generator=g).to(DT[dtype])
+    d_x, d_w = moe.moe_prenorm_backward(dh.cuda(), x.cuda(), w.cuda(), EPS)
+    r = rstd(x.double())
+    n, gg = x.double() * r, dh.double() * w.double()
+    ref = r * (gg - n * mean(gg * n))
+    within(d_x, ref, half(DT[dtype]) * ref.abs() + FUZZ * r * (gg.abs() + n.abs() * mean((gg * n).abs())), "d_x")
+    within(d_w, (dh.double() * n).sum(0), (FUZZ + T * 2.0 ** -24) * (dh.double() * n).abs().sum(0), "d_w")
+    assert moe.moe_get_status() == 0
