@@ -210,3 +210,24 @@ def test_product_that_overflows(moe, T, out_t):
     assert bool((got[d["ids"] < 0] == 0).all())
     rest = (d["ids"] >= 0) & (torch.arange(T) % 3 != 0)
     assert bool(got[rest].isfinite().all())
+
+
+def test_two_streams_at_once(moe):
+    """Calls in flight on two streams, each with its own workspace, beside a norm's gradient: as one after the other."""
+    sets = [{n: v.cuda() for n, v in make(T, 1024, 2056, 64, 6, T).items()} for T in (3000, 1700)]
+    assert all(sorts(moe, T, 1024, 2056, 64, 6) for T in (3000, 1700))
+    h = torch.randn(2000, 1024, device="cuda").to(torch.bfloat16)
+    w = torch.rand(1024, device="cuda")
+    call = lambda c, **k: moe.moe_lora(c["x"], c["a"], c["b"], c["ids"], scale=c["scale"], base=c["base"], **k)  # noqa: E731
+    refs, norm = [call(c) for c in sets], moe.moe_prenorm_backward(h, h, w)
+    torch.cuda.synchronize()
+    sides, got, norms = [torch.cuda.Stream() for _ in sets], ([], []), []
+    for _ in range(10):
+        for i, side in enumerate(sides):
+            with torch.cuda.stream(side):
+                got[i].append(call(sets[i]))
+                norms.append(moe.moe_prenorm_backward(h, h, w))
+    torch.cuda.synchronize()
+    assert all(torch.equal(v, ref) for outs, ref in zip(got, refs) for v in outs)
+    assert all(torch.equal(a, b) for n in norms for a, b in zip(n, norm))
+    assert moe.moe_get_status() == 0
