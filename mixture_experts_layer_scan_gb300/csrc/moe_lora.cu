@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(256) k_lora_shrink(const LoraDev p) {
 // A CTA to a token and a run of output columns: G lanes share a column's row of B (16 bytes each),
 // and a warp walks 32 / G columns at a time, kExpandUnroll steps in flight.
 constexpr int kExpandUnroll = 8;
+constexpr int kExpandStep = 1 << 23;  // columns from a CTA's step to its next, at most (N is below 2^31 - 2^24)
 template <typename T, int G>
 __global__ void __launch_bounds__(256) k_lora_expand(const LoraDev p) {
   pdl_enter();
@@ -153,7 +154,8 @@ cudaError_t launch_few(const LoraDev& p, cudaStream_t s) {
   constexpr int kRun = 8 * (32 / G) * kExpandUnroll;
   const int rows = std::min(p.T, 1 << 16);
   MOE_LAUNCH(k_lora_shrink, dim3(rows, p.r / kShrinkRows), dim3(256), 0, s, p);
-  MOE_LAUNCH((k_lora_expand<T, G>), dim3(rows, std::min((p.N + kRun - 1) / kRun, 65535)), dim3(256), 0, s, p);
+  const int runs = std::min((p.N + kRun - 1) / kRun, std::min(kExpandStep / kRun, 65535));
+  MOE_LAUNCH((k_lora_expand<T, G>), dim3(rows, runs), dim3(256), 0, s, p);
   return cudaGetLastError();
 }
 template <typename T>

@@ -1,0 +1,36 @@
+"""What a GPU run of the adapters' kernels could not show without a fault, read from their source: counters that stay
+in range."""
+import re
+
+from test_block_bounded_waits_cpu import body, source
+
+
+def constants(text: str) -> dict:
+    """The file's integer constants, those made of others too."""
+    known = {}
+    for name, expr in re.findall(r"constexpr (?:int|long long) (\w+) = ([^;]+);", text):
+        try:
+            known[name] = int(eval(re.sub(r"(?<=\d)ll\b", "", expr).replace("/", "//"), {}, dict(known)))
+        except (NameError, SyntaxError):
+            pass
+    return known
+
+
+def test_columns_of_few_tokens_stay_below_2_31():
+    """The column counter of a token at a time is 32 bits wide, and a CTA goes gridDim.y runs of columns further at each
+    step: from the last column that a call may have, the sum has to stay in range."""
+    text = source("moe_lora.cu")
+    limit = constants(source("moe_api.cu"))["kBlockMaxDim"]
+    known = constants(text)
+    assert re.search(r"for \(int n0 = blockIdx\.y \* kRun \+ .*; n0 \+= gridDim\.y \* kRun\)", body(text, "k_lora_expand(const LoraDev p)"))
+    launch = body(text, "cudaError_t launch_few(const LoraDev& p, cudaStream_t s)")
+    assert "MOE_LAUNCH((k_lora_expand<T, G>), dim3(rows, runs), " in launch
+    grid = re.search(r"const int runs = (.*);", launch).group(1)
+    grid = grid.replace("std::min", "min").replace("/", "//").replace("p.N", "N")
+    for G in (1, 2, 4, 8, 16):
+        run = 8 * (32 // G) * known["kExpandUnroll"]
+        for N in (8, 4096, 1 << 30, limit - 1):
+            runs = eval(grid, {"min": min}, {**known, "kRun": run, "N": N})
+            assert 1 <= runs <= 65535
+            # the furthest start of a step, the step behind it, and the columns of a run
+            assert (N - 1) + runs * run + run < 1 << 31, (G, N, runs)
