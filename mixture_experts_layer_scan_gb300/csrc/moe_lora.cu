@@ -645,6 +645,7 @@ __global__ void __launch_bounds__(kExpandThreads)
         // (the products with the block before have to have ended)
         if (i && !__all_sync(0xffffffffu, mbar_wait_one(b.tfull + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, b.abort, p.status)))
           break;
+        tc_fence_after();  // (and the stores below come behind them)
         with_h = w.blk;
 #pragma unroll
         for (int u = 0; u < kHeld; ++u)

@@ -1,5 +1,5 @@
 """What a GPU run of the adapters' kernels could not show without a fault, read from their source: counters that stay
-in range."""
+in range, and the order of tensor memory's readers and writers."""
 import re
 
 from test_block_bounded_waits_cpu import body, source
@@ -18,7 +18,7 @@ def constants(text: str) -> dict:
 
 def test_columns_of_few_tokens_stay_below_2_31():
     """The column counter of a token at a time is 32 bits wide, and a CTA goes gridDim.y runs of columns further at each
-    step: from the last column that a call may have, the sum has to stay in range."""
+    step: from the last column that a call may have, the sum has to stay in range, and the order of tensor memory's readers and writers."""
     text = source("moe_lora.cu")
     limit = constants(source("moe_api.cu"))["kBlockMaxDim"]
     known = constants(text)
@@ -34,3 +34,15 @@ def test_columns_of_few_tokens_stay_below_2_31():
             assert 1 <= runs <= 65535
             # the furthest start of a step, the step behind it, and the columns of a run
             assert (N - 1) + runs * run + run < 1 << 31, (G, N, runs)
+
+
+def test_new_h_is_written_behind_the_products_with_the_old():
+    """An epilogue warp that puts the next block's h into tensor memory has waited for the products that read the
+    last one's; its stores are ordered behind that wait by a fence of their own."""
+    kernel = body(source("moe_lora.cu"), "k_lora_expand_tc(const __grid_constant__")
+    stores = [m.start() for m in re.finditer(r"tmem_st4\(", kernel)]
+    assert len(stores) == 2
+    wait = kernel.rfind("mbar_wait_one(b.tfull", 0, stores[0])
+    assert 0 < wait < kernel.find("tc_fence_after();", wait) < stores[0]
+    ready = kernel.index("mbar_arrive(b.done)", stores[1])
+    assert stores[1] < kernel.find("tmem_wait_st();", stores[1]) < kernel.find("tc_fence_before();", stores[1]) < ready
