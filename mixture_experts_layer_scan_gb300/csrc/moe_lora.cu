@@ -15,8 +15,8 @@
 //   expand   persistent over (block, tile of 256 bytes of output columns): h becomes the A operand in tensor
 //            memory, B's rows come by TMA, and the epilogue adds the base
 // A token's row of D depends on that token alone, so what padding rows of a block hold does not matter.
-// Bound by HBM: 8192 tokens of rank 64 through 4096 x 8192 take 83 us, 49 of them the expand kernel's tiles at 5.5 TB/s;
-// 777 of rank 32 through 2040 x 5000 27, mostly what three dependent launches cost.
+// Bound by HBM: 8192 tokens of rank 64 through 4096 x 8192 take 84 us, 49 of them the expand kernel's tiles at 5.5 TB/s;
+// 777 of rank 32 through 2040 x 5000 28, mostly what three dependent launches cost.
 // Two launches rather than clusters that exchange h: a CTA that holds tensor memory never waits for another
 // CTA, so calls on several streams cannot block one another.
 #include <algorithm>
@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(kShrinkThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cols = pow2_cols(p.rn);
   const uint32_t tmem = tc_setup(b, cols, 5, 1);
-  // Dependents launch once the permutation is complete (this kernel's own wait) and every CTA here holds its
-  // tensor memory: the expand kernel's CTAs take theirs before they wait for this kernel.
+  // Dependents launch once every CTA here holds its tensor memory: the expand kernel's CTAs take theirs before they wait
+  // for this kernel.
   pdl_launch_dependents();
   const int kb0 = split * p.kb_per, kb1 = min(kb0 + p.kb_per, p.kb_total);
   constexpr uint32_t kXBytes = kBlk * 128;
@@ -499,8 +499,9 @@ __global__ void __launch_bounds__(kExpandThreads)
   const TcBars b = tc_bars(smem, p.bar_off);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t tmem = tc_setup(b, kExpandCols, 1, 16);
-  // The permutation, base and the weights were complete before the preceding kernel let this one start; only
-  // its sums are not.
+  // (every thread, before it reads anything: the permutation and base are of kernels before the preceding one, and only
+  // this wait makes them visible here; reading them ahead of it took 777 tokens from 27.9 to 26.8 us, 8192 from 84.5 to 83.3)
+  pdl_wait();
   const int nblk = lora_blocks(p);
   const uint32_t hcols = (uint32_t)(p.rn / 2);  // columns of one part of h
   const uint32_t h0 = tmem + kBufs * kNT;
@@ -530,7 +531,6 @@ __global__ void __launch_bounds__(kExpandThreads)
         phase ^= 1u;
       }
     }
-    pdl_wait();
     pdl_launch_dependents();
     if (!ok && lane == 0) {
       const uint32_t from = issued > (uint32_t)p.stages ? issued - p.stages : 0u;
@@ -631,7 +631,6 @@ __global__ void __launch_bounds__(kExpandThreads)
       for (int u = 0; u < kHeld; ++u)
         if (group + 4 * u < pieces) held[u] = __ldcg(p.hp + ((size_t)blk * pieces + group + 4 * u) * kBlk + q * 32 + lane);
     };
-    pdl_wait();
     if (w.more() && w.blk < nblk) fetch(w.blk);
     const int last_blk = w.more() ? min(nblk - 1, (w.end - 1) / w.tiles) : 0;
     int had = -1, with_h = -1, si = 0;

@@ -1,5 +1,5 @@
 """What a GPU run of the adapters' kernels could not show without a fault, read from their source: counters that stay
-in range, and the order of tensor memory's readers and writers."""
+in range, the order of tensor memory's readers and writers, and what is read before a kernel's dependency wait."""
 import re
 
 from test_block_bounded_waits_cpu import body, source
@@ -18,7 +18,7 @@ def constants(text: str) -> dict:
 
 def test_columns_of_few_tokens_stay_below_2_31():
     """The column counter of a token at a time is 32 bits wide, and a CTA goes gridDim.y runs of columns further at each
-    step: from the last column that a call may have, the sum has to stay in range, and the order of tensor memory's readers and writers."""
+    step: from the last column that a call may have, the sum has to stay in range, the order of tensor memory's readers and writers, and what is read before a kernel's dependency wait."""
     text = source("moe_lora.cu")
     limit = constants(source("moe_api.cu"))["kBlockMaxDim"]
     known = constants(text)
@@ -46,3 +46,14 @@ def test_new_h_is_written_behind_the_products_with_the_old():
     assert 0 < wait < kernel.find("tc_fence_after();", wait) < stores[0]
     ready = kernel.index("mbar_arrive(b.done)", stores[1])
     assert stores[1] < kernel.find("tmem_wait_st();", stores[1]) < kernel.find("tc_fence_before();", stores[1]) < ready
+
+
+def test_nothing_of_an_earlier_kernel_is_read_ahead_of_the_wait():
+    """The wait for the preceding kernel is what makes the memory of all before it visible, to the thread that waits:
+    every thread of the tensor-core kernels passes it before it reads anything but the launch's own arguments."""
+    text = source("moe_lora.cu")
+    for name in ("k_lora_shrink_tc(const __grid_constant__", "k_lora_expand_tc(const __grid_constant__"):
+        kernel = body(text, name)
+        assert kernel.count("pdl_wait();") == 1
+        before = kernel[: kernel.index("pdl_wait();")]
+        assert "if (" not in before and "lora_blocks" not in before and "p." not in before.replace("p.bar_off", "")
