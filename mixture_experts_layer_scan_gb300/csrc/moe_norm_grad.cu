@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
         so *= ry;
       }
       r = dh ? rsqrtf(ee * p.inv_h + p.eps) : 0.f;
-      m = oe * r * p.inv_h;
+      m = dh ? oe * r * p.inv_h : 0.f;
       // sum over the row of scale D c, which is a token gate's gradient times r_y's inverse
       const float u = p.scale * (dh ? sd + r * se - r * r * m * so : sd);
       mean = u * p.inv_h;
@@ -161,8 +161,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
 #pragma unroll
       for (int i = 0; i < C2; ++i) {
         if constexpr (POST) x[i] = fma2(both(b), yc[i], mul2(both(p.res_scale), x[i]));  // out
-        acc_n[c][i] = fma2(d[i], mul2(x[i], r2), acc_n[c][i]);
-        D[i] = fma2(r2, e[i], fma2(rm, x[i], D[i]));
+        if (dh) {  // (without h nothing depends on out, which may be infinite or NaN)
+          acc_n[c][i] = fma2(d[i], mul2(x[i], r2), acc_n[c][i]);
+          D[i] = fma2(r2, e[i], fma2(rm, x[i], D[i]));
+        }
       }
       if constexpr (!POST) {
         rows.store(p.d_x, c, D);
