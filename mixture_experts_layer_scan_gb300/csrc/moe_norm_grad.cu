@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
           }
           acc_s[c][i] = fma2(z, n, acc_s[c][i]);
           z = mul2(z, cw[HOLD ? c : 0][i]);
-          D[i] = fma2(c1, y[i], mul2(ry2, z));  // d_y
+          D[i] = mul2(ry2, z);  // d_y, which without a norm does not depend on y
+          if (post) D[i] = fma2(c1, y[i], D[i]);
         }
         rows.store(p.d_y, c, D);
         if constexpr (FULL) {

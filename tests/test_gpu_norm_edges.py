@@ -57,3 +57,25 @@ def test_gradient_without_a_next_norm_does_not_see_x(moe, T, H, dtype, gate):
             assert same(got, ref), (post, nxt)
             assert not nxt or bool((got.d_next_w == 0).all())
     assert moe.moe_get_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", EDGES)
+def test_gradient_without_norms_sees_y_in_the_gate_alone(moe, T, H, dtype):
+    """out = res x + scale G y: d_x and d_y hold neither x nor y, and a gate's gradient holds y where it gates it."""
+    g = torch.Generator().manual_seed(T + H)
+    rows = (1, T // 2, T - 1)
+    for gate in ("none", "channel", "token", "full"):
+        d = inputs(T, H, DT[dtype], torch.float32, g, False, gate, False)
+        bad = spoil(d["y"], rows)
+        ref, got = grads(moe, d), grads(moe, d, y=bad)
+        assert torch.equal(got.d_x, ref.d_x) and torch.equal(got.d_y, ref.d_y), gate
+        if gate == "token":
+            keep = torch.ones(T, dtype=torch.bool, device="cuda")
+            keep[list(rows)] = False
+            assert torch.equal(got.d_gate[keep], ref.d_gate[keep]) and not bool(got.d_gate[~keep].isfinite().any())
+        elif gate == "full":
+            finite = bad.isfinite().cuda()
+            assert torch.equal(got.d_gate[finite], ref.d_gate[finite])
+            assert not bool(got.d_gate[~finite & (d["d_out"].cuda() != 0)].isfinite().any())
+    assert moe.moe_get_status() == 0
