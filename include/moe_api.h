@@ -424,7 +424,8 @@ MOE_API int moe_unpermute_backward(const void* d_out, const void* rows, int n_ro
  *   d_out and d_h.  The forward pass is recomputed: nothing has to be kept but its inputs.
  *   T = 0: the weights' gradients (and a channel gate's) are set to zero.
  * x, y, out, h, d_* of tokens have `dtype` (MOE_F32 or MOE_BF16); the weights w_dtype, either of the two as well.
- * Arithmetic is fp32 throughout, every result rounded once.  1 <= H <= 16384 (MOE_ERR_UNSUPPORTED above).
+ * Arithmetic is fp32 throughout, every result rounded once; a sigmoid and its slope beside bf16 rows are off by up to
+ * 2^-20 of themselves, and by 1.3 |gate| 2^-24 more for a full gate.  1 <= H <= 16384 (MOE_ERR_UNSUPPORTED above).
  * The gradients' workspace: moe_norm_workspace_size bytes, 256-byte aligned, contents ignored (the same for both
  * calls).  A token gate and its gradient 4-byte aligned, the other pointers 16. */
 enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 };

@@ -20,12 +20,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
   R rows(p, smem);
   __syncthreads();
   rows.start();
-  if constexpr (POST) rows.fetch_token(blockIdx.x);
+  if constexpr (KIND == N_POST) rows.fetch_token(blockIdx.x);
   float2 cw[HOLD && POST ? CH : 1][C2], nw[HOLD ? CH : 1][C2];
   if constexpr (HOLD) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if constexpr (POST) rows.factor(c, cw[c]);
+      if constexpr (POST) rows.template factor<KIND == N_POST>(c, cw[c]);
       if (next) rows.weight(p.next_w, p.w_f32, 0, c, nw[c]);
     }
   }
@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
     for (int c = 0; c < CH; ++c) {
       rows.load(S_X, c, o[c]);
       if constexpr (POST) {
-        if constexpr (!HOLD) rows.factor(c, cw[0]);
+        if constexpr (!HOLD) rows.template factor<KIND == N_POST>(c, cw[0]);
         float2 g[C2];
         rows.load(S_Y, c, y[c]);
         if constexpr (KIND == N_FULL) rows.full_gate(c, g);
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
         for (int e = 0; e < C2; ++e) {
           a1 = fma2(y[c][e], y[c][e], a1);
           y[c][e] = mul2(y[c][e], cw[HOLD ? c : 0][e]);
-          if constexpr (KIND == N_FULL) y[c][e] = mul2(y[c][e], g[e]);
+          if constexpr (KIND == N_FULL) y[c][e] = mul2(y[c][e], rows.gate_of(g[e]));
           a2 = fma2(o[c][e], y[c][e], a2);
           a3 = fma2(y[c][e], y[c][e], a3);
         }
@@ -59,7 +59,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
       float v[4] = {flat(a0), flat(a1), flat(a2), flat(a3)};
       block_sums(v, s2[0]);
       rows.refill(t);
-      b = p.scale * rows.token_gate(t);
+      b = p.scale;
+      if constexpr (KIND == N_POST) b *= rows.token_gate(t).x;
       if (post) b *= rsqrtf(v[1] * p.inv_h + p.eps);
       const float pp = p.res_scale * p.res_scale * v[0], qq = b * b * v[3], ee = pp + qq + 2.f * p.res_scale * b * v[2];
       r = ee;

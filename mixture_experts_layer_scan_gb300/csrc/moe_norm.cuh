@@ -67,13 +67,44 @@ __device__ __forceinline__ float load_one(const void* w, bool f32, size_t i) {
   return f32 ? static_cast<const float*>(w)[i] : bf16_bits_to_f32(static_cast<const uint16_t*>(w)[i]);
 }
 
-// bf16 rows take the approximate exponential and quotient (off by some 2^-21, far below a step of theirs): with the
-// rounded ones a full gate of 16384 x 4096 was bound by their instructions.
-template <typename T>
-__device__ __forceinline__ float sigmoid(float z) {
-  if constexpr (sizeof(T) == 2) return __fdividef(1.0f, 1.0f + __expf(-z));
-  return 1.0f / (1.0f + expf(-z));
+// exp(-a), a >= 0.  For bf16 rows in a few instructions: 2^t for the rounded product t = -a log2(e), times 1 + r ln(2) for
+// what that rounding left (a fused multiply-add gives a product's rounding error exactly; log2(e) in two parts).  Off by 2^-22;
+// 0 below 2^-126.  NEAR leaves r out and is off by 2^-22 + 1.3 a 2^-24.
+template <typename T, bool NEAR>
+__device__ __forceinline__ float exp_minus(float a) {
+  if constexpr (sizeof(T) == 4) return expf(-a);
+  constexpr float kLog2e = 1.44269502162933349609375f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;
+  float e;
+  if constexpr (NEAR) {
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-a * kLog2e));
+    return e;
+  }
+  asm("min.NaN.f32 %0, %0, 0f43000000;" : "+f"(a));  // (128, where e is 0: an infinite a would have no r)
+  const float t = -a * kLog2e, r = fmaf(-a, kRest, fmaf(-a, kLog2e, -t));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  return fmaf(e, r * kLn2, e);
 }
+// A quotient by a number from 1 to 2.  (bf16 rows: off by two units instead of a half)
+template <typename T>
+__device__ __forceinline__ float quotient(float a, float b) {
+  if constexpr (sizeof(T) == 4) return a / b;
+  return __fdividef(a, b);
+}
+// A gate's sigmoid s and its slope s (1 - s).  With e = exp(-|z|) and q = 1 / (1 + e), q and e q are the sigmoids of |z| and
+// -|z|, and their product the slope: nothing cancels where the gate is nearly open.
+template <typename T>
+__device__ __forceinline__ float2 sigmoid(float z) {
+  const float e = exp_minus<T, false>(fabsf(z)), q = quotient<T>(1.0f, 1.0f + e);
+  return make_float2(z >= 0.0f ? q : e * q, e * q * q);
+}
+// Both in one number w, for gates that wait in registers: the smaller of s and 1 - s, negative where that is 1 - s.
+template <typename T>
+__device__ __forceinline__ float gate_word(float z) {
+  const float e = exp_minus<T, true>(fabsf(z));
+  return copysignf(quotient<T>(e, 1.0f + e), -z);
+}
+__device__ __forceinline__ float word_gate(float w) { return w + __int_as_float(__float_as_int(w) >> 31 & 0x3f800000); }
+__device__ __forceinline__ float word_slope(float w) { return fmaf(-w, w, fabsf(w)); }
 
 // The sums of K <= 8 values over the CTA, in every thread, in a fixed order.  s: 8 floats a warp.
 template <int K>
@@ -343,41 +374,55 @@ struct Rows {
 #pragma unroll
     for (int c = 0; c < N; ++c) put(f, c, g[c]);
   }
-  __device__ __forceinline__ void squash(float2 (&g)[C2]) const {
+  // A gate by channels, and its slope (1 without a sigmoid).
+  __device__ __forceinline__ void channel_gate(int i, float2 (&g)[C2], float2 (&slope)[C2]) const {
+    weight(p.gate, p.gate_f32, 0, i, g);
+#pragma unroll
+    for (int e = 0; e < C2; ++e) slope[e] = both(1.f);
     if (p.sigmoid)
 #pragma unroll
-      for (int e = 0; e < C2; ++e) g[e] = make_float2(sigmoid<T>(g[e].x), sigmoid<T>(g[e].y));
-  }
-  __device__ __forceinline__ void channel_gate(int i, float2 (&g)[C2]) const {
-    weight(p.gate, p.gate_f32, 0, i, g);
-    squash(g);
+      for (int e = 0; e < C2; ++e) {
+        const float2 a = sigmoid<T>(g[e].x), b = sigmoid<T>(g[e].y);
+        g[e] = make_float2(a.x, b.x);
+        slope[e] = make_float2(a.y, b.y);
+      }
   }
   // The factor of the columns after the block: post_w times a gate by channels (1 where there is neither).
+  template <bool CHANNELS>
   __device__ __forceinline__ void factor(int i, float2 (&f)[C2]) const {
 #pragma unroll
     for (int e = 0; e < C2; ++e) f[e] = both(1.f);
     if (p.post_w) weight(p.post_w, p.w_f32, 0, i, f);
-    if (p.gate_kind == MOE_GATE_CHANNEL) {
-      float2 g[C2];
-      channel_gate(i, g);
+    if (CHANNELS && p.gate_kind == MOE_GATE_CHANNEL) {
+      float2 g[C2], slope[C2];
+      channel_gate(i, g, slope);
 #pragma unroll
       for (int e = 0; e < C2; ++e) f[e] = mul2(f[e], g[e]);
     }
   }
-  __device__ __forceinline__ void full_gate(int i, float2 (&g)[C2]) const {
-    if (p.gate_ring) load(S_GATE, i, g);
-    else weight(p.stream[S_GATE], p.gate_f32, at, i, g);
-    squash(g);
+  // A full gate (with a sigmoid as words), its value, and its slope where it has one.  bf16 rows take the near exponential:
+  // with the other the gradient of 8192 x 4096 took 122 us instead of 105 (told apart by the gate's type, 107; its forward
+  // pass of 2048 x 16384 86 instead of 80).
+  __device__ __forceinline__ void full_gate(int i, float2 (&w)[C2]) const {
+    if (p.gate_ring) load(S_GATE, i, w);
+    else weight(p.stream[S_GATE], p.gate_f32, at, i, w);
+    if (p.sigmoid)
+#pragma unroll
+      for (int e = 0; e < C2; ++e) w[e] = make_float2(gate_word<T>(w[e].x), gate_word<T>(w[e].y));
   }
-  // A token's gate, loaded a row ahead.
+  __device__ __forceinline__ float2 gate_of(float2 w) const {
+    return p.sigmoid ? make_float2(word_gate(w.x), word_gate(w.y)) : w;
+  }
+  __device__ __forceinline__ static float2 slope_of(float2 w) { return make_float2(word_slope(w.x), word_slope(w.y)); }
+  // A token's gate and its slope, loaded a row ahead.
   __device__ __forceinline__ void fetch_token(long t) {
     if (p.gate_kind == MOE_GATE_TOKEN && t < p.T) token = load_one(p.gate, p.gate_f32, t);
   }
-  __device__ __forceinline__ float token_gate(int t) {
-    if (p.gate_kind != MOE_GATE_TOKEN) return 1.0f;
+  __device__ __forceinline__ float2 token_gate(int t) {
+    if (p.gate_kind != MOE_GATE_TOKEN) return both(1.0f);
     const float g = token;
     fetch_token((long)t + gridDim.x);
-    return p.sigmoid ? sigmoid<T>(g) : g;
+    return p.sigmoid ? sigmoid<T>(g) : make_float2(g, 1.0f);
   }
 };
 

@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
   R rows(p, smem);
   __syncthreads();
   rows.start();
-  if constexpr (POST) rows.fetch_token(blockIdx.x);
+  if constexpr (POST && !FULL) rows.fetch_token(blockIdx.x);
   const bool dh = FAST || !POST || p.stream[S_DH], dout = FAST || p.stream[S_DOUT], post = FAST || p.post_w;
   float2 cw[HOLD ? CP : 1][C2], nw[HOLD ? CH : 1][C2], acc_n[CH][C2], acc_s[CP][C2];
 #pragma unroll
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
       if constexpr (POST) acc_s[c][e] = both(0.f);
     }
   auto weights = [&](int c, float2 (&f)[C2], float2 (&n)[C2]) {
-    if constexpr (POST) rows.factor(c, f);
+    if constexpr (POST) rows.template factor<!FULL>(c, f);
     if (dh) {
       rows.weight(p.next_w, p.w_f32, 0, c, n);
     } else {
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
 #pragma unroll
         for (int i = 0; i < C2; ++i) {
           yc[i] = mul2(y[i], cw[HOLD ? c : 0][i]);
-          if constexpr (FULL) yc[i] = mul2(yc[i], g[i]);
+          if constexpr (FULL) yc[i] = mul2(yc[i], rows.gate_of(g[i]));
         }
       }
       rows.load(S_DH, c, d, dh);
@@ -90,12 +90,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
         for (int i = 0; i < C2; ++i) dc = fma2(d[i], yc[i], dc);
       }
     }
-    float ry = 1.f, tok = 1.f, b = 0.f, r, m, mean = 0.f;  // r: 1 / rms of out; m: mean(e out r)
+    float ry = 1.f, tok = 1.f, tok_slope = 1.f, b = 0.f, r, m, mean = 0.f;  // r: 1 / rms of out; m: mean(e out r)
     if constexpr (POST) {
       float v[7] = {flat(xx), flat(yy), flat(xc), flat(cc), flat(xe), flat(ce), flat(dc)};
       block_sums(v, s2[0]);
       rows.refill(t);
-      tok = rows.token_gate(t);
+      if constexpr (!FULL) {
+        const float2 tg = rows.token_gate(t);
+        tok = tg.x;
+        tok_slope = tg.y;
+      }
       if (post) ry = rsqrtf(v[1] * p.inv_h + p.eps);
       b = p.scale * tok * ry;
       const float pp = p.res_scale * p.res_scale * v[0], qq = b * b * v[3];
@@ -137,8 +141,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
       // sum over the row of scale D c, which is a token gate's gradient times r_y's inverse
       const float u = p.scale * (dh ? sd + r * se - r * r * m * so : sd);
       mean = u * p.inv_h;
-      if (p.gate_kind == MOE_GATE_TOKEN && p.d_gate && threadIdx.x == 0)
-        static_cast<float*>(p.d_gate)[t] = p.sigmoid ? u * tok * (1.0f - tok) : u;
+      if (!FULL && p.gate_kind == MOE_GATE_TOKEN && p.d_gate && threadIdx.x == 0)
+        static_cast<float*>(p.d_gate)[t] = FAST ? u * tok_slope : u;
     } else {
       float v[2] = {flat(xx), flat(xe)};
       block_sums(v, s2[0]);
@@ -178,8 +182,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
           const float2 n = mul2(y[i], ry2);
           if constexpr (FULL) {  // d_gate, in place of out
             const float2 u = mul2(mul2(z, cw[HOLD ? c : 0][i]), n);
-            x[i] = p.sigmoid ? mul2(u, make_float2(g[i].x * (1.0f - g[i].x), g[i].y * (1.0f - g[i].y))) : u;
-            z = mul2(z, g[i]);
+            x[i] = p.sigmoid ? mul2(u, R::slope_of(g[i])) : u;
+            z = mul2(z, rows.gate_of(g[i]));
           }
           acc_s[c][i] = fma2(z, n, acc_s[c][i]);
           z = mul2(z, cw[HOLD ? c : 0][i]);
@@ -214,26 +218,32 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
   for (int c = 0; c < CH; ++c) {
     if (p.sum_next) rows.store_part(part + plane, c, acc_n[c]);
     if constexpr (POST) {
-      float2 f[C2], g[C2];
-      if (p.gate_kind == MOE_GATE_CHANNEL) rows.channel_gate(c, g);
-      if (p.sum_gate) {
+      float2 f[C2], g[C2], gs[C2];
+      if (!FULL && p.gate_kind == MOE_GATE_CHANNEL) rows.channel_gate(c, g, gs);
+      if (!FULL && p.sum_gate) {
 #pragma unroll
         for (int i = 0; i < C2; ++i) f[i] = both(1.f);
         if (p.post_w) rows.weight(p.post_w, p.w_f32, 0, c, f);
 #pragma unroll
-        for (int i = 0; i < C2; ++i) {
-          f[i] = mul2(f[i], acc_s[c][i]);
-          if (p.sigmoid) f[i] = mul2(f[i], make_float2(g[i].x * (1.0f - g[i].x), g[i].y * (1.0f - g[i].y)));
-        }
+        for (int i = 0; i < C2; ++i) f[i] = mul2(mul2(f[i], acc_s[c][i]), gs[i]);
         rows.store_part(part + 2 * plane, c, f);
       }
       if (p.sum_post) {
 #pragma unroll
-        for (int i = 0; i < C2; ++i) f[i] = p.gate_kind == MOE_GATE_CHANNEL ? mul2(acc_s[c][i], g[i]) : acc_s[c][i];
+        for (int i = 0; i < C2; ++i) f[i] = !FULL && p.gate_kind == MOE_GATE_CHANNEL ? mul2(acc_s[c][i], g[i]) : acc_s[c][i];
         rows.store_part(part, c, f);
       }
     }
   }
+  // A token gate's slope, behind the rows: in the loop it would hold a register (8192 x 4096 without the next norm 81.4 us, so
+  // 78.7).  FAST, where the registers lie otherwise, has it there (8192 x 4096: 72 us, so 85).
+  if constexpr (KIND == N_POST && !FAST)
+    if (p.gate_kind == MOE_GATE_TOKEN && p.d_gate && p.sigmoid) {
+      __syncthreads();
+#pragma unroll 1
+      for (long t = blockIdx.x + (long)threadIdx.x * gridDim.x; t < p.T; t += (long)blockDim.x * gridDim.x)
+        static_cast<float*>(p.d_gate)[t] *= sigmoid<T>(load_one(p.gate, p.gate_f32, t)).y;
+    }
 }
 
 // out[z][c] = sum_g part[z][g][lead(g) + c]: COLS columns to a CTA, the runs of rows of its threads added in their
