@@ -456,7 +456,8 @@ MOE_API int moe_postnorm_backward(const void* d_out, const void* d_h, const void
  *   out[t] = base[t] + scale[l] * b[l] . (a[l] . x[t]),  l = ids[t];  out[t] = base[t] where ids[t] is -1
  *   x [T][K], a [L][rank][K], b [L][N][rank] bf16;  ids [T] int32, in any order;  scale [L] fp32 (null: 1);
  *   base [T][N] of out's type, the projection's output (null: 0; may be out itself);  out [T][N] MOE_BF16 or MOE_F32
- * Sums are fp32, out is rounded once.  An id outside [-1, L) counts as -1 and is flagged MOE_ERR_DEVICE_INDEX.
+ * Sums are fp32, out is rounded once; for MOE_BF16 a . x may enter the second product off by 2^-16 of itself (as two bf16
+ * parts; for MOE_F32 with all of its bits).  An id outside [-1, L) counts as -1 and is flagged MOE_ERR_DEVICE_INDEX.
  * An adapter of lower rank is padded with zero rows of a and zero columns of b.  What an adapter that no
  * token names holds does not matter.
  * T >= 0, K, N, rank, L >= 1; rank <= 128 and K, N, rank multiples of 8 (MOE_ERR_UNSUPPORTED otherwise); T, K

@@ -10,8 +10,8 @@
 //   shrink   a CTA to a block and a run of K: D[128 tokens x r] += X A^T over blocks of 64 K, A by TMA, X's rows by
 //            16-byte asynchronous copies (TMA gathers of four rows of 128 bytes took about 1 us for a block);
 //            the CTAs of a block are a cluster and add up their fp32 sums in the order of K through distributed
-//            shared memory: h = s A x, as bf16 parts that add up to it (2 for a bf16 output: off by 2^-17 of
-//            h at most; 3 for an fp32 one: 2^-25)
+//            shared memory: h = s A x, as bf16 parts that add up to it (2 for a bf16 output: off by 2^-16 of
+//            h at most; 3 for an fp32 one: all of its bits)
 //   expand   persistent over (block, tile of 256 bytes of output columns): h becomes the A operand in tensor
 //            memory, B's rows come by TMA, and the epilogue adds the base
 // A token's row of D depends on that token alone, so what padding rows of a block hold does not matter.
@@ -273,7 +273,8 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// 8 columns of a row of h from c on, scaled and as `parts` bf16 numbers that add up to each
+// 8 columns of a row of h from c on, scaled and as `parts` bf16 numbers that add up to each: all but the last cut off, not
+// rounded, so that none of a finite h is infinite
 __device__ __forceinline__ void lora_store_h(const LoraTcDev& p, int blk, int row, int c, float s, float (&h)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) h[e] = c + e < p.r ? h[e] * s : 0.f;
@@ -282,7 +283,8 @@ __device__ __forceinline__ void lora_store_h(const LoraTcDev& p, int blk, int ro
     uint32_t u[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      u[e] = pack_bf16x2(h[2 * e], h[2 * e + 1]);
+      u[e] = part + 1 < p.parts ? __byte_perm(__float_as_uint(h[2 * e]), __float_as_uint(h[2 * e + 1]), 0x7632)
+                                : pack_bf16x2(h[2 * e], h[2 * e + 1]);
       const float lo = bf16_bits_to_f32(u[e] & 0xffffu), hi = bf16_bits_to_f32(u[e] >> 16);
       h[2 * e] = isinf(lo) ? 0.f : h[2 * e] - lo;  // (an infinite h is its first part alone, not inf - inf)
       h[2 * e + 1] = isinf(hi) ? 0.f : h[2 * e + 1] - hi;

@@ -1,0 +1,49 @@
+"""Adapters whose numbers leave the ordinary: infinite weights, products near the end of fp32, results that need all of fp32.
+The tensor cores and the path of a token at a time give the same answers."""
+import pytest
+import torch
+
+from test_gpu_lora import DT, formula, make, sorts
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+# (tokens, K, N, rank, adapters), whether the tokens are sorted by adapter and multiplied on the tensor cores
+PATHS = [((5, 64, 264, 16, 3), False), ((4000, 64, 1032, 16, 3), True), ((1030, 72, 520, 128, 2), True),
+         ((3000, 64, 1032, 24, 6), True)]
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import mixture_experts_layer_scan_gb300 as m
+
+    assert torch.cuda.is_available()
+    return m
+
+
+def call(moe, d, base, dtype, **kw):
+    c = {n: v.cuda() for n, v in d.items()}
+    return moe.moe_lora(c["x"], c["a"], c["b"], c["ids"], scale=c["scale"], base=None if base is None else base.cuda(),
+                        out_dtype=dtype, **kw).cpu()
+
+
+@pytest.mark.parametrize("out_t", ["bf16", "f32"])
+@pytest.mark.parametrize("size,tc", PATHS)
+def test_product_between_the_largest_bf16_and_the_largest_fp32(moe, size, tc, out_t):
+    """A x is finite in fp32 though it rounds to an infinite bf16; b brings it back into range.  h = 511.5 2^119 exactly,
+    b a power of two: the result is h's, off by its type's rounding and by 2^-16 where a bf16 result takes h as two parts."""
+    T, K, N, r, L = size
+    assert sorts(moe, *size) == tc
+    d = make(*size, seed=T, none=0.0)
+    d["x"].zero_(), d["a"].zero_(), d["b"].zero_()
+    d["x"][:, 0], d["x"][:, 1] = 2.0 ** 60, 2.0 ** 52
+    d["a"][:, 1, 0], d["a"][:, 1, 1] = 255 * 2.0 ** 60, 192 * 2.0 ** 60  # (255 + 0.75) 2^120
+    d["b"][:, :, 1] = 2.0 ** -100
+    d["x"][1::2] = -d["x"][1::2]
+    d["scale"][:] = 1.0
+    want = 255.75 * 2.0 ** 20
+    got = call(moe, d, None, DT[out_t]).double()
+    sign = torch.where(torch.arange(T) % 2 == 1, -1.0, 1.0)[:, None].double()
+    tol = (torch.finfo(DT[out_t]).eps / 2 + (2.0 ** -16 if out_t == "bf16" else 2.0 ** -23)) * want
+    assert bool(((got - sign * want).abs() <= tol).all())
+    assert moe.moe_get_status() == 0
