@@ -273,8 +273,16 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// What is left of h behind its part.
+__device__ __forceinline__ float lora_rest(float h, float part) {
+  if (isinf(part)) return copysignf(1.0f, part);
+  const float rest = h - part;
+  return rest == 0.0f ? part * 0x1p-32f : rest;
+}
+
 // 8 columns of a row of h from c on, scaled and as `parts` bf16 numbers that add up to each: all but the last cut off, not
-// rounded, so that none of a finite h is infinite
+// rounded, so that none of a finite h is infinite and all have its sign.  Where nothing is left for one, it is 2^-32 of the
+// one before (of an infinite one 1), so that with an infinite b no product is NaN (an h below 2^-62 still gives one).
 __device__ __forceinline__ void lora_store_h(const LoraTcDev& p, int blk, int row, int c, float s, float (&h)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) h[e] = c + e < p.r ? h[e] * s : 0.f;
@@ -286,8 +294,8 @@ __device__ __forceinline__ void lora_store_h(const LoraTcDev& p, int blk, int ro
       u[e] = part + 1 < p.parts ? __byte_perm(__float_as_uint(h[2 * e]), __float_as_uint(h[2 * e + 1]), 0x7632)
                                 : pack_bf16x2(h[2 * e], h[2 * e + 1]);
       const float lo = bf16_bits_to_f32(u[e] & 0xffffu), hi = bf16_bits_to_f32(u[e] >> 16);
-      h[2 * e] = isinf(lo) ? 0.f : h[2 * e] - lo;  // (an infinite h is its first part alone, not inf - inf)
-      h[2 * e + 1] = isinf(hi) ? 0.f : h[2 * e + 1] - hi;
+      h[2 * e] = lora_rest(h[2 * e], lo);
+      h[2 * e + 1] = lora_rest(h[2 * e + 1], hi);
     }
     dst[(size_t)part * (p.rn / 8) * kBlk] = make_uint4(u[0], u[1], u[2], u[3]);
   }

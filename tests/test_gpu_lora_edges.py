@@ -29,6 +29,36 @@ def call(moe, d, base, dtype, **kw):
 
 @pytest.mark.parametrize("out_t", ["bf16", "f32"])
 @pytest.mark.parametrize("size,tc", PATHS)
+def test_infinite_weights_of_b(moe, size, tc, out_t):
+    """An infinite element of b times h is infinite with h's sign, whatever h is made of; two of unlike signs, or one beside
+    an h of exactly 0, give NaN; a NaN gives NaN; other columns are as the formula has them."""
+    T, K, N, r, L = size
+    assert sorts(moe, *size) == tc
+    d = make(*size, seed=T)
+    d["ids"][:4] = torch.tensor([0, 1, 0, -1], dtype=torch.int32)
+    d["x"][2] = 0.0                                   # h = 0
+    d["b"][:, 3, 1], d["b"][:, 70, 2], d["b"][0, N - 1, r - 1] = INF, -INF, INF
+    d["b"][1, 8, 0], d["b"][1, 8, 5] = INF, -INF      # of h's unlike or like signs
+    d["b"][0, 40, 4] = float("nan")
+    d["a"][:, 7] = 0.0                                # an h of exactly 0 in every token
+    d["b"][:, 100, 7] = INF
+    d["x"][:, 1:] = torch.where(torch.arange(T)[:, None] % 5 == 4, 0.0, d["x"][:, 1:].float()).to(torch.bfloat16)
+    d["x"][4::5, 0], d["a"][:, :7, 0] = 1.0, d["a"][:, :7, 0].abs() + 0.5  # every fifth token: h is one bf16 number
+    d["scale"][:] = 1.0
+    for base in (None, d["base"].to(DT[out_t])):
+        ref, mag = formula(d, base, d["scale"])
+        got = call(moe, d, base, DT[out_t]).double()
+        assert torch.equal(got.isnan(), ref.isnan())
+        assert torch.equal(torch.where(got.isinf(), got.sign(), 0.0), torch.where(ref.isinf(), ref.sign(), 0.0))
+        ok = ref.isfinite()
+        # (the tolerance of ordinary values: bf16 parts of h, and fp32 sums)
+        tol = torch.finfo(DT[out_t]).eps / 2 * ref.abs() + ((K + r + 4) * 2.0 ** -24 + 2.0 ** -16) * mag
+        assert bool(((got - ref).abs() <= tol)[ok].all())
+    assert moe.moe_get_status() == 0
+
+
+@pytest.mark.parametrize("out_t", ["bf16", "f32"])
+@pytest.mark.parametrize("size,tc", PATHS)
 def test_product_between_the_largest_bf16_and_the_largest_fp32(moe, size, tc, out_t):
     """A x is finite in fp32 though it rounds to an infinite bf16; b brings it back into range.  h = 511.5 2^119 exactly,
     b a power of two: the result is h's, off by its type's rounding and by 2^-16 where a bf16 result takes h as two parts."""
