@@ -77,3 +77,35 @@ def test_product_between_the_largest_bf16_and_the_largest_fp32(moe, size, tc, ou
     tol = (torch.finfo(DT[out_t]).eps / 2 + (2.0 ** -16 if out_t == "bf16" else 2.0 ** -23)) * want
     assert bool(((got - sign * want).abs() <= tol).all())
     assert moe.moe_get_status() == 0
+
+
+@pytest.mark.parametrize("size,tc", PATHS)
+def test_results_in_32_bits_hold_all_of_h(moe, size, tc):
+    """h = c0 + c1 2^-8 + c2 2^-16 with odd c of 8 bits has 24, all of which reach an fp32 result: K sums without a
+    rounding, one b of 1.  On the CUDA cores the result is h; the tensor cores may lose a unit (2^-23) when they add
+    the parts of h.  h as two bf16 parts would not do, however they are rounded."""
+    T, K, N, r, L = size
+    assert sorts(moe, *size) == tc
+    g = torch.Generator().manual_seed(T)
+    d = make(*size, seed=T, none=0.0)
+    d["x"].zero_(), d["a"].zero_(), d["b"].zero_()
+    c = torch.randint(64, 128, (T, 3), generator=g) * 2 + 1
+    x = c.double() * torch.tensor([1.0, 2.0 ** -8, 2.0 ** -16], dtype=torch.float64)
+    at = [0, K // 2, K - 1]
+    d["x"][:, at] = x.to(torch.bfloat16)
+    assert torch.equal(d["x"][:, at].double(), x)
+    row, col = r - 3, torch.arange(0, N, 3)
+    d["a"][:, row, at] = 1.0
+    for l in range(L):
+        d["b"][l, col, row] = (-1.0) ** l
+    d["scale"][:] = 1.0
+    got = call(moe, d, None, torch.float32).double()
+    want = (x.sum(1) * (1 - 2 * (d["ids"] % 2)))[:, None].expand(T, N).clone()
+    want[:, torch.arange(N) % 3 != 0] = 0.0
+    assert torch.equal(want.float().double(), want)
+    h = x.sum(1)
+    for first in (h.bfloat16().double(), (h.float().view(torch.int32) & -65536).view(torch.float32).double()):
+        assert float(((h - first - (h - first).bfloat16().double()).abs() / h).max()) > 2.0 ** -20
+    err = (got - want).abs() / x.sum(1)[:, None]
+    assert float(err.max()) <= (2.0 ** -23 if tc else 0.0)
+    assert moe.moe_get_status() == 0
