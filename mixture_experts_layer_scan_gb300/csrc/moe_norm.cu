@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ Nor
         rows.store(p.h, c, o[c]);
       }
     }
-    rows.close(t);
+    rows.close();
   }
   rows.drain();
 }

@@ -171,13 +171,13 @@ struct Rows {
   int k, stage;                  // rows so far; the present one's place
   uint32_t phase, first;         // first: this thread's first unit in the present stage
   size_t at;                     // element offset of the present row
-  bool ok, refilled;
+  bool ok;
   float token;                   // the next row's gate
   int place[S_MAX];              // of a stream among those of a stage
   uint32_t in[ODD ? NV : 1];     // which elements of a unit are in the row: the same in every row, so found once
 
   __device__ __forceinline__ Rows(const NormDev& q, uint8_t* smem)
-      : p(q), lead(0), behind(0), k(0), stage(0), phase(0), first(0), at(0), ok(true), refilled(false), token(1.0f) {
+      : p(q), lead(0), behind(0), k(0), stage(0), phase(0), first(0), at(0), ok(true), token(1.0f) {
     if (ODD) lead = (int)((size_t)blockIdx.x * p.H % N);
     units = (lead + p.H + N - 1) / N;
     if constexpr (ODD) {
@@ -240,7 +240,6 @@ struct Rows {
   __device__ __forceinline__ void open(int t) {
     at = (size_t)t * p.H;
     if constexpr (RING) {
-      refilled = false;
       if (ok) ok = mbar_wait_one(bars + 8 * stage, phase, abort, p.status);
       first = buf + (uint32_t)(stage * p.streams) * p.pitch + threadIdx.x * 16;
       if (ODD && min(p.T - 1 - t, N) * p.H < behind) last_unit();
@@ -261,20 +260,14 @@ struct Rows {
   // Called behind a barrier in every row: the row before has been read by all.
   __device__ __forceinline__ void refill(int t) {
     if constexpr (RING) {
-      if (refilled) return;
-      refilled = true;
       if (threadIdx.x == 0 && k > 0) {
         const long next = t + (long)(p.stages - 1) * gridDim.x;
         if (next < p.T) issue((int)next, stage == 0 ? p.stages - 1 : stage - 1);
       }
     }
   }
-  __device__ __forceinline__ void close(int t) {
+  __device__ __forceinline__ void close() {
     if constexpr (RING) {
-      if (!refilled) {  // (a row without a sum)
-        __syncthreads();
-        refill(t);
-      }
       ++k;
       if (++stage == p.stages) {
         stage = 0;

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
         }
       }
     }
-    rows.close(t);
+    rows.close();
   }
   rows.drain();
   // partial sums
