@@ -106,7 +106,7 @@ __device__ __forceinline__ float gate_word(float z) {
 __device__ __forceinline__ float word_gate(float w) { return w + __int_as_float(__float_as_int(w) >> 31 & 0x3f800000); }
 __device__ __forceinline__ float word_slope(float w) { return fmaf(-w, w, fabsf(w)); }
 
-// The sums of K <= 8 values over the CTA, in every thread, in a fixed order.  s: 8 floats a warp.
+// The sums of K <= 8 values over the CTA, in every thread, in a fixed order, and a barrier of its threads.  s: 8 floats a warp.
 template <int K>
 __device__ __forceinline__ void block_sums(float (&v)[K], float* s) {
 #pragma unroll
@@ -114,7 +114,10 @@ __device__ __forceinline__ void block_sums(float (&v)[K], float* s) {
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  if (warps == 1) return;
+  if (warps == 1) {
+    __syncwarp();  // (the row before may be overwritten behind this: a shuffle alone orders no reads)
+    return;
+  }
   if (lane == 0) {
     float* at = s + (threadIdx.x >> 5) * 8;
 #pragma unroll
