@@ -780,7 +780,8 @@ int grid_for(size_t work, int threads, int cap_blocks = 152 * 16) {
 }  // namespace
 
 // Long batches: 16 CTAs, where the device holds such a cluster with the most shared memory that the kernel takes.
-// (65536 pairs over 64 experts: 14.1 us with 8, 9.7 with 16; 131072 28.6 and 14.1.)
+// (65536 pairs over 64 experts: 14.1 us with 8, 9.7 with 16; 131072 28.6 and 14.1.  Beside a stream that moves rows, with what
+// the call waits for its SMs: 65536 39 and 29, 131072 74 and 37; beside one of products or norms, whose CTAs it waits for, the same.)
 constexpr long kAlignWidePairs = 16384;
 static bool wide_cluster(int dev) {
   static int known[64] = {};  // 1: no, 2: yes
