@@ -20,6 +20,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
   using R = Rows<T, NV, RING, FAST, ODD>;
   constexpr int N = R::N, C2 = R::C2, CH = NV, CP = KIND != N_PRE ? CH : 1;
   constexpr bool POST = KIND != N_PRE, FULL = KIND == N_FULL, HOLD = THREADS <= 512;
+  // A token gate's slope, behind the rows: in the loop it would hold a register (8192 x 4096 without the next norm 81.4 us, so
+  // 78.7).  FAST, where the registers lie otherwise, has it there (8192 x 4096: 72 us, so 85), and so have few rows, for which
+  // a way to memory and back counts (64 x 4096 6.2 us, so 6.7).
+  constexpr bool BEHIND = KIND == N_POST && RING && !FAST;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float sums[2][2][THREADS / 4];
   R rows(p, smem);
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
       const float u = p.scale * (dh ? sd + r * se - r * r * m * so : sd);
       mean = u * p.inv_h;
       if (!FULL && p.gate_kind == MOE_GATE_TOKEN && p.d_gate && threadIdx.x == 0)
-        static_cast<float*>(p.d_gate)[t] = FAST ? u * tok_slope : u;
+        static_cast<float*>(p.d_gate)[t] = BEHIND ? u : u * tok_slope;
     } else {
       float v[2] = {flat(xx), flat(xe)};
       block_sums(v, s2[0]);
@@ -235,9 +239,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_g
       }
     }
   }
-  // A token gate's slope, behind the rows: in the loop it would hold a register (8192 x 4096 without the next norm 81.4 us, so
-  // 78.7).  FAST, where the registers lie otherwise, has it there (8192 x 4096: 72 us, so 85).
-  if constexpr (KIND == N_POST && !FAST)
+  if constexpr (BEHIND)
     if (p.gate_kind == MOE_GATE_TOKEN && p.d_gate && p.sigmoid) {
       __syncthreads();
 #pragma unroll 1
