@@ -395,6 +395,7 @@ MOE_API int moe_gemm_block(const void* a, const float* a_scale, const void* w, c
  *   (not computed); rows may be null without d_w.  With sorted_ids and num_post_pad (both or neither) padding
  *   rows of d_rows below *num_post_pad become zero; other rows that no pair names are left as they were.  The
  *   entries of row_of in range have to differ.  d_rows may be rows.
+ * T = 0: nothing is written, the maps and counts included.
  * x, rows, out, d_x, d_out and d_rows have `dtype` (MOE_F32 or MOE_BF16); weights and d_w are fp32.  1 <= H < 2^25.
  * topk_w, row_of and d_w 4-byte aligned, the other pointers 16.  Limits as moe_align; n_rows >= 0. */
 MOE_API int moe_permute(const void* x, const int32_t* topk_ids, int T, int H, int E, int topk, int block,

@@ -15,7 +15,7 @@
 //   expand   persistent over (block, tile of 256 bytes of output columns): h becomes the A operand in tensor
 //            memory, B's rows come by TMA, and the epilogue adds the base
 // A token's row of D depends on that token alone, so what padding rows of a block hold does not matter.
-// Bound by HBM: 8192 tokens of rank 64 through 4096 x 8192 take 84 us, 49 of them the expand kernel's tiles at 5.5 TB/s;
+// Bound by HBM: 8192 tokens of rank 64 through 4096 x 8192 take 85 us, 50 of them the expand kernel's tiles at 5.4 TB/s;
 // 777 of rank 32 through 2040 x 5000 28, mostly what three dependent launches cost.
 // Two launches rather than clusters that exchange h: a CTA that holds tensor memory never waits for another
 // CTA, so calls on several streams cannot block one another.
@@ -473,7 +473,7 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
 }
 
 // The tiles of one CTA: an equal run of the (block, tile) pairs.  (Neighbouring tiles to neighbouring CTAs, so that
-// what is in flight lies together in memory, was slower: 120 us instead of 91.)
+// what is in flight lies together in memory, was slower: a call of 8192 tokens of rank 64 took 120 us where it then took 92.)
 struct LoraWalk {
   int blk, tile, at, end, tiles;
   __device__ __forceinline__ LoraWalk(const LoraTcDev& p, int nblk) {  // (of the first nblk blocks)
@@ -495,7 +495,7 @@ struct LoraWalk {
 };
 
 // Persistent; a CTA's two sets of epilogue warps take its tiles in turn (a warp's way through a tile is a chain
-// of latencies: with one set 91 us for 8192 x 8192 bf16).  A
+// of latencies: a call of 8192 tokens of rank 64 took 113 us with one set, 92 with two).  A
 // warp owns 32 rows x 128 bytes of a tile: it copies that piece of base into shared memory ahead of time,
 // adds D there with a row to a thread, and stores it with 8 lanes to a row, without a barrier beyond its own.
 template <typename T, int PARTS>
@@ -741,9 +741,9 @@ LoraPlan lora_plan(int T, int K, int N, int r, int L) {
   LoraPlan q = {};
   const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   // Which path, by what each was measured to cost (us).  A token at a time: 5, and the adapters' rows of every
-  // token at 9 TB/s (mostly from L2: 512 tokens of rank 8 through 4096 x 4096 12.2, 256 of rank 64 35, 1024 of rank
-  // 16 42, 256 of rank 128 through 8192 x 8192 119).  Tensor cores: 13, every adapter's rows once from memory, and
-  // 0.009 for each output tile of a block, however few its tokens (the same four: 18.6, 21.2, 36, 33).
+  // token at 9 TB/s (mostly from L2: with 16 adapters 512 tokens of rank 8 through 4096 x 4096 11.9, 256 of rank 64 35, 1024
+  // of rank 16 41, 256 of rank 128 through 8192 x 8192 119).  Tensor cores: 13, every adapter's rows once from memory, and
+  // 0.009 for each output tile of a block, however few its tokens (the same four: 19.9, 22, 21.3, 35).
   const long named = std::min(L, T), blocks = std::max(named, T / kBlk + named / 2 + 1);  // (as far as T and L tell)
   const double adapter = 2.0 * r * ((double)K + N);
   const double one_by_one = 5.0 + T * adapter / 9e6;

@@ -7,7 +7,7 @@ namespace {
 
 // The sums' shared memory alternates from row to row: what a row wrote is overwritten behind the next row's barrier.
 // FAST: whole units in every thread, and both norms: nothing is asked for each unit.
-// 16384 x 4096 bf16: postnorm 87.5 us (6.1 TB/s, 90 % of a copy's rate), prenorm 46; one row 1.7 us.
+// 16384 x 4096 bf16: postnorm 88.6 us (6.1 TB/s, 89 % of a copy's rate), prenorm 46.6; one row 1.7 us.
 template <typename T, int NV, int KIND, bool RING, int THREADS, bool FAST, bool ODD>
 __global__ void __launch_bounds__(THREADS, 1) k_norm(const __grid_constant__ NormDev p) {
   pdl_enter();

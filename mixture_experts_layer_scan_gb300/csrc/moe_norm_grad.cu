@@ -12,7 +12,7 @@ constexpr int kTwoCtas = 320;
 // With z = scale G D (G a token's gate) and cw the columns' factor: d_post_w = sum_t z gate n and d_gate = sum_t z n post_w.
 // For a gate by channels both are sum_t z n times the other factor, and one sum is kept.
 // FAST: whole units in every thread, both norms and both incoming gradients: nothing is asked for each unit.
-// 8192 x 4096 bf16: postnorm 72 us with the sums over CTAs (5.6 TB/s), prenorm 36; 4096 x 2047, off the 16-byte grid,
+// 8192 x 4096 bf16: postnorm 72 us with the sums over CTAs (5.6 TB/s), prenorm 37; 4096 x 2047, off the 16-byte grid,
 // prenorm 17.7 (4096 x 2048: 15.3).
 template <typename T, int NV, int KIND, bool RING, int THREADS, bool FAST, bool ODD>
 __global__ void __launch_bounds__(THREADS, THREADS == kTwoCtas ? 2 : 1) k_norm_grad(const __grid_constant__ NormDev p) {
