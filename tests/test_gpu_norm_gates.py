@@ -56,3 +56,25 @@ def test_gradients_in_32_bits_take_the_gate_in_32_bits(moe, gate, gate_dtype):
         ref = Ref(d["x"], d["y"], d["post_w"], d["gate"], True, 0.5, 1.25, None, d["d_out"], None)
         got = grads(moe, d, True).d_post_w
         within(got, ref.d_post_w, (2.0 ** -17 if gate == "full" else 2.0 ** -19) * ref.d_post_w.abs(), f"d_post_w at {z}")
+
+
+@pytest.mark.parametrize("gate", ["channel", "token", "full"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(9, 264), (700, 1024), (700, 2047), (5, 16384)])
+def test_infinite_gates_are_saturated_ones(moe, T, H, dtype, gate):
+    """exp(-10^4) is 0 in fp32: a gate of it and an infinite one are open or shut alike, bit for bit; a NaN is one."""
+    g = torch.Generator().manual_seed(T + H)
+    d = inputs(T, H, DT[dtype], torch.float32, g, True, gate, True)
+    ends = [torch.where(torch.arange(d["gate"].numel()) % 2 == 0, v, -v).view(d["gate"].shape).to(DT[dtype])
+            for v in (1e4, float("inf"))]
+    for a, b in zip(*(grads(moe, {**d, "gate": v}, True) for v in ends)):
+        assert bool(a.isfinite().all()) and torch.equal(a, b)
+    kw = dict(post_w=d["post_w"].cuda(), sigmoid=True, next_w=d["next_w"].cuda())
+    a, b = (moe.moe_postnorm(d["x"].cuda(), d["y"].cuda(), gate=v.cuda(), **kw) for v in ends)
+    assert all(bool(u.isfinite().all()) and torch.equal(u, v) for u, v in zip(a, b))
+    bad = d["gate"].clone()
+    bad.view(-1)[0] = float("nan")
+    out = moe.moe_postnorm(d["x"].cuda(), d["y"].cuda(), gate=bad.cuda(), **kw)[0]
+    assert bool({"channel": out[:, 0], "token": out[0], "full": out[0, :1]}[gate].isnan().all())
+    assert bool(grads(moe, {**d, "gate": bad}, True).d_gate.view(-1)[0].isnan())
+    assert moe.moe_get_status() == 0
